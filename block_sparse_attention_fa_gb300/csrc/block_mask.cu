@@ -14,6 +14,10 @@
 //   causal   i >= j        : some pair  <=> r1 >= c0;  all pairs <=> r0 >= c1
 //   window   0 <= i-j <= W : i - j spans [r0 - c1, r1 - c0]; some pair <=> that
 //                            range meets [0, W]; all pairs <=> it lies inside
+//   sinks    i >= j and (i-j <= W or j < S): some pair <=> r1 >= c0 and (the
+//                            window's test or c0 < S); all pairs <=> r0 >= c1
+//                            and the columns past the sinks, if any, lie within
+//                            the window of the last row
 //   prefix   j < P or i>=j : some pair  <=> c0 < P or r1 >= c0;
 //                            all pairs  <=> c1 < P or r0 >= c1
 //   document seg[i]==seg[j]: ids are non-decreasing, so the q rows carry the
@@ -58,6 +62,12 @@ __device__ __forceinline__ TileClass classify(const MaskParams& m, const int32_t
         case FA_MASK_SLIDING_WINDOW: {
             const long long dmin = (long long)r0 - c1, dmax = (long long)r1 - c0;
             return {dmax >= 0 && dmin <= m.window, dmin >= 0 && dmax <= m.window};
+        }
+        case FA_MASK_SINK_WINDOW: {
+            const long long dmin = (long long)r0 - c1;
+            const bool any = r1 >= c0 && (dmin <= m.window || c0 < m.prefix_len);
+            const long long past = c0 > m.prefix_len ? c0 : m.prefix_len;   // first column that is no sink
+            return {any, r0 >= c1 && (past > c1 || r1 - past <= m.window)};
         }
         case FA_MASK_PREFIX_LM:
             return {c0 < m.prefix_len || r1 >= c0, c1 < m.prefix_len || r0 >= c1};

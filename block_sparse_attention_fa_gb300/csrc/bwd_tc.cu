@@ -329,6 +329,7 @@ __device__ __forceinline__ bool tc_visible(const BwdParams& p, int b, int i, int
         case FA_MASK_CAUSAL: return i >= j;
         case FA_MASK_SLIDING_WINDOW: return i >= j && i - j <= p.mask.window;
         case FA_MASK_PREFIX_LM: return j < p.mask.prefix_len || i >= j;
+        case FA_MASK_SINK_WINDOW: return i >= j && (i - j <= p.mask.window || j < p.mask.prefix_len);
         case FA_MASK_DOCUMENT: {
             const int32_t* row = p.mask.seg + (size_t)(p.mask.seg_batch == 1 ? 0 : b) * p.mask.seg_len;
             return __ldg(row + i) == __ldg(row + j);
@@ -360,6 +361,7 @@ __device__ __forceinline__ uint32_t chunk_mask(const BwdParams& p, int b, int ro
         return m;
     }
     int lo, hi;
+    uint32_t sinks = 0u;
     if (MODE == DKDV) {
         const int j = row;
         lo = 0;
@@ -367,6 +369,10 @@ __device__ __forceinline__ uint32_t chunk_mask(const BwdParams& p, int b, int ro
         if (kind == FA_MASK_CAUSAL) lo = j - c0;
         if (kind == FA_MASK_SLIDING_WINDOW) { lo = j - c0; hi = min(hi, j + p.mask.window - c0); }
         if (kind == FA_MASK_PREFIX_LM && j >= p.mask.prefix_len) lo = j - c0;
+        if (kind == FA_MASK_SINK_WINDOW) {
+            lo = j - c0;
+            if (j >= p.mask.prefix_len) hi = min(hi, j + p.mask.window - c0);
+        }
     } else {
         const int i = row;
         lo = 0;
@@ -374,11 +380,18 @@ __device__ __forceinline__ uint32_t chunk_mask(const BwdParams& p, int b, int ro
         if (kind == FA_MASK_CAUSAL) hi = min(hi, i - c0);
         if (kind == FA_MASK_SLIDING_WINDOW) { hi = min(hi, i - c0); lo = i - p.mask.window - c0; }
         if (kind == FA_MASK_PREFIX_LM) hi = min(hi, max(i, p.mask.prefix_len - 1) - c0);
+        if (kind == FA_MASK_SINK_WINDOW) {
+            // two intervals: the sinks (all of the chunk or a part), then the window
+            hi = min(hi, i - c0);
+            lo = i - p.mask.window - c0;
+            const int ns = min(hi, p.mask.prefix_len - 1 - c0);     // the last visible sink
+            if (ns >= 0 && lo > 0) sinks = 0xffffffffu >> (31 - min(ns, kW - 1));
+        }
     }
     lo = max(lo, 0);
     hi = min(hi, kW - 1);
-    if (hi < lo) return 0u;
-    return (0xffffffffu >> (31 - hi)) & (0xffffffffu << lo);
+    if (hi < lo) return sinks;
+    return ((0xffffffffu >> (31 - hi)) & (0xffffffffu << lo)) | sinks;
 }
 
 __global__ void __launch_bounds__(256) bwd_rowstats_kernel(const BwdParams p) {

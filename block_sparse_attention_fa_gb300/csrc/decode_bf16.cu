@@ -134,6 +134,7 @@ __device__ __forceinline__ bool visible(const DecodeParams& p, int i, int j) {
         case FA_MASK_CAUSAL: return i >= j;
         case FA_MASK_SLIDING_WINDOW: return i >= j && i - j <= p.mask.window;
         case FA_MASK_PREFIX_LM: return j < p.mask.prefix_len || i >= j;
+        case FA_MASK_SINK_WINDOW: return i >= j && (i - j <= p.mask.window || j < p.mask.prefix_len);
         default: return true;   // FULL; TABLE is read per tile by the caller
     }
 }

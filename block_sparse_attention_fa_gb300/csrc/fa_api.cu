@@ -54,6 +54,11 @@ fa_status check_mask_desc(const fa_mask_desc& m, int B, int q_len, int kv_len) {
         case FA_MASK_PREFIX_LM:
             if (m.prefix_len < 0) return fail(FA_ERR_INVALID_ARG, "prefix_len must be >= 0 (got %d)", m.prefix_len);
             return FA_OK;
+        case FA_MASK_SINK_WINDOW:
+            if (m.window < 0) return fail(FA_ERR_INVALID_ARG, "sliding window must be >= 0 (got %d)", m.window);
+            if (m.prefix_len < 0)
+                return fail(FA_ERR_INVALID_ARG, "the sink count (prefix_len) must be >= 0 (got %d)", m.prefix_len);
+            return FA_OK;
         case FA_MASK_DOCUMENT:
             if (!m.seg_ids) return fail(FA_ERR_INVALID_ARG, "document mask needs seg_ids");
             if (m.seg_batch != 1 && m.seg_batch != B)
@@ -105,6 +110,12 @@ fa::MaskParams mask_params(const fa_block_mask* bm) {
     m.table = bm->mask.table;
     m.table_batch = bm->mask.table_batch;
     m.table_words = (bm->kv_len + 31) / 32;
+    if (m.kind == FA_MASK_SINK_WINDOW) {
+        // no pair is further apart, and no key index larger, than these: the
+        // kernels' i - window and j + window then stay within 32 bits
+        m.window = std::min(m.window, std::max(bm->q_len, bm->kv_len));
+        m.prefix_len = std::min(m.prefix_len, bm->kv_len);
+    }
     return m;
 }
 

@@ -379,8 +379,8 @@ struct PairSeq {
 // to 14 % on the document workload, the documents' id counting 10 % on
 // causal soft-cap, when compiled into the other kernels): the closed-form
 // interval masks (full, causal, window, prefix-LM), document masks, lookup
-// tables.
-enum MaskFamily { MK_INTERVAL = 0, MK_DOCUMENT = 1, MK_TABLE = 2 };
+// tables, and the window with sinks (two intervals per row).
+enum MaskFamily { MK_INTERVAL = 0, MK_DOCUMENT = 1, MK_TABLE = 2, MK_SINK = 3 };
 template <int D, int SCORE, int MK>
 __global__ void __launch_bounds__(kThreads, 1)
 fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -1004,6 +1004,20 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                             x[e] = (tw0 & (1u << e)) ? x[e] : off;
                             x[32 + e] = (tw1 & (1u << e)) ? x[32 + e] : off;
                         }
+                    } else if (partial && MK == MK_SINK) {
+                        // [0, min(i, S - 1)] and [i - W, i]
+                        const int hi = min(p.kv_len - 1, i) - ch;
+                        const int lo = i - p.mask.window - ch, ns = p.mask.prefix_len - ch;
+                        const float off = -CUDART_INF_F;
+                        const bool clip_lo = __any_sync(0xffffffffu, lo > 0 && ns < 64);
+                        const bool clip_hi = __any_sync(0xffffffffu, hi < 63);
+                        if (clip_lo) {
+#pragma unroll
+                            for (int e = 0; e < 64; ++e) x[e] = (e <= hi && (e >= lo || e < ns)) ? x[e] : off;
+                        } else if (clip_hi) {
+#pragma unroll
+                            for (int e = 0; e < 64; ++e) x[e] = e <= hi ? x[e] : off;
+                        }
                     } else if (partial) {
                         int lo = -ch, hi = p.kv_len - 1 - ch;
                         if (doc) {
@@ -1265,6 +1279,7 @@ cudaError_t launch_d(const FwdParams& p, const CUtensorMap& tq, const CUtensorMa
     switch (p.mask.kind) {
         case FA_MASK_TABLE: return launch_dt<D, MK_TABLE>(p, tq, tk, tv, s);
         case FA_MASK_DOCUMENT: return launch_dt<D, MK_DOCUMENT>(p, tq, tk, tv, s);
+        case FA_MASK_SINK_WINDOW: return launch_dt<D, MK_SINK>(p, tq, tk, tv, s);
         default: return launch_dt<D, MK_INTERVAL>(p, tq, tk, tv, s);
     }
 }

@@ -112,6 +112,8 @@ __global__ void __launch_bounds__(kThreads32) fwd_fp32_kernel(const FwdParams p)
             case FA_MASK_CAUSAL: return cs <= cr1;
             case FA_MASK_SLIDING_WINDOW: return cs <= cr1 && ce >= cr0 - p.mask.window;
             case FA_MASK_PREFIX_LM: return cs < p.mask.prefix_len || cs <= cr1;
+            case FA_MASK_SINK_WINDOW:
+                return cs <= cr1 && (ce >= cr0 - p.mask.window || cs < p.mask.prefix_len);
             case FA_MASK_DOCUMENT: return seg_row[cs] <= seg_hi && seg_row[ce] >= seg_lo;
             default: return true;
         }
@@ -248,6 +250,9 @@ __global__ void __launch_bounds__(kThreads32) fwd_fp32_kernel(const FwdParams p)
                         break;
                     case FA_MASK_PREFIX_LM:
                         keep = keep && (col < p.mask.prefix_len || i >= col);
+                        break;
+                    case FA_MASK_SINK_WINDOW:
+                        keep = keep && i >= col && (i - col <= p.mask.window || col < p.mask.prefix_len);
                         break;
                     case FA_MASK_DOCUMENT: keep = keep && segs[kk] == my_seg; break;
                     case FA_MASK_TABLE:

@@ -18,7 +18,8 @@ LIB_PATH = os.path.join(_HERE, "_lib", "libfa_gb300.so")
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_TIMEOUT, ERR_DEVICE_CHECK = range(6)
 BF16, FP32 = 0, 1
-MASK_KINDS = {"full": 0, "causal": 1, "sliding_window": 2, "document": 3, "prefix_lm": 4, "table": 5}
+MASK_KINDS = {"full": 0, "causal": 1, "sliding_window": 2, "document": 3, "prefix_lm": 4, "table": 5,
+              "sink_window": 6}
 SCORE_KINDS = {"none": 0, "softcap": 1, "alibi": 2, "rel_bias": 3, "alibi_softcap": 4}
 OUT_FP32 = 1
 DEBUG_DROP_FIRST_LOAD = 1
@@ -255,8 +256,11 @@ class BlockMask:
 
 def block_mask(mask: str, B: int, H: int, q_len: int, kv_len: int, *, window: int = 0, prefix_len: int = 0,
                seg_ids: Optional[torch.Tensor] = None, table: Optional[torch.Tensor] = None, device=None,
-               stream=None, workspace: Optional[Workspace] = None) -> BlockMask:
+               stream=None, workspace: Optional[Workspace] = None, sinks: int = 0) -> BlockMask:
     """Build a BlockMask (fa_block_mask_build) for a built-in mask_mod.
+
+    mask "sink_window": causal, and a key is visible while i - j <= ``window``
+    or j < ``sinks`` (the C ABI's prefix_len).
 
     mask "table": ``table`` is the packed lookup table of the C ABI, a CUDA
     int32 tensor [table_batch, q_len, ceil(kv_len / 32)] whose bit j % 32 of
@@ -278,6 +282,10 @@ def block_mask(mask: str, B: int, H: int, q_len: int, kv_len: int, *, window: in
                              f"(got {tuple(seg_ids.shape)})")
         seg_ids = seg_ids.contiguous()
         device = seg_ids.device
+    if sinks:
+        if mask != "sink_window" or prefix_len:
+            raise ValueError("sinks applies to the sink_window mask (and excludes prefix_len)")
+        prefix_len = sinks
     device = torch.device(device or "cuda")
     bm = BlockMask(B, H, q_len, kv_len, mask, window, prefix_len, seg_ids, device, table=table)
     ws = workspace or default_workspace(device, stream)

@@ -59,7 +59,10 @@ typedef enum fa_mask_kind {
     FA_MASK_SLIDING_WINDOW = 2,  /* i >= j and i - j <= window (inclusive edge)     */
     FA_MASK_DOCUMENT = 3,        /* seg[b][i] == seg[b][j] (document / group packing) */
     FA_MASK_PREFIX_LM = 4,       /* j < prefix_len or i >= j                        */
-    FA_MASK_TABLE = 5            /* bit j of row i of a lookup table (tree attention) */
+    FA_MASK_TABLE = 5,           /* bit j of row i of a lookup table (tree attention) */
+    FA_MASK_SINK_WINDOW = 6      /* i >= j and (i - j <= window or j < prefix_len): a
+                                    sliding window whose first tokens ("sinks") stay
+                                    visible to every later query                    */
 } fa_mask_kind;
 
 /* Built-in score_mods on the scaled score s = scale * q.k (FlexAttention
@@ -76,8 +79,10 @@ typedef enum fa_score_kind {
 } fa_score_kind;
 
 /* A mask_mod and its parameters.
- *   window      SLIDING_WINDOW: i - j <= window (must be >= 0).
+ *   window      SLIDING_WINDOW, SINK_WINDOW: i - j <= window (must be >= 0).
  *   prefix_len  PREFIX_LM: keys j < prefix_len are visible to every query.
+ *               SINK_WINDOW: keys j < prefix_len (the sinks, >= 0 of them)
+ *               are visible to every query i >= j, however far.
  *   seg_ids     DOCUMENT: device int32 [seg_batch, kv_len], non-decreasing in
  *               every row (packed documents / variate groups).  The builder
  *               checks the order on the device; a violation sets

@@ -33,6 +33,8 @@
  *   causal      i >= j                    ("Implementation" script)
  *   window      i >= j and i - j <= W     ("Implementation" script: the
  *               sliding-window mask is causal and (q_idx - kv_idx) <= 512)
+ *   sinks       the window, and the first prefix_len keys with it for every
+ *               later query (i >= j and (i - j <= W or j < S))
  *   document    seg[i] == seg[j]          ("Production Engineering", item 1)
  *   prefix-LM   j < P or i >= j           ("Production Engineering", item 2)
  *   table       table[b][i][j] != 0       ("Production Engineering", item 3:
@@ -49,7 +51,7 @@
 #include <string.h>
 
 enum { OR_MASK_FULL = 0, OR_MASK_CAUSAL = 1, OR_MASK_SLIDING_WINDOW = 2,
-       OR_MASK_DOCUMENT = 3, OR_MASK_PREFIX_LM = 4, OR_MASK_TABLE = 5 };
+       OR_MASK_DOCUMENT = 3, OR_MASK_PREFIX_LM = 4, OR_MASK_TABLE = 5, OR_MASK_SINK_WINDOW = 6 };
 enum { OR_SCORE_NONE = 0, OR_SCORE_SOFTCAP = 1, OR_SCORE_ALIBI = 2,
        OR_SCORE_REL_BIAS = 3, OR_SCORE_ALIBI_SOFTCAP = 4 };
 
@@ -88,6 +90,9 @@ static int or_mask_mod(const or_mask *m, int b, int i, int j)
         const int32_t *row = m->seg + (size_t)(m->seg_batch == 1 ? 0 : b) * m->seg_len;
         return row[i] == row[j];
     }
+    case OR_MASK_SINK_WINDOW:
+        if (j > i) return 0;
+        return j < m->prefix_len || i - j <= m->window;
     case OR_MASK_PREFIX_LM:
         return j < m->prefix_len || i >= j;
     case OR_MASK_TABLE: {
