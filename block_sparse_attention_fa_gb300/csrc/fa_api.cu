@@ -241,6 +241,24 @@ void decode_shape(const fa_fwd_args* a, const fa_block_mask* bm, int* rows, int*
 
 }  // namespace
 
+fa_status fa::check_score_desc(const fa_score_desc* sc, fa_score_desc* out) { return check_score(sc, out); }
+
+int fa::device_sm_count() { return sm_count(); }
+
+fa_status fa::page_tensor_map(CUtensorMap* map, const void* base, long long blocks, int page_size, int D) {
+    auto fn = encode_fn();
+    if (!fn) return fail(FA_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)page_size, (cuuint64_t)blocks};
+    const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)page_size * D * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)std::min(page_size, kBlock), 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(FA_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);
+    return FA_OK;
+}
+
 fa_status fa::report(fa_status st, const char* msg) {
     g_last_error = msg;
     return st;
@@ -547,7 +565,7 @@ fa_status fa_workspace_check(void* workspace, void* stream) {
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaStreamSynchronize(s);
     if (e != cudaSuccess) return cuda_fail(e, "stream synchronize");
-    uint32_t w[3] = {0, 0, 0};
+    uint32_t w[4] = {0, 0, 0, 0};
     e = cudaMemcpy(w, workspace, sizeof(w), cudaMemcpyDeviceToHost);
     if (e != cudaSuccess) return cuda_fail(e, "workspace read");
     if (w[0] == 0) return ok();
@@ -555,6 +573,10 @@ fa_status fa_workspace_check(void* workspace, void* stream) {
     if (e != cudaSuccess) return cuda_fail(e, "workspace clear");
     if (w[0] & fa::WS_FLAG_TIMEOUT)
         return fail(FA_ERR_TIMEOUT, "a device-side pipeline wait ran out of time (site %u)", w[1]);
+    if (!(w[0] & fa::WS_FLAG_CHECK))
+        return fail(FA_ERR_DEVICE_CHECK,
+                    "paged batch: sequence %u has lengths, offsets, pages or positions outside the given arrays",
+                    w[3] ? w[3] - 1 : 0);
     return fail(FA_ERR_DEVICE_CHECK, "segment ids of batch row %u are not non-decreasing", w[2] ? w[2] - 1 : 0);
 }
 

@@ -123,6 +123,80 @@ struct BuildParams {
     int fast_rows;                // set by the launcher: rows built in shared memory, stored as int4
 };
 
+// The paged cache and the step's batch as the kernels see them (fa_paged_kv).
+struct PagedView {
+    int B, Hkv, num_pages, page_size, page_shift, max_pages, total_q;
+    const int32_t* page_table;
+    const int32_t* kv_len;
+    const int32_t* q_start;
+};
+
+// The mask of a paged call: causal or not, window (-1: none), sinks.
+struct PagedMask {
+    int causal, window, sinks;
+};
+
+struct AppendParams {
+    PagedView c;
+    int Hq, D, rot, rope_len, interleaved;
+    const uint16_t *q, *k, *v;
+    uint16_t *q_out, *kc, *vc;
+    long long qs[2], ks[2], vs[2], os[2];   // token and head strides, elements
+    const float *cos, *sin;
+    const int32_t* positions;
+    uint32_t* ws;
+};
+
+// What a unit of work that was split over several CTAs needs to be joined:
+// CTA c's last unit starts there and runs on over `count` CTAs (0: it does not).
+struct PagedMeta {
+    int count, q0, row0, rows, h, pad[3];
+};
+
+// The partial results of one kernel (the sequences' own keys, or the shared
+// prefix).  A partial is an unnormalised row of O with its running max and
+// sum (base 2).  Slot 2 c holds the partial of the unit that CTA c continues
+// from the CTA before, slot 2 c + 1 that of the unit that starts in CTA c and
+// continues in the next one.
+struct PagedParts {
+    float* slot_o;        // [2 ctas][rows_per_unit][D]
+    float2* slot_ml;
+    float* row_o;         // [total_q][Hq][D]: units that one CTA finishes, with a shared prefix
+    float2* row_ml;
+};
+
+struct PagedParams {
+    PagedView c;
+    PagedMask mask;
+    int Hq, group, D;
+    int max_q;
+    int shared;           // length of the shared prefix
+    int prefix;           // 1: this kernel attends to the shared prefix, 0: to the sequences' own keys
+    int join_rows;        // 1: every unit leaves partials, joined row by row with the prefix's
+    int ctas;             // CTAs that share the work
+    int min_tiles;        // least tiles per CTA
+    float scale;
+    ScoreParams score;
+    const uint16_t* q;
+    long long qs[2];
+    void* o;
+    float* lse;
+    PagedParts parts;
+    PagedMeta* meta;      // [ctas] (join_rows = 0)
+    int2* rowdesc;        // [total_q][Hq] {first slot row or -1, count} (join_rows = 1, own keys)
+    int* hdr;             // {tiles of a prefix unit, tiles per CTA} of the prefix kernel
+    uint32_t* ws;
+    uint64_t timeout_ns;
+    uint32_t flags;
+};
+
+// The joining kernel with a shared prefix: both kernels' partials.
+struct PagedJoin {
+    PagedParams own;
+    PagedParts pre;
+    int own_rows, pre_rows;   // rows per unit of each kernel
+};
+
 // Sets this thread's fa_last_error() message and returns `st`.
 fa_status report(fa_status st, const char* msg);
 
@@ -140,6 +214,23 @@ cudaError_t launch_decode_bf16(const DecodeParams& p, const CUtensorMap& tk, con
 cudaError_t launch_block_mask_build_cols(const BuildParams& p, cudaStream_t s);
 cudaError_t launch_bwd_tc(const BwdParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                           const CUtensorMap& tg, cudaStream_t s);
+cudaError_t launch_kv_append(const AppendParams& p, cudaStream_t s);
+// Rows of a unit of the two attention kernels over pages.
+constexpr int kPagedSmallRows = 16;
+constexpr int kPagedTileRows = 256;
+constexpr int kPagedMaxSeqs = 2048;
+cudaError_t launch_paged_small(const PagedParams& p, const CUtensorMap& tk, const CUtensorMap& tv, bool after_prefix,
+                               cudaStream_t s);
+cudaError_t launch_paged_tiles(const PagedParams& p, const CUtensorMap& tk, const CUtensorMap& tv, bool after_prefix,
+                               cudaStream_t s);
+cudaError_t launch_paged_join_units(const PagedParams& p, int rows_per_unit, cudaStream_t s);
+cudaError_t launch_paged_join_rows(const PagedJoin& p, cudaStream_t s);
+// Validates a score_mod (NULL becomes FA_SCORE_NONE in *out).
+fa_status check_score_desc(const fa_score_desc* sc, fa_score_desc* out);
+int device_sm_count();
+// [blocks][page_size][D] bf16, boxes of min(page_size, 128) rows x 64 columns
+// with 128-byte swizzle.
+fa_status page_tensor_map(CUtensorMap* map, const void* base, long long blocks, int page_size, int D);
 int decode_max_splits();
 int decode_max_rows();
 

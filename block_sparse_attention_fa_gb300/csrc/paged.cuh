@@ -1,0 +1,211 @@
+// paged.cuh -- what the paged-cache kernels share: the batch as they read and
+// check it, the keys a unit of work can see, and the split of the work.
+#pragma once
+
+#include <climits>
+
+#include "fa_internal.h"
+#include "ptx.cuh"
+
+namespace fa {
+
+__host__ __device__ __forceinline__ int imin(int a, int b) { return a < b ? a : b; }
+__host__ __device__ __forceinline__ int imax(int a, int b) { return a > b ? a : b; }
+
+// A sequence of the step: its rows of the step's tensors and its length.
+// n = 0: nothing to do (no new tokens, or numbers that contradict each other).
+struct SeqInfo {
+    int q0, n, kv;
+};
+
+__device__ __forceinline__ void report_sequence(uint32_t* ws, int b) {
+    atomicCAS(ws + WS_PAGED_DETAIL, 0u, static_cast<uint32_t>(b) + 1u);
+    atomicOr(ws + WS_FLAGS, WS_FLAG_PAGED);
+}
+
+// Checks sequence b's numbers: s.n > 0 only if its rows lie in the step's
+// tensors and its keys in its row of the page table.  `max_q`: INT_MAX where
+// any number of new tokens will do; `shared`: the length that kv must reach.
+// Returns false for numbers that contradict each other.
+__host__ __device__ __forceinline__ bool check_sequence(const PagedView& c, int b, int q0, int q1, int kv, int max_q,
+                                                        int shared, SeqInfo& s) {
+    s.q0 = q0;
+    s.n = 0;
+    s.kv = kv;
+    const bool placed = q0 >= 0 && q0 <= q1 && q1 <= c.total_q && (b > 0 || q0 == 0);
+    if (placed && q0 == q1) return true;
+    // (q1 - q0 cannot overflow once placed)
+    if (!placed || q1 - q0 > max_q || kv < q1 - q0 || kv < shared ||
+        kv > static_cast<long long>(c.max_pages) * c.page_size)
+        return false;
+    s.n = q1 - q0;
+    return true;
+}
+
+// Reads and checks sequence b; every kernel takes its numbers from here, so
+// that none of them indexes with numbers that were not checked.
+__device__ __forceinline__ SeqInfo seq_info(const PagedView& c, int b, int max_q, int shared, uint32_t* ws) {
+    SeqInfo s;
+    if (!check_sequence(c, b, __ldg(c.q_start + b), __ldg(c.q_start + b + 1), __ldg(c.kv_len + b), max_q, shared, s) && ws)
+        report_sequence(ws, b);
+    return s;
+}
+
+// The keys that rows at positions i0 .. i1 (any of them) can see among the
+// keys jlo .. jhi - 1: [s0, s1), the sinks, and [lo, hi), in tiles of 128.
+struct Hull {
+    int lo, hi, s0, s1;
+    int st0, ns, wt0;      // first sink tile, sink tiles, first tile of [lo, hi)
+    int tiles;             // all of them (at least 1: a unit that sees nothing has one masked tile)
+    __host__ __device__ __forceinline__ bool live(int j) const { return (j >= lo && j < hi) || (j >= s0 && j < s1); }
+    // whether any / every key of [a, b) is live
+    __host__ __device__ __forceinline__ bool any(int a, int b) const {
+        return (a < hi && b > lo && hi > lo) || (a < s1 && b > s0 && s1 > s0);
+    }
+    __host__ __device__ __forceinline__ bool all(int a, int b) const {
+        return (a >= lo && b <= hi) || (a >= s0 && b <= s1) || (a >= s0 && s1 == lo && b <= hi);
+    }
+    __host__ __device__ __forceinline__ int tile(int k) const { return k < ns ? st0 + k : wt0 + (k - ns); }
+};
+
+__host__ __device__ __forceinline__ Hull make_hull(const PagedMask& m, int i0, int i1, int jlo, int jhi) {
+    Hull u;
+    int lo = jlo, hi = jhi;
+    if (m.causal) hi = imin(hi, i1 + 1);
+    if (m.window >= 0) lo = imax(lo, i0 - m.window);
+    const int s1 = imin(imin(m.sinks, hi), lo);      // sinks beyond the window's reach
+    u.s0 = jlo;
+    u.s1 = imax(s1, jlo);
+    u.lo = lo;
+    u.hi = imax(hi, lo);
+    const bool win = hi > lo;
+    u.wt0 = lo >> 7;
+    const int wt1 = win ? (hi + 127) >> 7 : u.wt0;
+    u.st0 = u.s0 >> 7;
+    int st1 = u.s1 > u.s0 ? (u.s1 + 127) >> 7 : u.st0;
+    if (win) st1 = imin(st1, u.wt0);
+    u.ns = imax(st1 - u.st0, 0);
+    u.tiles = imax(u.ns + wt1 - u.wt0, 1);
+    if (u.ns + wt1 - u.wt0 == 0) u.wt0 = u.st0;    // nothing seen: any tile, no page of it is read
+    return u;
+}
+
+// Whether the row at position i sees key j (jlo <= j < jhi is the part's range).
+__host__ __device__ __forceinline__ bool paged_visible(const PagedMask& m, int i, int j, int jlo, int jhi) {
+    return j >= jlo && j < jhi && (!m.causal || j <= i) && (m.window < 0 || i - j <= m.window || j < m.sinks);
+}
+
+// Whether every row at positions i0 .. i1 sees every key of tile kb.
+__host__ __device__ __forceinline__ bool tile_open(const PagedMask& m, int kb, int i0, int i1, int jlo, int jhi) {
+    const int c0 = kb * kBlock, c1 = c0 + kBlock - 1;
+    return c0 >= jlo && c1 < jhi && (!m.causal || c1 <= i0) && (m.window < 0 || i1 - c0 <= m.window || c1 < m.sinks);
+}
+
+// score_mod on s = scale q.k (natural units), in the reference forms.
+template <int SCORE>
+__device__ __forceinline__ float paged_score(const ScoreParams& sc, float s, int hq, int i, int j) {
+    if (SCORE == FA_SCORE_SOFTCAP) return sc.softcap * tanhf(s / sc.softcap);
+    if (SCORE == FA_SCORE_ALIBI) return s - __ldg(sc.slopes + hq) * fabsf(static_cast<float>(i - j));
+    if (SCORE == FA_SCORE_ALIBI_SOFTCAP) {
+        const float u = s - __ldg(sc.slopes + hq) * fabsf(static_cast<float>(i - j));
+        return sc.softcap * tanhf(u / sc.softcap);
+    }
+    if (SCORE == FA_SCORE_REL_BIAS) {
+        const int R = sc.rel_max;
+        return s + __ldg(sc.rel_bias + (size_t)hq * (2 * R + 1) + min(max(i - j, -R), R) + R);
+    }
+    return s;
+}
+
+// The loader's share of one tile: lane l of the warp stands for the tile's
+// page l.  Reads the page's id ahead of the copy (-1: no live key, not read).
+__device__ __forceinline__ int tile_page(const PagedView& c, const int32_t* table, const Hull& u, int kb, int lane,
+                                         int b, uint32_t* ws) {
+    const int span = min(c.page_size, kBlock), a = kb * kBlock + lane * span;
+    if (lane * span >= kBlock || !u.any(a, a + span)) return -1;
+    const int id = __ldg(table + (a >> c.page_shift));
+    if (id < 0 || id >= c.num_pages) {
+        report_sequence(ws, b);
+        return 0;                                  // reported; read something that exists
+    }
+    return id;
+}
+
+// 3-d tiled load into shared memory (as tma_load_4d).
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+}
+
+// Orders this thread's earlier shared-memory writes before later accesses by
+// the async proxy (TMA copies, tcgen05 operands).
+__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Programmatic dependent launch: let the next kernel's blocks start, and wait
+// until the kernel before this one is complete and its writes are visible.
+__device__ __forceinline__ void pdl_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// A wait that only time ends (it guards copies and products still writing).
+__device__ __forceinline__ bool paged_drain_wait(uint32_t bar, uint32_t parity, const WaitCtl& c, uint32_t site) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 15u) == 0u && globaltimer_ns() - t0 > c.timeout_ns) {
+            record_timeout(c, site);
+            return false;
+        }
+    }
+}
+
+// Exclusive prefix sums of value(b), b < n, into pre[0 .. n] by the whole
+// block (THREADS threads, a multiple of 32); `warp_sums` holds THREADS / 32.
+template <int THREADS, class F>
+__device__ __forceinline__ void block_prefix(int n, int* pre, int* warp_sums, F value) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int base = 0;
+    for (int b0 = 0; b0 < n; b0 += THREADS) {
+        const int b = b0 + tid;
+        const int v = b < n ? value(b) : 0;
+        int x = v;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, d);
+            if (lane >= d) x += y;
+        }
+        if (lane == 31) warp_sums[warp] = x;
+        __syncthreads();
+        int before = 0, total = 0;
+#pragma unroll
+        for (int w = 0; w < THREADS / 32; ++w) {
+            if (w < warp) before += warp_sums[w];
+            total += warp_sums[w];
+        }
+        if (b < n) pre[b] = base + before + x - v;
+        base += total;
+        __syncthreads();
+    }
+    if (tid == 0) pre[n] = base;
+    __syncthreads();
+}
+
+template <class K, class... A>
+cudaError_t paged_launch(K kern, dim3 grid, int threads, size_t smem, bool overlap, cudaStream_t s, A... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = overlap ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+}  // namespace fa

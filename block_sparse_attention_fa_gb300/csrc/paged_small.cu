@@ -1,0 +1,593 @@
+// paged_small.cu -- attention over the paged cache for a few rows per
+// (sequence, kv head), and the kernels that join split units.
+//
+// The definition is fa_fwd's, for rows at position i of their sequence and
+// keys on pages.  A unit of work is a (sequence, kv head): its n x Hq / Hkv
+// rows (at most 16) against the keys that some row sees.  With one row per
+// query head there is nothing to reuse: every K and V byte is read once and
+// HBM bounds the kernel.
+//
+// Split.  The tiles (128 keys) of all units stand in one line, unit after
+// unit; CTA c of the grid (one per SM) takes an equal stretch of it, whatever
+// the sequences' lengths.  Only the first and the last unit of a stretch can
+// be shared with a neighbour; those leave partials (unnormalised O, running
+// max and sum) in two slots per CTA, and a second kernel joins them in the
+// order of the keys, so that results do not depend on timing.  The loader runs
+// over the whole stretch without a stop at unit boundaries.  Every CTA finds
+// its stretch by itself: the lengths are on the device, and a prefix sum over
+// the sequences costs about a microsecond.
+//
+// CTA: 8 consumer warps and a loader warp.  The loader's lanes stand for the
+// tile's pages: each reads its page's id ahead of time and issues the page's
+// TMA boxes into a ring of stages.  Pages without a visible key are neither
+// looked up nor read.  Consumer warp w computes S for keys 16 w .. 16 w + 15
+// of the tile (mma.sync m16n8k16; 16 rows are too few for a tcgen05 tile, and
+// the tensor pipe is not the bound), the warps exchange their row maxima and
+// then P (bf16) through shared memory, and warp w accumulates columns
+// w D / 8 .. of O over all 128 keys: no warp holds a second copy of O, so a
+// unit's end needs no merge and costs one barrier.
+//
+// V rows of keys that no row of the unit sees (past the end of the sequence,
+// before the window, on pages that were not read) are cleared in shared
+// memory before the product: their P is 0, but 0 x NaN is not.
+#include <algorithm>
+#include <cuda_bf16.h>
+#include <math_constants.h>
+
+#include "paged.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kWarps = 8;                        // consumers; warp 8 loads
+constexpr int kThreadsS = 32 * (kWarps + 1);
+constexpr int kRows = kPagedSmallRows;
+constexpr float kLog2eP = 1.4426950408889634f;
+constexpr float kLn2P = 0.6931471805599453f;
+enum PagedSite : uint32_t { S_PG_FULL = 64, S_PG_EMPTY, S_PG_DRAIN };
+
+template <int D>
+struct SmallLayout {
+    static constexpr int kStages = D == 64 ? 5 : 3;
+    static constexpr uint32_t kBox = 128u * 64u * 2u;            // 128 keys x 64 columns
+    static constexpr uint32_t kStage = 2u * (D / 64) * kBox;     // K then V
+    static constexpr uint32_t kPRow = 272u;                      // 128 bf16 + 16 bytes: rows on distinct banks
+    static constexpr uint32_t kP = kStages * kStage;
+    static constexpr uint32_t kMax = kP + kRows * kPRow;         // [16 rows][8 warps] fp32
+    static constexpr uint32_t kSum = kMax + kRows * kWarps * 4u;
+    static constexpr uint32_t kBars = kSum + kRows * kWarps * 4u;
+    static constexpr uint32_t kAbort = kBars + 16u * kStages;
+    static constexpr uint32_t kScan = kAbort + 16u;              // warp sums
+    static constexpr uint32_t kPre = kScan + 64u;                // [B + 1] first tile, [B] length, [B] new tokens
+    static constexpr uint32_t kUsed = kPre;                      // + 4 (3 B + 1)
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+// c += a b, one m16n8k16 tile: a 16x16 bf16 (row), b 16x8 bf16 (col), c fp32
+__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Byte offset of 16-byte chunk `chunk` of row `row` in a box of 128-byte rows
+// written with 128-byte swizzle.
+__device__ __forceinline__ uint32_t swz(int row, int chunk) {
+    return static_cast<uint32_t>(row * 128 + ((chunk ^ (row & 7)) << 4));
+}
+__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+// The same barrier with a vote: whether `ok` holds in every thread.
+__device__ __forceinline__ bool consumers_all(bool ok) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.and.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(ok))
+        : "memory");
+    return r != 0;
+}
+
+// The part of one unit that falls into a CTA's stretch: tiles k0 .. k1 - 1 of
+// the unit's list.
+struct SmallSeg {
+    int b, h, kv, n, q0;
+    int tiles, k0, k1, count;      // count: CTAs that share the unit from here on
+    Hull hull;
+    __device__ __forceinline__ bool begins() const { return k0 == 0; }
+    __device__ __forceinline__ bool ends() const { return k1 == tiles; }
+};
+
+// A CTA's stretch [t, t1) of the line of tiles.
+struct Line {
+    const int* pre;
+    const int* kv;
+    const int* rows;
+    int t, t1, per, b;
+};
+
+__device__ __forceinline__ bool next_seg(const PagedParams& p, Line& ln, SmallSeg& s) {
+    if (ln.t >= ln.t1) return false;
+    while (p.c.Hkv * ln.pre[ln.b + 1] <= ln.t) ++ln.b;
+    s.b = ln.b;
+    s.tiles = ln.pre[ln.b + 1] - ln.pre[ln.b];
+    const int off = ln.t - p.c.Hkv * ln.pre[ln.b];
+    s.h = off / s.tiles;
+    s.k0 = off - s.h * s.tiles;
+    s.k1 = min(s.tiles, s.k0 + (ln.t1 - ln.t));
+    s.kv = ln.kv[ln.b];
+    s.n = ln.rows[ln.b];
+    s.q0 = __ldg(p.c.q_start + ln.b);
+    s.hull = make_hull(p.mask, s.kv - s.n, s.kv - 1, p.shared, s.kv);
+    const int last = ln.t - s.k0 + s.tiles - 1;        // the unit's last tile in the line
+    s.count = last / ln.per - ln.t / ln.per + 1;
+    ln.t += s.k1 - s.k0;
+    return true;
+}
+
+template <int D, int SCORE>
+__global__ void __launch_bounds__(kThreadsS, 1)
+paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                   const PagedParams p) {
+    using L = SmallLayout<D>;
+    constexpr int ST = L::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const uint32_t sbase = smem_addr(smem);
+    auto full_bar = [&](int st) { return sbase + L::kBars + 8u * st; };
+    auto empty_bar = [&](int st) { return sbase + L::kBars + 8u * (ST + st); };
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kAbort);
+    int* const pre = reinterpret_cast<int*>(smem + L::kPre);
+    int* const len_s = pre + p.c.B + 1;
+    int* const rows_s = len_s + p.c.B;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
+
+    pdl_launch_next();
+    if (threadIdx.x == 0) {
+        for (int st = 0; st < ST; ++st) {
+            mbar_init(full_bar(st), 1);
+            mbar_init(empty_bar(st), kWarps);
+        }
+        *abort_flag = 0;
+        mbar_fence_init();
+    }
+    // the line of tiles
+    block_prefix<kThreadsS>(p.c.B, pre, reinterpret_cast<int*>(smem + L::kScan), [&](int b) {
+        const SeqInfo s = seq_info(p.c, b, p.max_q, p.shared, cta == 0 ? p.ws : nullptr);
+        len_s[b] = s.kv;
+        rows_s[b] = s.n;
+        return s.n == 0 ? 0 : make_hull(p.mask, s.kv - s.n, s.kv - 1, p.shared, s.kv).tiles;
+    });
+    const int total = p.c.Hkv * pre[p.c.B];
+    Line line;
+    line.pre = pre;
+    line.kv = len_s;
+    line.rows = rows_s;
+    line.per = max((total + p.ctas - 1) / p.ctas, p.min_tiles);
+    line.t = (int)min((long long)cta * line.per, (long long)total);
+    line.t1 = (int)min((long long)line.t + line.per, (long long)total);
+    line.b = 0;
+    if (line.t < line.t1) {
+        int lo = 0, hi = p.c.B - 1;                // the last sequence that starts at or before t
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (p.c.Hkv * pre[mid] <= line.t) lo = mid; else hi = mid - 1;
+        }
+        line.b = lo;
+    }
+    const WaitCtl wc{abort_flag, p.ws, p.timeout_ns};
+
+    if (warp == kWarps) {
+        // ------------------------------------------------------------ loader
+        if (lane == 0) {
+            tma_prefetch_desc(&tmK);
+            tma_prefetch_desc(&tmV);
+        }
+        const int span = min(p.c.page_size, kBlock);
+        const uint32_t page_bytes = static_cast<uint32_t>(span) * D * 4u;    // K and V
+        int last[ST];
+#pragma unroll
+        for (int st = 0; st < ST; ++st) last[st] = -1;
+        int g = 0;
+        bool ok = true;
+        SmallSeg s;
+        while (ok && next_seg(p, line, s)) {
+            const int32_t* table = p.c.page_table + (size_t)s.b * p.c.max_pages;
+            int page = tile_page(p.c, table, s.hull, s.hull.tile(s.k0), lane, s.b, p.ws);
+            for (int k = s.k0; k < s.k1; ++k, ++g) {
+                const int kb = s.hull.tile(k), st = g % ST;
+                const int id = page;
+                if (k + 1 < s.k1) page = tile_page(p.c, table, s.hull, s.hull.tile(k + 1), lane, s.b, p.ws);
+                if (g >= ST && !mbar_wait_warp(empty_bar(st), (g / ST - 1) & 1, wc, S_PG_EMPTY)) { ok = false; break; }
+                const uint32_t pages = __popc(__ballot_sync(0xffffffffu, id >= 0));
+                if (lane == 0) mbar_arrive_expect_tx(full_bar(st), pages * page_bytes);
+                __syncwarp();
+                if (id >= 0) {
+                    const uint32_t dst = sbase + st * L::kStage + static_cast<uint32_t>(lane * span) * 128u;
+                    const int row = (kb * kBlock + lane * span) & (p.c.page_size - 1);
+                    const int block = id * p.c.Hkv + s.h;
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c) {
+                        tma_load_3d(dst + c * L::kBox, &tmK, full_bar(st), c * 64, row, block);
+                        tma_load_3d(dst + (D / 64 + c) * L::kBox, &tmV, full_bar(st), c * 64, row, block);
+                    }
+                }
+                last[st] = g;
+            }
+        }
+        // every issued copy lands before the CTA exits
+        if (lane == 0) {
+#pragma unroll
+            for (int st = 0; st < ST; ++st)
+                if (last[st] >= 0) paged_drain_wait(full_bar(st), (last[st] / ST) & 1, wc, S_PG_DRAIN);
+        }
+        __syncwarp();
+        pdl_wait_previous();
+        return;
+    }
+
+    // --------------------------------------------------------------- consumers
+    const int gr = lane >> 2, tq = lane & 3, mi = lane >> 3, l8 = lane & 7;
+    float* const smax = reinterpret_cast<float*>(smem + L::kMax);
+    float* const ssum = reinterpret_cast<float*>(smem + L::kSum);
+    const uint32_t sP = sbase + L::kP;
+    const float sl2 = SCORE == FA_SCORE_NONE ? p.scale * kLog2eP : kLog2eP;   // to base 2
+    constexpr int kNT = D / 64;                    // n8 tiles of O per warp
+    const int col0 = warp * (D / 8);               // the warp's first column of O
+    int g = 0;
+    bool ok = true;
+    PagedMeta meta{};
+    SmallSeg s;
+    while (ok && next_seg(p, line, s)) {
+        const int rows = s.n * p.group, i0 = s.kv - s.n, i1 = s.kv - 1;
+        int tok[2], hq[2];
+        uint32_t qa[D / 16][4];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = min(gr + 8 * e, rows - 1);
+            tok[e] = r / p.group;
+            hq[e] = s.h * p.group + r - tok[e] * p.group;
+            const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q + (long long)(s.q0 + tok[e]) * p.qs[0] +
+                                                                    (long long)hq[e] * p.qs[1]);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+                qa[ks][e] = __ldg(src + 8 * ks + tq);
+                qa[ks][2 + e] = __ldg(src + 8 * ks + 4 + tq);
+            }
+        }
+        float m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f};
+        float o[kNT][4];
+#pragma unroll
+        for (int n = 0; n < kNT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+
+        for (int k = s.k0; k < s.k1; ++k, ++g) {
+            const int st = g % ST, kb = s.hull.tile(k), c0 = kb * kBlock;
+            const uint32_t kbase = sbase + st * L::kStage, vbase = kbase + (D / 64) * L::kBox;
+            const bool here = mbar_wait_warp(full_bar(st), (g / ST) & 1, wc, S_PG_FULL);
+            float x[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+            float mx[2] = {-CUDART_INF_F, -CUDART_INF_F};
+            bool cleared = false;
+            if (here) {
+                const int key = 16 * warp + 8 * (mi >> 1) + l8;
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    uint32_t kf[4];
+                    ldsm4(kbase + (ks >> 2) * L::kBox + swz(key, 2 * (ks & 3) + (mi & 1)), kf);
+                    mma_16816(x[0], qa[ks], kf[0], kf[1]);
+                    mma_16816(x[1], qa[ks], kf[2], kf[3]);
+                }
+                const bool open = tile_open(p.mask, kb, i0, i1, p.shared, s.kv);
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const int e = c >> 1, j = c0 + 16 * warp + 8 * nt + 2 * tq + (c & 1);
+                        float v = x[nt][c];
+                        if (SCORE != FA_SCORE_NONE) v = paged_score<SCORE>(p.score, v * p.scale, hq[e], i0 + tok[e], j);
+                        v *= sl2;
+                        if (!open && !paged_visible(p.mask, i0 + tok[e], j, p.shared, s.kv)) v = -CUDART_INF_F;
+                        x[nt][c] = v;
+                        mx[e] = fmaxf(mx[e], v);
+                    }
+                }
+                // V rows that no row of the unit sees
+                const int a = c0 + 16 * warp;
+                if (!s.hull.all(a, a + 16)) {
+                    cleared = true;
+                    for (int r = 0; r < 16; ++r) {
+                        if (s.hull.live(a + r)) continue;
+                        if (lane < D / 8)
+                            *reinterpret_cast<uint4*>(smem + st * L::kStage + (D / 64 + (lane >> 3)) * L::kBox +
+                                                      swz(16 * warp + r, lane & 7)) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
+                    mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
+                    if (tq == 0) smax[(gr + 8 * e) * kWarps + warp] = mx[e];
+                }
+            }
+            // (a warp whose wait ran out still comes here, so that all leave together)
+            if (!consumers_all(here)) { ok = false; break; }
+            float alpha[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float4 a = *reinterpret_cast<const float4*>(smax + (gr + 8 * e) * kWarps);
+                const float4 b = *reinterpret_cast<const float4*>(smax + (gr + 8 * e) * kWarps + 4);
+                const float m_new = fmaxf(fmaxf(fmaxf(fmaxf(a.x, a.y), fmaxf(a.z, a.w)),
+                                                fmaxf(fmaxf(b.x, b.y), fmaxf(b.z, b.w))), m[e]);
+                alpha[e] = m_new == m[e] ? 1.f : ex2_approx(m[e] - m_new);
+                const float nm = m_new == -CUDART_INF_F ? 0.f : -m_new;
+                m[e] = m_new;
+                l[e] *= alpha[e];
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt) {
+                    const float p0 = ex2_approx(x[nt][2 * e] + nm), p1 = ex2_approx(x[nt][2 * e + 1] + nm);
+                    l[e] += p0 + p1;
+                    *reinterpret_cast<uint32_t*>(smem + L::kP + (gr + 8 * e) * L::kPRow +
+                                                 2 * (16 * warp + 8 * nt + 2 * tq)) = pack_bf16x2(p0, p1);
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < kNT; ++n) {
+                o[n][0] *= alpha[0];
+                o[n][1] *= alpha[0];
+                o[n][2] *= alpha[1];
+                o[n][3] *= alpha[1];
+            }
+            consumers_sync();
+            // O[:, col0 ..] += P V over the tile's 128 keys
+            const uint32_t p_row = sP + (l8 + 8 * (mi & 1)) * L::kPRow + 16 * (mi >> 1);
+#pragma unroll
+            for (int ks = 0; ks < 8; ks += 2) {
+                uint32_t pa[4], pb[4], vf[4];
+                ldsm4(p_row + 32 * ks, pa);
+                ldsm4(p_row + 32 * (ks + 1), pb);
+                if constexpr (kNT == 2) {
+                    const int dt = 2 * warp + (mi >> 1);
+                    const uint32_t v0 = vbase + (dt >> 3) * L::kBox;
+                    uint32_t vg[4];
+                    ldsm4_t(v0 + swz(16 * ks + 8 * (mi & 1) + l8, dt & 7), vf);
+                    ldsm4_t(v0 + swz(16 * (ks + 1) + 8 * (mi & 1) + l8, dt & 7), vg);
+                    mma_16816(o[0], pa, vf[0], vf[1]);
+                    mma_16816(o[1], pa, vf[2], vf[3]);
+                    mma_16816(o[0], pb, vg[0], vg[1]);
+                    mma_16816(o[1], pb, vg[2], vg[3]);
+                } else {
+                    ldsm4_t(vbase + swz(16 * ks + 8 * mi + l8, warp), vf);
+                    mma_16816(o[0], pa, vf[0], vf[1]);
+                    mma_16816(o[0], pb, vf[2], vf[3]);
+                }
+            }
+            if (cleared) fence_async_shared();     // the next copy into this stage comes after the clearing
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty_bar(st));
+        }
+        if (!ok) break;
+
+        // the unit's end in this CTA: row sums over the lanes and warps
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+            if (tq == 0) ssum[(gr + 8 * e) * kWarps + warp] = l[e];
+        }
+        consumers_sync();
+        const bool whole = s.begins() && s.ends();
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = gr + 8 * e;
+            if (r >= rows) continue;
+            const float4 a = *reinterpret_cast<const float4*>(ssum + r * kWarps);
+            const float4 b = *reinterpret_cast<const float4*>(ssum + r * kWarps + 4);
+            const float sum = ((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w));
+            const long long row = (long long)(s.q0 + tok[e]) * p.Hq + hq[e];
+            if (whole && !p.join_rows) {
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;      // a NaN stays one
+#pragma unroll
+                for (int n = 0; n < kNT; ++n) {
+                    const long long at = row * D + col0 + 8 * n + 2 * tq;
+                    const float y0 = o[n][2 * e] * inv, y1 = o[n][2 * e + 1] * inv;
+                    if (p.flags & FA_OUT_FP32)
+                        *reinterpret_cast<float2*>(static_cast<float*>(p.o) + at) = make_float2(y0, y1);
+                    else
+                        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + at) = pack_bf16x2(y0, y1);
+                }
+                if (warp == 0 && tq == 0) p.lse[row] = sum == 0.f ? -CUDART_INF_F : (m[e] + log2f(sum)) * kLn2P;
+            } else {
+                const long long slot = whole ? row : (2LL * cta + (s.begins() ? 1 : 0)) * kRows + r;
+                float* dst = (whole ? p.parts.row_o : p.parts.slot_o) + slot * D + col0 + 2 * tq;
+#pragma unroll
+                for (int n = 0; n < kNT; ++n)
+                    *reinterpret_cast<float2*>(dst + 8 * n) = make_float2(o[n][2 * e], o[n][2 * e + 1]);
+                if (warp == 0 && tq == 0) {
+                    (whole ? p.parts.row_ml : p.parts.slot_ml)[slot] = make_float2(m[e], sum);
+                    if (p.join_rows && s.begins())
+                        p.rowdesc[row] = whole ? make_int2(-1, 1)
+                                               : make_int2((2 * cta + 1) * kRows + r, s.count);
+                }
+            }
+        }
+        if (s.begins() && !s.ends()) {
+            meta.count = s.count;
+            meta.q0 = s.q0;
+            meta.rows = rows;
+            meta.h = s.h;
+        }
+    }
+    if (!p.join_rows && threadIdx.x == 0) p.meta[cta] = ok ? meta : PagedMeta{};
+    pdl_wait_previous();
+}
+
+// One row's partials -> O and lse.  Lane: kV adjacent columns.
+template <int D>
+struct RowJoin {
+    static constexpr int kV = D / 32;
+    float m, l, o[kV];
+    __device__ __forceinline__ void init() {
+        m = -CUDART_INF_F;
+        l = 0.f;
+#pragma unroll
+        for (int c = 0; c < kV; ++c) o[c] = 0.f;
+    }
+    __device__ __forceinline__ void add(const float* src, float2 ml, int lane) {
+        float v[kV];
+        if constexpr (kV == 4) {
+            const float4 x = *reinterpret_cast<const float4*>(src + 4 * lane);
+            v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+        } else {
+            const float2 x = *reinterpret_cast<const float2*>(src + 2 * lane);
+            v[0] = x.x; v[1] = x.y;
+        }
+        if (ml.y == 0.f) return;                   // the part has no visible key for this row
+        const float mn = fmaxf(m, ml.x);
+        const float f = l == 0.f ? 0.f : ex2_approx(m - mn), w = ex2_approx(ml.x - mn);
+        m = mn;
+        l = l * f + ml.y * w;
+#pragma unroll
+        for (int c = 0; c < kV; ++c) o[c] = o[c] * f + v[c] * w;
+    }
+    // `count` partials: slot rows first, first + stride, first + 3 stride, ..
+    // (slots 2 c + 1, 2 (c + 1), 2 (c + 2), ..)
+    __device__ __forceinline__ void add_slots(const PagedParts& s, long long first, int count, int stride, int lane) {
+#pragma unroll 4
+        for (int k = 0; k < count; ++k) {
+            const long long at = first + (k ? (2LL * k - 1) * stride : 0);
+            add(s.slot_o + at * D, s.slot_ml[at], lane);
+        }
+    }
+    __device__ __forceinline__ void store(const PagedParams& p, long long row, int lane) const {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        if (p.flags & FA_OUT_FP32) {
+            float* dst = static_cast<float*>(p.o) + row * D + kV * lane;
+#pragma unroll
+            for (int c = 0; c < kV; c += 2) *reinterpret_cast<float2*>(dst + c) = make_float2(o[c] * inv, o[c + 1] * inv);
+        } else {
+            uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + row * D + kV * lane);
+#pragma unroll
+            for (int c = 0; c < kV; c += 2) dst[c / 2] = pack_bf16x2(o[c] * inv, o[c + 1] * inv);
+        }
+        if (lane == 0) p.lse[row] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * kLn2P;
+    }
+};
+
+constexpr int kJoinWarps = 8;
+
+// Without a shared prefix: block (c, y) joins rows of the unit that starts in
+// CTA c of the attention kernel and runs on into the next ones.
+template <int D>
+__global__ void __launch_bounds__(32 * kJoinWarps) paged_join_units_kernel(const PagedParams p, int rows_per_unit) {
+    pdl_wait_previous();
+    const PagedMeta t = p.meta[blockIdx.x];
+    if (t.count == 0) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int r = blockIdx.y * kJoinWarps + warp; r < t.rows; r += gridDim.y * kJoinWarps) {
+        RowJoin<D> j;
+        j.init();
+        j.add_slots(p.parts, (2LL * blockIdx.x + 1) * rows_per_unit + r, t.count, rows_per_unit, lane);
+        const int R = t.row0 + r, tok = R / p.group;
+        j.store(p, (long long)(t.q0 + tok) * p.Hq + t.h * p.group + R - tok * p.group, lane);
+    }
+}
+
+// With a shared prefix: block (t, h) joins the rows of token t and kv head h,
+// the prefix's partials first, then those of the sequence's own keys.
+template <int D>
+__global__ void __launch_bounds__(32 * kJoinWarps) paged_join_rows_kernel(const PagedJoin j) {
+    const PagedParams& p = j.own;
+    const int t = blockIdx.x, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int b = 0;
+    for (int b0 = 0; b0 < p.c.B; b0 += 32 * kJoinWarps) {
+        const int x = b0 + threadIdx.x;
+        b += __syncthreads_count(x < p.c.B && __ldg(p.c.q_start + min(x, p.c.B - 1) + 1) <= t);
+    }
+    if (b >= p.c.B) return;
+    const SeqInfo s = seq_info(p.c, b, p.max_q, p.shared, nullptr);
+    if (s.n == 0 || t < s.q0 || t >= s.q0 + s.n) return;
+    pdl_wait_previous();
+    const int tiles = p.hdr[0], per = p.hdr[1];
+    for (int gq = warp; gq < p.group; gq += kJoinWarps) {
+        const long long row = (long long)t * p.Hq + h * p.group + gq;
+        RowJoin<D> x;
+        x.init();
+        const int R = t * p.group + gq, rt = R / j.pre_rows, r = R - rt * j.pre_rows;
+        const int first = (rt * p.c.Hkv + h) * tiles, ca = first / per, cb = (first + tiles - 1) / per;
+        if (ca == cb)
+            x.add(j.pre.row_o + row * D, j.pre.row_ml[row], lane);
+        else
+            x.add_slots(j.pre, (2LL * ca + 1) * j.pre_rows + r, cb - ca + 1, j.pre_rows, lane);
+        const int2 d = p.rowdesc[row];
+        if (d.x < 0)
+            x.add(p.parts.row_o + row * D, p.parts.row_ml[row], lane);
+        else
+            x.add_slots(p.parts, d.x, d.y, j.own_rows, lane);
+        x.store(p, row, lane);
+    }
+}
+
+template <int D, int SCORE>
+cudaError_t launch_small(const PagedParams& p, const CUtensorMap& tk, const CUtensorMap& tv, bool overlap,
+                         cudaStream_t s) {
+    auto kern = paged_small_kernel<D, SCORE>;
+    using L = SmallLayout<D>;
+    constexpr size_t most = L::kUsed + 4u * (3u * kPagedMaxSeqs + 1u) + 1024u;
+    static_assert(most <= 227u * 1024u, "shared memory budget");
+    static bool attr_set[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) attr_set[dev] = true;
+    }
+    const size_t smem = L::kUsed + 4u * (3u * p.c.B + 1u) + 1024u;
+    return paged_launch(kern, dim3(p.ctas), kThreadsS, smem, overlap, s, tk, tv, p);
+}
+
+template <int D>
+cudaError_t launch_small_d(const PagedParams& p, const CUtensorMap& tk, const CUtensorMap& tv, bool overlap,
+                           cudaStream_t s) {
+    switch (p.score.kind) {
+        case FA_SCORE_SOFTCAP: return launch_small<D, FA_SCORE_SOFTCAP>(p, tk, tv, overlap, s);
+        case FA_SCORE_ALIBI: return launch_small<D, FA_SCORE_ALIBI>(p, tk, tv, overlap, s);
+        case FA_SCORE_REL_BIAS: return launch_small<D, FA_SCORE_REL_BIAS>(p, tk, tv, overlap, s);
+        case FA_SCORE_ALIBI_SOFTCAP: return launch_small<D, FA_SCORE_ALIBI_SOFTCAP>(p, tk, tv, overlap, s);
+        default: return launch_small<D, FA_SCORE_NONE>(p, tk, tv, overlap, s);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_paged_small(const PagedParams& p, const CUtensorMap& tk, const CUtensorMap& tv, bool after_prefix,
+                               cudaStream_t s) {
+    return p.D == 64 ? launch_small_d<64>(p, tk, tv, after_prefix, s) : launch_small_d<128>(p, tk, tv, after_prefix, s);
+}
+
+cudaError_t launch_paged_join_units(const PagedParams& p, int rows_per_unit, cudaStream_t s) {
+    const dim3 grid(p.ctas, rows_per_unit <= 16 ? 2 : 8);
+    return p.D == 64 ? paged_launch(paged_join_units_kernel<64>, grid, 32 * kJoinWarps, 0, true, s, p, rows_per_unit)
+                     : paged_launch(paged_join_units_kernel<128>, grid, 32 * kJoinWarps, 0, true, s, p, rows_per_unit);
+}
+
+cudaError_t launch_paged_join_rows(const PagedJoin& p, cudaStream_t s) {
+    const dim3 grid(p.own.c.total_q, p.own.c.Hkv);
+    return p.own.D == 64 ? paged_launch(paged_join_rows_kernel<64>, grid, 32 * kJoinWarps, 0, true, s, p)
+                         : paged_launch(paged_join_rows_kernel<128>, grid, 32 * kJoinWarps, 0, true, s, p);
+}
+
+}  // namespace fa

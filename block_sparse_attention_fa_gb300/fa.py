@@ -1,4 +1,5 @@
-"""Thin ctypes binding over the C ABI in ``include/fa.h``.
+"""Thin ctypes binding over the C ABI in ``include/fa.h`` and
+``include/fa_paged.h``.
 
 Argument marshalling only: every step of the computation runs in the CUDA
 kernels of ``_lib/libfa_gb300.so``.  PyTorch supplies device memory and the
@@ -8,6 +9,7 @@ raises; there is no CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -28,6 +30,8 @@ BLOCK = 128
 SYMBOLS = ("fa_workspace_bytes", "fa_block_mask_shape", "fa_block_mask_size", "fa_block_mask_build", "fa_fwd",
            "fa_fwd_noalloc", "fa_fwd_decode", "fa_decode_partials_bytes", "fa_decode_splits", "fa_bwd",
            "fa_block_mask_build_cols", "fa_bwd_rowstats_bytes", "fa_workspace_check", "fa_last_error", "fa_version")
+
+PAGED_SYMBOLS = ("fa_kv_append", "fa_fwd_paged", "fa_paged_scratch_bytes")
 
 
 class FAError(RuntimeError):
@@ -80,6 +84,29 @@ class BlockMaskColsStruct(ctypes.Structure):
                 ("full_q_num_blocks", ctypes.c_void_p), ("full_q_indices", ctypes.c_void_p)]
 
 
+class PagedKVStruct(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("total_q", ctypes.c_int32),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p), ("q_start", ctypes.c_void_p)]
+
+
+class KVAppendArgs(ctypes.Structure):
+    _fields_ = [("Hq", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("rope_len", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("q", ctypes.c_void_p), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("q_out", ctypes.c_void_p), ("q_stride", ctypes.c_int64 * 2),
+                ("k_stride", ctypes.c_int64 * 2), ("v_stride", ctypes.c_int64 * 2),
+                ("q_out_stride", ctypes.c_int64 * 2), ("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p),
+                ("positions", ctypes.c_void_p)]
+
+
+class PagedFwdArgs(ctypes.Structure):
+    _fields_ = [("Hq", ctypes.c_int32), ("max_q_len", ctypes.c_int32), ("shared_len", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("q", ctypes.c_void_p), ("q_stride", ctypes.c_int64 * 2),
+                ("o", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("timeout_ms", ctypes.c_uint32),
+                ("flags", ctypes.c_uint32)]
+
+
 _lib = None
 
 
@@ -125,6 +152,15 @@ def load_library(path: str = LIB_PATH):
     h.fa_bwd.argtypes = [ctypes.POINTER(BwdArgs), ctypes.POINTER(BlockMaskStruct),
                          ctypes.POINTER(BlockMaskColsStruct), ctypes.POINTER(ScoreDesc), ctypes.c_void_p,
                          ctypes.c_void_p]
+    h.fa_kv_append.restype = ctypes.c_int
+    h.fa_kv_append.argtypes = [ctypes.POINTER(PagedKVStruct), ctypes.POINTER(KVAppendArgs), ctypes.c_void_p,
+                               ctypes.c_void_p]
+    h.fa_paged_scratch_bytes.restype = ctypes.c_size_t
+    h.fa_paged_scratch_bytes.argtypes = [ctypes.POINTER(PagedKVStruct), ctypes.POINTER(PagedFwdArgs)]
+    h.fa_fwd_paged.restype = ctypes.c_int
+    h.fa_fwd_paged.argtypes = [ctypes.POINTER(PagedKVStruct), ctypes.POINTER(PagedFwdArgs), ctypes.POINTER(MaskDesc),
+                               ctypes.POINTER(ScoreDesc), ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p,
+                               ctypes.c_void_p]
     h.fa_workspace_check.restype = ctypes.c_int
     h.fa_workspace_check.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
     h.fa_last_error.restype = ctypes.c_char_p
@@ -531,6 +567,185 @@ def bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor, lse:
     _check(load_library().fa_bwd(ctypes.byref(a), ctypes.byref(bm.struct), ctypes.byref(bm._cols_struct),
                                  ctypes.byref(sc), ws.ptr, _stream_ptr(stream)))
     return dq, dk, dv
+
+
+def _paged_kv(k_cache, v_cache, page_table, kv_len, q_start, total_q, dev):
+    """The fa_paged_kv of these tensors, which the C ABI reads through raw pointers: everything it cannot see is
+    checked here."""
+    if k_cache.dim() != 4 or k_cache.dtype != torch.bfloat16 or v_cache.dtype != torch.bfloat16 \
+            or k_cache.shape != v_cache.shape or not k_cache.is_contiguous() or not v_cache.is_contiguous() \
+            or k_cache.get_device() != dev or v_cache.get_device() != dev:
+        raise ValueError("k_cache and v_cache must be contiguous CUDA bf16 tensors [num_pages, Hkv, page_size, D] "
+                         "on the queries' device")
+    for name, t, dims in (("page_table", page_table, 2), ("kv_len", kv_len, 1), ("q_start", q_start, 1)):
+        if t.dtype != torch.int32 or t.dim() != dims or t.get_device() != dev or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 tensor of {dims} dimensions on the queries' device")
+    B, max_pages = page_table.shape
+    if kv_len.shape[0] != B or q_start.shape[0] != B + 1:
+        raise ValueError(f"page_table has {B} rows: kv_len must hold {B} lengths and q_start {B + 1} offsets "
+                         f"(got {kv_len.shape[0]}, {q_start.shape[0]})")
+    num_pages, Hkv, page, D = k_cache.shape
+    return PagedKVStruct(B, Hkv, D, num_pages, page, max_pages, total_q, k_cache.data_ptr(), v_cache.data_ptr(),
+                         page_table.data_ptr(), kv_len.data_ptr(), q_start.data_ptr())
+
+
+def _rows(name, t, total, H, D, dev):
+    """Token and head strides of bf16 rows [total, H, D]."""
+    if t.dtype != torch.bfloat16 or t.dim() != 3 or t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA bf16 tensor [tokens, heads, D] on one device with the cache")
+    if t.shape[0] != total or (H is not None and t.shape[1] != H) or t.shape[2] != D:
+        raise ValueError(f"{name} must be [{total}, {'heads' if H is None else H}, {D}] (got {tuple(t.shape)})")
+    st = t.stride()
+    if st[2] != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    # the stride of a dimension of one entry says nothing
+    return (st[0] if t.shape[0] > 1 else D, st[1] if t.shape[1] > 1 else D)
+
+
+def _on_device(fn):
+    """Runs a binding function with the cache's device current."""
+    @functools.wraps(fn)
+    def run(q, k, v, *args, **kw):
+        at = (k if q is None else q).get_device()
+        if at < 0 or at == torch.cuda.current_device():
+            return fn(q, k, v, *args, **kw)
+        with torch.cuda.device(at):
+            return fn(q, k, v, *args, **kw)
+    return run
+
+
+@_on_device
+def kv_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
+              v_cache: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tensor, q_start: torch.Tensor, *,
+              cos: Optional[torch.Tensor] = None, sin: Optional[torch.Tensor] = None, interleaved: bool = False,
+              positions: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+              workspace: Optional[Workspace] = None, stream=None):
+    """Append a step's keys and values to the paged cache (fa_kv_append), rotating queries and keys on the way;
+    returns the rotated queries.
+
+    q [tokens, Hq, D], k and v [tokens, Hkv, D]: bf16 rows, any token and head strides that are multiples of 8 (slices
+    of a fused projection); q may be None.  k_cache and v_cache [num_pages, Hkv, page_size, D]; page_table int32
+    [B, max_pages]; kv_len int32 [B] counts the new tokens; sequence b's rows are q_start[b] .. q_start[b + 1] - 1,
+    rows from q_start[B] on are left as they were.  cos and sin: fp32 [positions, rot_dim / 2], both or neither.
+    q_out may be q."""
+    dev = k.get_device()
+    if dev < 0 or k.dim() != 3:
+        raise ValueError("k must be a CUDA bf16 tensor [tokens, Hkv, D]")
+    total = k.shape[0]
+    c = _paged_kv(k_cache, v_cache, page_table, kv_len, q_start, total, dev)
+    a = KVAppendArgs()
+    a.k_stride[:] = _rows("k", k, total, c.Hkv, c.D, dev)
+    a.v_stride[:] = _rows("v", v, total, c.Hkv, c.D, dev)
+    a.k, a.v = k.data_ptr(), v.data_ptr()
+    if q is not None:
+        a.q_stride[:] = _rows("q", q, total, None, c.D, dev)
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            if stream is not None:
+                q_out.record_stream(stream)
+        a.q_out_stride[:] = a.q_stride[:] if q_out is q else _rows("q_out", q_out, total, q.shape[1], c.D, dev)
+        a.Hq, a.q, a.q_out = q.shape[1], q.data_ptr(), q_out.data_ptr()
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin come together")
+    if cos is not None:
+        for t in (cos, sin):
+            if t.dtype != torch.float32 or t.dim() != 2 or t.get_device() != dev or not t.is_contiguous() \
+                    or t.shape != cos.shape:
+                raise ValueError("cos and sin must be contiguous float32 tensors [positions, rot_dim / 2] on the "
+                                 "cache's device")
+        a.rope_len, a.rot_dim = cos.shape[0], 2 * cos.shape[1]
+        a.cos, a.sin, a.interleaved = cos.data_ptr(), sin.data_ptr(), 1 if interleaved else 0
+    if positions is not None:
+        if positions.dtype != torch.int32 or positions.get_device() != dev or not positions.is_contiguous() \
+                or positions.numel() != total:
+            raise ValueError("positions must be a contiguous int32 tensor with one entry per row")
+        a.positions = positions.data_ptr()
+    ws = workspace or default_workspace(k.device, stream)
+    _check(load_library().fa_kv_append(ctypes.byref(c), ctypes.byref(a), ws.ptr, _stream_ptr(stream)))
+    return q_out
+
+
+@_on_device
+def fwd_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
+              kv_len: torch.Tensor, q_start: torch.Tensor, *, max_q_len: Optional[int] = None, mask: str = "causal",
+              window: int = 0, sinks: int = 0, shared_len: int = 0, score: str = "none", softcap: float = 0.0,
+              alibi_slopes: Optional[torch.Tensor] = None, rel_bias: Optional[torch.Tensor] = None, rel_max: int = 0,
+              scale: Optional[float] = None, out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+              scratch: Optional[torch.Tensor] = None, workspace: Optional[Workspace] = None, stream=None,
+              timeout_ms: int = 0, out_fp32: bool = False):
+    """Attention from a step's queries to the paged cache (fa_fwd_paged); returns (o, lse), o [tokens, Hq, D] and lse
+    float32 [tokens, Hq].
+
+    q [tokens, Hq, D] bf16, token and head strides multiples of 8; the cache and the batch as for kv_append.
+    ``max_q_len`` bounds the new tokens of a sequence (default: all of q's rows; a tight bound lets single tokens take
+    the decoding kernel).  mask: "full", "causal", "sliding_window" (``window``) or "sink_window" (``window`` and
+    ``sinks``), by position.  ``shared_len``: length of a prefix all sequences share, read once through page_table[0].
+    Rows behind the last sequence are left as they were; ``scratch`` is allocated when not given."""
+    dev = q.get_device()
+    if dev < 0 or q.dim() != 3:
+        raise ValueError("q must be a CUDA bf16 tensor [tokens, Hq, D]")
+    total, Hq, D = q.shape
+    c = _paged_kv(k_cache, v_cache, page_table, kv_len, q_start, total, dev)
+    a = PagedFwdArgs()
+    a.q_stride[:] = _rows("q", q, total, None, c.D, dev)
+    want = torch.float32 if out_fp32 else torch.bfloat16
+    made = []
+    if out is None:
+        out = torch.empty((total, Hq, D), dtype=want, device=q.device)
+        made.append(out)
+    elif out.dtype != want or out.get_device() != dev or not out.is_contiguous() or tuple(out.shape) != (total, Hq, D):
+        raise ValueError(f"out must be a contiguous {want} tensor of q's shape on q's device")
+    if lse is None:
+        lse = torch.empty((total, Hq), dtype=torch.float32, device=q.device)
+        made.append(lse)
+    elif lse.dtype != torch.float32 or lse.get_device() != dev or not lse.is_contiguous() \
+            or tuple(lse.shape) != (total, Hq):
+        raise ValueError("lse must be a contiguous float32 tensor [tokens, Hq] on q's device")
+    for name, t, need in (("alibi_slopes", alibi_slopes, Hq), ("rel_bias", rel_bias, Hq * (2 * rel_max + 1))):
+        if t is not None and (t.dtype != torch.float32 or t.get_device() != dev or not t.is_contiguous()
+                              or t.numel() < need):
+            raise ValueError(f"{name} must be a contiguous float32 tensor of at least {need} entries on q's device")
+    if mask not in MASK_KINDS:
+        raise ValueError(f"unknown mask {mask!r}")
+    a.Hq, a.max_q_len, a.shared_len = Hq, max(total, 1) if max_q_len is None else max_q_len, shared_len
+    a.scale = 0.0 if scale is None else float(scale)
+    a.q, a.o, a.lse = q.data_ptr(), out.data_ptr(), lse.data_ptr()
+    a.timeout_ms, a.flags = timeout_ms, OUT_FP32 if out_fp32 else 0
+    m = MaskDesc()
+    m.kind, m.window, m.prefix_len = MASK_KINDS[mask], window, sinks
+    if sinks and mask != "sink_window":
+        raise ValueError("sinks applies to the sink_window mask")
+    sc = _score_desc(score, softcap, alibi_slopes, rel_bias, rel_max)
+    lib = load_library()
+    ca, aa = ctypes.byref(c), ctypes.byref(a)
+    if scratch is None:
+        # no bytes: the arguments are wrong, and the call below says how
+        scratch = torch.empty(max(lib.fa_paged_scratch_bytes(ca, aa), 16), dtype=torch.uint8, device=q.device)
+        made.append(scratch)
+    elif scratch.get_device() != dev or not scratch.is_contiguous():
+        raise ValueError("scratch must be a contiguous tensor on q's device")
+    if stream is not None:
+        for t in made:
+            t.record_stream(stream)
+    ws = workspace or default_workspace(q.device, stream)
+    _check(lib.fa_fwd_paged(ca, aa, ctypes.byref(m), ctypes.byref(sc), ctypes.c_void_p(scratch.data_ptr()),
+                            scratch.numel() * scratch.element_size(), ws.ptr, _stream_ptr(stream)))
+    return out, lse
+
+
+def paged_scratch(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
+                  kv_len: torch.Tensor, q_start: torch.Tensor, *, max_q_len: Optional[int] = None,
+                  shared_len: int = 0) -> torch.Tensor:
+    """Scratch for fwd_paged calls of these shapes, for callers that keep their own."""
+    with torch.cuda.device(q.device):
+        c = _paged_kv(k_cache, v_cache, page_table, kv_len, q_start, q.shape[0], q.get_device())
+        a = PagedFwdArgs()
+        a.Hq, a.shared_len = q.shape[1], shared_len
+        a.max_q_len = max(q.shape[0], 1) if max_q_len is None else max_q_len
+        n = load_library().fa_paged_scratch_bytes(ctypes.byref(c), ctypes.byref(a))
+        if n == 0:
+            raise FAError(ERR_INVALID_ARG, load_library().fa_last_error().decode())
+        return torch.empty(n, dtype=torch.uint8, device=q.device)
 
 
 def version() -> str:
