@@ -152,6 +152,7 @@ fa_status fa_kv_append(const fa_paged_kv* c, const fa_kv_append_args* a, void* w
     if (a->interleaved != 0 && a->interleaved != 1)
         return fail(FA_ERR_INVALID_ARG, "interleaved must be 0 or 1 (got %d)", a->interleaved);
     if ((long long)a->Hq + 2LL * c->Hkv > 1 << 24) return fail(FA_ERR_UNSUPPORTED, "too many heads");
+    if (c->total_q == 0) return fa::report(FA_OK, "");     // no rows: their pointers may be NULL
     if ((st = check_rows("k", a->k, a->k_stride)) != FA_OK) return st;
     if ((st = check_rows("v", a->v, a->v_stride)) != FA_OK) return st;
     if (a->Hq > 0) {
@@ -231,6 +232,7 @@ fa_status fa_fwd_paged(const fa_paged_kv* c, const fa_paged_fwd_args* a, const f
     }
     fa_score_desc score;
     if ((st = fa::check_score_desc(sc, &score)) != FA_OK) return st;
+    if (c->total_q == 0) return fa::report(FA_OK, "");     // no rows: their pointers may be NULL
     if ((st = check_rows("q", a->q, a->q_stride)) != FA_OK) return st;
     if (!a->o || !a->lse) return fail(FA_ERR_INVALID_ARG, "o and lse must be non-NULL");
     if (!aligned(a->o, 16) || !aligned(a->lse, 4))
@@ -244,7 +246,6 @@ fa_status fa_fwd_paged(const fa_paged_kv* c, const fa_paged_fwd_args* a, const f
     const Scratch lay = layout(c, a, ctas);
     if (scratch_bytes < lay.bytes)
         return fail(FA_ERR_INVALID_ARG, "scratch holds %zu bytes, %zu needed", scratch_bytes, lay.bytes);
-    if (c->total_q == 0) return fa::report(FA_OK, "");
 
     uint8_t* base = static_cast<uint8_t*>(scratch);
     fa::PagedParams p{};
