@@ -245,12 +245,13 @@ fa_status fa::check_score_desc(const fa_score_desc* sc, fa_score_desc* out) { re
 
 int fa::device_sm_count() { return sm_count(); }
 
-fa_status fa::page_tensor_map(CUtensorMap* map, const void* base, long long blocks, int page_size, int D) {
+fa_status fa::page_tensor_map(CUtensorMap* map, const void* base, long long blocks, int page_size, int D,
+                              int tile_keys) {
     auto fn = encode_fn();
     if (!fn) return fail(FA_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
     const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)page_size, (cuuint64_t)blocks};
     const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)page_size * D * 2};
-    const cuuint32_t box[3] = {64, (cuuint32_t)std::min(page_size, kBlock), 1};
+    const cuuint32_t box[3] = {64, (cuuint32_t)std::min(page_size, tile_keys), 1};
     const cuuint32_t estr[3] = {1, 1, 1};
     CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

@@ -165,10 +165,24 @@ struct PagedParts {
     float2* row_ml;
 };
 
+// n / d for 0 <= n < 2^31 by a multiplication: with 2^s >= d and
+// m = floor(2^32 (2^s - d) / d) + 1, n / d = (mulhi(m, n) + n) >> s
+// (Granlund and Montgomery).
+struct FastDiv {
+    uint32_t d, m, s;
+};
+inline FastDiv fast_div(uint32_t d) {
+    FastDiv f{d, 0, 0};
+    while ((1ull << f.s) < d) ++f.s;
+    f.m = static_cast<uint32_t>((((1ull << f.s) - d) << 32) / d + 1);
+    return f;
+}
+
 struct PagedParams {
     PagedView c;
     PagedMask mask;
     int Hq, group, D;
+    FastDiv by_group;
     int max_q;
     int shared;           // length of the shared prefix
     int prefix;           // 1: this kernel attends to the shared prefix, 0: to the sequences' own keys
@@ -219,6 +233,11 @@ cudaError_t launch_kv_append(const AppendParams& p, cudaStream_t s);
 constexpr int kPagedSmallRows = 16;
 constexpr int kPagedTileRows = 256;
 constexpr int kPagedMaxSeqs = 2048;
+// Keys of a tile: 32 KB of K and V for the small kernel (three such stages and
+// two CTAs per SM), 128 keys for the other.
+inline int paged_small_keys(int D) { return D == 64 ? 128 : 64; }
+constexpr int kPagedTileKeys = 128;
+constexpr int kPagedSmallCtasPerSm = 2;
 cudaError_t launch_paged_small(const PagedParams& p, const CUtensorMap& tk, const CUtensorMap& tv, bool after_prefix,
                                cudaStream_t s);
 cudaError_t launch_paged_tiles(const PagedParams& p, const CUtensorMap& tk, const CUtensorMap& tv, bool after_prefix,
@@ -228,9 +247,9 @@ cudaError_t launch_paged_join_rows(const PagedJoin& p, cudaStream_t s);
 // Validates a score_mod (NULL becomes FA_SCORE_NONE in *out).
 fa_status check_score_desc(const fa_score_desc* sc, fa_score_desc* out);
 int device_sm_count();
-// [blocks][page_size][D] bf16, boxes of min(page_size, 128) rows x 64 columns
-// with 128-byte swizzle.
-fa_status page_tensor_map(CUtensorMap* map, const void* base, long long blocks, int page_size, int D);
+// [blocks][page_size][D] bf16, boxes of min(page_size, tile_keys) rows x 64
+// columns with 128-byte swizzle.
+fa_status page_tensor_map(CUtensorMap* map, const void* base, long long blocks, int page_size, int D, int tile_keys);
 int decode_max_splits();
 int decode_max_rows();
 

@@ -12,6 +12,10 @@ namespace fa {
 __host__ __device__ __forceinline__ int imin(int a, int b) { return a < b ? a : b; }
 __host__ __device__ __forceinline__ int imax(int a, int b) { return a > b ? a : b; }
 
+__device__ __forceinline__ int quotient(int n, const FastDiv& f) {
+    return static_cast<int>((__umulhi(f.m, static_cast<uint32_t>(n)) + static_cast<uint32_t>(n)) >> f.s);
+}
+
 // A sequence of the step: its rows of the step's tensors and its length.
 // n = 0: nothing to do (no new tokens, or numbers that contradict each other).
 struct SeqInfo {
@@ -52,7 +56,8 @@ __device__ __forceinline__ SeqInfo seq_info(const PagedView& c, int b, int max_q
 }
 
 // The keys that rows at positions i0 .. i1 (any of them) can see among the
-// keys jlo .. jhi - 1: [s0, s1), the sinks, and [lo, hi), in tiles of 128.
+// keys jlo .. jhi - 1: [s0, s1), the sinks, and [lo, hi), in tiles of 2^shift
+// keys.
 struct Hull {
     int lo, hi, s0, s1;
     int st0, ns, wt0;      // first sink tile, sink tiles, first tile of [lo, hi)
@@ -68,7 +73,8 @@ struct Hull {
     __host__ __device__ __forceinline__ int tile(int k) const { return k < ns ? st0 + k : wt0 + (k - ns); }
 };
 
-__host__ __device__ __forceinline__ Hull make_hull(const PagedMask& m, int i0, int i1, int jlo, int jhi) {
+__host__ __device__ __forceinline__ Hull make_hull(const PagedMask& m, int i0, int i1, int jlo, int jhi, int shift) {
+    const int up = (1 << shift) - 1;
     Hull u;
     int lo = jlo, hi = jhi;
     if (m.causal) hi = imin(hi, i1 + 1);
@@ -79,10 +85,10 @@ __host__ __device__ __forceinline__ Hull make_hull(const PagedMask& m, int i0, i
     u.lo = lo;
     u.hi = imax(hi, lo);
     const bool win = hi > lo;
-    u.wt0 = lo >> 7;
-    const int wt1 = win ? (hi + 127) >> 7 : u.wt0;
-    u.st0 = u.s0 >> 7;
-    int st1 = u.s1 > u.s0 ? (u.s1 + 127) >> 7 : u.st0;
+    u.wt0 = lo >> shift;
+    const int wt1 = win ? (hi + up) >> shift : u.wt0;
+    u.st0 = u.s0 >> shift;
+    int st1 = u.s1 > u.s0 ? (u.s1 + up) >> shift : u.st0;
     if (win) st1 = imin(st1, u.wt0);
     u.ns = imax(st1 - u.st0, 0);
     u.tiles = imax(u.ns + wt1 - u.wt0, 1);
@@ -96,8 +102,9 @@ __host__ __device__ __forceinline__ bool paged_visible(const PagedMask& m, int i
 }
 
 // Whether every row at positions i0 .. i1 sees every key of tile kb.
-__host__ __device__ __forceinline__ bool tile_open(const PagedMask& m, int kb, int i0, int i1, int jlo, int jhi) {
-    const int c0 = kb * kBlock, c1 = c0 + kBlock - 1;
+__host__ __device__ __forceinline__ bool tile_open(const PagedMask& m, int kb, int i0, int i1, int jlo, int jhi,
+                                                   int shift) {
+    const int c0 = kb << shift, c1 = c0 + (1 << shift) - 1;
     return c0 >= jlo && c1 < jhi && (!m.causal || c1 <= i0) && (m.window < 0 || i1 - c0 <= m.window || c1 < m.sinks);
 }
 
@@ -117,12 +124,14 @@ __device__ __forceinline__ float paged_score(const ScoreParams& sc, float s, int
     return s;
 }
 
-// The loader's share of one tile: lane l of the warp stands for the tile's
-// page l.  Reads the page's id ahead of the copy (-1: no live key, not read).
+// The loader's share of one tile of KT keys: lane l of the warp stands for the
+// tile's page l.  Reads the page's id ahead of the copy (-1: no live key, not
+// read).
+template <int KT>
 __device__ __forceinline__ int tile_page(const PagedView& c, const int32_t* table, const Hull& u, int kb, int lane,
                                          int b, uint32_t* ws) {
-    const int span = min(c.page_size, kBlock), a = kb * kBlock + lane * span;
-    if (lane * span >= kBlock || !u.any(a, a + span)) return -1;
+    const int span = min(c.page_size, KT), a = kb * KT + lane * span;
+    if (lane * span >= KT || !u.any(a, a + span)) return -1;
     const int id = __ldg(table + (a >> c.page_shift));
     if (id < 0 || id >= c.num_pages) {
         report_sequence(ws, b);

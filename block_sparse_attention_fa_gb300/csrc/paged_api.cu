@@ -95,7 +95,7 @@ fa_status check_fwd(const fa_paged_kv* c, const fa_paged_fwd_args* a) {
     if (c->Hkv > 65535) return fail(FA_ERR_UNSUPPORTED, "Hkv must be <= 65535");
     // the line of tiles is counted in 32 bits: units (at most one partly
     // filled one per sequence) x kv heads x tiles
-    const long long group = a->Hq / c->Hkv, tiles = cap / fa::kBlock + 2;
+    const long long group = a->Hq / c->Hkv, tiles = cap / 64 + 2;
     const double units = (double)c->B + (double)c->total_q * group / fa::kPagedTileRows + 1;
     if (units * c->Hkv * tiles > 2147483647.0 || (long long)c->total_q * a->Hq > 2147483647LL)
         return fail(FA_ERR_UNSUPPORTED, "too much work for one call (%d rows of %d heads against up to %lld keys)",
@@ -109,7 +109,12 @@ struct Scratch {
     size_t hdr, meta, slot_o, slot_ml, row_o, row_ml, desc, pre_slot_o, pre_slot_ml, pre_row_o, pre_row_ml, bytes;
 };
 
-Scratch layout(const fa_paged_kv* c, const fa_paged_fwd_args* a, int ctas) {
+// CTAs that share the work of a call's own keys.
+int own_ctas(const fa_paged_kv* c, const fa_paged_fwd_args* a) {
+    return fa::device_sm_count() * (small_rows(c, a) ? fa::kPagedSmallCtasPerSm : 1);
+}
+
+Scratch layout(const fa_paged_kv* c, const fa_paged_fwd_args* a) {
     Scratch s{};
     size_t at = 0;
     auto take = [&](size_t bytes) {
@@ -117,14 +122,14 @@ Scratch layout(const fa_paged_kv* c, const fa_paged_fwd_args* a, int ctas) {
         at += (bytes + 255) & ~(size_t)255;
         return here;
     };
-    const size_t slots = 2u * (size_t)ctas, D = c->D;
-    const size_t own = slots * (small_rows(c, a) ? fa::kPagedSmallRows : fa::kPagedTileRows);
+    const size_t ctas = own_ctas(c, a), D = c->D;
+    const size_t own = 2 * ctas * (small_rows(c, a) ? fa::kPagedSmallRows : fa::kPagedTileRows);
     s.hdr = take(256);
     s.meta = take(ctas * sizeof(fa::PagedMeta));
     s.slot_o = take(own * D * 4);
     s.slot_ml = take(own * 8);
     if (a->shared_len > 0) {
-        const size_t rows = (size_t)c->total_q * a->Hq, pre = slots * fa::kPagedTileRows;
+        const size_t rows = (size_t)c->total_q * a->Hq, pre = 2 * (size_t)fa::device_sm_count() * fa::kPagedTileRows;
         s.row_o = take(rows * D * 4);
         s.row_ml = take(rows * 8);
         s.desc = take(rows * 8);
@@ -204,7 +209,7 @@ fa_status fa_kv_append(const fa_paged_kv* c, const fa_kv_append_args* a, void* w
 size_t fa_paged_scratch_bytes(const fa_paged_kv* c, const fa_paged_fwd_args* a) {
     if (check_fwd(c, a) != FA_OK) return 0;
     fa::report(FA_OK, "");
-    return layout(c, a, fa::device_sm_count()).bytes;
+    return layout(c, a).bytes;
 }
 
 fa_status fa_fwd_paged(const fa_paged_kv* c, const fa_paged_fwd_args* a, const fa_mask_desc* mask,
@@ -242,8 +247,7 @@ fa_status fa_fwd_paged(const fa_paged_kv* c, const fa_paged_fwd_args* a, const f
     if (!workspace) return fail(FA_ERR_INVALID_ARG, "workspace is NULL");
     if (!scratch || !aligned(scratch, 16))
         return fail(FA_ERR_INVALID_ARG, "scratch must be non-NULL and 16-byte aligned");
-    const int ctas = fa::device_sm_count();
-    const Scratch lay = layout(c, a, ctas);
+    const Scratch lay = layout(c, a);
     if (scratch_bytes < lay.bytes)
         return fail(FA_ERR_INVALID_ARG, "scratch holds %zu bytes, %zu needed", scratch_bytes, lay.bytes);
 
@@ -253,11 +257,12 @@ fa_status fa_fwd_paged(const fa_paged_kv* c, const fa_paged_fwd_args* a, const f
     p.mask = m;
     p.Hq = a->Hq;
     p.group = a->Hq / c->Hkv;
+    p.by_group = fa::fast_div(p.group);
     p.D = c->D;
     p.max_q = a->max_q_len;
     p.shared = a->shared_len;
     p.join_rows = a->shared_len > 0;
-    p.ctas = ctas;
+    p.ctas = own_ctas(c, a);
     p.min_tiles = 1;
     p.scale = a->scale > 0.f ? a->scale : 1.0f / std::sqrt((float)c->D);
     p.score = {score.kind, score.softcap, score.alibi_slopes, score.rel_bias, score.rel_max};
@@ -279,21 +284,29 @@ fa_status fa_fwd_paged(const fa_paged_kv* c, const fa_paged_fwd_args* a, const f
     p.timeout_ns = (uint64_t)(a->timeout_ms ? a->timeout_ms : 2000u) * 1000000ull;
     p.flags = a->flags;
 
-    alignas(64) CUtensorMap tk, tv;
-    const long long blocks = (long long)c->num_pages * c->Hkv;
-    if ((st = fa::page_tensor_map(&tk, c->k, blocks, c->page_size, c->D)) != FA_OK) return st;
-    if ((st = fa::page_tensor_map(&tv, c->v, blocks, c->page_size, c->D)) != FA_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool small = small_rows(c, a);
+    const long long blocks = (long long)c->num_pages * c->Hkv;
+    alignas(64) CUtensorMap tk, tv, sk, sv;       // boxes of the tile kernel, of the small one
+    if (!small || p.join_rows) {
+        if ((st = fa::page_tensor_map(&tk, c->k, blocks, c->page_size, c->D, fa::kPagedTileKeys)) != FA_OK) return st;
+        if ((st = fa::page_tensor_map(&tv, c->v, blocks, c->page_size, c->D, fa::kPagedTileKeys)) != FA_OK) return st;
+    }
+    if (small) {
+        const int keys = fa::paged_small_keys(c->D);
+        if ((st = fa::page_tensor_map(&sk, c->k, blocks, c->page_size, c->D, keys)) != FA_OK) return st;
+        if ((st = fa::page_tensor_map(&sv, c->v, blocks, c->page_size, c->D, keys)) != FA_OK) return st;
+    }
     fa::PagedParams pre = p;
     if (p.join_rows) {
         pre.prefix = 1;
+        pre.ctas = fa::device_sm_count();
         pre.parts = {reinterpret_cast<float*>(base + lay.pre_slot_o), reinterpret_cast<float2*>(base + lay.pre_slot_ml),
                      reinterpret_cast<float*>(base + lay.pre_row_o), reinterpret_cast<float2*>(base + lay.pre_row_ml)};
         cudaError_t e = fa::launch_paged_tiles(pre, tk, tv, false, s);
         if (e != cudaSuccess) return cuda_fail(e, "shared prefix launch");
     }
-    cudaError_t e = small ? fa::launch_paged_small(p, tk, tv, p.join_rows, s)
+    cudaError_t e = small ? fa::launch_paged_small(p, sk, sv, p.join_rows, s)
                           : fa::launch_paged_tiles(p, tk, tv, p.join_rows, s);
     if (e != cudaSuccess) return cuda_fail(e, "paged forward launch");
     const int unit_rows = small ? fa::kPagedSmallRows : fa::kPagedTileRows;

@@ -7,9 +7,9 @@
 // query head there is nothing to reuse: every K and V byte is read once and
 // HBM bounds the kernel.
 //
-// Split.  The tiles (128 keys) of all units stand in one line, unit after
-// unit; CTA c of the grid (one per SM) takes an equal stretch of it, whatever
-// the sequences' lengths.  Only the first and the last unit of a stretch can
+// Split.  The tiles of all units stand in one line, unit after unit; CTA c of
+// the grid (two per SM) takes an equal stretch of it, whatever the sequences'
+// lengths.  Only the first and the last unit of a stretch can
 // be shared with a neighbour; those leave partials (unnormalised O, running
 // max and sum) in two slots per CTA, and a second kernel joins them in the
 // order of the keys, so that results do not depend on timing.  The loader runs
@@ -17,14 +17,21 @@
 // its stretch by itself: the lengths are on the device, and a prefix sum over
 // the sequences costs about a microsecond.
 //
+// A tile is 32 KB of K and V (128 keys of 64 columns, 64 of 128), three of them
+// are in flight per CTA, and two CTAs share an SM: what one CTA waits for (the
+// start, the barriers of a tile, the change from one unit to the next) the
+// other's work covers.  One CTA of three 64 KB stages per SM read as much at
+// once, but its tiles of 64 columns took 1.05 us instead of the 0.73 us that
+// HBM needs, and units of 512 keys 31 us instead of SMALL_512.
+//
 // CTA: 8 consumer warps and a loader warp.  The loader's lanes stand for the
 // tile's pages: each reads its page's id ahead of time and issues the page's
 // TMA boxes into a ring of stages.  Pages without a visible key are neither
-// looked up nor read.  Consumer warp w computes S for keys 16 w .. 16 w + 15
-// of the tile (mma.sync m16n8k16; 16 rows are too few for a tcgen05 tile, and
+// looked up nor read.  Consumer warp w computes S for an eighth of the tile's
+// keys (mma.sync m16n8k16; 16 rows are too few for a tcgen05 tile, and
 // the tensor pipe is not the bound), the warps exchange their row maxima and
 // then P (bf16) through shared memory, and warp w accumulates columns
-// w D / 8 .. of O over all 128 keys: no warp holds a second copy of O, so a
+// w D / 8 .. of O over all the tile's keys: no warp holds a second copy of O, so a
 // unit's end needs no merge and costs one barrier.
 //
 // V rows of keys that no row of the unit sees (past the end of the sequence,
@@ -48,18 +55,22 @@ enum PagedSite : uint32_t { S_PG_FULL = 64, S_PG_EMPTY, S_PG_DRAIN };
 
 template <int D>
 struct SmallLayout {
-    static constexpr int kStages = D == 64 ? 5 : 3;
-    static constexpr uint32_t kBox = 128u * 64u * 2u;            // 128 keys x 64 columns
+    static constexpr int kStages = 3;
+    static constexpr int kKeys = D == 64 ? 128 : 64;             // = paged_small_keys(D)
+    static constexpr int kShift = D == 64 ? 7 : 6;
+    static constexpr uint32_t kBox = kKeys * 64u * 2u;           // the tile's keys x 64 columns
     static constexpr uint32_t kStage = 2u * (D / 64) * kBox;     // K then V
-    static constexpr uint32_t kPRow = 272u;                      // 128 bf16 + 16 bytes: rows on distinct banks
+    static constexpr uint32_t kPRow = 2u * kKeys + 16u;          // 16 bytes of padding: rows on distinct banks
     static constexpr uint32_t kP = kStages * kStage;
     static constexpr uint32_t kMax = kP + kRows * kPRow;         // [16 rows][8 warps] fp32
     static constexpr uint32_t kSum = kMax + kRows * kWarps * 4u;
     static constexpr uint32_t kBars = kSum + kRows * kWarps * 4u;
     static constexpr uint32_t kAbort = kBars + 16u * kStages;
     static constexpr uint32_t kScan = kAbort + 16u;              // warp sums
-    static constexpr uint32_t kPre = kScan + 64u;                // [B + 1] first tile, [B] length, [B] new tokens
-    static constexpr uint32_t kUsed = kPre;                      // + 4 (3 B + 1)
+    static constexpr uint32_t kPre = kScan + 64u;                // [B + 1] first tile of each sequence
+    static constexpr uint32_t bytes(int B) { return kPre + 4u * (B + 1u) + 1024u; }
+    // two CTAs per SM: 228 KB less 1 KB for each
+    static_assert(2u * (kPre + 4u * (kPagedMaxSeqs + 1u) + 1024u) <= 226u * 1024u, "shared memory budget");
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -113,11 +124,10 @@ struct SmallSeg {
 // A CTA's stretch [t, t1) of the line of tiles.
 struct Line {
     const int* pre;
-    const int* kv;
-    const int* rows;
     int t, t1, per, b;
 };
 
+template <int SHIFT>
 __device__ __forceinline__ bool next_seg(const PagedParams& p, Line& ln, SmallSeg& s) {
     if (ln.t >= ln.t1) return false;
     while (p.c.Hkv * ln.pre[ln.b + 1] <= ln.t) ++ln.b;
@@ -127,10 +137,10 @@ __device__ __forceinline__ bool next_seg(const PagedParams& p, Line& ln, SmallSe
     s.h = off / s.tiles;
     s.k0 = off - s.h * s.tiles;
     s.k1 = min(s.tiles, s.k0 + (ln.t1 - ln.t));
-    s.kv = ln.kv[ln.b];
-    s.n = ln.rows[ln.b];
+    s.kv = __ldg(p.c.kv_len + ln.b);               // (checked when the line was made)
     s.q0 = __ldg(p.c.q_start + ln.b);
-    s.hull = make_hull(p.mask, s.kv - s.n, s.kv - 1, p.shared, s.kv);
+    s.n = __ldg(p.c.q_start + ln.b + 1) - s.q0;
+    s.hull = make_hull(p.mask, s.kv - s.n, s.kv - 1, p.shared, s.kv, SHIFT);
     const int last = ln.t - s.k0 + s.tiles - 1;        // the unit's last tile in the line
     s.count = last / ln.per - ln.t / ln.per + 1;
     ln.t += s.k1 - s.k0;
@@ -138,11 +148,11 @@ __device__ __forceinline__ bool next_seg(const PagedParams& p, Line& ln, SmallSe
 }
 
 template <int D, int SCORE>
-__global__ void __launch_bounds__(kThreadsS, 1)
+__global__ void __launch_bounds__(kThreadsS, 2)
 paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                    const PagedParams p) {
     using L = SmallLayout<D>;
-    constexpr int ST = L::kStages;
+    constexpr int ST = L::kStages, KT = L::kKeys, SH = L::kShift;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -151,8 +161,6 @@ paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
     auto empty_bar = [&](int st) { return sbase + L::kBars + 8u * (ST + st); };
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kAbort);
     int* const pre = reinterpret_cast<int*>(smem + L::kPre);
-    int* const len_s = pre + p.c.B + 1;
-    int* const rows_s = len_s + p.c.B;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
 
     pdl_launch_next();
@@ -167,15 +175,11 @@ paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
     // the line of tiles
     block_prefix<kThreadsS>(p.c.B, pre, reinterpret_cast<int*>(smem + L::kScan), [&](int b) {
         const SeqInfo s = seq_info(p.c, b, p.max_q, p.shared, cta == 0 ? p.ws : nullptr);
-        len_s[b] = s.kv;
-        rows_s[b] = s.n;
-        return s.n == 0 ? 0 : make_hull(p.mask, s.kv - s.n, s.kv - 1, p.shared, s.kv).tiles;
+        return s.n == 0 ? 0 : make_hull(p.mask, s.kv - s.n, s.kv - 1, p.shared, s.kv, SH).tiles;
     });
     const int total = p.c.Hkv * pre[p.c.B];
     Line line;
     line.pre = pre;
-    line.kv = len_s;
-    line.rows = rows_s;
     line.per = max((total + p.ctas - 1) / p.ctas, p.min_tiles);
     line.t = (int)min((long long)cta * line.per, (long long)total);
     line.t1 = (int)min((long long)line.t + line.per, (long long)total);
@@ -196,7 +200,7 @@ paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
             tma_prefetch_desc(&tmK);
             tma_prefetch_desc(&tmV);
         }
-        const int span = min(p.c.page_size, kBlock);
+        const int span = min(p.c.page_size, KT);
         const uint32_t page_bytes = static_cast<uint32_t>(span) * D * 4u;    // K and V
         int last[ST];
 #pragma unroll
@@ -204,20 +208,20 @@ paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         int g = 0;
         bool ok = true;
         SmallSeg s;
-        while (ok && next_seg(p, line, s)) {
+        while (ok && next_seg<SH>(p, line, s)) {
             const int32_t* table = p.c.page_table + (size_t)s.b * p.c.max_pages;
-            int page = tile_page(p.c, table, s.hull, s.hull.tile(s.k0), lane, s.b, p.ws);
+            int page = tile_page<KT>(p.c, table, s.hull, s.hull.tile(s.k0), lane, s.b, p.ws);
             for (int k = s.k0; k < s.k1; ++k, ++g) {
                 const int kb = s.hull.tile(k), st = g % ST;
                 const int id = page;
-                if (k + 1 < s.k1) page = tile_page(p.c, table, s.hull, s.hull.tile(k + 1), lane, s.b, p.ws);
+                if (k + 1 < s.k1) page = tile_page<KT>(p.c, table, s.hull, s.hull.tile(k + 1), lane, s.b, p.ws);
                 if (g >= ST && !mbar_wait_warp(empty_bar(st), (g / ST - 1) & 1, wc, S_PG_EMPTY)) { ok = false; break; }
                 const uint32_t pages = __popc(__ballot_sync(0xffffffffu, id >= 0));
                 if (lane == 0) mbar_arrive_expect_tx(full_bar(st), pages * page_bytes);
                 __syncwarp();
                 if (id >= 0) {
                     const uint32_t dst = sbase + st * L::kStage + static_cast<uint32_t>(lane * span) * 128u;
-                    const int row = (kb * kBlock + lane * span) & (p.c.page_size - 1);
+                    const int row = (kb * KT + lane * span) & (p.c.page_size - 1);
                     const int block = id * p.c.Hkv + s.h;
 #pragma unroll
                     for (int c = 0; c < D / 64; ++c) {
@@ -246,19 +250,20 @@ paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
     const uint32_t sP = sbase + L::kP;
     const float sl2 = SCORE == FA_SCORE_NONE ? p.scale * kLog2eP : kLog2eP;   // to base 2
     constexpr int kNT = D / 64;                    // n8 tiles of O per warp
+    constexpr int kKW = KT / 8, kNK = kKW / 8;     // keys per warp, n8 tiles of S
     const int col0 = warp * (D / 8);               // the warp's first column of O
     int g = 0;
     bool ok = true;
     PagedMeta meta{};
     SmallSeg s;
-    while (ok && next_seg(p, line, s)) {
+    while (ok && next_seg<SH>(p, line, s)) {
         const int rows = s.n * p.group, i0 = s.kv - s.n, i1 = s.kv - 1;
         int tok[2], hq[2];
         uint32_t qa[D / 16][4];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int r = min(gr + 8 * e, rows - 1);
-            tok[e] = r / p.group;
+            tok[e] = quotient(r, p.by_group);
             hq[e] = s.h * p.group + r - tok[e] * p.group;
             const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q + (long long)(s.q0 + tok[e]) * p.qs[0] +
                                                                     (long long)hq[e] * p.qs[1]);
@@ -274,27 +279,43 @@ paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         for (int n = 0; n < kNT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
 
         for (int k = s.k0; k < s.k1; ++k, ++g) {
-            const int st = g % ST, kb = s.hull.tile(k), c0 = kb * kBlock;
+            const int st = g % ST, kb = s.hull.tile(k), c0 = kb * KT;
             const uint32_t kbase = sbase + st * L::kStage, vbase = kbase + (D / 64) * L::kBox;
             const bool here = mbar_wait_warp(full_bar(st), (g / ST) & 1, wc, S_PG_FULL);
-            float x[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+            float x[kNK][4];
+#pragma unroll
+            for (int nt = 0; nt < kNK; ++nt) x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.f;
             float mx[2] = {-CUDART_INF_F, -CUDART_INF_F};
             bool cleared = false;
             if (here) {
-                const int key = 16 * warp + 8 * (mi >> 1) + l8;
+                if constexpr (kNK == 2) {
+                    const int key = 16 * warp + 8 * (mi >> 1) + l8;
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    uint32_t kf[4];
-                    ldsm4(kbase + (ks >> 2) * L::kBox + swz(key, 2 * (ks & 3) + (mi & 1)), kf);
-                    mma_16816(x[0], qa[ks], kf[0], kf[1]);
-                    mma_16816(x[1], qa[ks], kf[2], kf[3]);
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                        uint32_t kf[4];
+                        ldsm4(kbase + (ks >> 2) * L::kBox + swz(key, 2 * (ks & 3) + (mi & 1)), kf);
+                        mma_16816(x[0], qa[ks], kf[0], kf[1]);
+                        mma_16816(x[1], qa[ks], kf[2], kf[3]);
+                    }
+                } else {
+                    // 8 keys: two K steps per load; two sums, so that the products do not all wait in one chain
+                    float y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ks += 2) {
+                        uint32_t kf[4];
+                        ldsm4(kbase + (ks >> 2) * L::kBox + swz(8 * warp + l8, 2 * (ks & 3) + mi), kf);
+                        mma_16816(x[0], qa[ks], kf[0], kf[1]);
+                        mma_16816(y, qa[ks + 1], kf[2], kf[3]);
+                    }
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) x[0][c] += y[c];
                 }
-                const bool open = tile_open(p.mask, kb, i0, i1, p.shared, s.kv);
+                const bool open = tile_open(p.mask, kb, i0, i1, p.shared, s.kv, SH);
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt) {
+                for (int nt = 0; nt < kNK; ++nt) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        const int e = c >> 1, j = c0 + 16 * warp + 8 * nt + 2 * tq + (c & 1);
+                        const int e = c >> 1, j = c0 + kKW * warp + 8 * nt + 2 * tq + (c & 1);
                         float v = x[nt][c];
                         if (SCORE != FA_SCORE_NONE) v = paged_score<SCORE>(p.score, v * p.scale, hq[e], i0 + tok[e], j);
                         v *= sl2;
@@ -304,14 +325,14 @@ paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                     }
                 }
                 // V rows that no row of the unit sees
-                const int a = c0 + 16 * warp;
-                if (!s.hull.all(a, a + 16)) {
+                const int a = c0 + kKW * warp;
+                if (!s.hull.all(a, a + kKW)) {
                     cleared = true;
-                    for (int r = 0; r < 16; ++r) {
+                    for (int r = 0; r < kKW; ++r) {
                         if (s.hull.live(a + r)) continue;
                         if (lane < D / 8)
                             *reinterpret_cast<uint4*>(smem + st * L::kStage + (D / 64 + (lane >> 3)) * L::kBox +
-                                                      swz(16 * warp + r, lane & 7)) = make_uint4(0u, 0u, 0u, 0u);
+                                                      swz(kKW * warp + r, lane & 7)) = make_uint4(0u, 0u, 0u, 0u);
                     }
                 }
 #pragma unroll
@@ -335,11 +356,11 @@ paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                 m[e] = m_new;
                 l[e] *= alpha[e];
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt) {
+                for (int nt = 0; nt < kNK; ++nt) {
                     const float p0 = ex2_approx(x[nt][2 * e] + nm), p1 = ex2_approx(x[nt][2 * e + 1] + nm);
                     l[e] += p0 + p1;
                     *reinterpret_cast<uint32_t*>(smem + L::kP + (gr + 8 * e) * L::kPRow +
-                                                 2 * (16 * warp + 8 * nt + 2 * tq)) = pack_bf16x2(p0, p1);
+                                                 2 * (kKW * warp + 8 * nt + 2 * tq)) = pack_bf16x2(p0, p1);
                 }
             }
 #pragma unroll
@@ -350,10 +371,10 @@ paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                 o[n][3] *= alpha[1];
             }
             consumers_sync();
-            // O[:, col0 ..] += P V over the tile's 128 keys
+            // O[:, col0 ..] += P V over the tile's keys
             const uint32_t p_row = sP + (l8 + 8 * (mi & 1)) * L::kPRow + 16 * (mi >> 1);
 #pragma unroll
-            for (int ks = 0; ks < 8; ks += 2) {
+            for (int ks = 0; ks < KT / 16; ks += 2) {
                 uint32_t pa[4], pb[4], vf[4];
                 ldsm4(p_row + 32 * ks, pa);
                 ldsm4(p_row + 32 * (ks + 1), pb);
@@ -433,74 +454,93 @@ paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
     pdl_wait_previous();
 }
 
-// One row's partials -> O and lse.  Lane: kV adjacent columns.
-template <int D>
-struct RowJoin {
-    static constexpr int kV = D / 32;
-    float m, l, o[kV];
-    __device__ __forceinline__ void init() {
-        m = -CUDART_INF_F;
-        l = 0.f;
-#pragma unroll
-        for (int c = 0; c < kV; ++c) o[c] = 0.f;
-    }
-    __device__ __forceinline__ void add(const float* src, float2 ml, int lane) {
-        float v[kV];
-        if constexpr (kV == 4) {
-            const float4 x = *reinterpret_cast<const float4*>(src + 4 * lane);
-            v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-        } else {
-            const float2 x = *reinterpret_cast<const float2*>(src + 2 * lane);
-            v[0] = x.x; v[1] = x.y;
-        }
-        if (ml.y == 0.f) return;                   // the part has no visible key for this row
-        const float mn = fmaxf(m, ml.x);
-        const float f = l == 0.f ? 0.f : ex2_approx(m - mn), w = ex2_approx(ml.x - mn);
-        m = mn;
-        l = l * f + ml.y * w;
-#pragma unroll
-        for (int c = 0; c < kV; ++c) o[c] = o[c] * f + v[c] * w;
-    }
-    // `count` partials: slot rows first, first + stride, first + 3 stride, ..
-    // (slots 2 c + 1, 2 (c + 1), 2 (c + 2), ..)
-    __device__ __forceinline__ void add_slots(const PagedParts& s, long long first, int count, int stride, int lane) {
-#pragma unroll 4
-        for (int k = 0; k < count; ++k) {
-            const long long at = first + (k ? (2LL * k - 1) * stride : 0);
-            add(s.slot_o + at * D, s.slot_ml[at], lane);
-        }
-    }
-    __device__ __forceinline__ void store(const PagedParams& p, long long row, int lane) const {
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        if (p.flags & FA_OUT_FP32) {
-            float* dst = static_cast<float*>(p.o) + row * D + kV * lane;
-#pragma unroll
-            for (int c = 0; c < kV; c += 2) *reinterpret_cast<float2*>(dst + c) = make_float2(o[c] * inv, o[c + 1] * inv);
-        } else {
-            uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + row * D + kV * lane);
-#pragma unroll
-            for (int c = 0; c < kV; c += 2) dst[c / 2] = pack_bf16x2(o[c] * inv, o[c + 1] * inv);
-        }
-        if (lane == 0) p.lse[row] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * kLn2P;
-    }
+// Where a row's partials lie: `count` rows of a kernel's slots, from `first`
+// on: slots 2 c + 1, 2 (c + 1), 2 (c + 2), .. of `stride` rows each (or the
+// one partial that is kept by row).
+struct RowParts {
+    const float* o;
+    const float2* ml;
+    long long first;
+    int count, stride;
+    __device__ __forceinline__ long long at(int k) const { return first + (k ? (2LL * k - 1) * stride : 0); }
 };
 
-constexpr int kJoinWarps = 8;
+// Joins a row's partials, the parts of `a` and then those of `b`, by one warp:
+//   M = max m_k, L = sum 2^(m_k - M) l_k, O = sum 2^(m_k - M) O_k / L.
+// The lanes take a part each for its weight (32 at a time, so that the loads
+// of all of them are in flight together), then kV columns each for the sum,
+// whose loads do not wait for one another either.
+template <int D>
+__device__ __forceinline__ void join_row(const PagedParams& p, const RowParts& a, const RowParts& b, long long row,
+                                         int lane) {
+    constexpr int kV = D / 32;
+    const int n = a.count + b.count;
+    auto ml_of = [&](int k) {
+        if (k >= n) return make_float2(-CUDART_INF_F, 0.f);
+        return k < a.count ? __ldcg(a.ml + a.at(k)) : __ldcg(b.ml + b.at(k - a.count));
+    };
+    float m = -CUDART_INF_F;
+    const float2 head = ml_of(lane);
+    for (int k0 = 0; k0 < n; k0 += 32) m = fmaxf(m, (k0 ? ml_of(k0 + lane) : head).x);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    const float ref = m == -CUDART_INF_F ? 0.f : m;
+    float l = 0.f, o[kV];
+#pragma unroll
+    for (int c = 0; c < kV; ++c) o[c] = 0.f;
+    for (int k0 = 0; k0 < n; k0 += 32) {
+        const float2 ml = k0 ? ml_of(k0 + lane) : head;
+        const float w = ml.y == 0.f ? 0.f : ex2_approx(ml.x - ref);    // 0: the part has no visible key for this row
+        l += ml.y * w;
+        const int here = min(32, n - k0);
+#pragma unroll 8
+        for (int e = 0; e < here; ++e) {
+            const int k = k0 + e;
+            const float we = __shfl_sync(0xffffffffu, w, e);
+            const float* src = (k < a.count ? a.o + a.at(k) * D : b.o + b.at(k - a.count) * D) + kV * lane;
+            float v[kV];
+            if constexpr (kV == 4) {
+                const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
+                v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+            } else {
+                const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
+                v[0] = x.x; v[1] = x.y;
+            }
+#pragma unroll
+            for (int c = 0; c < kV; ++c) o[c] = fmaf(we, v[c], o[c]);
+        }
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    if (p.flags & FA_OUT_FP32) {
+        float* dst = static_cast<float*>(p.o) + row * D + kV * lane;
+#pragma unroll
+        for (int c = 0; c < kV; c += 2) *reinterpret_cast<float2*>(dst + c) = make_float2(o[c] * inv, o[c + 1] * inv);
+    } else {
+        uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + row * D + kV * lane);
+#pragma unroll
+        for (int c = 0; c < kV; c += 2) dst[c / 2] = pack_bf16x2(o[c] * inv, o[c + 1] * inv);
+    }
+    if (lane == 0) p.lse[row] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * kLn2P;
+}
+
+constexpr int kJoinWarps = 8;          // with a shared prefix: a warp per query head of the group
+constexpr int kJoinUnitWarps = 16;     // without: a warp per row of the unit
 
 // Without a shared prefix: block (c, y) joins rows of the unit that starts in
 // CTA c of the attention kernel and runs on into the next ones.
 template <int D>
-__global__ void __launch_bounds__(32 * kJoinWarps) paged_join_units_kernel(const PagedParams p, int rows_per_unit) {
+__global__ void __launch_bounds__(32 * kJoinUnitWarps) paged_join_units_kernel(const PagedParams p, int rows_per_unit) {
     pdl_wait_previous();
     const PagedMeta t = p.meta[blockIdx.x];
     if (t.count == 0) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int r = blockIdx.y * kJoinWarps + warp; r < t.rows; r += gridDim.y * kJoinWarps) {
-        RowJoin<D> j;
-        j.init();
-        j.add_slots(p.parts, (2LL * blockIdx.x + 1) * rows_per_unit + r, t.count, rows_per_unit, lane);
-        const int R = t.row0 + r, tok = R / p.group;
-        j.store(p, (long long)(t.q0 + tok) * p.Hq + t.h * p.group + R - tok * p.group, lane);
+    const RowParts none{nullptr, nullptr, 0, 0, 0};
+    for (int r = blockIdx.y * kJoinUnitWarps + warp; r < t.rows; r += gridDim.y * kJoinUnitWarps) {
+        const RowParts a{p.parts.slot_o, p.parts.slot_ml, (2LL * blockIdx.x + 1) * rows_per_unit + r, t.count, rows_per_unit};
+        const int R = t.row0 + r, tok = quotient(R, p.by_group);
+        join_row<D>(p, a, none, (long long)(t.q0 + tok) * p.Hq + t.h * p.group + R - tok * p.group, lane);
     }
 }
 
@@ -522,20 +562,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_rows_kernel(const 
     const int tiles = p.hdr[0], per = p.hdr[1];
     for (int gq = warp; gq < p.group; gq += kJoinWarps) {
         const long long row = (long long)t * p.Hq + h * p.group + gq;
-        RowJoin<D> x;
-        x.init();
+        const int2 d = p.rowdesc[row];
         const int R = t * p.group + gq, rt = R / j.pre_rows, r = R - rt * j.pre_rows;
         const int first = (rt * p.c.Hkv + h) * tiles, ca = first / per, cb = (first + tiles - 1) / per;
-        if (ca == cb)
-            x.add(j.pre.row_o + row * D, j.pre.row_ml[row], lane);
-        else
-            x.add_slots(j.pre, (2LL * ca + 1) * j.pre_rows + r, cb - ca + 1, j.pre_rows, lane);
-        const int2 d = p.rowdesc[row];
-        if (d.x < 0)
-            x.add(p.parts.row_o + row * D, p.parts.row_ml[row], lane);
-        else
-            x.add_slots(p.parts, d.x, d.y, j.own_rows, lane);
-        x.store(p, row, lane);
+        RowParts a{j.pre.slot_o, j.pre.slot_ml, (2LL * ca + 1) * j.pre_rows + r, cb - ca + 1, j.pre_rows};
+        if (ca == cb) a = RowParts{j.pre.row_o, j.pre.row_ml, row, 1, 0};
+        RowParts own{p.parts.slot_o, p.parts.slot_ml, d.x, d.y, j.own_rows};
+        if (d.x < 0) own = RowParts{p.parts.row_o, p.parts.row_ml, row, 1, 0};
+        join_row<D>(p, a, own, row, lane);
     }
 }
 
@@ -544,8 +578,7 @@ cudaError_t launch_small(const PagedParams& p, const CUtensorMap& tk, const CUte
                          cudaStream_t s) {
     auto kern = paged_small_kernel<D, SCORE>;
     using L = SmallLayout<D>;
-    constexpr size_t most = L::kUsed + 4u * (3u * kPagedMaxSeqs + 1u) + 1024u;
-    static_assert(most <= 227u * 1024u, "shared memory budget");
+    constexpr size_t most = L::bytes(kPagedMaxSeqs);
     static bool attr_set[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -555,8 +588,7 @@ cudaError_t launch_small(const PagedParams& p, const CUtensorMap& tk, const CUte
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) attr_set[dev] = true;
     }
-    const size_t smem = L::kUsed + 4u * (3u * p.c.B + 1u) + 1024u;
-    return paged_launch(kern, dim3(p.ctas), kThreadsS, smem, overlap, s, tk, tv, p);
+    return paged_launch(kern, dim3(p.ctas), kThreadsS, L::bytes(p.c.B), overlap, s, tk, tv, p);
 }
 
 template <int D>
@@ -579,9 +611,10 @@ cudaError_t launch_paged_small(const PagedParams& p, const CUtensorMap& tk, cons
 }
 
 cudaError_t launch_paged_join_units(const PagedParams& p, int rows_per_unit, cudaStream_t s) {
-    const dim3 grid(p.ctas, rows_per_unit <= 16 ? 2 : 8);
-    return p.D == 64 ? paged_launch(paged_join_units_kernel<64>, grid, 32 * kJoinWarps, 0, true, s, p, rows_per_unit)
-                     : paged_launch(paged_join_units_kernel<128>, grid, 32 * kJoinWarps, 0, true, s, p, rows_per_unit);
+    const dim3 grid(p.ctas, rows_per_unit <= kJoinUnitWarps ? 1 : 8);
+    const int threads = 32 * kJoinUnitWarps;
+    return p.D == 64 ? paged_launch(paged_join_units_kernel<64>, grid, threads, 0, true, s, p, rows_per_unit)
+                     : paged_launch(paged_join_units_kernel<128>, grid, threads, 0, true, s, p, rows_per_unit);
 }
 
 cudaError_t launch_paged_join_rows(const PagedJoin& p, cudaStream_t s) {

@@ -41,6 +41,11 @@ namespace fa {
 namespace {
 
 constexpr int kThreadsT = 384;
+// Registers per thread: launched with 168 (65536 / 384, rounded down to 8); the
+// loader, MMA and clearing warps hand theirs to the two softmax warpgroups:
+// 128 x (2 x 184 + 136) = 384 x 168.  build.py checks the launch count.
+constexpr uint32_t kRegsSoftmaxT = 184, kRegsOtherT = 136;
+static_assert(2 * kRegsSoftmaxT + kRegsOtherT == 3 * 168, "register split must match the launch");
 constexpr uint32_t kTmemColsT = 512;
 constexpr float kLog2eQ = 1.4426950408889634f;
 constexpr float kLn2Q = 0.6931471805599453f;
@@ -72,18 +77,15 @@ struct TileLayout {
     static constexpr uint32_t kQ = 0;
     static constexpr uint32_t kK = kQ + 2 * kTile;
     static constexpr uint32_t kV = kK + kStages * kTile;
-    // per softmax warp, 32 rows x 64 bytes of O, rows padded to distinct banks
-    static constexpr uint32_t kOStageRow = 80;
-    static constexpr uint32_t kOStage = kV + kStages * kTile;
-    static constexpr uint32_t kBars = kOStage + 8 * 32 * kOStageRow;
+    static constexpr uint32_t kBars = kV + kStages * kTile;
     static constexpr uint32_t kTmemSlot = kBars + 8 * T_COUNT;
     static constexpr uint32_t kAbort = kTmemSlot + 4;
     static constexpr uint32_t kMinMax = kAbort + 4;          // positions of the batch (shared prefix)
     static constexpr uint32_t kScan = kMinMax + 8;
-    static constexpr uint32_t kPre = kScan + 4 * (kThreadsT / 32);   // [B + 1] first tile of each sequence
-    static constexpr uint32_t kUsed = kPre;
+    static constexpr uint32_t kPre = kScan + 4 * (kThreadsT / 32);   // TileLine's arrays
+    static constexpr uint32_t bytes(int B) { return kPre + 4u * (3u * B + 2u) + 1024u; }
     static_assert(kStages <= kMaxRing, "ring");
-    static_assert(kUsed + 4 * (kPagedMaxSeqs + 1) + 1024 <= 227u * 1024u, "shared memory budget");
+    static_assert(kPre + 4 * (3 * kPagedMaxSeqs + 2) + 1024 <= 227u * 1024u, "shared memory budget");
 };
 
 // C log2(e) tanh(u) through 1 - 2 / (2^(2 log2(e) |u|) + 1).
@@ -99,6 +101,18 @@ __device__ __forceinline__ void exp2_pair(float& p0, float& p1, float x0, float 
     p1 = ex2_approx(a1);
 }
 
+// Eight words; `wide`: to a 32-byte boundary (16 otherwise).
+__device__ __forceinline__ void store8(void* dst, const uint32_t* w, bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        static_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        static_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
 // The part of a unit in a CTA's stretch.
 struct TileSeg {
     int b, h, row0, rows, q0, n, kv;
@@ -110,16 +124,16 @@ struct TileSeg {
 };
 
 struct TileLine {
-    const int* pre;
+    const int *pre, *kv, *q0;           // [B + 1] first tile, [B] length, [B + 1] first row
     int t, t1, per, b, rt, start;       // start: where unit group (b, rt), its Hkv units, begins in the line
     int prefix_tiles, prefix_rows, imin, imax;
 };
 
-// Rows 256 rt .. of sequence s (group query heads per token): their positions.
-__device__ __forceinline__ void unit_rows(const SeqInfo& s, int group, int rt, int& i0, int& i1) {
-    const int r0 = rt * kPagedTileRows, r1 = min(r0 + kPagedTileRows, s.n * group) - 1;
-    i0 = s.kv - s.n + r0 / group;
-    i1 = s.kv - s.n + r1 / group;
+// The positions of rows 256 rt .. of a sequence of n new tokens.
+__device__ __forceinline__ void unit_rows(const FastDiv& by_group, int n, int kv, int rt, int& i0, int& i1) {
+    const int r0 = rt * kPagedTileRows, r1 = min(r0 + kPagedTileRows, n * static_cast<int>(by_group.d)) - 1;
+    i0 = kv - n + quotient(r0, by_group);
+    i1 = kv - n + quotient(r1, by_group);
 }
 
 __device__ __forceinline__ bool next_seg(const PagedParams& p, TileLine& ln, TileSeg& s) {
@@ -136,7 +150,7 @@ __device__ __forceinline__ bool next_seg(const PagedParams& p, TileLine& ln, Til
         s.jhi = p.shared;
         s.i0 = ln.imin;
         s.i1 = ln.imax;
-        s.hull = make_hull(p.mask, s.i0, s.i1, s.jlo, s.jhi);
+        s.hull = make_hull(p.mask, s.i0, s.i1, s.jlo, s.jhi, 7);
     } else {
         while (p.c.Hkv * ln.pre[ln.b + 1] <= ln.t) {
             ++ln.b;
@@ -144,15 +158,14 @@ __device__ __forceinline__ bool next_seg(const PagedParams& p, TileLine& ln, Til
             ln.start = p.c.Hkv * ln.pre[ln.b];
         }
         s.b = ln.b;
-        s.q0 = __ldg(p.c.q_start + s.b);
-        s.n = __ldg(p.c.q_start + s.b + 1) - s.q0;
-        s.kv = __ldg(p.c.kv_len + s.b);
-        const SeqInfo si{s.q0, s.n, s.kv};
+        s.q0 = ln.q0[s.b];
+        s.n = ln.q0[s.b + 1] - s.q0;
+        s.kv = ln.kv[s.b];
         s.jlo = p.shared;
         s.jhi = s.kv;
         for (;;) {
-            unit_rows(si, p.group, ln.rt, s.i0, s.i1);
-            s.hull = make_hull(p.mask, s.i0, s.i1, s.jlo, s.jhi);
+            unit_rows(p.by_group, s.n, s.kv, ln.rt, s.i0, s.i1);
+            s.hull = make_hull(p.mask, s.i0, s.i1, s.jlo, s.jhi, 7);
             const int next = ln.start + p.c.Hkv * s.hull.tiles;
             if (ln.t < next) break;
             ln.start = next;
@@ -187,6 +200,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kAbort);
     int* const minmax = reinterpret_cast<int*>(smem + L::kMinMax);
     int* const pre = reinterpret_cast<int*>(smem + L::kPre);
+    int* const q0_s = pre + p.c.B + 1;
+    int* const len_s = q0_s + p.c.B + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
 
     pdl_launch_next();
@@ -217,6 +232,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
     // the line of tiles
     TileLine line{};
     line.pre = pre;
+    line.kv = len_s;
+    line.q0 = q0_s;
     int total;
     if (p.prefix) {
         for (int b = threadIdx.x; b < p.c.B; b += kThreadsT) {
@@ -232,7 +249,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         const int rows = min(max(__ldg(p.c.q_start + p.c.B), 0), p.c.total_q) * p.group;
         line.prefix_rows = line.imin <= line.imax ? rows : 0;      // no sequence has rows: nothing to do
         line.prefix_tiles =
-            line.prefix_rows ? make_hull(p.mask, line.imin, line.imax, 0, p.shared).tiles : 1;
+            line.prefix_rows ? make_hull(p.mask, line.imin, line.imax, 0, p.shared, 7).tiles : 1;
         total = (line.prefix_rows + kPagedTileRows - 1) / kPagedTileRows * p.c.Hkv * line.prefix_tiles;
     } else {
         block_prefix<kThreadsT>(p.c.B, pre, reinterpret_cast<int*>(smem + L::kScan), [&](int b) {
@@ -240,9 +257,12 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
             int sum = 0;
             for (int rt = 0; rt * kPagedTileRows < s.n * p.group; ++rt) {
                 int i0, i1;
-                unit_rows(s, p.group, rt, i0, i1);
-                sum += make_hull(p.mask, i0, i1, p.shared, s.kv).tiles;
+                unit_rows(p.by_group, s.n, s.kv, rt, i0, i1);
+                sum += make_hull(p.mask, i0, i1, p.shared, s.kv, 7).tiles;
             }
+            len_s[b] = s.kv;
+            q0_s[b] = s.q0;
+            if (b == p.c.B - 1) q0_s[p.c.B] = s.q0 + s.n;
             return sum;
         });
         total = p.c.Hkv * pre[p.c.B];
@@ -268,6 +288,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
     // Barrier phases run on counters that every role keeps alike: g counts
     // steps (ring stage g % ST), uq units in which row tile t has rows, n the
     // steps of tile t.
+    if (warp >= 8) {
+    regs_decrease<kRegsOtherT>();
     if (warp == 8) {
         // ------------------------------------------------------------ loader
         if (lane == 0) {
@@ -299,11 +321,11 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         };
         while (ok && next_seg(p, line, s)) {
             const int32_t* table = p.c.page_table + (size_t)s.b * p.c.max_pages;
-            int page = tile_page(p.c, table, s.hull, s.hull.tile(s.k0), lane, s.b, p.ws);
+            int page = tile_page<kBlock>(p.c, table, s.hull, s.hull.tile(s.k0), lane, s.b, p.ws);
             int id_v = -1, row_v = 0;
             for (int k = s.k0; k < s.k1; ++k) {
                 const int id = page, row = (s.hull.tile(k) * kBlock + lane * span) & (p.c.page_size - 1);
-                if (k + 1 < s.k1) page = tile_page(p.c, table, s.hull, s.hull.tile(k + 1), lane, s.b, p.ws);
+                if (k + 1 < s.k1) page = tile_page<kBlock>(p.c, table, s.hull, s.hull.tile(k + 1), lane, s.b, p.ws);
                 if (!load(&tmK, L::kK, T_K_FULL, T_K_EMPTY, g, id, row, S_T_K_EMPTY)) { ok = false; break; }
                 last_k = static_cast<int>(g);
                 if (k > s.k0) {
@@ -354,7 +376,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                 if (lane == 0) mbar_arrive(bar(T_V_OK + st));
             }
         }
-    } else if (warp >= 9) {
+    } else {
         // --------------------------------------------------------------- MMA
         const int t = warp - 9;
         constexpr uint32_t idesc_qk = idesc_bf16_f32(128, 64, false);
@@ -428,8 +450,10 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         mma_commit_elect(bar(T_DRAIN + t));
         paged_drain_wait(bar(T_DRAIN + t), 0, wc, S_T_DRAIN);
         __syncwarp();
+    }
     } else {
         // ----------------------------------------------------------- softmax
+        regs_increase<kRegsSoftmaxT>();
         const int t = warp >> 2, wq = warp & 3, r = wq * 32 + lane;
         const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
         const uint32_t tS = tmem + 128u * t + lane_off, tO = tmem + 256u + D * t + lane_off;
@@ -454,7 +478,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
             // this thread's row: token, query head, position
             const int ur = 128 * t + r;
             const bool valid = ur < s.rows;
-            const int R = s.row0 + min(ur, s.rows - 1), tok = R / p.group;
+            const int R = s.row0 + min(ur, s.rows - 1), tok = quotient(R, p.by_group);
             const int hq = s.h * p.group + R - tok * p.group, trow = s.q0 + tok;
             int i = s.kv - s.n + tok;
             if (p.prefix) {
@@ -465,15 +489,30 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                 }
                 i = max(__ldg(p.c.kv_len + lo) - __ldg(p.c.q_start + lo + 1) + trow, -1);
             }
-            // its row of Q: the previous unit's products have read theirs
-            // (this warp has seen their S)
+            // The warp's 32 rows of Q, D / 8 lanes to a row, so that whole lines
+            // are read (a row per lane asks for 16-byte pieces of 32 lines, 5 us
+            // for the tile; there is hardly an L1 beside this much shared
+            // memory).  The previous unit's products have read theirs: this
+            // warp has seen their S.
             {
-                const uint4* src = reinterpret_cast<const uint4*>(p.q + (long long)trow * p.qs[0] + (long long)hq * p.qs[1]);
-                uint8_t* dst = smem + L::kQ + t * L::kTile + r * 128;
+                constexpr int kLanes = D / 8, kPer = 32 / kLanes;     // lanes per row, rows per load
+                const long long mine = valid ? (long long)trow * p.qs[0] + (long long)hq * p.qs[1] : -1;
+                const int c = lane % kLanes;
+                uint8_t* const tile = smem + L::kQ + t * L::kTile + (c >> 3) * 16384;
 #pragma unroll
-                for (int c = 0; c < D / 8; ++c)
-                    *reinterpret_cast<uint4*>(dst + (c >> 3) * 16384 + (((c & 7) ^ (r & 7)) << 4)) =
-                        valid ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+                for (int b0 = 0; b0 < kLanes; b0 += 8) {
+                    uint4 w[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const long long at = __shfl_sync(0xffffffffu, mine, (b0 + e) * kPer + lane / kLanes);
+                        w[e] = at >= 0 ? __ldg(reinterpret_cast<const uint4*>(p.q + at) + c) : make_uint4(0u, 0u, 0u, 0u);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int rr = wq * 32 + (b0 + e) * kPer + lane / kLanes;
+                        *reinterpret_cast<uint4*>(tile + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = w[e];
+                    }
+                }
                 fence_async_shared();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(T_Q_FULL + t));
@@ -490,7 +529,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
             float m_use = -CUDART_INF_F, l = 0.f;
             for (int k = s.k0; ok && k < s.k1; ++k, ++n) {
                 const int kb = s.hull.tile(k);
-                const bool open = tile_open(p.mask, kb, s.i0, s.i1, s.jlo, s.jhi);
+                const bool open = tile_open(p.mask, kb, s.i0, s.i1, s.jlo, s.jhi, 7);
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
                     const uint32_t tSh = tS + 64u * h;
@@ -606,40 +645,30 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
             const long long row = (long long)trow * p.Hq + hq;
             const long long at = whole ? row : (2LL * cta + (s.begins() ? 1 : 0)) * kPagedTileRows + ur;
             const bool f32 = !last || out32;
-            uint8_t* const dst0 = static_cast<uint8_t*>(last ? p.o : static_cast<void*>(whole ? p.parts.row_o : p.parts.slot_o));
+            uint8_t* const dst = static_cast<uint8_t*>(last ? p.o : static_cast<void*>(whole ? p.parts.row_o : p.parts.slot_o)) +
+                                 at * (D * (f32 ? 4 : 2));
+            const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31u) == 0;
             const float inv = !last ? 1.f : l == 0.f ? 0.f : 1.f / l;
-            uint8_t* stage = smem + L::kOStage + warp * 32 * L::kOStageRow;
-            const int nchunk = f32 ? D / 16 : D / 32;
+            // Straight from the registers, 32 bytes (a sector) per store: through
+            // shared memory, for whole lines, it took 2.5 us instead of STORE_US.
 #pragma unroll 1
-            for (int c = 0; c < nchunk; ++c) {
-                uint32_t w[16];
-                if (f32) {
-                    uint32_t o[16];
-                    tmem_ld16(tO + 16u * c, o);
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32(tO + 32u * c, o);
+                if (!valid) {
+                } else if (f32) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
+                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) store8(dst + 128 * c + 4 * e, o + e, wide);
                 } else {
-                    uint32_t o[32];
-                    tmem_ld32(tO + 32u * c, o);
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
-                        w[e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-                }
-                __syncwarp();
+                        o[e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    *reinterpret_cast<uint4*>(stage + lane * L::kOStageRow + 16 * q) =
-                        make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
-                __syncwarp();
-#pragma unroll
-                for (int it = 0; it < 4; ++it) {
-                    const int rr = it * 8 + (lane >> 2), piece = lane & 3;
-                    const long long to = __shfl_sync(0xffffffffu, at, rr);
-                    const bool there = __shfl_sync(0xffffffffu, (int)valid, rr) != 0;
-                    if (there)
-                        *reinterpret_cast<uint4*>(dst0 + to * (D * (f32 ? 4 : 2)) + 64 * c + 16 * piece) =
-                            *reinterpret_cast<const uint4*>(stage + rr * L::kOStageRow + 16 * piece);
+                    for (int e = 0; e < 16; e += 8) store8(dst + 64 * c + 4 * e, o + e, wide);
                 }
+                __syncwarp();                      // together again for the next load
             }
             if (valid) {
                 if (last) {
@@ -674,11 +703,11 @@ cudaError_t launch_tiles(const PagedParams& p, const CUtensorMap& tk, const CUte
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64 || !attr_set[dev]) {
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)(L::kUsed + 4u * (kPagedMaxSeqs + 1u) + 1024u));
+                                 (int)L::bytes(kPagedMaxSeqs));
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) attr_set[dev] = true;
     }
-    return paged_launch(kern, dim3(p.ctas), kThreadsT, L::kUsed + 4u * (p.c.B + 1u) + 1024u, overlap, s, tk, tv, p);
+    return paged_launch(kern, dim3(p.ctas), kThreadsT, L::bytes(p.c.B), overlap, s, tk, tv, p);
 }
 
 template <int D>

@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -84,6 +85,15 @@ class BlockMaskColsStruct(ctypes.Structure):
                 ("full_q_num_blocks", ctypes.c_void_p), ("full_q_indices", ctypes.c_void_p)]
 
 
+# The paged calls' structs are packed by these (a ctypes structure costs some
+# microseconds to fill); the layouts are those of the classes below.
+_PAGED_KV = struct.Struct("7i5P")
+_KV_APPEND = struct.Struct("4i4P8q3P")
+_PAGED_FWD = struct.Struct("3ifP2q2P2I")
+_MASK = struct.Struct("4i2Pi0P")
+_SCORE = struct.Struct("if2Pi0P")
+
+
 class PagedKVStruct(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32), ("num_pages", ctypes.c_int32),
                 ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("total_q", ctypes.c_int32),
@@ -153,14 +163,11 @@ def load_library(path: str = LIB_PATH):
                          ctypes.POINTER(BlockMaskColsStruct), ctypes.POINTER(ScoreDesc), ctypes.c_void_p,
                          ctypes.c_void_p]
     h.fa_kv_append.restype = ctypes.c_int
-    h.fa_kv_append.argtypes = [ctypes.POINTER(PagedKVStruct), ctypes.POINTER(KVAppendArgs), ctypes.c_void_p,
-                               ctypes.c_void_p]
+    h.fa_kv_append.argtypes = [ctypes.c_void_p] * 4
     h.fa_paged_scratch_bytes.restype = ctypes.c_size_t
-    h.fa_paged_scratch_bytes.argtypes = [ctypes.POINTER(PagedKVStruct), ctypes.POINTER(PagedFwdArgs)]
+    h.fa_paged_scratch_bytes.argtypes = [ctypes.c_void_p] * 2
     h.fa_fwd_paged.restype = ctypes.c_int
-    h.fa_fwd_paged.argtypes = [ctypes.POINTER(PagedKVStruct), ctypes.POINTER(PagedFwdArgs), ctypes.POINTER(MaskDesc),
-                               ctypes.POINTER(ScoreDesc), ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p,
-                               ctypes.c_void_p]
+    h.fa_fwd_paged.argtypes = [ctypes.c_void_p] * 5 + [ctypes.c_size_t] + [ctypes.c_void_p] * 2
     h.fa_workspace_check.restype = ctypes.c_int
     h.fa_workspace_check.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
     h.fa_last_error.restype = ctypes.c_char_p
@@ -176,10 +183,16 @@ def _check(status: int):
         raise FAError(status, load_library().fa_last_error().decode())
 
 
+# The current device and stream without building Python objects for them (a
+# microsecond or two each, as much as a small kernel); the public calls where
+# these are missing.
+_device_now = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda idx: torch.cuda.current_stream(idx).cuda_stream)
+
+
 def _stream_ptr(stream) -> Optional[int]:
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()) if stream is None else stream.cuda_stream)
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -211,12 +224,14 @@ def default_workspace(device, stream=None) -> Workspace:
     queue there), so each stream gets its own."""
     dev = torch.device(device)
     idx = dev.index if dev.index is not None else torch.cuda.current_device()
-    if stream is None:
-        stream = torch.cuda.current_stream(idx)
-    key = (idx, stream.cuda_stream)
-    if key not in _default_ws:
-        _default_ws[key] = Workspace(torch.device("cuda", idx))
-    return _default_ws[key]
+    return _workspace_of(idx, _raw_stream(idx) if stream is None else stream.cuda_stream)
+
+
+def _workspace_of(idx: int, raw: int) -> Workspace:
+    ws = _default_ws.get((idx, raw))
+    if ws is None:
+        ws = _default_ws[(idx, raw)] = Workspace(torch.device("cuda", idx))
+    return ws
 
 
 class BlockMask:
@@ -570,47 +585,49 @@ def bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor, lse:
 
 
 def _paged_kv(k_cache, v_cache, page_table, kv_len, q_start, total_q, dev):
-    """The fa_paged_kv of these tensors, which the C ABI reads through raw pointers: everything it cannot see is
-    checked here."""
-    if k_cache.dim() != 4 or k_cache.dtype != torch.bfloat16 or v_cache.dtype != torch.bfloat16 \
-            or k_cache.shape != v_cache.shape or not k_cache.is_contiguous() or not v_cache.is_contiguous() \
+    """The packed fa_paged_kv of these tensors and the cache's shape.  The C ABI reads them through raw pointers:
+    everything it cannot see is checked here."""
+    shape = k_cache.shape
+    if len(shape) != 4 or k_cache.dtype is not torch.bfloat16 or v_cache.dtype is not torch.bfloat16 \
+            or v_cache.shape != shape or not k_cache.is_contiguous() or not v_cache.is_contiguous() \
             or k_cache.get_device() != dev or v_cache.get_device() != dev:
         raise ValueError("k_cache and v_cache must be contiguous CUDA bf16 tensors [num_pages, Hkv, page_size, D] "
-                         "on the queries' device")
+                         "on the rows' device")
     for name, t, dims in (("page_table", page_table, 2), ("kv_len", kv_len, 1), ("q_start", q_start, 1)):
-        if t.dtype != torch.int32 or t.dim() != dims or t.get_device() != dev or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous int32 tensor of {dims} dimensions on the queries' device")
+        if t.dtype is not torch.int32 or t.dim() != dims or t.get_device() != dev or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 tensor of {dims} dimensions on the rows' device")
     B, max_pages = page_table.shape
-    if kv_len.shape[0] != B or q_start.shape[0] != B + 1:
+    if kv_len.numel() != B or q_start.numel() != B + 1:
         raise ValueError(f"page_table has {B} rows: kv_len must hold {B} lengths and q_start {B + 1} offsets "
-                         f"(got {kv_len.shape[0]}, {q_start.shape[0]})")
-    num_pages, Hkv, page, D = k_cache.shape
-    return PagedKVStruct(B, Hkv, D, num_pages, page, max_pages, total_q, k_cache.data_ptr(), v_cache.data_ptr(),
-                         page_table.data_ptr(), kv_len.data_ptr(), q_start.data_ptr())
+                         f"(got {kv_len.numel()}, {q_start.numel()})")
+    num_pages, Hkv, page, D = shape
+    return _PAGED_KV.pack(B, Hkv, D, num_pages, page, max_pages, total_q, k_cache.data_ptr(), v_cache.data_ptr(),
+                          page_table.data_ptr(), kv_len.data_ptr(), q_start.data_ptr()), Hkv, D
 
 
 def _rows(name, t, total, H, D, dev):
-    """Token and head strides of bf16 rows [total, H, D]."""
-    if t.dtype != torch.bfloat16 or t.dim() != 3 or t.get_device() != dev:
-        raise ValueError(f"{name} must be a CUDA bf16 tensor [tokens, heads, D] on one device with the cache")
-    if t.shape[0] != total or (H is not None and t.shape[1] != H) or t.shape[2] != D:
+    """Token and head strides of bf16 rows [total, H, D] (H None: any)."""
+    if t.dtype is not torch.bfloat16 or t.dim() != 3 or t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA bf16 tensor [tokens, heads, D] on the cache's device")
+    n, h, d = t.shape
+    if n != total or d != D or (H is not None and h != H):
         raise ValueError(f"{name} must be [{total}, {'heads' if H is None else H}, {D}] (got {tuple(t.shape)})")
-    st = t.stride()
-    if st[2] != 1:
+    ts, hs, es = t.stride()
+    if es != 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
     # the stride of a dimension of one entry says nothing
-    return (st[0] if t.shape[0] > 1 else D, st[1] if t.shape[1] > 1 else D)
+    return ts if n > 1 else D, hs if h > 1 else D
 
 
 def _on_device(fn):
-    """Runs a binding function with the cache's device current."""
+    """Runs a paged call with its rows' device current."""
     @functools.wraps(fn)
-    def run(q, k, v, *args, **kw):
+    def run(q, k, *args, **kw):
         at = (k if q is None else q).get_device()
-        if at < 0 or at == torch.cuda.current_device():
-            return fn(q, k, v, *args, **kw)
+        if at < 0 or at == _device_now():
+            return fn(q, k, *args, **kw)
         with torch.cuda.device(at):
-            return fn(q, k, v, *args, **kw)
+            return fn(q, k, *args, **kw)
     return run
 
 
@@ -632,36 +649,42 @@ def kv_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, k_cac
     if dev < 0 or k.dim() != 3:
         raise ValueError("k must be a CUDA bf16 tensor [tokens, Hkv, D]")
     total = k.shape[0]
-    c = _paged_kv(k_cache, v_cache, page_table, kv_len, q_start, total, dev)
-    a = KVAppendArgs()
-    a.k_stride[:] = _rows("k", k, total, c.Hkv, c.D, dev)
-    a.v_stride[:] = _rows("v", v, total, c.Hkv, c.D, dev)
-    a.k, a.v = k.data_ptr(), v.data_ptr()
+    c, Hkv, D = _paged_kv(k_cache, v_cache, page_table, kv_len, q_start, total, dev)
+    ks, vs = _rows("k", k, total, Hkv, D, dev), _rows("v", v, total, Hkv, D, dev)
+    Hq, qp, op, qs, os_ = 0, 0, 0, (0, 0), (0, 0)
     if q is not None:
-        a.q_stride[:] = _rows("q", q, total, None, c.D, dev)
+        qs = _rows("q", q, total, None, D, dev)
+        Hq, qp = q.shape[1], q.data_ptr()
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            q_out = torch.empty((total, Hq, D), dtype=torch.bfloat16, device=q.device)
             if stream is not None:
                 q_out.record_stream(stream)
-        a.q_out_stride[:] = a.q_stride[:] if q_out is q else _rows("q_out", q_out, total, q.shape[1], c.D, dev)
-        a.Hq, a.q, a.q_out = q.shape[1], q.data_ptr(), q_out.data_ptr()
+        os_ = qs if q_out is q else _rows("q_out", q_out, total, Hq, D, dev)
+        op = q_out.data_ptr()
+    rot, rope_len, cp, sp, pp = 0, 0, 0, 0, 0
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin come together")
     if cos is not None:
         for t in (cos, sin):
-            if t.dtype != torch.float32 or t.dim() != 2 or t.get_device() != dev or not t.is_contiguous() \
-                    or t.shape != cos.shape:
+            if t.dtype is not torch.float32 or t.dim() != 2 or t.get_device() != dev or not t.is_contiguous():
                 raise ValueError("cos and sin must be contiguous float32 tensors [positions, rot_dim / 2] on the "
                                  "cache's device")
-        a.rope_len, a.rot_dim = cos.shape[0], 2 * cos.shape[1]
-        a.cos, a.sin, a.interleaved = cos.data_ptr(), sin.data_ptr(), 1 if interleaved else 0
+        if sin.shape != cos.shape:
+            raise ValueError("cos and sin must have one shape")
+        rope_len, half = cos.shape
+        rot, cp, sp = 2 * half, cos.data_ptr(), sin.data_ptr()
     if positions is not None:
-        if positions.dtype != torch.int32 or positions.get_device() != dev or not positions.is_contiguous() \
+        if positions.dtype is not torch.int32 or positions.get_device() != dev or not positions.is_contiguous() \
                 or positions.numel() != total:
             raise ValueError("positions must be a contiguous int32 tensor with one entry per row")
-        a.positions = positions.data_ptr()
-    ws = workspace or default_workspace(k.device, stream)
-    _check(load_library().fa_kv_append(ctypes.byref(c), ctypes.byref(a), ws.ptr, _stream_ptr(stream)))
+        pp = positions.data_ptr()
+    a = _KV_APPEND.pack(Hq, rot, rope_len, 1 if interleaved else 0, qp, k.data_ptr(), v.data_ptr(), op, *qs, *ks, *vs,
+                        *os_, cp, sp, pp)
+    raw = _raw_stream(dev) if stream is None else stream.cuda_stream
+    ws = workspace or _workspace_of(dev, raw)
+    st = load_library().fa_kv_append(c, a, ws.tensor.data_ptr(), raw)
+    if st != OK:
+        _check(st)
     return q_out
 
 
@@ -684,52 +707,57 @@ def fwd_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, pag
     dev = q.get_device()
     if dev < 0 or q.dim() != 3:
         raise ValueError("q must be a CUDA bf16 tensor [tokens, Hq, D]")
-    total, Hq, D = q.shape
-    c = _paged_kv(k_cache, v_cache, page_table, kv_len, q_start, total, dev)
-    a = PagedFwdArgs()
-    a.q_stride[:] = _rows("q", q, total, None, c.D, dev)
+    total, Hq, _ = q.shape
+    c, _, D = _paged_kv(k_cache, v_cache, page_table, kv_len, q_start, total, dev)
+    qs = _rows("q", q, total, None, D, dev)
     want = torch.float32 if out_fp32 else torch.bfloat16
     made = []
     if out is None:
         out = torch.empty((total, Hq, D), dtype=want, device=q.device)
         made.append(out)
-    elif out.dtype != want or out.get_device() != dev or not out.is_contiguous() or tuple(out.shape) != (total, Hq, D):
+    elif out.dtype is not want or out.get_device() != dev or not out.is_contiguous() or out.shape != q.shape:
         raise ValueError(f"out must be a contiguous {want} tensor of q's shape on q's device")
     if lse is None:
         lse = torch.empty((total, Hq), dtype=torch.float32, device=q.device)
         made.append(lse)
-    elif lse.dtype != torch.float32 or lse.get_device() != dev or not lse.is_contiguous() \
+    elif lse.dtype is not torch.float32 or lse.get_device() != dev or not lse.is_contiguous() \
             or tuple(lse.shape) != (total, Hq):
         raise ValueError("lse must be a contiguous float32 tensor [tokens, Hq] on q's device")
-    for name, t, need in (("alibi_slopes", alibi_slopes, Hq), ("rel_bias", rel_bias, Hq * (2 * rel_max + 1))):
-        if t is not None and (t.dtype != torch.float32 or t.get_device() != dev or not t.is_contiguous()
-                              or t.numel() < need):
-            raise ValueError(f"{name} must be a contiguous float32 tensor of at least {need} entries on q's device")
-    if mask not in MASK_KINDS:
-        raise ValueError(f"unknown mask {mask!r}")
-    a.Hq, a.max_q_len, a.shared_len = Hq, max(total, 1) if max_q_len is None else max_q_len, shared_len
-    a.scale = 0.0 if scale is None else float(scale)
-    a.q, a.o, a.lse = q.data_ptr(), out.data_ptr(), lse.data_ptr()
-    a.timeout_ms, a.flags = timeout_ms, OUT_FP32 if out_fp32 else 0
-    m = MaskDesc()
-    m.kind, m.window, m.prefix_len = MASK_KINDS[mask], window, sinks
+    sp, bp = 0, 0
+    if alibi_slopes is not None or rel_bias is not None:
+        for name, t, need in (("alibi_slopes", alibi_slopes, Hq), ("rel_bias", rel_bias, Hq * (2 * rel_max + 1))):
+            if t is not None and (t.dtype is not torch.float32 or t.get_device() != dev or not t.is_contiguous()
+                                  or t.numel() < need):
+                raise ValueError(f"{name} must be a contiguous float32 tensor of at least {need} entries on q's device")
+        sp = 0 if alibi_slopes is None else alibi_slopes.data_ptr()
+        bp = 0 if rel_bias is None else rel_bias.data_ptr()
+    if mask not in MASK_KINDS or score not in SCORE_KINDS:
+        raise ValueError(f"unknown mask {mask!r} or score {score!r}")
     if sinks and mask != "sink_window":
         raise ValueError("sinks applies to the sink_window mask")
-    sc = _score_desc(score, softcap, alibi_slopes, rel_bias, rel_max)
+    a = _PAGED_FWD.pack(Hq, (total or 1) if max_q_len is None else max_q_len, shared_len,
+                        0.0 if scale is None else scale, q.data_ptr(), *qs, out.data_ptr(), lse.data_ptr(), timeout_ms,
+                        OUT_FP32 if out_fp32 else 0)
+    m = _MASK.pack(MASK_KINDS[mask], window, sinks, 0, 0, 0, 0)
+    sc = _SCORE.pack(SCORE_KINDS[score], softcap, sp, bp, rel_max)
     lib = load_library()
-    ca, aa = ctypes.byref(c), ctypes.byref(a)
     if scratch is None:
-        # no bytes: the arguments are wrong, and the call below says how
-        scratch = torch.empty(max(lib.fa_paged_scratch_bytes(ca, aa), 16), dtype=torch.uint8, device=q.device)
+        # (no bytes: the arguments are wrong, and the call below says how)
+        scratch = torch.empty(lib.fa_paged_scratch_bytes(c, a) or 16, dtype=torch.uint8, device=q.device)
         made.append(scratch)
     elif scratch.get_device() != dev or not scratch.is_contiguous():
         raise ValueError("scratch must be a contiguous tensor on q's device")
-    if stream is not None:
+    if stream is None:
+        raw = _raw_stream(dev)
+    else:
+        raw = stream.cuda_stream
         for t in made:
             t.record_stream(stream)
-    ws = workspace or default_workspace(q.device, stream)
-    _check(lib.fa_fwd_paged(ca, aa, ctypes.byref(m), ctypes.byref(sc), ctypes.c_void_p(scratch.data_ptr()),
-                            scratch.numel() * scratch.element_size(), ws.ptr, _stream_ptr(stream)))
+    ws = workspace or _workspace_of(dev, raw)
+    st = lib.fa_fwd_paged(c, a, m, sc, scratch.data_ptr(), scratch.numel() * scratch.element_size(),
+                          ws.tensor.data_ptr(), raw)
+    if st != OK:
+        _check(st)
     return out, lse
 
 
@@ -738,11 +766,10 @@ def paged_scratch(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                   shared_len: int = 0) -> torch.Tensor:
     """Scratch for fwd_paged calls of these shapes, for callers that keep their own."""
     with torch.cuda.device(q.device):
-        c = _paged_kv(k_cache, v_cache, page_table, kv_len, q_start, q.shape[0], q.get_device())
-        a = PagedFwdArgs()
-        a.Hq, a.shared_len = q.shape[1], shared_len
-        a.max_q_len = max(q.shape[0], 1) if max_q_len is None else max_q_len
-        n = load_library().fa_paged_scratch_bytes(ctypes.byref(c), ctypes.byref(a))
+        c, _, _ = _paged_kv(k_cache, v_cache, page_table, kv_len, q_start, q.shape[0], q.get_device())
+        a = _PAGED_FWD.pack(q.shape[1], max(q.shape[0], 1) if max_q_len is None else max_q_len, shared_len, 0.0, 0, 0, 0,
+                            0, 0, 0, 0)
+        n = load_library().fa_paged_scratch_bytes(c, a)
         if n == 0:
             raise FAError(ERR_INVALID_ARG, load_library().fa_last_error().decode())
         return torch.empty(n, dtype=torch.uint8, device=q.device)

@@ -55,6 +55,17 @@ def test_header_and_binding_agree(fa, tmp_path):
     src.write_text(f'#include <stdio.h>\n#include <stddef.h>\n#include "fa_paged.h"\nint main(void) {{ {lines} return 0; }}')
     exe = tmp_path / "layout"
     subprocess.run(["gcc", "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe)], check=True)
+    for packer, t in ((fa._PAGED_KV, fa.PagedKVStruct), (fa._KV_APPEND, fa.KVAppendArgs), (fa._MASK, fa.MaskDesc),
+                      (fa._PAGED_FWD, fa.PagedFwdArgs), (fa._SCORE, fa.ScoreDesc)):
+        assert packer.size == ctypes.sizeof(t)
+        # the k-th value packed lands in the k-th field
+        n = sum(getattr(f[1], "_length_", 1) for f in t._fields_)
+        s, k = t.from_buffer_copy(packer.pack(*range(1, n + 1))), 1
+        for f in t._fields_:
+            got = getattr(s, f[0])
+            for x in (got if hasattr(got, "__len__") else [got]):
+                assert x == k, (t, f[0])
+                k += 1
     for line in subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.splitlines():
         key, off = line.split()
         s, _, f = key.partition(".")

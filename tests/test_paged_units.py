@@ -47,36 +47,44 @@ int main() {
         const int cut = pick(0, 2) ? 0 : pick(0, kv);
         const bool prefix = cut > 0 && pick(0, 1);
         const int jlo = prefix ? 0 : cut, jhi = prefix ? cut : kv;
-        const Hull u = make_hull(m, i0, i1, jlo, jhi);
+        const int sh = pick(6, 7), T = 1 << sh;
+        const Hull u = make_hull(m, i0, i1, jlo, jhi, sh);
         std::set<int> tiles;
         for (int k = 0; k < u.tiles; ++k) {
             const int kb = u.tile(k);
             CHECK(kb >= 0 && (k == 0 || kb > u.tile(k - 1)));
             tiles.insert(kb);
             // what is read lies inside the sequence
-            for (int a = kb * 128; a < kb * 128 + 128; a += 16)
+            for (int a = kb * T; a < kb * T + T; a += 16)
                 if (u.any(a, a + 16)) CHECK(a < kv);
             bool every = true, open = true;
-            for (int j = kb * 128; j < kb * 128 + 128; ++j) {
+            for (int j = kb * T; j < kb * T + T; ++j) {
                 every &= u.live(j);
                 for (int i = i0; i <= i1; ++i) open &= paged_visible(m, i, j, jlo, jhi);
             }
-            CHECK(u.all(kb * 128, kb * 128 + 128) <= every);
-            CHECK(tile_open(m, kb, i0, i1, jlo, jhi) <= open);
+            CHECK(u.all(kb * T, kb * T + T) <= every);
+            CHECK(tile_open(m, kb, i0, i1, jlo, jhi, sh) <= open);
             CHECK(open <= every);
         }
         for (int j = -130; j < kv + 200; ++j) {
             bool seen = false;
             for (int i = i0; i <= i1; ++i) seen |= paged_visible(m, i, j, jlo, jhi);
             CHECK(seen <= u.live(j));                                   // nothing that is seen is left out
-            if (seen) CHECK(tiles.count(j >> 7));
-            if (u.live(j)) CHECK(j >= jlo && j < jhi && u.any(j, j + 1) && tiles.count(j >> 7));
+            if (seen) CHECK(tiles.count(j >> sh));
+            if (u.live(j)) CHECK(j >= jlo && j < jhi && u.any(j, j + 1) && tiles.count(j >> sh));
             if (j >= 0 && j % 16 == 0) {
                 bool any = false;
                 for (int e = 0; e < 16; ++e) any |= u.live(j + e);
                 CHECK(any == u.any(j, j + 16));
             }
         }
+    }
+    // the division by the group size
+    for (uint32_t d : {1u, 2u, 3u, 5u, 6u, 7u, 8u, 12u, 31u, 64u, 100u, 255u, 65537u, 2147483647u}) {
+        const FastDiv f = fast_div(d);
+        auto q = [&](uint32_t n) { return (uint32_t)((((unsigned long long)f.m * n) >> 32) + n) >> f.s; };
+        for (uint32_t n : {0u, 1u, d - 1, d, d + 1, 2147483646u, 2147483647u}) CHECK((int)n < 0 || q(n) == n / d);
+        for (int it = 0; it < 20000; ++it) { const uint32_t n = rng() >> 1; CHECK(q(n) == n / d); }
     }
     printf("%d\n", bad);
     return bad != 0;
