@@ -238,10 +238,8 @@ constexpr int kPagedMaxSeqs = 2048;
 inline int paged_small_keys(int D) { return D == 64 ? 128 : 64; }
 constexpr int kPagedTileKeys = 128;
 constexpr int kPagedSmallCtasPerSm = 2;
-cudaError_t launch_paged_small(const PagedParams& p, const CUtensorMap& tk, const CUtensorMap& tv, bool after_prefix,
-                               cudaStream_t s);
-cudaError_t launch_paged_tiles(const PagedParams& p, const CUtensorMap& tk, const CUtensorMap& tv, bool after_prefix,
-                               cudaStream_t s);
+cudaError_t launch_paged_small(const PagedParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s);
+cudaError_t launch_paged_tiles(const PagedParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s);
 cudaError_t launch_paged_join_units(const PagedParams& p, int rows_per_unit, cudaStream_t s);
 cudaError_t launch_paged_join_rows(const PagedJoin& p, cudaStream_t s);
 // Validates a score_mod (NULL becomes FA_SCORE_NONE in *out).

@@ -202,6 +202,10 @@ __device__ __forceinline__ void block_prefix(int n, int* pre, int* warp_sums, F 
     __syncthreads();
 }
 
+// A launch; `overlap`: as a programmatic dependent of the kernel before it.  Such
+// a kernel starts (barriers, TMEM) while that one ends, and touches no memory
+// that others write before pdl_wait_previous(); a kernel that signals early
+// itself has waited for its own predecessor first, or does so before it ends.
 template <class K, class... A>
 cudaError_t paged_launch(K kern, dim3 grid, int threads, size_t smem, bool overlap, cudaStream_t s, A... args) {
     cudaLaunchConfig_t cfg{};

@@ -303,11 +303,10 @@ fa_status fa_fwd_paged(const fa_paged_kv* c, const fa_paged_fwd_args* a, const f
         pre.ctas = fa::device_sm_count();
         pre.parts = {reinterpret_cast<float*>(base + lay.pre_slot_o), reinterpret_cast<float2*>(base + lay.pre_slot_ml),
                      reinterpret_cast<float*>(base + lay.pre_row_o), reinterpret_cast<float2*>(base + lay.pre_row_ml)};
-        cudaError_t e = fa::launch_paged_tiles(pre, tk, tv, false, s);
+        cudaError_t e = fa::launch_paged_tiles(pre, tk, tv, s);
         if (e != cudaSuccess) return cuda_fail(e, "shared prefix launch");
     }
-    cudaError_t e = small ? fa::launch_paged_small(p, sk, sv, p.join_rows, s)
-                          : fa::launch_paged_tiles(p, tk, tv, p.join_rows, s);
+    cudaError_t e = small ? fa::launch_paged_small(p, sk, sv, s) : fa::launch_paged_tiles(p, tk, tv, s);
     if (e != cudaSuccess) return cuda_fail(e, "paged forward launch");
     const int unit_rows = small ? fa::kPagedSmallRows : fa::kPagedTileRows;
     if (p.join_rows) {

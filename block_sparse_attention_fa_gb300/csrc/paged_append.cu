@@ -54,6 +54,8 @@ template <int D>
 __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendParams p) {
     constexpr int kItems = D / 16;               // 16-element items per head
     const int t = blockIdx.x, tid = threadIdx.x;
+    pdl_wait_previous();
+    pdl_launch_next();
     // the sequence of row t: how many of q_start[1 ..] are <= t
     int b = 0;
     for (int b0 = 0; b0 < p.c.B; b0 += kAppendThreads)
@@ -123,11 +125,8 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendP
 
 cudaError_t launch_kv_append(const AppendParams& p, cudaStream_t s) {
     if (p.c.total_q == 0) return cudaSuccess;
-    if (p.D == 64)
-        kv_append_kernel<64><<<p.c.total_q, kAppendThreads, 0, s>>>(p);
-    else
-        kv_append_kernel<128><<<p.c.total_q, kAppendThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    return p.D == 64 ? paged_launch(kv_append_kernel<64>, dim3(p.c.total_q), kAppendThreads, 0, true, s, p)
+                     : paged_launch(kv_append_kernel<128>, dim3(p.c.total_q), kAppendThreads, 0, true, s, p);
 }
 
 }  // namespace fa

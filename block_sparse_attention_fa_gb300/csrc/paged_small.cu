@@ -163,7 +163,6 @@ paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
     int* const pre = reinterpret_cast<int*>(smem + L::kPre);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
 
-    pdl_launch_next();
     if (threadIdx.x == 0) {
         for (int st = 0; st < ST; ++st) {
             mbar_init(full_bar(st), 1);
@@ -172,6 +171,9 @@ paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         *abort_flag = 0;
         mbar_fence_init();
     }
+    // (a shared prefix's kernel is no input of this one: it is waited for at the end)
+    if (!p.join_rows) pdl_wait_previous();
+    pdl_launch_next();
     // the line of tiles
     block_prefix<kThreadsS>(p.c.B, pre, reinterpret_cast<int*>(smem + L::kScan), [&](int b) {
         const SeqInfo s = seq_info(p.c, b, p.max_q, p.shared, cta == 0 ? p.ws : nullptr);
@@ -239,7 +241,7 @@ paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                 if (last[st] >= 0) paged_drain_wait(full_bar(st), (last[st] / ST) & 1, wc, S_PG_DRAIN);
         }
         __syncwarp();
-        pdl_wait_previous();
+        if (p.join_rows) pdl_wait_previous();
         return;
     }
 
@@ -451,7 +453,7 @@ paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         }
     }
     if (!p.join_rows && threadIdx.x == 0) p.meta[cta] = ok ? meta : PagedMeta{};
-    pdl_wait_previous();
+    if (p.join_rows) pdl_wait_previous();
 }
 
 // Where a row's partials lie: `count` rows of a kernel's slots, from `first`
@@ -465,91 +467,127 @@ struct RowParts {
     __device__ __forceinline__ long long at(int k) const { return first + (k ? (2LL * k - 1) * stride : 0); }
 };
 
-// Joins a row's partials, the parts of `a` and then those of `b`, by one warp:
+// Joins the partials of rows, the parts of `a` and then those of `b`:
 //   M = max m_k, L = sum 2^(m_k - M) l_k, O = sum 2^(m_k - M) O_k / L.
-// The lanes take a part each for its weight (32 at a time, so that the loads
-// of all of them are in flight together), then kV columns each for the sum,
-// whose loads do not wait for one another either.
-template <int D>
-__device__ __forceinline__ void join_row(const PagedParams& p, const RowParts& a, const RowParts& b, long long row,
-                                         int lane) {
-    constexpr int kV = D / 32;
-    const int n = a.count + b.count;
+// Eight lanes to a row, four rows to a warp.  What it costs is the loads'
+// latency, so as many as possible are in flight at once: a lane reads the
+// (m, l) of every eighth part for the weights, then its 4 x D / 32 columns of
+// four parts at a time.  SPLIT: the block's four warps take every fourth part
+// of the same four rows (single tokens and shared prefixes, where a row has
+// tens of parts) and add up through shared memory; otherwise each warp has
+// rows of its own.  Summing is in a fixed order either way.
+constexpr int kJoinWarps = 4;
+template <int D, bool SPLIT>
+__device__ __forceinline__ void join_rows(const PagedParams& p, const RowParts& a, const RowParts& b, long long row,
+                                          bool valid, float4* sums) {
+    constexpr int kC = D / 32;                     // float4 columns per lane, 32 apart
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane & 7;
+    const int n = valid ? a.count + b.count : 0;
     auto ml_of = [&](int k) {
         if (k >= n) return make_float2(-CUDART_INF_F, 0.f);
         return k < a.count ? __ldcg(a.ml + a.at(k)) : __ldcg(b.ml + b.at(k - a.count));
     };
+    const int longest = __reduce_max_sync(0xffffffffu, n);
+    const float2 head = ml_of(sub);
     float m = -CUDART_INF_F;
-    const float2 head = ml_of(lane);
-    for (int k0 = 0; k0 < n; k0 += 32) m = fmaxf(m, (k0 ? ml_of(k0 + lane) : head).x);
+    for (int k0 = 0; k0 < longest; k0 += 8) m = fmaxf(m, (k0 ? ml_of(k0 + sub) : head).x);
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    for (int d = 4; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
     const float ref = m == -CUDART_INF_F ? 0.f : m;
-    float l = 0.f, o[kV];
+    float l = 0.f;
+    float4 o[kC];
 #pragma unroll
-    for (int c = 0; c < kV; ++c) o[c] = 0.f;
-    for (int k0 = 0; k0 < n; k0 += 32) {
-        const float2 ml = k0 ? ml_of(k0 + lane) : head;
+    for (int c = 0; c < kC; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = 0; k0 < longest; k0 += 8) {
+        const float2 ml = k0 ? ml_of(k0 + sub) : head;
         const float w = ml.y == 0.f ? 0.f : ex2_approx(ml.x - ref);    // 0: the part has no visible key for this row
         l += ml.y * w;
-        const int here = min(32, n - k0);
-#pragma unroll 8
-        for (int e = 0; e < here; ++e) {
-            const int k = k0 + e;
-            const float we = __shfl_sync(0xffffffffu, w, e);
-            const float* src = (k < a.count ? a.o + a.at(k) * D : b.o + b.at(k - a.count) * D) + kV * lane;
-            float v[kV];
-            if constexpr (kV == 4) {
-                const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
-                v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-            } else {
-                const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
-                v[0] = x.x; v[1] = x.y;
-            }
+        const int e0 = SPLIT ? warp : 0;
+        constexpr int kStep = SPLIT ? kJoinWarps : 1;
 #pragma unroll
-            for (int c = 0; c < kV; ++c) o[c] = fmaf(we, v[c], o[c]);
+        for (int e = 0; e < 8; e += kStep) {
+            const int k = k0 + e + e0;
+            const float we = __shfl_sync(0xffffffffu, w, (lane & 24) + e + e0);
+            if (k >= n) continue;
+            const float4* src = reinterpret_cast<const float4*>(
+                k < a.count ? a.o + a.at(k) * D : b.o + b.at(k - a.count) * D) + sub;
+#pragma unroll
+            for (int c = 0; c < kC; ++c) {
+                const float4 v = __ldcg(src + 8 * c);
+                o[c].x = fmaf(we, v.x, o[c].x);
+                o[c].y = fmaf(we, v.y, o[c].y);
+                o[c].z = fmaf(we, v.z, o[c].z);
+                o[c].w = fmaf(we, v.w, o[c].w);
+            }
         }
     }
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    if (p.flags & FA_OUT_FP32) {
-        float* dst = static_cast<float*>(p.o) + row * D + kV * lane;
+    for (int d = 4; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+    if (SPLIT) {
+        if (warp > 0) {
 #pragma unroll
-        for (int c = 0; c < kV; c += 2) *reinterpret_cast<float2*>(dst + c) = make_float2(o[c] * inv, o[c + 1] * inv);
-    } else {
-        uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + row * D + kV * lane);
+            for (int c = 0; c < kC; ++c) sums[((warp - 1) * kC + c) * 32 + lane] = o[c];
+        }
+        __syncthreads();
+        if (warp > 0) return;
 #pragma unroll
-        for (int c = 0; c < kV; c += 2) dst[c / 2] = pack_bf16x2(o[c] * inv, o[c + 1] * inv);
+        for (int w = 0; w < kJoinWarps - 1; ++w) {
+#pragma unroll
+            for (int c = 0; c < kC; ++c) {
+                const float4 v = sums[(w * kC + c) * 32 + lane];
+                o[c].x += v.x;
+                o[c].y += v.y;
+                o[c].z += v.z;
+                o[c].w += v.w;
+            }
+        }
     }
-    if (lane == 0) p.lse[row] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * kLn2P;
+    if (!valid) return;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int c = 0; c < kC; ++c) {
+        const long long at = row * D + 32 * c + 4 * sub;
+        if (p.flags & FA_OUT_FP32)
+            *reinterpret_cast<float4*>(static_cast<float*>(p.o) + at) =
+                make_float4(o[c].x * inv, o[c].y * inv, o[c].z * inv, o[c].w * inv);
+        else
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + at) =
+                make_uint2(pack_bf16x2(o[c].x * inv, o[c].y * inv), pack_bf16x2(o[c].z * inv, o[c].w * inv));
+    }
+    if (sub == 0) p.lse[row] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * kLn2P;
 }
-
-constexpr int kJoinWarps = 8;          // with a shared prefix: a warp per query head of the group
-constexpr int kJoinUnitWarps = 16;     // without: a warp per row of the unit
 
 // Without a shared prefix: block (c, y) joins rows of the unit that starts in
 // CTA c of the attention kernel and runs on into the next ones.
-template <int D>
-__global__ void __launch_bounds__(32 * kJoinUnitWarps) paged_join_units_kernel(const PagedParams p, int rows_per_unit) {
+template <int D, bool SPLIT>
+__global__ void __launch_bounds__(32 * kJoinWarps) paged_join_units_kernel(const PagedParams p, int rows_per_unit) {
+    __shared__ float4 sums[SPLIT ? (kJoinWarps - 1) * (D / 32) * 32 : 1];
+    pdl_launch_next();
     pdl_wait_previous();
     const PagedMeta t = p.meta[blockIdx.x];
-    if (t.count == 0) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int r = (SPLIT ? blockIdx.y : blockIdx.y * kJoinWarps + (threadIdx.x >> 5)) * 4 + ((threadIdx.x & 31) >> 3);
+    if (t.count == 0 || (r & ~3) >= t.rows) return;        // (uniform: four rows to a warp, and to a block if SPLIT)
+    const bool valid = r < t.rows;
+    const RowParts a{p.parts.slot_o, p.parts.slot_ml, (2LL * blockIdx.x + 1) * rows_per_unit + r, t.count, rows_per_unit};
     const RowParts none{nullptr, nullptr, 0, 0, 0};
-    for (int r = blockIdx.y * kJoinUnitWarps + warp; r < t.rows; r += gridDim.y * kJoinUnitWarps) {
-        const RowParts a{p.parts.slot_o, p.parts.slot_ml, (2LL * blockIdx.x + 1) * rows_per_unit + r, t.count, rows_per_unit};
-        const int R = t.row0 + r, tok = quotient(R, p.by_group);
-        join_row<D>(p, a, none, (long long)(t.q0 + tok) * p.Hq + t.h * p.group + R - tok * p.group, lane);
-    }
+    const int R = t.row0 + r, tok = quotient(R, p.by_group);
+    join_rows<D, SPLIT>(p, a, none, (long long)(t.q0 + tok) * p.Hq + t.h * p.group + R - tok * p.group, valid, sums);
 }
 
-// With a shared prefix: block (t, h) joins the rows of token t and kv head h,
-// the prefix's partials first, then those of the sequence's own keys.
+// With a shared prefix: block (t, h, y) joins four rows of token t and kv head
+// h, the prefix's partials first, then those of the sequence's own keys.
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_rows_kernel(const PagedJoin j) {
+    __shared__ float4 sums[(kJoinWarps - 1) * (D / 32) * 32];
     const PagedParams& p = j.own;
-    const int t = blockIdx.x, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_launch_next();
+    pdl_wait_previous();
+    const int t = blockIdx.x, h = blockIdx.y;
+    const int2 pre = *reinterpret_cast<const int2*>(p.hdr);
+    const int gq = blockIdx.z * 4 + ((threadIdx.x & 31) >> 3);
+    const bool valid = gq < p.group;
+    const long long row = (long long)t * p.Hq + h * p.group + min(gq, p.group - 1);
+    const int2 d = __ldcg(p.rowdesc + row);        // (what it says of a row without a unit is not used)
     int b = 0;
     for (int b0 = 0; b0 < p.c.B; b0 += 32 * kJoinWarps) {
         const int x = b0 + threadIdx.x;
@@ -558,23 +596,18 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_rows_kernel(const 
     if (b >= p.c.B) return;
     const SeqInfo s = seq_info(p.c, b, p.max_q, p.shared, nullptr);
     if (s.n == 0 || t < s.q0 || t >= s.q0 + s.n) return;
-    pdl_wait_previous();
-    const int tiles = p.hdr[0], per = p.hdr[1];
-    for (int gq = warp; gq < p.group; gq += kJoinWarps) {
-        const long long row = (long long)t * p.Hq + h * p.group + gq;
-        const int2 d = p.rowdesc[row];
-        const int R = t * p.group + gq, rt = R / j.pre_rows, r = R - rt * j.pre_rows;
-        const int first = (rt * p.c.Hkv + h) * tiles, ca = first / per, cb = (first + tiles - 1) / per;
-        RowParts a{j.pre.slot_o, j.pre.slot_ml, (2LL * ca + 1) * j.pre_rows + r, cb - ca + 1, j.pre_rows};
-        if (ca == cb) a = RowParts{j.pre.row_o, j.pre.row_ml, row, 1, 0};
-        RowParts own{p.parts.slot_o, p.parts.slot_ml, d.x, d.y, j.own_rows};
-        if (d.x < 0) own = RowParts{p.parts.row_o, p.parts.row_ml, row, 1, 0};
-        join_row<D>(p, a, own, row, lane);
-    }
+    const int tiles = pre.x, per = pre.y;
+    const int R = t * p.group + min(gq, p.group - 1), rt = R / j.pre_rows, r = R - rt * j.pre_rows;
+    const int first = (rt * p.c.Hkv + h) * tiles, ca = first / per, cb = (first + tiles - 1) / per;
+    RowParts a{j.pre.slot_o, j.pre.slot_ml, (2LL * ca + 1) * j.pre_rows + r, cb - ca + 1, j.pre_rows};
+    if (ca == cb) a = RowParts{j.pre.row_o, j.pre.row_ml, row, 1, 0};
+    RowParts own{p.parts.slot_o, p.parts.slot_ml, d.x, d.y, j.own_rows};
+    if (d.x < 0) own = RowParts{p.parts.row_o, p.parts.row_ml, row, 1, 0};
+    join_rows<D, true>(p, a, own, row, valid, sums);
 }
 
 template <int D, int SCORE>
-cudaError_t launch_small(const PagedParams& p, const CUtensorMap& tk, const CUtensorMap& tv, bool overlap,
+cudaError_t launch_small(const PagedParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
                          cudaStream_t s) {
     auto kern = paged_small_kernel<D, SCORE>;
     using L = SmallLayout<D>;
@@ -588,37 +621,42 @@ cudaError_t launch_small(const PagedParams& p, const CUtensorMap& tk, const CUte
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) attr_set[dev] = true;
     }
-    return paged_launch(kern, dim3(p.ctas), kThreadsS, L::bytes(p.c.B), overlap, s, tk, tv, p);
+    return paged_launch(kern, dim3(p.ctas), kThreadsS, L::bytes(p.c.B), true, s, tk, tv, p);
 }
 
 template <int D>
-cudaError_t launch_small_d(const PagedParams& p, const CUtensorMap& tk, const CUtensorMap& tv, bool overlap,
+cudaError_t launch_small_d(const PagedParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
                            cudaStream_t s) {
     switch (p.score.kind) {
-        case FA_SCORE_SOFTCAP: return launch_small<D, FA_SCORE_SOFTCAP>(p, tk, tv, overlap, s);
-        case FA_SCORE_ALIBI: return launch_small<D, FA_SCORE_ALIBI>(p, tk, tv, overlap, s);
-        case FA_SCORE_REL_BIAS: return launch_small<D, FA_SCORE_REL_BIAS>(p, tk, tv, overlap, s);
-        case FA_SCORE_ALIBI_SOFTCAP: return launch_small<D, FA_SCORE_ALIBI_SOFTCAP>(p, tk, tv, overlap, s);
-        default: return launch_small<D, FA_SCORE_NONE>(p, tk, tv, overlap, s);
+        case FA_SCORE_SOFTCAP: return launch_small<D, FA_SCORE_SOFTCAP>(p, tk, tv, s);
+        case FA_SCORE_ALIBI: return launch_small<D, FA_SCORE_ALIBI>(p, tk, tv, s);
+        case FA_SCORE_REL_BIAS: return launch_small<D, FA_SCORE_REL_BIAS>(p, tk, tv, s);
+        case FA_SCORE_ALIBI_SOFTCAP: return launch_small<D, FA_SCORE_ALIBI_SOFTCAP>(p, tk, tv, s);
+        default: return launch_small<D, FA_SCORE_NONE>(p, tk, tv, s);
     }
 }
 
 }  // namespace
 
-cudaError_t launch_paged_small(const PagedParams& p, const CUtensorMap& tk, const CUtensorMap& tv, bool after_prefix,
+cudaError_t launch_paged_small(const PagedParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
                                cudaStream_t s) {
-    return p.D == 64 ? launch_small_d<64>(p, tk, tv, after_prefix, s) : launch_small_d<128>(p, tk, tv, after_prefix, s);
+    return p.D == 64 ? launch_small_d<64>(p, tk, tv, s) : launch_small_d<128>(p, tk, tv, s);
 }
 
 cudaError_t launch_paged_join_units(const PagedParams& p, int rows_per_unit, cudaStream_t s) {
-    const dim3 grid(p.ctas, rows_per_unit <= kJoinUnitWarps ? 1 : 8);
-    const int threads = 32 * kJoinUnitWarps;
-    return p.D == 64 ? paged_launch(paged_join_units_kernel<64>, grid, threads, 0, true, s, p, rows_per_unit)
-                     : paged_launch(paged_join_units_kernel<128>, grid, threads, 0, true, s, p, rows_per_unit);
+    const int threads = 32 * kJoinWarps;
+    if (rows_per_unit == kPagedSmallRows) {
+        const dim3 grid(p.ctas, kPagedSmallRows / 4);
+        return p.D == 64 ? paged_launch(paged_join_units_kernel<64, true>, grid, threads, 0, true, s, p, rows_per_unit)
+                         : paged_launch(paged_join_units_kernel<128, true>, grid, threads, 0, true, s, p, rows_per_unit);
+    }
+    const dim3 grid(p.ctas, rows_per_unit / (4 * kJoinWarps));
+    return p.D == 64 ? paged_launch(paged_join_units_kernel<64, false>, grid, threads, 0, true, s, p, rows_per_unit)
+                     : paged_launch(paged_join_units_kernel<128, false>, grid, threads, 0, true, s, p, rows_per_unit);
 }
 
 cudaError_t launch_paged_join_rows(const PagedJoin& p, cudaStream_t s) {
-    const dim3 grid(p.own.c.total_q, p.own.c.Hkv);
+    const dim3 grid(p.own.c.total_q, p.own.c.Hkv, (p.own.group + 3) / 4);
     return p.own.D == 64 ? paged_launch(paged_join_rows_kernel<64>, grid, 32 * kJoinWarps, 0, true, s, p)
                          : paged_launch(paged_join_rows_kernel<128>, grid, 32 * kJoinWarps, 0, true, s, p);
 }

@@ -204,7 +204,6 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
     int* const len_s = q0_s + p.c.B + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
 
-    pdl_launch_next();
     if (threadIdx.x == 0) {
         for (int k = 0; k < T_COUNT; ++k) {
             uint32_t cnt = 1;
@@ -229,6 +228,10 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
     const uint32_t tmem = *tmem_slot;
     const WaitCtl wc{abort_flag, p.ws, p.timeout_ns};
 
+    // (a shared prefix's kernel is no input of the sequences' own: that one
+    // waits for it at the end)
+    if (p.prefix || !p.join_rows) pdl_wait_previous();
+    pdl_launch_next();
     // the line of tiles
     TileLine line{};
     line.pre = pre;
@@ -238,6 +241,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
     if (p.prefix) {
         for (int b = threadIdx.x; b < p.c.B; b += kThreadsT) {
             const SeqInfo s = seq_info(p.c, b, p.max_q, p.shared, cta == 0 ? p.ws : nullptr);
+            len_s[b] = s.kv;
+            q0_s[b + 1] = __ldg(p.c.q_start + b + 1);
             if (s.n > 0) {
                 atomicMin(minmax, s.kv - s.n);
                 atomicMax(minmax + 1, s.kv - 1);
@@ -328,6 +333,9 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                 if (k + 1 < s.k1) page = tile_page<kBlock>(p.c, table, s.hull, s.hull.tile(k + 1), lane, s.b, p.ws);
                 if (!load(&tmK, L::kK, T_K_FULL, T_K_EMPTY, g, id, row, S_T_K_EMPTY)) { ok = false; break; }
                 last_k = static_cast<int>(g);
+                // the first unit's rows of Q come before the rest of the ring:
+                // behind it they would wait for all of it to arrive
+                if (g == 0 && !mbar_wait_warp(bar(T_Q_FULL), 0, wc, S_T_Q)) { ok = false; break; }
                 if (k > s.k0) {
                     if (!load(&tmV, L::kV, T_V_FULL, T_V_EMPTY, g - 1, id_v, row_v, S_T_V_EMPTY)) { ok = false; break; }
                     last_v = static_cast<int>(g - 1);
@@ -485,9 +493,9 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                 int lo = 0, hi = p.c.B - 1;        // the first sequence that ends behind the row
                 while (lo < hi) {
                     const int mid = (lo + hi) >> 1;
-                    if (__ldg(p.c.q_start + mid + 1) <= trow) lo = mid + 1; else hi = mid;
+                    if (q0_s[mid + 1] <= trow) lo = mid + 1; else hi = mid;
                 }
-                i = max(__ldg(p.c.kv_len + lo) - __ldg(p.c.q_start + lo + 1) + trow, -1);
+                i = max(len_s[lo] - q0_s[lo + 1] + trow, -1);
             }
             // The warp's 32 rows of Q, D / 8 lanes to a row, so that whole lines
             // are read (a row per lane asks for 16-byte pieces of 32 lines, 5 us
@@ -689,11 +697,11 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         tc_fence_after();
         tmem_dealloc(tmem, kTmemColsT);
     }
-    pdl_wait_previous();
+    if (!p.prefix && p.join_rows) pdl_wait_previous();
 }
 
 template <int D, int SCORE>
-cudaError_t launch_tiles(const PagedParams& p, const CUtensorMap& tk, const CUtensorMap& tv, bool overlap,
+cudaError_t launch_tiles(const PagedParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
                          cudaStream_t s) {
     auto kern = paged_tiles_kernel<D, SCORE>;
     using L = TileLayout<D>;
@@ -707,26 +715,26 @@ cudaError_t launch_tiles(const PagedParams& p, const CUtensorMap& tk, const CUte
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) attr_set[dev] = true;
     }
-    return paged_launch(kern, dim3(p.ctas), kThreadsT, L::bytes(p.c.B), overlap, s, tk, tv, p);
+    return paged_launch(kern, dim3(p.ctas), kThreadsT, L::bytes(p.c.B), true, s, tk, tv, p);
 }
 
 template <int D>
-cudaError_t launch_tiles_d(const PagedParams& p, const CUtensorMap& tk, const CUtensorMap& tv, bool overlap,
+cudaError_t launch_tiles_d(const PagedParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
                            cudaStream_t s) {
     switch (p.score.kind) {
-        case FA_SCORE_SOFTCAP: return launch_tiles<D, FA_SCORE_SOFTCAP>(p, tk, tv, overlap, s);
-        case FA_SCORE_ALIBI: return launch_tiles<D, FA_SCORE_ALIBI>(p, tk, tv, overlap, s);
-        case FA_SCORE_REL_BIAS: return launch_tiles<D, FA_SCORE_REL_BIAS>(p, tk, tv, overlap, s);
-        case FA_SCORE_ALIBI_SOFTCAP: return launch_tiles<D, FA_SCORE_ALIBI_SOFTCAP>(p, tk, tv, overlap, s);
-        default: return launch_tiles<D, FA_SCORE_NONE>(p, tk, tv, overlap, s);
+        case FA_SCORE_SOFTCAP: return launch_tiles<D, FA_SCORE_SOFTCAP>(p, tk, tv, s);
+        case FA_SCORE_ALIBI: return launch_tiles<D, FA_SCORE_ALIBI>(p, tk, tv, s);
+        case FA_SCORE_REL_BIAS: return launch_tiles<D, FA_SCORE_REL_BIAS>(p, tk, tv, s);
+        case FA_SCORE_ALIBI_SOFTCAP: return launch_tiles<D, FA_SCORE_ALIBI_SOFTCAP>(p, tk, tv, s);
+        default: return launch_tiles<D, FA_SCORE_NONE>(p, tk, tv, s);
     }
 }
 
 }  // namespace
 
-cudaError_t launch_paged_tiles(const PagedParams& p, const CUtensorMap& tk, const CUtensorMap& tv, bool after_prefix,
+cudaError_t launch_paged_tiles(const PagedParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
                                cudaStream_t s) {
-    return p.D == 64 ? launch_tiles_d<64>(p, tk, tv, after_prefix, s) : launch_tiles_d<128>(p, tk, tv, after_prefix, s);
+    return p.D == 64 ? launch_tiles_d<64>(p, tk, tv, s) : launch_tiles_d<128>(p, tk, tv, s);
 }
 
 }  // namespace fa

@@ -9,9 +9,9 @@ raises; there is no CPU fallback.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 import struct
+import threading
 from typing import Optional
 
 import torch
@@ -182,6 +182,8 @@ def _check(status: int):
     if status != OK:
         raise FAError(status, load_library().fa_last_error().decode())
 
+
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
 
 # The current device and stream without building Python objects for them (a
 # microsecond or two each, as much as a small kernel); the public calls where
@@ -619,19 +621,22 @@ def _rows(name, t, total, H, D, dev):
     return ts if n > 1 else D, hs if h > 1 else D
 
 
-def _on_device(fn):
-    """Runs a paged call with its rows' device current."""
-    @functools.wraps(fn)
-    def run(q, k, *args, **kw):
-        at = (k if q is None else q).get_device()
-        if at < 0 or at == _device_now():
-            return fn(q, k, *args, **kw)
-        with torch.cuda.device(at):
-            return fn(q, k, *args, **kw)
-    return run
+def _call_on(dev, fn, *args):
+    """A paged call with its tensors' device current."""
+    if dev == _device_now():
+        return fn(*args)
+    with torch.cuda.device(dev):
+        return fn(*args)
 
 
-@_on_device
+# Scratch of eager calls on a device's current stream, grown as needed: calls
+# on one stream run one after another, and the lock keeps the launches of one
+# call together where several threads share a stream.  A captured call gets
+# scratch of its own, which its graph keeps.
+_paged_scratch = {}
+_paged_lock = threading.Lock()
+
+
 def kv_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
               v_cache: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tensor, q_start: torch.Tensor, *,
               cos: Optional[torch.Tensor] = None, sin: Optional[torch.Tensor] = None, interleaved: bool = False,
@@ -688,7 +693,6 @@ def kv_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, k_cac
     return q_out
 
 
-@_on_device
 def fwd_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
               kv_len: torch.Tensor, q_start: torch.Tensor, *, max_q_len: Optional[int] = None, mask: str = "causal",
               window: int = 0, sinks: int = 0, shared_len: int = 0, score: str = "none", softcap: float = 0.0,
@@ -741,21 +745,37 @@ def fwd_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, pag
     m = _MASK.pack(MASK_KINDS[mask], window, sinks, 0, 0, 0, 0)
     sc = _SCORE.pack(SCORE_KINDS[score], softcap, sp, bp, rel_max)
     lib = load_library()
-    if scratch is None:
-        # (no bytes: the arguments are wrong, and the call below says how)
-        scratch = torch.empty(lib.fa_paged_scratch_bytes(c, a) or 16, dtype=torch.uint8, device=q.device)
+    raw = _raw_stream(dev) if stream is None else stream.cuda_stream
+    ws = workspace or _workspace_of(dev, raw)
+
+    def call(t):
+        return _call_on(dev, lib.fa_fwd_paged, c, a, m, sc, t.data_ptr(), t.numel() * t.element_size(),
+                        ws.tensor.data_ptr(), raw)
+
+    def fresh():
+        # (no bytes: the arguments are wrong, and the call says how)
+        return torch.empty(_call_on(dev, lib.fa_paged_scratch_bytes, c, a) or 16, dtype=torch.uint8, device=q.device)
+
+    if scratch is not None:
+        if scratch.get_device() != dev or not scratch.is_contiguous():
+            raise ValueError("scratch must be a contiguous tensor on q's device")
+        st = call(scratch)
+    elif stream is not None or _capturing():
+        scratch = fresh()
         made.append(scratch)
-    elif scratch.get_device() != dev or not scratch.is_contiguous():
-        raise ValueError("scratch must be a contiguous tensor on q's device")
-    if stream is None:
-        raw = _raw_stream(dev)
+        st = call(scratch)
     else:
-        raw = stream.cuda_stream
+        with _paged_lock:
+            scratch = _paged_scratch.get((dev, raw))
+            st = ERR_INVALID_ARG if scratch is None else call(scratch)
+            if st == ERR_INVALID_ARG:              # none yet, or too small (or wrong arguments: the call says so again)
+                scratch = fresh()
+                st = call(scratch)
+                if st == OK:
+                    _paged_scratch[(dev, raw)] = scratch
+    if stream is not None:
         for t in made:
             t.record_stream(stream)
-    ws = workspace or _workspace_of(dev, raw)
-    st = lib.fa_fwd_paged(c, a, m, sc, scratch.data_ptr(), scratch.numel() * scratch.element_size(),
-                          ws.tensor.data_ptr(), raw)
     if st != OK:
         _check(st)
     return out, lse

@@ -795,3 +795,61 @@ def test_binding_refusals(fa):
     assert o.shape == (0, 4, 64) and lse.shape == (0, 4)
     fa.kv_append(empty, empty[:, :2], empty[:, :2], kc, vc, table, kv, zero)
     fa.default_workspace("cuda").check()
+
+
+@gpu
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("shared", [0, 64])
+def test_after_other_work_in_a_graph(fa, n, shared):
+    """A captured call behind a copy, a fill, a library kernel and another paged call: its kernels start early, but
+    read nothing before what comes in front is done."""
+    bt = Batch([n, n, n], [400 + n, 90 + n, 300 + n], 2, 64, 16, shared=shared)
+    dev = bt.device()
+    q = torch.from_numpy(bt.queries(4)).cuda().to(torch.bfloat16)
+    src, qd, kv = q.clone(), torch.zeros_like(q), torch.zeros_like(dev[3])
+    args = (dev[0], dev[1], dev[2], kv, dev[4])
+    call = lambda: fa.fwd_paged(qd, *args, max_q_len=n, shared_len=shared)   # noqa: E731
+    kv.copy_(dev[3])
+    qd.copy_(src)
+    call()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        qd.zero_()
+        kv.zero_()
+        torch.cuda._sleep(200000)
+        kv.add_(dev[3])
+        qd.copy_(src)
+        first = call()
+        qd.copy_(first[0])
+        qd.copy_(src)
+        second = call()
+    for _ in range(5):
+        g.replay()
+    torch.cuda.synchronize()
+    ref = reference(bt, bt.queries(4), "causal", 0, 0)
+    compare(first, ref)
+    assert torch.equal(first[0], second[0]) and torch.equal(first[1], second[1])
+
+
+@gpu
+def test_threads_on_one_stream(fa):
+    """Calls of several threads on one stream share the binding's scratch: each call's launches stay together."""
+    import threading
+    bts = [Batch([1] * 4, [300 + 900 * k + 50 * b for b in range(4)], 2, 64, 16, seed=k) for k in range(4)]
+    work = [(bt, bt.device(), torch.from_numpy(bt.queries(4)).cuda().to(torch.bfloat16)) for bt in bts]
+    torch.cuda.synchronize()
+    got = [[] for _ in bts]
+
+    def loop(k):
+        for _ in range(30):
+            got[k].append(fa.fwd_paged(work[k][2], *work[k][1], max_q_len=1))
+    ts = [threading.Thread(target=loop, args=(k,)) for k in range(4)]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    torch.cuda.synchronize()
+    for k, bt in enumerate(bts):
+        ref = reference(bt, bt.queries(4), "causal", 0, 0)
+        for x in got[k]:
+            compare(x, ref)
