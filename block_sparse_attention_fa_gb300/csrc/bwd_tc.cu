@@ -104,7 +104,7 @@ enum TcSite : uint32_t { TS_R = 101, TS_FULL, TS_EMPTY, TS_SD, TS_PDS, TS_ACC, T
                          TS_FULL_E, TS_R_EMPTY, TS_ACC_FREE, TS_UNIT_FULL, TS_UNIT_EMPTY };
 // A unit-queue slot: the unit (-1: none left), its visit count, b, first
 // query head, kv head, resident block.
-enum TcUnitWord { TU_UNIT = 0, TU_N, TU_B, TU_HQ0, TU_HK, TU_BLK, TU_WORDS = 8 };
+enum TcUnitWord { TU_UNIT = 0, TU_N, TU_B, TU_HQ0, TU_HK, TU_BLK, TU_PART, TU_WORDS = 8 };
 constexpr uint32_t kTcUnitConsumers = 17;   // the MMA warp and the 16 elementwise warps
 
 template <int D>
@@ -394,42 +394,116 @@ __device__ __forceinline__ uint32_t chunk_mask(const BwdParams& p, int b, int ro
     return ((0xffffffffu >> (31 - hi)) & (0xffffffffu << lo)) | sinks;
 }
 
+// A warp takes kStatRows padded rows at once.  They come in 16-byte pieces
+// through shared memory (two-byte loads from global memory, a row at a time,
+// took 48 us for 262144 rows of 128 columns instead of 31); every row is
+// summed in one order: lane l takes columns l, l + 32, .., then the lanes add
+// up pairwise.
+constexpr int kStatRows = 8;
+template <int D>
 __global__ void __launch_bounds__(256) bwd_rowstats_kernel(const BwdParams p) {
+    constexpr int kLanes = D / 8, kPer = 32 / kLanes;     // lanes per row, rows per load
+    __shared__ uint4 stage[8][2][kStatRows * kLanes];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long prow = (long long)blockIdx.x * 8 + warp;        // padded row
-    const long long rows_pad = (long long)p.B * p.Hq * p.bm.nq * 128;
-    if (prow >= rows_pad) return;
-    const long long bh = prow / ((long long)p.bm.nq * 128);
-    const int i = static_cast<int>(prow - bh * p.bm.nq * 128);
-    float acc = 0.f, nl = -CUDART_INF_F;      // -Delta and -lse log2(e) of the row
-    if (i < p.q_len) {
-        const long long row = bh * p.q_len + i;
-        const __nv_bfloat16* o = static_cast<const __nv_bfloat16*>(p.o) + row * p.D;
-        const __nv_bfloat16* g = static_cast<const __nv_bfloat16*>(p.dout) + row * p.D;
-        for (int d = lane; d < p.D; d += 32) acc = fmaf(__bfloat162float(o[d]), __bfloat162float(g[d]), acc);
-        const float lse = p.lse[row];
-        if (lse > -CUDART_INF_F) nl = -lse * kLog2eT;
-    }
+    const long long rows_pad = (long long)p.B * p.Hq * p.bm.nq * 128;      // (a multiple of kStatRows)
+    const long long prow0 = ((long long)blockIdx.x * 8 + warp) * kStatRows;
+    if (prow0 >= rows_pad) return;
+    // the rows are of one head: a head has a multiple of 128
+    const long long bh = prow0 / ((long long)p.bm.nq * 128);
+    const int i0 = static_cast<int>(prow0 - bh * p.bm.nq * 128);
+    const uint4* o = static_cast<const uint4*>(p.o) + bh * p.q_len * kLanes;
+    const uint4* g = static_cast<const uint4*>(p.dout) + bh * p.q_len * kLanes;
+    uint4 wo[kStatRows / kPer], wg[kStatRows / kPer];
 #pragma unroll
-    for (int k = 16; k > 0; k >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, k);
-    if (lane == 0) {
-        p.rowstats[prow] = -acc;
-        p.rowstats[rows_pad + prow] = nl;
+    for (int r = 0; r < kStatRows / kPer; ++r) {
+        const size_t at = (size_t)min(i0 + r * kPer + lane / kLanes, p.q_len - 1) * kLanes + lane % kLanes;
+        wo[r] = __ldg(o + at);
+        wg[r] = __ldg(g + at);
+    }
+    float lse = 0.f;
+    if (lane < kStatRows) lse = p.lse[bh * p.q_len + min(i0 + lane, p.q_len - 1)];
+#pragma unroll
+    for (int r = 0; r < kStatRows / kPer; ++r) {
+        stage[warp][0][r * 32 + lane] = wo[r];
+        stage[warp][1][r * 32 + lane] = wg[r];
+    }
+    __syncwarp();
+    float mine = 0.f;
+#pragma unroll
+    for (int r = 0; r < kStatRows; ++r) {
+        const __nv_bfloat16* so = reinterpret_cast<const __nv_bfloat16*>(&stage[warp][0][r * kLanes]);
+        const __nv_bfloat16* sg = reinterpret_cast<const __nv_bfloat16*>(&stage[warp][1][r * kLanes]);
+        float acc = 0.f;
+        if (i0 + r < p.q_len) {
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c)
+                acc = fmaf(__bfloat162float(so[32 * c + lane]), __bfloat162float(sg[32 * c + lane]), acc);
+        }
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, k);
+        if (lane == r) mine = acc;
+    }
+    if (lane < kStatRows) {                        // -Delta and -lse log2(e)
+        p.rowstats[prow0 + lane] = -mine;
+        p.rowstats[rows_pad + prow0 + lane] =
+            i0 + lane < p.q_len && lse > -CUDART_INF_F ? -lse * kLog2eT : -CUDART_INF_F;
+    }
+}
+
+// The split blocks' partial dV and dK, summed in the order of the parts.
+// Partials lie in dq, which the dQ kernel writes afterwards:
+// [B][Hkv][sink_blocks][sink_parts][2][128][D].  Block (x, kv head, batch):
+// 16 rows of dV or dK.
+template <int D>
+__global__ void __launch_bounds__(256) bwd_sink_sum_kernel(const BwdParams p) {
+    const int what = blockIdx.x & 1, rows16 = (blockIdx.x >> 1) & 7, blk = blockIdx.x >> 4;
+    const size_t bh = (size_t)blockIdx.z * p.Hkv + blockIdx.y;
+    const float4* src = reinterpret_cast<const float4*>(p.dq) +
+                        ((bh * p.sink_blocks + blk) * p.sink_parts * 2 + what) * (128 * D / 4);
+    float4* dst = reinterpret_cast<float4*>(what ? p.dk : p.dv) + bh * p.kv_len * (D / 4);
+    for (int e = threadIdx.x; e < 16 * (D / 4); e += 256) {
+        const int row = rows16 * 16 + e / (D / 4);
+        if (blk * kBlock + row >= p.kv_len) break;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int k = 0; k < p.sink_parts; ++k) {
+            const float4 x = __ldcg(src + (size_t)k * 2 * (128 * D / 4) + rows16 * 16 * (D / 4) + e);
+            a.x += x.x;
+            a.y += x.y;
+            a.z += x.z;
+            a.w += x.w;
+        }
+        dst[(size_t)(blk * kBlock + row) * (D / 4) + e % (D / 4)] = a;
     }
 }
 
 // The resident block of work unit u: dK/dV: kv block `blk` of (b, kv head
 // hk), lowest kv blocks first; dQ: q-block `blk` of (b, query head hq0),
 // highest q-blocks first.  Under causal masks both orders start with the
-// blocks that have the most visits.
+// blocks that have the most visits.  Under a window with sinks the first kv
+// blocks are visited by every q-block, the others by the window's few: with 64
+// q-blocks, a window of 8 and a group of 4, 256 visits against 40, more than a
+// CTA's share of all of them (135).  Such a block's visits are split into
+// sink_parts units, each with a partial sum of its own (8192 tokens, 32 heads
+// on 8: 504 us whole, 279 us split).  part: which one (-1: the whole block).
 struct TcUnit {
-    int b, hq0, hk, heads, blk;
+    int b, hq0, hk, heads, blk, part;
 };
 __device__ __forceinline__ TcUnit tc_decode_unit(const BwdParams& p, int mode, int u) {
     TcUnit x;
+    x.part = -1;
     if (mode == DKDV) {
         const int bh = u % (p.B * p.Hkv);
         x.blk = u / (p.B * p.Hkv);
+        if (p.sink_parts > 1) {
+            const int split = p.sink_blocks * p.sink_parts;
+            if (x.blk < split) {
+                x.part = x.blk % p.sink_parts;
+                x.blk /= p.sink_parts;
+            } else {
+                x.blk += p.sink_blocks - split;
+            }
+        }
         x.b = bh / p.Hkv;
         x.hk = bh % p.Hkv;
         x.hq0 = x.hk * p.group;
@@ -508,10 +582,14 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 int u = static_cast<int>(atomicAdd(p.ws + WS_SCHED_NEXT, 1u));
                 if (u >= num_units) u = -1;
                 TcUnit un{};
-                int n = 0;
+                int n = 0, skip = 0;
                 if (u >= 0) {
                     un = tc_decode_unit(p, MODE, u);
                     n = total_visits(p, MODE, un.b, un.hq0, un.heads, un.blk);
+                    if (MODE == DKDV && un.part >= 0) {       // visits skip .. skip + n - 1 of the block's
+                        skip = static_cast<int>((long long)n * un.part / p.sink_parts);
+                        n = static_cast<int>((long long)n * (un.part + 1) / p.sink_parts) - skip;
+                    }
                 }
                 volatile int* qs = unit_q + TU_WORDS * slot;
                 qs[TU_UNIT] = u;
@@ -520,6 +598,7 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 qs[TU_HQ0] = un.hq0;
                 qs[TU_HK] = un.hk;
                 qs[TU_BLK] = un.blk;
+                qs[TU_PART] = un.part;
                 mbar_arrive(bar(T_UNIT_FULL + slot));
                 ++k;
                 if (u < 0) break;
@@ -539,10 +618,13 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                     }
                 }
                 ++rr;
+                int left = n;
                 for (int g = 0; g < un.heads && ok; ++g) {
                     VisitSeq v;
                     v.row(p, MODE, un.b, un.hq0 + g, un.blk);
-                    for (int kv = 0; kv < v.np + v.nf; ++kv, ++i) {
+                    const int first = min(skip, v.np + v.nf);
+                    skip -= first;
+                    for (int kv = first; kv < v.np + v.nf && left > 0; ++kv, ++i, --left) {
                         const bool partial = kv < v.np;
                         const int other = __ldg(partial ? v.part + kv : v.full + (kv - v.np));
                         const int s = i % ST;
@@ -716,6 +798,7 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             if (!mbar_wait_warp(bar(T_UNIT_FULL + slot), (k >> 1) & 1, wc, TS_UNIT_FULL)) break;
             const volatile int* qs = unit_q + TU_WORDS * slot;
             const int u = qs[TU_UNIT], n = qs[TU_N], b = qs[TU_B], hq0 = qs[TU_HQ0], hk = qs[TU_HK], blk = qs[TU_BLK];
+            const int part = MODE == DKDV ? qs[TU_PART] : -1;
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(T_UNIT_EMPTY + slot));
             ++k;
@@ -830,6 +913,11 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 col_base = (h & 1) * kCols;
                 mul = is_dv ? 1.f : DsSign<SCORE>::kValue * p.scale;   // the elementwise step keeps +-dS
                 nrows = p.kv_len;
+                if (part >= 0) {                   // rows of the block's own partial tile
+                    out = p.dq + ((((((long long)b * p.Hkv + hk) * p.sink_blocks + blk) * p.sink_parts + part) * 2 +
+                                   (is_dv ? 0 : 1)) * 128 - (long long)blk * kBlock) * D;
+                    nrows = (blk + 1) * kBlock;
+                }
             } else {
                 out = p.dq + (((size_t)b * p.Hq + hq0) * p.q_len) * D;
                 tacc = tA1;
@@ -937,10 +1025,16 @@ cudaError_t launch_tc_score(const BwdParams& p, const CUtensorMap& tq, const CUt
         }
         sms = sm_count[dev];
     }
-    const int units_kv = p.B * p.Hkv * p.bm.nkv, units_q = p.B * p.Hq * p.bm.nq;
+    const int blocks_kv = p.bm.nkv + (p.sink_parts > 1 ? p.sink_blocks * (p.sink_parts - 1) : 0);
+    const int units_kv = p.B * p.Hkv * blocks_kv, units_q = p.B * p.Hq * p.bm.nq;
     bwd_tc_kernel<D, SCORE, DKDV><<<(unsigned)std::min(units_kv, sms), kTcThreads, smem, s>>>(tq, tk, tv, tg, p, units_kv);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
+    if (p.sink_parts > 1) {
+        bwd_sink_sum_kernel<D><<<dim3(p.sink_blocks * 16, p.Hkv, p.B), 256, 0, s>>>(p);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
     bwd_tc_kernel<D, SCORE, DQ><<<(unsigned)std::min(units_q, sms), kTcThreads, smem, s>>>(tq, tk, tv, tg, p, units_q);
     return cudaGetLastError();
 }
@@ -962,7 +1056,11 @@ cudaError_t launch_tc_d(const BwdParams& p, const CUtensorMap& tq, const CUtenso
 cudaError_t launch_bwd_tc(const BwdParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                           const CUtensorMap& tg, cudaStream_t s) {
     const long long rows_pad = (long long)p.B * p.Hq * p.bm.nq * 128;
-    bwd_rowstats_kernel<<<(unsigned)((rows_pad + 7) / 8), 256, 0, s>>>(p);
+    const unsigned stat_blocks = (unsigned)((rows_pad + 8 * kStatRows - 1) / (8 * kStatRows));
+    if (p.D == 64)
+        bwd_rowstats_kernel<64><<<stat_blocks, 256, 0, s>>>(p);
+    else
+        bwd_rowstats_kernel<128><<<stat_blocks, 256, 0, s>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     return p.D == 64 ? launch_tc_d<64>(p, tq, tk, tv, tg, s) : launch_tc_d<128>(p, tq, tk, tv, tg, s);

@@ -536,6 +536,21 @@ fa_status fa_bwd(const fa_bwd_args* a, const fa_block_mask* bm, const fa_block_m
     p.scale = a->scale > 0.f ? a->scale : 1.0f / std::sqrt((float)a->D);
     p.bm = {bm->B, bm->H, bm->nq, bm->nkv, bm->kv_num_blocks, bm->kv_indices, bm->full_kv_num_blocks,
             bm->full_kv_indices};
+    if (bm->mask.kind == FA_MASK_SINK_WINDOW) {
+        // The sinks' kv blocks have group x nq visits, the others about
+        // group x (window / 128 + 2): as many parts as bring the two together.
+        // The parts' partial tiles (2 x 128 x D each) lie in dq until its own
+        // kernel runs, which bounds them for sequences with few rows.
+        const long long other = std::min((long long)bm->mask.window, (long long)bm->q_len) / fa::kBlock + 2;
+        const long long blocks = std::min(ceil_div(std::min(bm->mask.prefix_len, bm->kv_len), fa::kBlock), bm->nkv);
+        long long parts = (bm->nq + other - 1) / other;
+        if (blocks > 0) parts = std::min(parts, (long long)a->Hq * a->q_len / (256 * blocks * a->Hkv));
+        if (blocks > 0 && parts > 1 && blocks * 16 <= 2147483647LL && a->B <= 65535 && a->Hkv <= 65535 &&
+            (long long)a->B * a->Hkv * (bm->nkv + blocks * parts) <= 2147483647LL) {
+            p.sink_blocks = (int)blocks;
+            p.sink_parts = (int)parts;
+        }
+    }
     p.cols = {cols->q_num_blocks, cols->q_indices, cols->full_q_num_blocks, cols->full_q_indices};
     p.mask = mask_params(bm);
     p.score = {score.kind, score.softcap, score.alibi_slopes, score.rel_bias, score.rel_max};

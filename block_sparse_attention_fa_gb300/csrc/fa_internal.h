@@ -108,6 +108,9 @@ struct BwdParams {
     float* dk;
     float* dv;
     BlockMaskColsView cols;
+    // Window masks with sinks: the dK/dV visits of the first sink_blocks kv
+    // blocks are split into sink_parts units each (0, 1: not split).
+    int sink_blocks, sink_parts;
     uint32_t* ws;
     uint64_t timeout_ns;
 };

@@ -210,3 +210,30 @@ def test_backward(fa, score, skw, D, q_len, kv_len, window, sinks):
         assert err.max() <= 2e-2 * max(1.0, np.abs(ref).max()), name
         norm = np.linalg.norm(ref)
         assert norm == 0 or np.linalg.norm(err) <= 1e-2 * norm, name
+
+
+@gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("B,Hq,Hkv,q_len,kv_len,window,sinks", [
+    (1, 4, 2, 2000, 2000, 60, 4), (2, 2, 2, 1300, 1300, 10, 300), (1, 6, 1, 1100, 1100, 300, 129),
+    (1, 2, 1, 3000, 200, 0, 150), (1, 3, 3, 900, 2000, 5, 1000), (1, 2, 2, 1500, 1500, 100, 2**31 - 1)])
+def test_backward_with_split_sinks(fa, D, B, Hq, Hkv, q_len, kv_len, window, sinks):
+    """Many more q-blocks than the window spans: the sinks' kv blocks are shared by several units, whose partial sums
+    are added in order, so that two runs agree to the bit."""
+    import torch
+    w = _case(B=B, Hq=Hq, Hkv=Hkv, T=kv_len, D=D, q_len=q_len)
+    q, k, v = w.qkv()
+    g = synth.round_to_bf16(synth.standard_normal(79, q.shape))
+    qd, kd, vd = parity.to_device(w, q, k, v)
+    gd = torch.from_numpy(g).cuda().to(torch.bfloat16)
+    bm = fa.block_mask("sink_window", 1, 1, q_len, kv_len, window=window, sinks=sinks)
+    o, lse = fa.fwd(qd, kd, vd, bm)
+    grads = fa.bwd(qd, kd, vd, o, lse, gd, bm)
+    again = fa.bwd(qd, kd, vd, o, lse, gd, bm)
+    fa.default_workspace("cuda").check()
+    refs = oracle.bwd(q, k, v, g, **_okw(window, sinks))
+    for name, got, twice, ref in zip(("dq", "dk", "dv"), grads, again, refs):
+        assert torch.equal(got, twice), name
+        err = np.abs(got.double().cpu().numpy() - ref)
+        assert err.max() <= 2e-2 * max(1.0, np.abs(ref).max()), name
+        assert np.linalg.norm(err) <= 1e-2 * np.linalg.norm(ref), name
