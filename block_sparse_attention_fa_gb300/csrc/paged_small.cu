@@ -51,7 +51,7 @@ constexpr int kThreadsS = 32 * (kWarps + 1);
 constexpr int kRows = kPagedSmallRows;
 constexpr float kLog2eP = 1.4426950408889634f;
 constexpr float kLn2P = 0.6931471805599453f;
-enum PagedSite : uint32_t { S_PG_FULL = 64, S_PG_EMPTY, S_PG_DRAIN };
+enum PagedSite : uint32_t { S_PG_FULL = 64, S_PG_EMPTY, S_PG_DRAIN, S_PG_Q, S_PG_Q_EMPTY };
 
 template <int D>
 struct SmallLayout {
@@ -64,13 +64,16 @@ struct SmallLayout {
     static constexpr uint32_t kP = kStages * kStage;
     static constexpr uint32_t kMax = kP + kRows * kPRow;         // [16 rows][8 warps] fp32
     static constexpr uint32_t kSum = kMax + kRows * kWarps * 4u;
-    static constexpr uint32_t kBars = kSum + kRows * kWarps * 4u;
-    static constexpr uint32_t kAbort = kBars + 16u * kStages;
+    static constexpr uint32_t kQRow = 2u * D + 16u;
+    static constexpr uint32_t kQ = kSum + kRows * kWarps * 4u;   // two units' rows of Q
+    static constexpr uint32_t kBars = kQ + 2u * kRows * kQRow;   // FULL, EMPTY [stage], Q_FULL, Q_EMPTY [2]
+    static constexpr uint32_t kAbort = kBars + 16u * kStages + 32u;
     static constexpr uint32_t kScan = kAbort + 16u;              // warp sums
     static constexpr uint32_t kPre = kScan + 64u;                // [B + 1] first tile of each sequence
     static constexpr uint32_t bytes(int B) { return kPre + 4u * (B + 1u) + 1024u; }
-    // two CTAs per SM: 228 KB less 1 KB for each
-    static_assert(2u * (kPre + 4u * (kPagedMaxSeqs + 1u) + 1024u) <= 226u * 1024u, "shared memory budget");
+    // two CTAs fit on an SM (228 KB less 1 KB for each) while B <= 1000; with
+    // more sequences one after the other
+    static_assert(2u * (kPre + 4u * 1001u + 1024u) <= 226u * 1024u, "shared memory budget");
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -159,6 +162,8 @@ paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
     const uint32_t sbase = smem_addr(smem);
     auto full_bar = [&](int st) { return sbase + L::kBars + 8u * st; };
     auto empty_bar = [&](int st) { return sbase + L::kBars + 8u * (ST + st); };
+    auto q_full = [&](int u) { return sbase + L::kBars + 8u * (2 * ST + (u & 1)); };
+    auto q_empty = [&](int u) { return sbase + L::kBars + 8u * (2 * ST + 2 + (u & 1)); };
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kAbort);
     int* const pre = reinterpret_cast<int*>(smem + L::kPre);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
@@ -167,6 +172,10 @@ paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         for (int st = 0; st < ST; ++st) {
             mbar_init(full_bar(st), 1);
             mbar_init(empty_bar(st), kWarps);
+        }
+        for (int u = 0; u < 2; ++u) {
+            mbar_init(q_full(u), 1);
+            mbar_init(q_empty(u), kWarps);
         }
         *abort_flag = 0;
         mbar_fence_init();
@@ -207,12 +216,25 @@ paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         int last[ST];
 #pragma unroll
         for (int st = 0; st < ST; ++st) last[st] = -1;
-        int g = 0;
+        int g = 0, nu = 0;
         bool ok = true;
         SmallSeg s;
-        while (ok && next_seg<SH>(p, line, s)) {
+        for (; ok && next_seg<SH>(p, line, s); ++nu) {
             const int32_t* table = p.c.page_table + (size_t)s.b * p.c.max_pages;
             int page = tile_page<KT>(p.c, table, s.hull, s.hull.tile(s.k0), lane, s.b, p.ws);
+            // the unit's rows of Q, a lane to each, into the buffer that the
+            // unit before the last has left
+            const int rows = s.n * p.group;
+            if (nu >= 2 && !mbar_wait_warp(q_empty(nu), ((nu >> 1) - 1) & 1, wc, S_PG_Q_EMPTY)) break;
+            if (lane == 0) mbar_arrive_expect_tx(q_full(nu), static_cast<uint32_t>(rows) * 2u * D);
+            __syncwarp();
+            if (lane < rows) {
+                const int tok = quotient(lane, p.by_group);
+                bulk_load(sbase + L::kQ + ((nu & 1) * kRows + lane) * L::kQRow,
+                          p.q + (long long)(s.q0 + tok) * p.qs[0] +
+                              (long long)(s.h * p.group + lane - tok * p.group) * p.qs[1],
+                          2u * D, q_full(nu));
+            }
             for (int k = s.k0; k < s.k1; ++k, ++g) {
                 const int kb = s.hull.tile(k), st = g % ST;
                 const int id = page;
@@ -239,6 +261,7 @@ paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
 #pragma unroll
             for (int st = 0; st < ST; ++st)
                 if (last[st] >= 0) paged_drain_wait(full_bar(st), (last[st] / ST) & 1, wc, S_PG_DRAIN);
+            for (int u = max(nu - 2, 0); u < nu; ++u) paged_drain_wait(q_full(u), (u >> 1) & 1, wc, S_PG_DRAIN);
         }
         __syncwarp();
         if (p.join_rows) pdl_wait_previous();
@@ -254,26 +277,28 @@ paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
     constexpr int kNT = D / 64;                    // n8 tiles of O per warp
     constexpr int kKW = KT / 8, kNK = kKW / 8;     // keys per warp, n8 tiles of S
     const int col0 = warp * (D / 8);               // the warp's first column of O
-    int g = 0;
+    int g = 0, nu = 0;
     bool ok = true;
     PagedMeta meta{};
     SmallSeg s;
-    while (ok && next_seg<SH>(p, line, s)) {
+    for (; ok && next_seg<SH>(p, line, s); ++nu) {
         const int rows = s.n * p.group, i0 = s.kv - s.n, i1 = s.kv - 1;
         int tok[2], hq[2];
-        uint32_t qa[D / 16][4];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int r = min(gr + 8 * e, rows - 1);
             tok[e] = quotient(r, p.by_group);
             hq[e] = s.h * p.group + r - tok[e] * p.group;
-            const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q + (long long)(s.q0 + tok[e]) * p.qs[0] +
-                                                                    (long long)hq[e] * p.qs[1]);
+        }
+        // Q's fragments (what the rows past the unit's hold stays in those rows)
+        uint32_t qa[D / 16][4];
+        const bool q_here = mbar_wait_warp(q_full(nu), (nu >> 1) & 1, wc, S_PG_Q);
+        {
+            const uint32_t q_row = sbase + L::kQ + ((nu & 1) * kRows + l8 + 8 * (mi & 1)) * L::kQRow + 16 * (mi >> 1);
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-                qa[ks][e] = __ldg(src + 8 * ks + tq);
-                qa[ks][2 + e] = __ldg(src + 8 * ks + 4 + tq);
-            }
+            for (int ks = 0; ks < D / 16; ++ks) ldsm4(q_row + 32 * ks, qa[ks]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_empty(nu));
         }
         float m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f};
         float o[kNT][4];
@@ -283,7 +308,7 @@ paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         for (int k = s.k0; k < s.k1; ++k, ++g) {
             const int st = g % ST, kb = s.hull.tile(k), c0 = kb * KT;
             const uint32_t kbase = sbase + st * L::kStage, vbase = kbase + (D / 64) * L::kBox;
-            const bool here = mbar_wait_warp(full_bar(st), (g / ST) & 1, wc, S_PG_FULL);
+            const bool here = q_here && mbar_wait_warp(full_bar(st), (g / ST) & 1, wc, S_PG_FULL);
             float x[kNK][4];
 #pragma unroll
             for (int nt = 0; nt < kNK; ++nt) x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.f;
