@@ -51,7 +51,19 @@ constexpr int kThreadsS = 32 * (kWarps + 1);
 constexpr int kRows = kPagedSmallRows;
 constexpr float kLog2eP = 1.4426950408889634f;
 constexpr float kLn2P = 0.6931471805599453f;
+constexpr int kTileOpen = 1, kTileClear = 2;    // every row sees every key; some key is seen by no row
 enum PagedSite : uint32_t { S_PG_FULL = 64, S_PG_EMPTY, S_PG_DRAIN, S_PG_Q, S_PG_Q_EMPTY };
+
+// The part of one unit that falls into a CTA's stretch: tiles k0 .. k1 - 1 of
+// the unit's list.  The loader finds it, ahead of the consumers, who read it
+// from a slot in shared memory (with its rows of Q).
+struct SmallSeg {
+    int b, h, kv, n, q0;
+    int tiles, k0, k1, count;      // count: CTAs that share the unit from here on
+    Hull hull;
+    __device__ __forceinline__ bool begins() const { return k0 == 0; }
+    __device__ __forceinline__ bool ends() const { return k1 == tiles; }
+};
 
 template <int D>
 struct SmallLayout {
@@ -66,7 +78,9 @@ struct SmallLayout {
     static constexpr uint32_t kSum = kMax + kRows * kWarps * 4u;
     static constexpr uint32_t kQRow = 2u * D + 16u;
     static constexpr uint32_t kQ = kSum + kRows * kWarps * 4u;   // two units' rows of Q
-    static constexpr uint32_t kBars = kQ + 2u * kRows * kQRow;   // FULL, EMPTY [stage], Q_FULL, Q_EMPTY [2]
+    static constexpr uint32_t kSeg = kQ + 2u * kRows * kQRow;    // two units, the last one flagged by b < 0
+    static constexpr uint32_t kInfo = kSeg + 2u * sizeof(SmallSeg);   // [stage]: 4 x tile + kTileOpen, kTileClear
+    static constexpr uint32_t kBars = (kInfo + 4u * kStages + 7u) & ~7u;  // FULL, EMPTY [stage], Q_FULL, Q_EMPTY [2]
     static constexpr uint32_t kAbort = kBars + 16u * kStages + 32u;
     static constexpr uint32_t kScan = kAbort + 16u;              // warp sums
     static constexpr uint32_t kPre = kScan + 64u;                // [B + 1] first tile of each sequence
@@ -114,16 +128,6 @@ __device__ __forceinline__ bool consumers_all(bool ok) {
     return r != 0;
 }
 
-// The part of one unit that falls into a CTA's stretch: tiles k0 .. k1 - 1 of
-// the unit's list.
-struct SmallSeg {
-    int b, h, kv, n, q0;
-    int tiles, k0, k1, count;      // count: CTAs that share the unit from here on
-    Hull hull;
-    __device__ __forceinline__ bool begins() const { return k0 == 0; }
-    __device__ __forceinline__ bool ends() const { return k1 == tiles; }
-};
-
 // A CTA's stretch [t, t1) of the line of tiles.
 struct Line {
     const int* pre;
@@ -166,6 +170,8 @@ paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
     auto q_empty = [&](int u) { return sbase + L::kBars + 8u * (2 * ST + 2 + (u & 1)); };
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kAbort);
     int* const pre = reinterpret_cast<int*>(smem + L::kPre);
+    SmallSeg* const seg_s = reinterpret_cast<SmallSeg*>(smem + L::kSeg);
+    volatile int* const info_s = reinterpret_cast<volatile int*>(smem + L::kInfo);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
 
     if (threadIdx.x == 0) {
@@ -217,16 +223,28 @@ paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
 #pragma unroll
         for (int st = 0; st < ST; ++st) last[st] = -1;
         int g = 0, nu = 0;
-        bool ok = true;
+        bool ok = true, marked = false;
         SmallSeg s;
-        for (; ok && next_seg<SH>(p, line, s); ++nu) {
+        for (; ok; ++nu) {
+            const bool more = next_seg<SH>(p, line, s);
+            if (nu >= 2 && !mbar_wait_warp(q_empty(nu), ((nu >> 1) - 1) & 1, wc, S_PG_Q_EMPTY)) break;
+            if (!more) {
+                if (lane == 0) {
+                    seg_s[nu & 1].b = -1;
+                    mbar_arrive(q_full(nu));
+                }
+                marked = true;
+                break;
+            }
             const int32_t* table = p.c.page_table + (size_t)s.b * p.c.max_pages;
             int page = tile_page<KT>(p.c, table, s.hull, s.hull.tile(s.k0), lane, s.b, p.ws);
-            // the unit's rows of Q, a lane to each, into the buffer that the
-            // unit before the last has left
-            const int rows = s.n * p.group;
-            if (nu >= 2 && !mbar_wait_warp(q_empty(nu), ((nu >> 1) - 1) & 1, wc, S_PG_Q_EMPTY)) break;
-            if (lane == 0) mbar_arrive_expect_tx(q_full(nu), static_cast<uint32_t>(rows) * 2u * D);
+            // the unit and its rows of Q, a lane to each, into the slots that
+            // the unit before the last has left
+            const int rows = s.n * p.group, i0 = s.kv - s.n, i1 = s.kv - 1;
+            if (lane == 0) {
+                seg_s[nu & 1] = s;
+                mbar_arrive_expect_tx(q_full(nu), static_cast<uint32_t>(rows) * 2u * D);
+            }
             __syncwarp();
             if (lane < rows) {
                 const int tok = quotient(lane, p.by_group);
@@ -241,7 +259,11 @@ paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                 if (k + 1 < s.k1) page = tile_page<KT>(p.c, table, s.hull, s.hull.tile(k + 1), lane, s.b, p.ws);
                 if (g >= ST && !mbar_wait_warp(empty_bar(st), (g / ST - 1) & 1, wc, S_PG_EMPTY)) { ok = false; break; }
                 const uint32_t pages = __popc(__ballot_sync(0xffffffffu, id >= 0));
-                if (lane == 0) mbar_arrive_expect_tx(full_bar(st), pages * page_bytes);
+                if (lane == 0) {
+                    info_s[st] = 4 * kb + (tile_open(p.mask, kb, i0, i1, p.shared, s.kv, SH) ? kTileOpen : 0) +
+                                 (s.hull.all(kb * KT, kb * KT + KT) ? 0 : kTileClear);
+                    mbar_arrive_expect_tx(full_bar(st), pages * page_bytes);
+                }
                 __syncwarp();
                 if (id >= 0) {
                     const uint32_t dst = sbase + st * L::kStage + static_cast<uint32_t>(lane * span) * 128u;
@@ -261,7 +283,10 @@ paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
 #pragma unroll
             for (int st = 0; st < ST; ++st)
                 if (last[st] >= 0) paged_drain_wait(full_bar(st), (last[st] / ST) & 1, wc, S_PG_DRAIN);
-            for (int u = max(nu - 2, 0); u < nu; ++u) paged_drain_wait(q_full(u), (u >> 1) & 1, wc, S_PG_DRAIN);
+            // (behind the end mark only the last unit's rows can be on their
+            // way: the mark's slot had been read)
+            for (int u = max(nu - (marked ? 1 : 2), 0); u < nu; ++u)
+                paged_drain_wait(q_full(u), (u >> 1) & 1, wc, S_PG_DRAIN);
         }
         __syncwarp();
         if (p.join_rows) pdl_wait_previous();
@@ -277,12 +302,16 @@ paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
     constexpr int kNT = D / 64;                    // n8 tiles of O per warp
     constexpr int kKW = KT / 8, kNK = kKW / 8;     // keys per warp, n8 tiles of S
     const int col0 = warp * (D / 8);               // the warp's first column of O
-    int g = 0, nu = 0;
+    int g = 0;
     bool ok = true;
     PagedMeta meta{};
-    SmallSeg s;
-    for (; ok && next_seg<SH>(p, line, s); ++nu) {
-        const int rows = s.n * p.group, i0 = s.kv - s.n, i1 = s.kv - 1;
+    for (int nu = 0;; ++nu) {
+        const bool q_here = mbar_wait_warp(q_full(nu), (nu >> 1) & 1, wc, S_PG_Q);
+        // (the vote keeps the warps together where a wait has run out)
+        if (!consumers_all(q_here)) { ok = false; break; }
+        const SmallSeg s = seg_s[nu & 1];
+        if (s.b < 0) break;
+        const int rows = s.n * p.group, i0 = s.kv - s.n;
         int tok[2], hq[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -292,7 +321,6 @@ paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         }
         // Q's fragments (what the rows past the unit's hold stays in those rows)
         uint32_t qa[D / 16][4];
-        const bool q_here = mbar_wait_warp(q_full(nu), (nu >> 1) & 1, wc, S_PG_Q);
         {
             const uint32_t q_row = sbase + L::kQ + ((nu & 1) * kRows + l8 + 8 * (mi & 1)) * L::kQRow + 16 * (mi >> 1);
 #pragma unroll
@@ -306,9 +334,10 @@ paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         for (int n = 0; n < kNT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
 
         for (int k = s.k0; k < s.k1; ++k, ++g) {
-            const int st = g % ST, kb = s.hull.tile(k), c0 = kb * KT;
+            const int st = g % ST;
             const uint32_t kbase = sbase + st * L::kStage, vbase = kbase + (D / 64) * L::kBox;
-            const bool here = q_here && mbar_wait_warp(full_bar(st), (g / ST) & 1, wc, S_PG_FULL);
+            const bool here = mbar_wait_warp(full_bar(st), (g / ST) & 1, wc, S_PG_FULL);
+            const int info = info_s[st], c0 = (info >> 2) * KT;
             float x[kNK][4];
 #pragma unroll
             for (int nt = 0; nt < kNK; ++nt) x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.f;
@@ -337,7 +366,7 @@ paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
 #pragma unroll
                     for (int c = 0; c < 4; ++c) x[0][c] += y[c];
                 }
-                const bool open = tile_open(p.mask, kb, i0, i1, p.shared, s.kv, SH);
+                const bool open = (info & kTileOpen) != 0;
 #pragma unroll
                 for (int nt = 0; nt < kNK; ++nt) {
 #pragma unroll
@@ -353,7 +382,7 @@ paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                 }
                 // V rows that no row of the unit sees
                 const int a = c0 + kKW * warp;
-                if (!s.hull.all(a, a + kKW)) {
+                if (info & kTileClear) {
                     cleared = true;
                     for (int r = 0; r < kKW; ++r) {
                         if (s.hull.live(a + r)) continue;
