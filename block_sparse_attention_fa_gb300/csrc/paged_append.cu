@@ -11,9 +11,15 @@
 // Every byte is read and written once, so memory bounds it.  A thread takes 16
 // elements of one head as two 16-byte pieces: the two halves of 8 pairs
 // ((d, d + rot / 2): pieces half a rotation apart; (2 d, 2 d + 1): adjacent
-// pieces), for which it needs 8 cosines and 8 sines.  One CTA per token: its
-// threads find the token's sequence together (each tests a part of q_start,
-// one block-wide count adds them up).
+// pieces), for which it needs 8 cosines and 8 sines.
+//
+// Finding a token's slot takes three loads that wait for one another (q_start,
+// the sequence's numbers, its page).  A CTA takes up to four tokens, one warp
+// to a token for that part, and then moves the data of two tokens at a time,
+// so that enough loads are in flight: 107 us for 26418 tokens of 32 + 16 heads
+// of 128 columns (656 MB, 0.90 of the copy rate), 128 us with a CTA per token;
+// eight tokens took 109 us, sixteen 117.  A step of few tokens gives each a CTA
+// of its own.
 #include <cuda_bf16.h>
 
 #include "paged.cuh"
@@ -22,6 +28,7 @@ namespace fa {
 namespace {
 
 constexpr int kAppendThreads = 256;
+constexpr int kAppendTokens = 4;
 
 struct Piece16 {
     uint32_t a[4], b[4];     // two pieces of 8 bf16
@@ -50,74 +57,124 @@ __device__ __forceinline__ void rotate_pairs(Piece16& x, const float (&c)[8], co
     }
 }
 
-template <int D>
-__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendParams p) {
-    constexpr int kItems = D / 16;               // 16-element items per head
-    const int t = blockIdx.x, tid = threadIdx.x;
-    pdl_wait_previous();
-    pdl_launch_next();
+// Where a token goes: the row of the tables (-1: nowhere), and its slot's first
+// element in the cache.
+struct Place {
+    int at;
+    size_t kv_row;
+};
+
+// One warp finds the place of row t.
+__device__ __forceinline__ Place place_of(const AppendParams& p, int t, int lane) {
+    Place none{-1, 0};
     // the sequence of row t: how many of q_start[1 ..] are <= t
     int b = 0;
-    for (int b0 = 0; b0 < p.c.B; b0 += kAppendThreads)
-        b += __syncthreads_count(b0 + tid < p.c.B && __ldg(p.c.q_start + min(b0 + tid, p.c.B - 1) + 1) <= t);
-    if (b >= p.c.B) return;                      // behind the last sequence
-    const SeqInfo s = seq_info(p.c, b, INT_MAX, 0, tid == 0 ? p.ws : nullptr);
-    if (s.n == 0) return;
-    if (t < s.q0 || t >= s.q0 + s.n) {           // q_start is not in order
-        if (tid == 0) report_sequence(p.ws, b);
-        return;
+    for (int b0 = 0; b0 < p.c.B; b0 += 128) {
+        int ends[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) ends[k] = __ldg(p.c.q_start + min(b0 + 32 * k + lane, p.c.B - 1) + 1);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            b += __popc(__ballot_sync(0xffffffffu, b0 + 32 * k + lane < p.c.B && ends[k] <= t));
     }
-    const int i = s.kv - s.n + (t - s.q0);
+    if (b >= p.c.B) return none;                 // behind the last sequence
+    const SeqInfo s = seq_info(p.c, b, INT_MAX, 0, lane == 0 ? p.ws : nullptr);
+    if (s.n == 0) return none;
+    const bool placed = t >= s.q0 && t < s.q0 + s.n;         // (not where q_start decreases)
+    const int i = placed ? s.kv - s.n + (t - s.q0) : 0;
     const int at = p.positions ? __ldg(p.positions + t) : i;
     const int page = __ldg(p.c.page_table + (size_t)b * p.c.max_pages + (i >> p.c.page_shift));
-    if (page < 0 || page >= p.c.num_pages || (p.rot && (at < 0 || at >= p.rope_len))) {
-        if (tid == 0) report_sequence(p.ws, b);
-        return;
+    if (!placed || page < 0 || page >= p.c.num_pages || (p.rot && (at < 0 || at >= p.rope_len))) {
+        if (lane == 0) report_sequence(p.ws, b);
+        return none;
     }
-    const int slot = i & (p.c.page_size - 1);
-    const size_t kv_row = ((size_t)page * p.c.Hkv * p.c.page_size + slot) * D;
-    const size_t kv_head = (size_t)p.c.page_size * D;
-    const int heads = p.Hq + 2 * p.c.Hkv, rot_items = p.rot / 16;
-    for (int x = tid; x < heads * kItems; x += kAppendThreads) {
-        const int head = x / kItems, k = x % kItems;
+    // (without a rotation the position is not looked at, and may be anything)
+    return Place{p.rot ? at : 0, ((size_t)page * p.c.Hkv * p.c.page_size + (i & (p.c.page_size - 1))) * p.D};
+}
+
+template <int D>
+__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendParams p, int per_cta) {
+    constexpr int kItems = D / 16;               // 16-element items per head
+    constexpr int kAtOnce = 2;
+    __shared__ Place places[kAppendTokens];
+    const int t0 = blockIdx.x * per_cta, tid = threadIdx.x, threads = blockDim.x;
+    const int tokens = min(per_cta, p.c.total_q - t0);
+    const int items = (p.Hq + 2 * p.c.Hkv) * kItems;
+    pdl_wait_previous();
+    pdl_launch_next();
+    // an item's place in a head and in the cache, and its source
+    struct Item {
+        int head, k, h, ea, eb;
+        bool is_q, is_k, turn;
         const uint16_t* src;
-        uint16_t* dst;
-        bool turn = k < rot_items;
-        if (head < p.Hq) {
-            src = p.q + (long long)t * p.qs[0] + (long long)head * p.qs[1];
-            dst = p.q_out + (long long)t * p.os[0] + (long long)head * p.os[1];
-        } else if (head < p.Hq + p.c.Hkv) {
-            const int h = head - p.Hq;
-            src = p.k + (long long)t * p.ks[0] + (long long)h * p.ks[1];
-            dst = p.kc + kv_row + h * kv_head;
-        } else {
-            const int h = head - p.Hq - p.c.Hkv;
-            src = p.v + (long long)t * p.vs[0] + (long long)h * p.vs[1];
-            dst = p.vc + kv_row + h * kv_head;
-            turn = false;
-        }
+        long long step;
+    };
+    auto item_of = [&](int x) {
+        Item it;
+        it.head = x / kItems;
+        it.k = x % kItems;
+        it.is_q = it.head < p.Hq;
+        it.is_k = !it.is_q && it.head < p.Hq + p.c.Hkv;
+        it.h = it.is_q ? it.head : it.is_k ? it.head - p.Hq : it.head - p.Hq - p.c.Hkv;
+        it.src = it.is_q ? p.q + (long long)it.h * p.qs[1]
+                 : it.is_k ? p.k + (long long)it.h * p.ks[1] : p.v + (long long)it.h * p.vs[1];
+        it.step = it.is_q ? p.qs[0] : it.is_k ? p.ks[0] : p.vs[0];
         // the item's two pieces of 8: half a rotation apart where halves are
         // paired, adjacent otherwise (the items past the rotation pair up the
         // pieces that are left)
-        const bool halves = k < rot_items && !p.interleaved;
-        const int ea = halves ? 8 * k : 16 * k, eb = halves ? 8 * k + p.rot / 2 : 16 * k + 8;
-        Piece16 v;
-        *reinterpret_cast<uint4*>(v.a) = *reinterpret_cast<const uint4*>(src + ea);
-        *reinterpret_cast<uint4*>(v.b) = *reinterpret_cast<const uint4*>(src + eb);
-        if (turn) {
-            float c[8], sn[8];
-            const size_t row = (size_t)at * (p.rot / 2) + 8 * k;
-            *reinterpret_cast<float4*>(c) = __ldg(reinterpret_cast<const float4*>(p.cos + row));
-            *reinterpret_cast<float4*>(c + 4) = __ldg(reinterpret_cast<const float4*>(p.cos + row + 4));
-            *reinterpret_cast<float4*>(sn) = __ldg(reinterpret_cast<const float4*>(p.sin + row));
-            *reinterpret_cast<float4*>(sn + 4) = __ldg(reinterpret_cast<const float4*>(p.sin + row + 4));
-            if (p.interleaved)
-                rotate_pairs(v, c, sn);
-            else
-                rotate_halves(v, c, sn);
+        const bool rotated = it.k < p.rot / 16, halves = rotated && !p.interleaved;
+        it.turn = rotated && (it.is_q || it.is_k);
+        it.ea = halves ? 8 * it.k : 16 * it.k;
+        it.eb = halves ? 8 * it.k + p.rot / 2 : 16 * it.k + 8;
+        return it;
+    };
+    Piece16 v[kAtOnce];
+    auto load = [&](const Item& it, int g) {
+#pragma unroll
+        for (int e = 0; e < kAtOnce; ++e) {
+            if (g + e >= tokens) continue;
+            const uint16_t* from = it.src + (long long)(t0 + g + e) * it.step;
+            *reinterpret_cast<uint4*>(v[e].a) = __ldcs(reinterpret_cast<const uint4*>(from + it.ea));
+            *reinterpret_cast<uint4*>(v[e].b) = __ldcs(reinterpret_cast<const uint4*>(from + it.eb));
         }
-        *reinterpret_cast<uint4*>(dst + ea) = *reinterpret_cast<const uint4*>(v.a);
-        *reinterpret_cast<uint4*>(dst + eb) = *reinterpret_cast<const uint4*>(v.b);
+    };
+    // the thread's first data sets out before the places are known
+    Item it = item_of(min(tid, items - 1));
+    load(it, 0);
+    for (int w = tid >> 5; w < tokens; w += threads >> 5) {
+        const Place x = place_of(p, t0 + w, tid & 31);
+        if ((tid & 31) == 0) places[w] = x;
+    }
+    __syncthreads();
+    const size_t kv_head = (size_t)p.c.page_size * D;
+    for (int x = tid; x < items; x += threads) {
+        if (x != tid) it = item_of(x);
+        uint16_t* const cache = (it.is_k ? p.kc : p.vc) + it.h * kv_head;
+        for (int g = 0; g < tokens; g += kAtOnce) {
+            if (x != tid || g > 0) load(it, g);
+#pragma unroll
+            for (int e = 0; e < kAtOnce; ++e) {
+                if (g + e >= tokens) continue;
+                const Place at = places[g + e];
+                if (at.at < 0) continue;
+                if (it.turn) {
+                    float c[8], sn[8];
+                    const size_t row = (size_t)at.at * (p.rot / 2) + 8 * it.k;
+                    *reinterpret_cast<float4*>(c) = __ldg(reinterpret_cast<const float4*>(p.cos + row));
+                    *reinterpret_cast<float4*>(c + 4) = __ldg(reinterpret_cast<const float4*>(p.cos + row + 4));
+                    *reinterpret_cast<float4*>(sn) = __ldg(reinterpret_cast<const float4*>(p.sin + row));
+                    *reinterpret_cast<float4*>(sn + 4) = __ldg(reinterpret_cast<const float4*>(p.sin + row + 4));
+                    if (p.interleaved)
+                        rotate_pairs(v[e], c, sn);
+                    else
+                        rotate_halves(v[e], c, sn);
+                }
+                uint16_t* dst = it.is_q ? p.q_out + (long long)(t0 + g + e) * p.os[0] + (long long)it.h * p.os[1]
+                                        : cache + at.kv_row;
+                *reinterpret_cast<uint4*>(dst + it.ea) = *reinterpret_cast<const uint4*>(v[e].a);
+                *reinterpret_cast<uint4*>(dst + it.eb) = *reinterpret_cast<const uint4*>(v[e].b);
+            }
+        }
     }
 }
 
@@ -125,8 +182,14 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendP
 
 cudaError_t launch_kv_append(const AppendParams& p, cudaStream_t s) {
     if (p.c.total_q == 0) return cudaSuccess;
-    return p.D == 64 ? paged_launch(kv_append_kernel<64>, dim3(p.c.total_q), kAppendThreads, 0, true, s, p)
-                     : paged_launch(kv_append_kernel<128>, dim3(p.c.total_q), kAppendThreads, 0, true, s, p);
+    // the items shared evenly by the threads; several tokens to a CTA once
+    // every SM has some CTAs even so
+    const int items = (p.Hq + 2 * p.c.Hkv) * (p.D / 16), rounds = (items + kAppendThreads - 1) / kAppendThreads;
+    const int threads = ((items + rounds - 1) / rounds + 31) / 32 * 32;
+    const int per_cta = p.c.total_q >= kAppendTokens * 4 * device_sm_count() ? kAppendTokens : 1;
+    const dim3 grid((p.c.total_q + per_cta - 1) / per_cta);
+    return p.D == 64 ? paged_launch(kv_append_kernel<64>, grid, threads, 0, true, s, p, per_cta)
+                     : paged_launch(kv_append_kernel<128>, grid, threads, 0, true, s, p, per_cta);
 }
 
 }  // namespace fa

@@ -9,6 +9,7 @@ raises; there is no CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import struct
 import threading
@@ -236,8 +237,31 @@ def _workspace_of(idx: int, raw: int) -> Workspace:
     return ws
 
 
+class _IndexArrays:
+    """The two count and two index arrays of a (transposed) BlockMask in one allocation: four would take longer to
+    allocate than the arrays of a short sequence take to build.  Each starts on a 16-byte boundary."""
+
+    def __init__(self, counts, indices, device):
+        self.shapes = (counts, indices, counts, indices)
+        at = [0]
+        for s in self.shapes:
+            at.append(at[-1] + (math.prod(s) + 3) // 4 * 4)
+        self.at = at
+        self.buf = torch.empty(at[-1], dtype=torch.int32, device=device)
+        base = self.buf.data_ptr()
+        self.ptrs = [base + 4 * x for x in at[:-1]]
+
+    def __getitem__(self, k) -> torch.Tensor:
+        return self.buf[self.at[k]:self.at[k] + math.prod(self.shapes[k])].view(self.shapes[k])
+
+
 class BlockMask:
     """A BlockMask over 128 x 128 tiles (device int32 arrays + the mask_mod)."""
+
+    kv_num_blocks = property(lambda self: self._arrays[0])
+    kv_indices = property(lambda self: self._arrays[1])
+    full_kv_num_blocks = property(lambda self: self._arrays[2])
+    full_kv_indices = property(lambda self: self._arrays[3])
 
     def __init__(self, B, H, q_len, kv_len, mask, window, prefix_len, seg_ids, device, table=None):
         lib = load_library()
@@ -248,18 +272,14 @@ class BlockMask:
         self.mask, self.window, self.prefix_len = mask, window, prefix_len
         self.seg_ids = seg_ids
         self.table = table
-        self.kv_num_blocks = torch.empty((B, H, self.nq), dtype=torch.int32, device=device)
-        self.kv_indices = torch.empty((B, H, self.nq, self.nkv), dtype=torch.int32, device=device)
-        self.full_kv_num_blocks = torch.empty((B, H, self.nq), dtype=torch.int32, device=device)
-        self.full_kv_indices = torch.empty((B, H, self.nq, self.nkv), dtype=torch.int32, device=device)
+        self._arrays = _IndexArrays((B, H, self.nq), (B, H, self.nq, self.nkv), device)
+        self.device = self._arrays.buf.device
+        self._cols = None
         s = BlockMaskStruct()
         s.B, s.H, s.q_len, s.kv_len = B, H, q_len, kv_len
         s.block_q = s.block_kv = BLOCK
         s.nq, s.nkv = self.nq, self.nkv
-        s.kv_num_blocks = self.kv_num_blocks.data_ptr()
-        s.kv_indices = self.kv_indices.data_ptr()
-        s.full_kv_num_blocks = self.full_kv_num_blocks.data_ptr()
-        s.full_kv_indices = self.full_kv_indices.data_ptr()
+        s.kv_num_blocks, s.kv_indices, s.full_kv_num_blocks, s.full_kv_indices = self._arrays.ptrs
         s.mask.kind = MASK_KINDS[mask]
         s.mask.window = window
         s.mask.prefix_len = prefix_len
@@ -275,29 +295,24 @@ class BlockMask:
         """Run fa_block_mask_build again into this BlockMask's own buffers
         (e.g. after the segment ids changed in place); capturable in a CUDA
         graph since it allocates nothing."""
-        ws = workspace or default_workspace(self.kv_num_blocks.device, stream)
+        ws = workspace or default_workspace(self.device, stream)
         _check(load_library().fa_block_mask_build(ctypes.byref(self.struct), ws.ptr, _stream_ptr(stream)))
         return self
 
     def cols(self, stream=None, workspace: Optional["Workspace"] = None, rebuild: bool = False) -> dict:
         """The transposed lists (fa_block_mask_build_cols: the q-blocks that
         visit each kv block), built on first use and kept with the mask."""
-        if getattr(self, "_cols", None) is None or rebuild:
-            dev = self.kv_num_blocks.device
-            if getattr(self, "_cols", None) is None:
-                t = {"q_num_blocks": torch.empty((self.B, self.H, self.nkv), dtype=torch.int32, device=dev),
-                     "q_indices": torch.empty((self.B, self.H, self.nkv, self.nq), dtype=torch.int32, device=dev),
-                     "full_q_num_blocks": torch.empty((self.B, self.H, self.nkv), dtype=torch.int32, device=dev),
-                     "full_q_indices": torch.empty((self.B, self.H, self.nkv, self.nq), dtype=torch.int32,
-                                                   device=dev)}
-                cs = BlockMaskColsStruct()
-                for k, v in t.items():
-                    setattr(cs, k, v.data_ptr())
-                self._cols, self._cols_struct = t, cs
-            ws = workspace or default_workspace(dev, stream)
+        self._build_cols(stream, workspace, rebuild)
+        return {name: self._cols[k] for k, (name, _) in enumerate(BlockMaskColsStruct._fields_)}
+
+    def _build_cols(self, stream, workspace, rebuild=False):
+        if self._cols is None or rebuild:
+            if self._cols is None:
+                self._cols = _IndexArrays((self.B, self.H, self.nkv), (self.B, self.H, self.nkv, self.nq), self.device)
+                self._cols_struct = BlockMaskColsStruct(*self._cols.ptrs)
+            ws = workspace or default_workspace(self.device, stream)
             _check(load_library().fa_block_mask_build_cols(ctypes.byref(self.struct), ctypes.byref(self._cols_struct),
                                                            ws.ptr, _stream_ptr(stream)))
-        return self._cols
 
     def visited_tiles(self) -> int:
         return int(self.kv_num_blocks.sum().item() + self.full_kv_num_blocks.sum().item())
@@ -580,7 +595,7 @@ def bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor, lse:
     a.timeout_ms = timeout_ms
     sc = _score_desc(score, softcap, alibi_slopes, rel_bias, rel_max)
     ws = workspace or default_workspace(q.device, stream)
-    bm.cols(stream=stream, workspace=ws)
+    bm._build_cols(stream, ws)
     _check(load_library().fa_bwd(ctypes.byref(a), ctypes.byref(bm.struct), ctypes.byref(bm._cols_struct),
                                  ctypes.byref(sc), ws.ptr, _stream_ptr(stream)))
     return dq, dk, dv
@@ -634,6 +649,7 @@ def _call_on(dev, fn, *args):
 # call together where several threads share a stream.  A captured call gets
 # scratch of its own, which its graph keeps.
 _paged_scratch = {}
+_PAGED_KEEP = 64 << 20         # larger ones go back to the allocator
 _paged_lock = threading.Lock()
 
 
@@ -748,31 +764,27 @@ def fwd_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, pag
     raw = _raw_stream(dev) if stream is None else stream.cuda_stream
     ws = workspace or _workspace_of(dev, raw)
 
-    def call(t):
-        return _call_on(dev, lib.fa_fwd_paged, c, a, m, sc, t.data_ptr(), t.numel() * t.element_size(),
-                        ws.tensor.data_ptr(), raw)
-
-    def fresh():
-        # (no bytes: the arguments are wrong, and the call says how)
-        return torch.empty(_call_on(dev, lib.fa_paged_scratch_bytes, c, a) or 16, dtype=torch.uint8, device=q.device)
-
     if scratch is not None:
         if scratch.get_device() != dev or not scratch.is_contiguous():
             raise ValueError("scratch must be a contiguous tensor on q's device")
-        st = call(scratch)
+        st = _call_on(dev, lib.fa_fwd_paged, c, a, m, sc, scratch.data_ptr(), scratch.numel() * scratch.element_size(),
+                      ws.tensor.data_ptr(), raw)
     elif stream is not None or _capturing():
-        scratch = fresh()
+        # (no bytes: the arguments are wrong, and the call says how)
+        scratch = torch.empty(_call_on(dev, lib.fa_paged_scratch_bytes, c, a) or 16, dtype=torch.uint8, device=q.device)
         made.append(scratch)
-        st = call(scratch)
+        st = _call_on(dev, lib.fa_fwd_paged, c, a, m, sc, scratch.data_ptr(), scratch.numel(), ws.tensor.data_ptr(), raw)
     else:
         with _paged_lock:
-            scratch = _paged_scratch.get((dev, raw))
-            st = ERR_INVALID_ARG if scratch is None else call(scratch)
+            kept = _paged_scratch.get((dev, raw))
+            st = ERR_INVALID_ARG if kept is None else \
+                _call_on(dev, lib.fa_fwd_paged, c, a, m, sc, kept.data_ptr(), kept.numel(), ws.tensor.data_ptr(), raw)
             if st == ERR_INVALID_ARG:              # none yet, or too small (or wrong arguments: the call says so again)
-                scratch = fresh()
-                st = call(scratch)
-                if st == OK:
-                    _paged_scratch[(dev, raw)] = scratch
+                kept = torch.empty(_call_on(dev, lib.fa_paged_scratch_bytes, c, a) or 16, dtype=torch.uint8,
+                                   device=q.device)
+                st = _call_on(dev, lib.fa_fwd_paged, c, a, m, sc, kept.data_ptr(), kept.numel(), ws.tensor.data_ptr(), raw)
+                if st == OK and kept.numel() <= _PAGED_KEEP:
+                    _paged_scratch[(dev, raw)] = kept
     if stream is not None:
         for t in made:
             t.record_stream(stream)
