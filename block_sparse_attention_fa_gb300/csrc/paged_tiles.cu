@@ -101,6 +101,15 @@ __device__ __forceinline__ void exp2_pair(float& p0, float& p1, float x0, float 
     p1 = ex2_approx(a1);
 }
 
+// 16 bytes from global into shared memory, without passing registers; zeros
+// where `there` does not hold.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16u : 0u) : "memory");
+}
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
 // Eight words; `wide`: to a 32-byte boundary (16 otherwise).
 __device__ __forceinline__ void store8(void* dst, const uint32_t* w, bool wide) {
     if (wide) {
@@ -117,10 +126,12 @@ __device__ __forceinline__ void store8(void* dst, const uint32_t* w, bool wide) 
 struct TileSeg {
     int b, h, row0, rows, q0, n, kv;
     int jlo, jhi, i0, i1;          // keys of this kernel's part, positions of the unit's rows
-    int tiles, k0, k1, count;
+    int tiles, k0, k1, t;          // t: where the part begins in the line
     Hull hull;
     __device__ __forceinline__ bool begins() const { return k0 == 0; }
     __device__ __forceinline__ bool ends() const { return k1 == tiles; }
+    // CTAs that share the unit, from this part on (per: tiles of a CTA)
+    __device__ __forceinline__ int count(int per) const { return (t - k0 + tiles - 1) / per - t / per + 1; }
 };
 
 struct TileLine {
@@ -179,8 +190,7 @@ __device__ __forceinline__ bool next_seg(const PagedParams& p, TileLine& ln, Til
     s.h = off / s.tiles;
     s.k0 = off - s.h * s.tiles;
     s.k1 = min(s.tiles, s.k0 + (ln.t1 - ln.t));
-    const int last = ln.t - s.k0 + s.tiles - 1;
-    s.count = last / ln.per - ln.t / ln.per + 1;
+    s.t = ln.t;
     ln.t += s.k1 - s.k0;
     return true;
 }
@@ -306,7 +316,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         uint32_t g = 0;
         int last_k = -1, last_v = -1;
         bool ok = true;
-        TileSeg s;
+        TileSeg s{};
         // the copies of one tile of K or V: `id` the lane's page, `row` its
         // first row within the page
         auto load = [&](const CUtensorMap* tm, uint32_t base, int full, int empty, uint32_t gg, int id, int row,
@@ -476,7 +486,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         TileSeg s;
         while (ok && next_seg(p, line, s)) {
             if (s.begins() && !s.ends()) {
-                meta.count = s.count;
+                meta.count = s.count(line.per);
                 meta.q0 = s.q0;
                 meta.row0 = s.row0;
                 meta.rows = s.rows;
@@ -507,20 +517,14 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                 const long long mine = valid ? (long long)trow * p.qs[0] + (long long)hq * p.qs[1] : -1;
                 const int c = lane % kLanes;
                 uint8_t* const tile = smem + L::kQ + t * L::kTile + (c >> 3) * 16384;
-#pragma unroll
-                for (int b0 = 0; b0 < kLanes; b0 += 8) {
-                    uint4 w[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const long long at = __shfl_sync(0xffffffffu, mine, (b0 + e) * kPer + lane / kLanes);
-                        w[e] = at >= 0 ? __ldg(reinterpret_cast<const uint4*>(p.q + at) + c) : make_uint4(0u, 0u, 0u, 0u);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int rr = wq * 32 + (b0 + e) * kPer + lane / kLanes;
-                        *reinterpret_cast<uint4*>(tile + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = w[e];
-                    }
+#pragma unroll 4
+                for (int e = 0; e < kLanes; ++e) {
+                    const long long at = __shfl_sync(0xffffffffu, mine, e * kPer + lane / kLanes);
+                    const int rr = wq * 32 + e * kPer + lane / kLanes;
+                    // (rows without a query are filled with zeros)
+                    copy16(smem_addr(tile + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)), p.q + (at >= 0 ? at + 8 * c : 0), at >= 0);
                 }
+                copies_wait();
                 fence_async_shared();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(T_Q_FULL + t));
@@ -684,7 +688,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                 } else {
                     (whole ? p.parts.row_ml : p.parts.slot_ml)[at] = make_float2(m_use, l);
                     if (p.join_rows && !p.prefix && s.begins())
-                        p.rowdesc[row] = whole ? make_int2(-1, 1) : make_int2(static_cast<int>(at), s.count);
+                        p.rowdesc[row] = whole ? make_int2(-1, 1) : make_int2(static_cast<int>(at), s.count(line.per));
                 }
             }
             tc_fence_before();
