@@ -65,10 +65,25 @@ enum TBar {
     T_O_DONE = T_P_FULL + 4,                     // two
     T_O_UPD = T_O_DONE + 2,                      // two
     T_DRAIN = T_O_UPD + 2,                       // two
-    T_COUNT = T_DRAIN + 2
+    T_SEG_FULL = T_DRAIN + 2,                    // two slots
+    T_SEG_EMPTY = T_SEG_FULL + 2,
+    T_COUNT = T_SEG_EMPTY + 2
 };
+constexpr uint32_t kSegReaders = 11;             // the MMA, clearing and softmax warps
 enum TSite : uint32_t { S_T_Q = 80, S_T_K_FULL, S_T_K_EMPTY, S_T_V_FULL, S_T_V_EMPTY, S_T_V_OK, S_T_S, S_T_P, S_T_O,
-                        S_T_UPD, S_T_DRAIN };
+                        S_T_UPD, S_T_DRAIN, S_T_SEG, S_T_SEG_EMPTY };
+
+// The part of a unit in a CTA's stretch.
+struct TileSeg {
+    int b, h, row0, rows, q0, n, kv;
+    int jlo, jhi, i0, i1;          // keys of this kernel's part, positions of the unit's rows
+    int tiles, k0, k1, t;          // t: where the part begins in the line
+    Hull hull;
+    __device__ __forceinline__ bool begins() const { return k0 == 0; }
+    __device__ __forceinline__ bool ends() const { return k1 == tiles; }
+    // CTAs that share the unit, from this part on (per: tiles of a CTA)
+    __device__ __forceinline__ int count(int per) const { return (t - k0 + tiles - 1) / per - t / per + 1; }
+};
 
 template <int D>
 struct TileLayout {
@@ -81,7 +96,8 @@ struct TileLayout {
     static constexpr uint32_t kTmemSlot = kBars + 8 * T_COUNT;
     static constexpr uint32_t kAbort = kTmemSlot + 4;
     static constexpr uint32_t kMinMax = kAbort + 4;          // positions of the batch (shared prefix)
-    static constexpr uint32_t kScan = kMinMax + 8;
+    static constexpr uint32_t kSeg = kMinMax + 8;            // two units
+    static constexpr uint32_t kScan = kSeg + 2 * sizeof(TileSeg);
     static constexpr uint32_t kPre = kScan + 4 * (kThreadsT / 32);   // TileLine's arrays
     static constexpr uint32_t bytes(int B) { return kPre + 4u * (3u * B + 2u) + 1024u; }
     static_assert(kStages <= kMaxRing, "ring");
@@ -122,17 +138,9 @@ __device__ __forceinline__ void store8(void* dst, const uint32_t* w, bool wide) 
     }
 }
 
-// The part of a unit in a CTA's stretch.
-struct TileSeg {
-    int b, h, row0, rows, q0, n, kv;
-    int jlo, jhi, i0, i1;          // keys of this kernel's part, positions of the unit's rows
-    int tiles, k0, k1, t;          // t: where the part begins in the line
-    Hull hull;
-    __device__ __forceinline__ bool begins() const { return k0 == 0; }
-    __device__ __forceinline__ bool ends() const { return k1 == tiles; }
-    // CTAs that share the unit, from this part on (per: tiles of a CTA)
-    __device__ __forceinline__ int count(int per) const { return (t - k0 + tiles - 1) / per - t / per + 1; }
-};
+// Bits a .. 31, and bits 0 .. a, of a word (any a).
+__device__ __forceinline__ uint32_t bits_from(int a) { return a <= 0 ? 0xffffffffu : a > 31 ? 0u : 0xffffffffu << a; }
+__device__ __forceinline__ uint32_t bits_to(int a) { return a < 0 ? 0u : a >= 31 ? 0xffffffffu : 0xffffffffu >> (31 - a); }
 
 struct TileLine {
     const int *pre, *kv, *q0;           // [B + 1] first tile, [B] length, [B + 1] first row
@@ -221,6 +229,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
             if (k >= T_P_FULL && k < T_P_FULL + 4) cnt = 4;
             if (k >= T_K_EMPTY && k < T_K_EMPTY + kMaxRing) cnt = 2;      // both MMA warps
             if (k >= T_V_EMPTY && k < T_V_EMPTY + kMaxRing) cnt = 2;
+            if (k >= T_SEG_EMPTY && k < T_SEG_EMPTY + 2) cnt = kSegReaders;
             mbar_init(bar(k), cnt);
         }
         *abort_flag = 0;
@@ -300,6 +309,20 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         line.start = p.c.Hkv * pre[lo];
     }
 
+    // Only the loader walks the line; it passes each unit through a two-slot
+    // queue (rows = 0: none left).  take(): the warp's next unit.
+    TileSeg* const seg_s = reinterpret_cast<TileSeg*>(smem + L::kSeg);
+    uint32_t nu = 0;
+    auto take = [&](TileSeg& s) -> bool {
+        const uint32_t slot = nu & 1;
+        if (!mbar_wait_warp(bar(T_SEG_FULL + slot), (nu >> 1) & 1, wc, S_T_SEG)) return false;
+        s = seg_s[slot];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(T_SEG_EMPTY + slot));
+        ++nu;
+        return s.rows > 0;
+    };
+
     // Barrier phases run on counters that every role keeps alike: g counts
     // steps (ring stage g % ST), uq units in which row tile t has rows, n the
     // steps of tile t.
@@ -334,7 +357,16 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
             }
             return true;
         };
-        while (ok && next_seg(p, line, s)) {
+        while (ok) {
+            if (nu >= 2 && !mbar_wait_warp(bar(T_SEG_EMPTY + (nu & 1)), ((nu >> 1) - 1) & 1, wc, S_T_SEG_EMPTY)) break;
+            const bool more = next_seg(p, line, s);
+            if (lane == 0) {
+                if (!more) s.rows = 0;
+                seg_s[nu & 1] = s;
+                mbar_arrive(bar(T_SEG_FULL + (nu & 1)));
+            }
+            ++nu;
+            if (!more) break;
             const int32_t* table = p.c.page_table + (size_t)s.b * p.c.max_pages;
             int page = tile_page<kBlock>(p.c, table, s.hull, s.hull.tile(s.k0), lane, s.b, p.ws);
             int id_v = -1, row_v = 0;
@@ -374,7 +406,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         uint32_t g = 0;
         bool ok = true;
         TileSeg s;
-        while (ok && next_seg(p, line, s)) {
+        while (ok && take(s)) {
             for (int k = s.k0; k < s.k1; ++k, ++g) {
                 const uint32_t st = g % ST;
                 const int c0 = s.hull.tile(k) * kBlock;
@@ -422,7 +454,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         uint32_t g = 0, uq = 0, np = 0;
         bool ok = true;
         TileSeg s;
-        while (ok && next_seg(p, line, s)) {
+        while (ok && take(s)) {
             const bool active = s.rows > 128 * t;
             const int steps = s.k1 - s.k0;
             // pass k: O += P V(k - 1), then S = Q K(k) into the buffer which
@@ -484,7 +516,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         bool ok = true;
         PagedMeta meta{};
         TileSeg s;
-        while (ok && next_seg(p, line, s)) {
+        while (ok && take(s)) {
             if (s.begins() && !s.ends()) {
                 meta.count = s.count(line.per);
                 meta.q0 = s.q0;
@@ -583,16 +615,15 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                         }
                     }
                     if (!open) {
-                        const int jl = s.jlo - ch, hi = vhi - ch, lo = vlo - ch, ns = p.mask.sinks - ch;
-                        const float off = -CUDART_INF_F;
-                        const bool clip_lo = __any_sync(0xffffffffu, jl > 0 || (lo > 0 && ns < 64));
-                        const bool clip_hi = __any_sync(0xffffffffu, hi < 63);
-                        if (clip_lo) {
+                        // the row's visible columns as bits: [jlo, vhi] within
+                        // the window or the sinks
 #pragma unroll
-                            for (int e = 0; e < 64; ++e) x[e] = (e >= jl && e <= hi && (e >= lo || e < ns)) ? x[e] : off;
-                        } else if (clip_hi) {
+                        for (int c = 0; c < 2; ++c) {
+                            const int c0 = ch + 32 * c;
+                            const uint32_t see = bits_from(s.jlo - c0) & bits_to(vhi - c0) &
+                                                 (bits_from(vlo - c0) | bits_to(p.mask.sinks - 1 - c0));
 #pragma unroll
-                            for (int e = 0; e < 64; ++e) x[e] = e <= hi ? x[e] : off;
+                            for (int e = 0; e < 32; ++e) x[32 * c + e] = (see >> e) & 1u ? x[32 * c + e] : -CUDART_INF_F;
                         }
                     }
                     float m4[4] = {x[0], x[1], x[2], x[3]};
