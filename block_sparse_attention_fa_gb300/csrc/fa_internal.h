@@ -191,7 +191,6 @@ struct PagedParams {
     int prefix;           // 1: this kernel attends to the shared prefix, 0: to the sequences' own keys
     int join_rows;        // 1: every unit leaves partials, joined row by row with the prefix's
     int ctas;             // CTAs that share the work
-    int min_tiles;        // least tiles per CTA
     float scale;
     ScoreParams score;
     const uint16_t* q;

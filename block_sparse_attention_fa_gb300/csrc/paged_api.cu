@@ -263,7 +263,6 @@ fa_status fa_fwd_paged(const fa_paged_kv* c, const fa_paged_fwd_args* a, const f
     p.shared = a->shared_len;
     p.join_rows = a->shared_len > 0;
     p.ctas = own_ctas(c, a);
-    p.min_tiles = 1;
     p.scale = a->scale > 0.f ? a->scale : 1.0f / std::sqrt((float)c->D);
     p.score = {score.kind, score.softcap, score.alibi_slopes, score.rel_bias, score.rel_max};
     p.q = static_cast<const uint16_t*>(a->q);

@@ -203,6 +203,26 @@ __device__ __forceinline__ bool next_seg(const PagedParams& p, TileLine& ln, Til
     return true;
 }
 
+// Rows r0 .. r0 + 31 of a unit's Q into their row tile at `tile` (128-byte
+// swizzled, zeros past the unit's rows), D / 8 lanes to a row, so that whole
+// lines are read.
+template <int D>
+__device__ __forceinline__ void load_rows(const PagedParams& p, const TileSeg& s, int r0, uint32_t tile, int lane) {
+    constexpr int kLanes = D / 8, kPer = 32 / kLanes;      // lanes per row, rows per copy
+    const int ur = r0 + lane, R = s.row0 + min(ur, s.rows - 1), tok = quotient(R, p.by_group);
+    const long long mine = ur < s.rows ? (long long)(s.q0 + tok) * p.qs[0] +
+                                             (long long)(s.h * p.group + R - tok * p.group) * p.qs[1]
+                                       : -1;
+    const int c = lane % kLanes;
+    tile += (c >> 3) * 16384u;
+#pragma unroll 4
+    for (int e = 0; e < kLanes; ++e) {
+        const long long at = __shfl_sync(0xffffffffu, mine, e * kPer + lane / kLanes);
+        const int rr = (r0 & 127) + e * kPer + lane / kLanes;
+        copy16(tile + rr * 128 + (((c & 7) ^ (rr & 7)) << 4), p.q + (at >= 0 ? at + 8 * c : 0), at >= 0);
+    }
+}
+
 template <int D, int SCORE>
 __global__ void __launch_bounds__(kThreadsT, 1)
 paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -291,7 +311,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         });
         total = p.c.Hkv * pre[p.c.B];
     }
-    line.per = max((total + p.ctas - 1) / p.ctas, p.min_tiles);
+    line.per = max((total + p.ctas - 1) / p.ctas, 1);
     line.t = (int)min((long long)cta * line.per, (long long)total);
     line.t1 = (int)min((long long)line.t + line.per, (long long)total);
     if (p.prefix) {
@@ -515,8 +535,79 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         uint32_t n = 0, uq = 0;
         bool ok = true;
         PagedMeta meta{};
-        TileSeg s;
-        while (ok && take(s)) {
+        // The warp's 32 rows of a unit's Q.  The unit before has no use for
+        // that buffer any more once its last S is there, so that the copies of
+        // the next unit run while this one's O is written out (4 x 1024 new
+        // tokens up to 8192 keys: 196 us; brought at the unit's start, 203).
+        auto bring = [&](const TileSeg& u) {
+            if (u.rows > 128 * t) load_rows<D>(p, u, 128 * t + 32 * wq, sbase + L::kQ + t * L::kTile, lane);
+        };
+        auto announce = [&](const TileSeg& u) {
+            if (u.rows <= 128 * t) return;
+            copies_wait();
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(T_Q_FULL + t));
+        };
+        // One pass: the next unit's Q sets out, the current unit's O is written
+        // out, the next unit's tiles.
+        TileSeg s{}, next{};
+        bool have = take(next), done = false;      // done: s has an O to write out
+        bool valid = false;
+        int ur = 0, hq = 0, trow = 0;
+        float m_use = -CUDART_INF_F, l = 0.f;
+        for (;;) {
+            if (have) bring(next);
+            if (done) {
+                // the unit's end in this CTA: O / l and lse, or a partial
+                if (!mbar_wait_warp(bar(T_O_DONE + t), uq & 1, wc, S_T_O)) { ok = false; break; }
+                tc_fence_after();
+                ++uq;
+                const bool whole = s.begins() && s.ends(), last = whole && !p.join_rows;
+                const long long row = (long long)trow * p.Hq + hq;
+                const long long at = whole ? row : (2LL * cta + (s.begins() ? 1 : 0)) * kPagedTileRows + ur;
+                const bool f32 = !last || out32;
+                uint8_t* const dst = static_cast<uint8_t*>(last ? p.o : static_cast<void*>(whole ? p.parts.row_o : p.parts.slot_o)) +
+                                     at * (D * (f32 ? 4 : 2));
+                const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31u) == 0;
+                const float inv = !last ? 1.f : l == 0.f ? 0.f : 1.f / l;
+                // Straight from the registers, 32 bytes (a sector) per store: a
+                // partial is 128 KB of fp32 per CTA at 128 columns, and their
+                // writing (3 us when all CTAs end together) is what the end of
+                // the kernel waits for.
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    tmem_ld32(tO + 32u * c, o);
+                    if (!valid) {
+                    } else if (f32) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) store8(dst + 128 * c + 4 * e, o + e, wide);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            o[e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+#pragma unroll
+                        for (int e = 0; e < 16; e += 8) store8(dst + 64 * c + 4 * e, o + e, wide);
+                    }
+                    __syncwarp();                      // together again for the next load
+                }
+                if (valid) {
+                    if (last) {
+                        p.lse[row] = l == 0.f ? -CUDART_INF_F : (m_use + log2f(l)) * kLn2Q;
+                    } else {
+                        (whole ? p.parts.row_ml : p.parts.slot_ml)[at] = make_float2(m_use, l);
+                        if (p.join_rows && !p.prefix && s.begins())
+                            p.rowdesc[row] = whole ? make_int2(-1, 1) : make_int2(static_cast<int>(at), s.count(line.per));
+                    }
+                }
+                tc_fence_before();
+            }
+            if (!have) break;
+            announce(next);
+            s = next;
             if (s.begins() && !s.ends()) {
                 meta.count = s.count(line.per);
                 meta.q0 = s.q0;
@@ -524,206 +615,146 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                 meta.rows = s.rows;
                 meta.h = s.h;
             }
-            if (s.rows <= 128 * t) continue;
-            // this thread's row: token, query head, position
-            const int ur = 128 * t + r;
-            const bool valid = ur < s.rows;
-            const int R = s.row0 + min(ur, s.rows - 1), tok = quotient(R, p.by_group);
-            const int hq = s.h * p.group + R - tok * p.group, trow = s.q0 + tok;
-            int i = s.kv - s.n + tok;
-            if (p.prefix) {
-                int lo = 0, hi = p.c.B - 1;        // the first sequence that ends behind the row
-                while (lo < hi) {
-                    const int mid = (lo + hi) >> 1;
-                    if (q0_s[mid + 1] <= trow) lo = mid + 1; else hi = mid;
+            done = s.rows > 128 * t;
+            if (done) {
+                // this thread's row: token, query head, position
+                ur = 128 * t + r;
+                valid = ur < s.rows;
+                const int R = s.row0 + min(ur, s.rows - 1), tok = quotient(R, p.by_group);
+                hq = s.h * p.group + R - tok * p.group;
+                trow = s.q0 + tok;
+                int i = s.kv - s.n + tok;
+                if (p.prefix) {
+                    int lo = 0, hi = p.c.B - 1;        // the first sequence that ends behind the row
+                    while (lo < hi) {
+                        const int mid = (lo + hi) >> 1;
+                        if (q0_s[mid + 1] <= trow) lo = mid + 1; else hi = mid;
+                    }
+                    i = max(len_s[lo] - q0_s[lo + 1] + trow, -1);
                 }
-                i = max(len_s[lo] - q0_s[lo + 1] + trow, -1);
-            }
-            // The warp's 32 rows of Q, D / 8 lanes to a row, so that whole lines
-            // are read (a row per lane asks for 16-byte pieces of 32 lines, 5 us
-            // for the tile; there is hardly an L1 beside this much shared
-            // memory).  The previous unit's products have read theirs: this
-            // warp has seen their S.
-            {
-                constexpr int kLanes = D / 8, kPer = 32 / kLanes;     // lanes per row, rows per load
-                const long long mine = valid ? (long long)trow * p.qs[0] + (long long)hq * p.qs[1] : -1;
-                const int c = lane % kLanes;
-                uint8_t* const tile = smem + L::kQ + t * L::kTile + (c >> 3) * 16384;
-#pragma unroll 4
-                for (int e = 0; e < kLanes; ++e) {
-                    const long long at = __shfl_sync(0xffffffffu, mine, e * kPer + lane / kLanes);
-                    const int rr = wq * 32 + e * kPer + lane / kLanes;
-                    // (rows without a query are filled with zeros)
-                    copy16(smem_addr(tile + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)), p.q + (at >= 0 ? at + 8 * c : 0), at >= 0);
-                }
-                copies_wait();
-                fence_async_shared();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(T_Q_FULL + t));
-            }
-            float slope = 0.f;
-            if (SCORE == FA_SCORE_ALIBI) slope = __ldg(p.score.slopes + hq) * kLog2eQ;
-            if (SCORE == FA_SCORE_ALIBI_SOFTCAP) slope = __ldg(p.score.slopes + hq);
-            const float* rb = nullptr;
-            if (SCORE == FA_SCORE_REL_BIAS) rb = p.score.rel_bias + (size_t)hq * (2 * p.score.rel_max + 1);
-            // the row's keys: [vlo, vhi] and the sinks from jlo on
-            const int vhi = p.mask.causal ? min(s.jhi - 1, i) : s.jhi - 1;
-            const int vlo = p.mask.window >= 0 ? max(s.jlo, i - p.mask.window) : s.jlo;
+                float slope = 0.f;
+                if (SCORE == FA_SCORE_ALIBI) slope = __ldg(p.score.slopes + hq) * kLog2eQ;
+                if (SCORE == FA_SCORE_ALIBI_SOFTCAP) slope = __ldg(p.score.slopes + hq);
+                const float* rb = nullptr;
+                if (SCORE == FA_SCORE_REL_BIAS) rb = p.score.rel_bias + (size_t)hq * (2 * p.score.rel_max + 1);
+                // the row's keys: [vlo, vhi] and the sinks from jlo on
+                const int vhi = p.mask.causal ? min(s.jhi - 1, i) : s.jhi - 1;
+                const int vlo = p.mask.window >= 0 ? max(s.jlo, i - p.mask.window) : s.jlo;
 
-            float m_use = -CUDART_INF_F, l = 0.f;
-            for (int k = s.k0; ok && k < s.k1; ++k, ++n) {
-                const int kb = s.hull.tile(k);
-                const bool open = tile_open(p.mask, kb, s.i0, s.i1, s.jlo, s.jhi, 7);
+                m_use = -CUDART_INF_F;
+                l = 0.f;
+                for (int k = s.k0; ok && k < s.k1; ++k, ++n) {
+                    const int kb = s.hull.tile(k);
+                    const bool open = tile_open(p.mask, kb, s.i0, s.i1, s.jlo, s.jhi, 7);
 #pragma unroll 1
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t tSh = tS + 64u * h;
-                    const int ch = kb * kBlock + 64 * h;
-                    if (!mbar_wait_warp(bar(T_S_FULL + 2 * t + h), n & 1, wc, S_T_S)) { ok = false; break; }
-                    tc_fence_after();
-                    float x[64];
-                    {
-                        uint32_t raw[64];
-                        tmem_ld64(tSh, raw);
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t tSh = tS + 64u * h;
+                        const int ch = kb * kBlock + 64 * h;
+                        if (!mbar_wait_warp(bar(T_S_FULL + 2 * t + h), n & 1, wc, S_T_S)) { ok = false; break; }
+                        tc_fence_after();
+                        float x[64];
+                        {
+                            uint32_t raw[64];
+                            tmem_ld64(tSh, raw);
 #pragma unroll
-                        for (int e = 0; e < 64; ++e) x[e] = __uint_as_float(raw[e]);
-                    }
-                    // score_mod: x stays the raw q.k without one, and is the
-                    // modified score in base 2 otherwise
-                    float sc = 1.f;
-                    if (SCORE == FA_SCORE_NONE) sc = sl2;
-                    if (SCORE == FA_SCORE_SOFTCAP) {
-#pragma unroll
-                        for (int e = 0; e < 64; ++e) x[e] = softcap2(x[e] * cap_in, cap_out);
-                    }
-                    if (SCORE == FA_SCORE_ALIBI) {
-                        const float di = static_cast<float>(i - ch);
-#pragma unroll
-                        for (int e = 0; e < 64; ++e)
-                            x[e] = fmaf(-slope, fabsf(di - static_cast<float>(e)), x[e] * sl2);
-                    }
-                    if (SCORE == FA_SCORE_ALIBI_SOFTCAP) {
-                        const float di = static_cast<float>(i - ch);
-#pragma unroll
-                        for (int e = 0; e < 64; ++e)
-                            x[e] = softcap2(fmaf(-slope, fabsf(di - static_cast<float>(e)), x[e] * p.scale) * cap_in, cap_out);
-                    }
-                    if (SCORE == FA_SCORE_REL_BIAS) {
-#pragma unroll
-                        for (int e = 0; e < 64; ++e) {
-                            const int rr = min(max(i - ch - e, -p.score.rel_max), p.score.rel_max);
-                            x[e] = fmaf(__ldg(rb + rr + p.score.rel_max), kLog2eQ, x[e] * sl2);
+                            for (int e = 0; e < 64; ++e) x[e] = __uint_as_float(raw[e]);
                         }
-                    }
-                    if (!open) {
-                        // the row's visible columns as bits: [jlo, vhi] within
-                        // the window or the sinks
+                        // score_mod: x stays the raw q.k without one, and is the
+                        // modified score in base 2 otherwise
+                        float sc = 1.f;
+                        if (SCORE == FA_SCORE_NONE) sc = sl2;
+                        if (SCORE == FA_SCORE_SOFTCAP) {
+#pragma unroll
+                            for (int e = 0; e < 64; ++e) x[e] = softcap2(x[e] * cap_in, cap_out);
+                        }
+                        if (SCORE == FA_SCORE_ALIBI) {
+                            const float di = static_cast<float>(i - ch);
+#pragma unroll
+                            for (int e = 0; e < 64; ++e)
+                                x[e] = fmaf(-slope, fabsf(di - static_cast<float>(e)), x[e] * sl2);
+                        }
+                        if (SCORE == FA_SCORE_ALIBI_SOFTCAP) {
+                            const float di = static_cast<float>(i - ch);
+#pragma unroll
+                            for (int e = 0; e < 64; ++e)
+                                x[e] = softcap2(fmaf(-slope, fabsf(di - static_cast<float>(e)), x[e] * p.scale) * cap_in, cap_out);
+                        }
+                        if (SCORE == FA_SCORE_REL_BIAS) {
+#pragma unroll
+                            for (int e = 0; e < 64; ++e) {
+                                const int rr = min(max(i - ch - e, -p.score.rel_max), p.score.rel_max);
+                                x[e] = fmaf(__ldg(rb + rr + p.score.rel_max), kLog2eQ, x[e] * sl2);
+                            }
+                        }
+                        if (!open) {
+                            // the row's visible columns as bits: [jlo, vhi] within
+                            // the window or the sinks
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                const int c0 = ch + 32 * c;
+                                const uint32_t see = bits_from(s.jlo - c0) & bits_to(vhi - c0) &
+                                                     (bits_from(vlo - c0) | bits_to(p.mask.sinks - 1 - c0));
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) x[32 * c + e] = (see >> e) & 1u ? x[32 * c + e] : -CUDART_INF_F;
+                            }
+                        }
+                        float m4[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+                        for (int e = 4; e < 60; e += 8) {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) m4[q] = fmax3(m4[q], x[e + q], x[e + 4 + q]);
+                        }
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) m4[q] = fmaxf(m4[q], x[60 + q]);
+                        const float mx = fmax3(fmaxf(m4[0], m4[1]), m4[2], m4[3]) * sc;
+                        const float m_new = fmaxf(m_use, mx);
+                        const bool unset = m_use == -CUDART_INF_F;
+                        const bool need = !unset && m_new > m_use + lazy;
+                        const float alpha = need ? ex2_approx(m_use - m_new) : 1.f;
+                        if (need) l *= alpha;
+                        if (unset || need) m_use = m_new;
+                        const float nm = m_use == -CUDART_INF_F ? 0.f : -m_use;
+                        float rs[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
-                            const int c0 = ch + 32 * c;
-                            const uint32_t see = bits_from(s.jlo - c0) & bits_to(vhi - c0) &
-                                                 (bits_from(vlo - c0) | bits_to(p.mask.sinks - 1 - c0));
+                            uint32_t pk[16];
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) x[32 * c + e] = (see >> e) & 1u ? x[32 * c + e] : -CUDART_INF_F;
+                            for (int e = 0; e < 16; ++e) {
+                                float p0, p1;
+                                exp2_pair(p0, p1, x[32 * c + 2 * e], x[32 * c + 2 * e + 1], sc, nm);
+                                const int a2 = (e & 1) * 2;
+                                fadd2(rs[a2], rs[a2 + 1], rs[a2], rs[a2 + 1], p0, p1);
+                                pk[e] = pack_bf16x2(p0, p1);
+                            }
+                            tmem_st16_nowait(tSh + 16u * c, pk);
                         }
-                    }
-                    float m4[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-                    for (int e = 4; e < 60; e += 8) {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) m4[q] = fmax3(m4[q], x[e + q], x[e + 4 + q]);
-                    }
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) m4[q] = fmaxf(m4[q], x[60 + q]);
-                    const float mx = fmax3(fmaxf(m4[0], m4[1]), m4[2], m4[3]) * sc;
-                    const float m_new = fmaxf(m_use, mx);
-                    const bool unset = m_use == -CUDART_INF_F;
-                    const bool need = !unset && m_new > m_use + lazy;
-                    const float alpha = need ? ex2_approx(m_use - m_new) : 1.f;
-                    if (need) l *= alpha;
-                    if (unset || need) m_use = m_new;
-                    const float nm = m_use == -CUDART_INF_F ? 0.f : -m_use;
-                    float rs[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        uint32_t pk[16];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            float p0, p1;
-                            exp2_pair(p0, p1, x[32 * c + 2 * e], x[32 * c + 2 * e + 1], sc, nm);
-                            const int a2 = (e & 1) * 2;
-                            fadd2(rs[a2], rs[a2 + 1], rs[a2], rs[a2 + 1], p0, p1);
-                            pk[e] = pack_bf16x2(p0, p1);
-                        }
-                        tmem_st16_nowait(tSh + 16u * c, pk);
-                    }
-                    l += (rs[0] + rs[1]) + (rs[2] + rs[3]);
-                    // O holds the products of the unit's earlier halves; wait
-                    // for the last of them and scale
-                    if (__any_sync(0xffffffffu, need)) {
-                        const uint32_t prev = 2 * n + h - 1;
-                        if (!mbar_wait_warp(bar(T_O_UPD + t), prev & 1, wc, S_T_UPD)) { ok = false; break; }
-                        tc_fence_after();
+                        l += (rs[0] + rs[1]) + (rs[2] + rs[3]);
+                        // O holds the products of the unit's earlier halves; wait
+                        // for the last of them and scale
+                        if (__any_sync(0xffffffffu, need)) {
+                            const uint32_t prev = 2 * n + h - 1;
+                            if (!mbar_wait_warp(bar(T_O_UPD + t), prev & 1, wc, S_T_UPD)) { ok = false; break; }
+                            tc_fence_after();
 #pragma unroll 1
-                        for (int c = 0; c < D / 32; ++c) {
-                            uint32_t o[32];
-                            tmem_ld32(tO + 32u * c, o);
+                            for (int c = 0; c < D / 32; ++c) {
+                                uint32_t o[32];
+                                tmem_ld32(tO + 32u * c, o);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                            tmem_st32_nowait(tO + 32u * c, o);
+                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                                tmem_st32_nowait(tO + 32u * c, o);
+                            }
                         }
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(T_P_FULL + 2 * t + h));
                     }
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(T_P_FULL + 2 * t + h));
                 }
+                if (!ok) break;
             }
-            if (!ok) break;
-
-            // the unit's end in this CTA: O / l and lse, or a partial
-            if (!mbar_wait_warp(bar(T_O_DONE + t), uq & 1, wc, S_T_O)) { ok = false; break; }
-            tc_fence_after();
-            ++uq;
-            const bool whole = s.begins() && s.ends(), last = whole && !p.join_rows;
-            const long long row = (long long)trow * p.Hq + hq;
-            const long long at = whole ? row : (2LL * cta + (s.begins() ? 1 : 0)) * kPagedTileRows + ur;
-            const bool f32 = !last || out32;
-            uint8_t* const dst = static_cast<uint8_t*>(last ? p.o : static_cast<void*>(whole ? p.parts.row_o : p.parts.slot_o)) +
-                                 at * (D * (f32 ? 4 : 2));
-            const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31u) == 0;
-            const float inv = !last ? 1.f : l == 0.f ? 0.f : 1.f / l;
-            // Straight from the registers, 32 bytes (a sector) per store: through
-            // shared memory, for whole lines, it took 2.5 us instead of STORE_US.
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-                uint32_t o[32];
-                tmem_ld32(tO + 32u * c, o);
-                if (!valid) {
-                } else if (f32) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8) store8(dst + 128 * c + 4 * e, o + e, wide);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        o[e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-#pragma unroll
-                    for (int e = 0; e < 16; e += 8) store8(dst + 64 * c + 4 * e, o + e, wide);
-                }
-                __syncwarp();                      // together again for the next load
-            }
-            if (valid) {
-                if (last) {
-                    p.lse[row] = l == 0.f ? -CUDART_INF_F : (m_use + log2f(l)) * kLn2Q;
-                } else {
-                    (whole ? p.parts.row_ml : p.parts.slot_ml)[at] = make_float2(m_use, l);
-                    if (p.join_rows && !p.prefix && s.begins())
-                        p.rowdesc[row] = whole ? make_int2(-1, 1) : make_int2(static_cast<int>(at), s.count(line.per));
-                }
-            }
-            tc_fence_before();
+            have = take(next);
         }
+        if (!ok) copies_wait();
         if (!p.join_rows && threadIdx.x == 0) p.meta[cta] = ok ? meta : PagedMeta{};
     }
     tc_fence_before();
