@@ -149,6 +149,23 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, 
         : "memory");
 }
 
+// Where a row's partials lie: `count` rows of a kernel's slots, from `first`
+// on: slots 2 c + 1, 2 (c + 1), 2 (c + 2), .. of `stride` rows each (or the
+// one partial that is kept by row).
+struct RowParts {
+    const float* o;
+    const float2* ml;
+    long long first;
+    int count, stride;
+    __host__ __device__ __forceinline__ long long at(int k) const {
+        return first + (k ? (2LL * k - 1) * stride : 0);
+    }
+    // whether all of them lie in `rows` rows
+    __host__ __device__ __forceinline__ bool within(long long rows) const {
+        return first >= 0 && count >= 1 && first < rows && at(count - 1) < rows;
+    }
+};
+
 // Orders this thread's earlier shared-memory writes before later accesses by
 // the async proxy (TMA copies, tcgen05 operands).
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }

@@ -163,11 +163,12 @@ fa_status fa_kv_append(const fa_paged_kv* c, const fa_kv_append_args* a, void* w
     if (a->Hq > 0) {
         if ((st = check_rows("q", a->q, a->q_stride)) != FA_OK) return st;
         if ((st = check_rows("q_out", a->q_out, a->q_out_stride)) != FA_OK) return st;
-        // an output row must not run into the next one
-        const int64_t hs = a->q_out_stride[1], ts = a->q_out_stride[0];
-        if ((a->Hq > 1 && hs < c->D) || (c->total_q > 1 && ts < c->D))
+        // an output row must not run into another: heads within tokens or
+        // tokens within heads
+        const int64_t hs = a->Hq > 1 ? a->q_out_stride[1] : c->D, ts = c->total_q > 1 ? a->q_out_stride[0] : c->D;
+        if ((double)(a->Hq - 1) * hs + c->D > ts && (double)(c->total_q - 1) * ts + c->D > hs)
             return fail(FA_ERR_INVALID_ARG, "q_out's strides (%lld, %lld) overlap its rows", (long long)ts, (long long)hs);
-        if (a->q_out == a->q && (ts != a->q_stride[0] || hs != a->q_stride[1]))
+        if (a->q_out == a->q && ((c->total_q > 1 && ts != a->q_stride[0]) || (a->Hq > 1 && hs != a->q_stride[1])))
             return fail(FA_ERR_INVALID_ARG, "q_out is q with other strides");
     }
     if (a->rot_dim > 0) {
@@ -177,6 +178,9 @@ fa_status fa_kv_append(const fa_paged_kv* c, const fa_kv_append_args* a, void* w
             return fail(FA_ERR_INVALID_ARG, "cos and sin must be 16-byte aligned");
     }
     if (!aligned(a->positions, 4)) return fail(FA_ERR_INVALID_ARG, "positions must be 4-byte aligned");
+    const uintptr_t kc = reinterpret_cast<uintptr_t>(c->k), vc = reinterpret_cast<uintptr_t>(c->v);
+    if ((double)(kc > vc ? kc - vc : vc - kc) < 2.0 * c->num_pages * c->Hkv * c->page_size * c->D)
+        return fail(FA_ERR_INVALID_ARG, "the cache's k and v overlap");
 
     fa::AppendParams p{};
     p.c = view(c);

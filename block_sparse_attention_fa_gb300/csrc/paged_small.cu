@@ -511,17 +511,6 @@ paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
     if (p.join_rows) pdl_wait_previous();
 }
 
-// Where a row's partials lie: `count` rows of a kernel's slots, from `first`
-// on: slots 2 c + 1, 2 (c + 1), 2 (c + 2), .. of `stride` rows each (or the
-// one partial that is kept by row).
-struct RowParts {
-    const float* o;
-    const float2* ml;
-    long long first;
-    int count, stride;
-    __device__ __forceinline__ long long at(int k) const { return first + (k ? (2LL * k - 1) * stride : 0); }
-};
-
 // Joins the partials of rows, the parts of `a` and then those of `b`:
 //   M = max m_k, L = sum 2^(m_k - M) l_k, O = sum 2^(m_k - M) O_k / L.
 // Eight lanes to a row, four rows to a warp.  What it costs is the loads'
@@ -658,6 +647,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_rows_kernel(const 
     if (ca == cb) a = RowParts{j.pre.row_o, j.pre.row_ml, row, 1, 0};
     RowParts own{p.parts.slot_o, p.parts.slot_ml, d.x, d.y, j.own_rows};
     if (d.x < 0) own = RowParts{p.parts.row_o, p.parts.row_ml, row, 1, 0};
+    // (a CTA whose wait ran out leaves its rows' places as the scratch held them)
+    if (d.x >= 0 && !own.within(2LL * p.ctas * j.own_rows)) own.count = 0;
     join_rows<D, true>(p, a, own, row, valid, sums);
 }
 

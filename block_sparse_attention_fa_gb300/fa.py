@@ -636,6 +636,18 @@ def _rows(name, t, total, H, D, dev):
     return ts if n > 1 else D, hs if h > 1 else D
 
 
+def _new(shape, dtype, device, stream):
+    """An output or scratch of a call on ``stream`` (None: the current one).  Memory of another stream is that
+    stream's: what the current one still does with the block's last tenant must not reach it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    now = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(now)                          # where the caller goes on with it
+    return t
+
+
 def _call_on(dev, fn, *args):
     """A paged call with its tensors' device current."""
     if dev == _device_now():
@@ -677,9 +689,7 @@ def kv_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, k_cac
         qs = _rows("q", q, total, None, D, dev)
         Hq, qp = q.shape[1], q.data_ptr()
         if q_out is None:
-            q_out = torch.empty((total, Hq, D), dtype=torch.bfloat16, device=q.device)
-            if stream is not None:
-                q_out.record_stream(stream)
+            q_out = _new((total, Hq, D), torch.bfloat16, q.device, stream)
         os_ = qs if q_out is q else _rows("q_out", q_out, total, Hq, D, dev)
         op = q_out.data_ptr()
     rot, rope_len, cp, sp, pp = 0, 0, 0, 0, 0
@@ -703,7 +713,7 @@ def kv_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, k_cac
                         *os_, cp, sp, pp)
     raw = _raw_stream(dev) if stream is None else stream.cuda_stream
     ws = workspace or _workspace_of(dev, raw)
-    st = load_library().fa_kv_append(c, a, ws.tensor.data_ptr(), raw)
+    st = _call_on(dev, load_library().fa_kv_append, c, a, ws.tensor.data_ptr(), raw)
     if st != OK:
         _check(st)
     return q_out
@@ -731,15 +741,12 @@ def fwd_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, pag
     c, _, D = _paged_kv(k_cache, v_cache, page_table, kv_len, q_start, total, dev)
     qs = _rows("q", q, total, None, D, dev)
     want = torch.float32 if out_fp32 else torch.bfloat16
-    made = []
     if out is None:
-        out = torch.empty((total, Hq, D), dtype=want, device=q.device)
-        made.append(out)
+        out = _new((total, Hq, D), want, q.device, stream)
     elif out.dtype is not want or out.get_device() != dev or not out.is_contiguous() or out.shape != q.shape:
         raise ValueError(f"out must be a contiguous {want} tensor of q's shape on q's device")
     if lse is None:
-        lse = torch.empty((total, Hq), dtype=torch.float32, device=q.device)
-        made.append(lse)
+        lse = _new((total, Hq), torch.float32, q.device, stream)
     elif lse.dtype is not torch.float32 or lse.get_device() != dev or not lse.is_contiguous() \
             or tuple(lse.shape) != (total, Hq):
         raise ValueError("lse must be a contiguous float32 tensor [tokens, Hq] on q's device")
@@ -771,8 +778,7 @@ def fwd_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, pag
                       ws.tensor.data_ptr(), raw)
     elif stream is not None or _capturing():
         # (no bytes: the arguments are wrong, and the call says how)
-        scratch = torch.empty(_call_on(dev, lib.fa_paged_scratch_bytes, c, a) or 16, dtype=torch.uint8, device=q.device)
-        made.append(scratch)
+        scratch = _new(_call_on(dev, lib.fa_paged_scratch_bytes, c, a) or 16, torch.uint8, q.device, stream)
         st = _call_on(dev, lib.fa_fwd_paged, c, a, m, sc, scratch.data_ptr(), scratch.numel(), ws.tensor.data_ptr(), raw)
     else:
         with _paged_lock:
@@ -785,9 +791,6 @@ def fwd_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, pag
                 st = _call_on(dev, lib.fa_fwd_paged, c, a, m, sc, kept.data_ptr(), kept.numel(), ws.tensor.data_ptr(), raw)
                 if st == OK and kept.numel() <= _PAGED_KEEP:
                     _paged_scratch[(dev, raw)] = kept
-    if stream is not None:
-        for t in made:
-            t.record_stream(stream)
     if st != OK:
         _check(st)
     return out, lse

@@ -315,12 +315,14 @@ fa_status fa_block_mask_build_cols(const fa_block_mask *bm, const fa_block_mask_
  *   dout      device bf16 [B][Hq][q_len][D].
  *   dq        device fp32 [B][Hq][q_len][D]; dk, dv device fp32
  *             [B][Hkv][kv_len][D] (summed over the query heads of each kv
- *             head).  All three are written in full.
+ *             head).  All three are written in full; under SINK_WINDOW dq
+ *             also holds partial dK and dV until the dQ kernel writes it.
  *   rowstats  device fp32 scratch of fa_bwd_rowstats_bytes() bytes: Delta and
  *             -lse log2(e) of every query row, padded to whole q-blocks.
  * bf16 tensors 16-byte aligned, dq, dk, dv 16-byte, lse 4-byte, rowstats
- * 16-byte.  Three kernel launches (row statistics, dK/dV, dQ), asynchronous on
- * `stream`; their pipeline waits are bounded and report through `workspace`
+ * 16-byte.  Three kernel launches (row statistics, dK/dV, dQ; under SINK_WINDOW
+ * a fourth that sums the sinks' partial dK and dV), asynchronous on `stream`;
+ * their pipeline waits are bounded and report through `workspace`
  * (fa_workspace_check).                                                     */
 typedef struct fa_bwd_args {
     int32_t B, Hq, Hkv, q_len, kv_len, D;

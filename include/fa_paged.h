@@ -52,7 +52,8 @@ extern "C" {
  * Keys and values past kv_len, outside every query's mask, or on pages that
  * no query sees may hold anything, NaN included.  A NaN or infinity among the
  * keys that some query of the sequence's step does see spreads as it does in
- * the products of the definition: 0 x NaN is NaN.                           */
+ * the products of the definition: 0 x NaN is NaN (in a shared prefix: that
+ * some query of the step's batch sees).                                      */
 typedef struct fa_paged_kv {
     int32_t B;
     int32_t Hkv;
@@ -79,6 +80,8 @@ typedef struct fa_paged_kv {
  *               aligned.  Slices of one fused projection are the usual case.
  *   q_out       device bf16, as q with its own strides; may be q itself (the
  *               same pointer and strides), but must not overlap it otherwise.
+ *               Its rows must not overlap: heads lie within the token stride,
+ *               or tokens within the head stride.
  *               Hq = 0: no queries (q and q_out are ignored).
  *   rot_dim     0 (no rotation: cos and sin are ignored) or a multiple of 16
  *               up to D.
@@ -87,7 +90,8 @@ typedef struct fa_paged_kv {
  *   positions   device int32 [total_q], or NULL for each token's place in its
  *               sequence.  Outside 0 .. rope_len - 1 the token is not written
  *               and the call is reported as above.
- * Two tokens must not have the same slot.  One kernel launch.               */
+ * The cache's k and v must not overlap, and two tokens must not have the same
+ * slot.  One kernel launch.                                                  */
 typedef struct fa_kv_append_args {
     int32_t Hq;
     int32_t rot_dim;

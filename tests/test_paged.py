@@ -128,6 +128,19 @@ def test_append_refusals(fa, kw, status):
     assert lib.fa_kv_append(ctypes.byref(c), None, ctypes.c_void_p(FAKE), None) == fa.ERR_INVALID_ARG
 
 
+def test_append_refuses_overlaps(fa):
+    lib, ws = fa.load_library(), ctypes.c_void_p(FAKE)
+    # tokens 1.. start on the heads of token 0, and heads 1.. on its tokens
+    for st in ((128, 128), (256, 128), (384, 128), (128, 384), (136, 128), (504, 128)):
+        a = _append(fa, q_out_stride=st, q_stride=st)
+        assert lib.fa_kv_append(ctypes.byref(_kv(fa)), ctypes.byref(a), ws, None) == fa.ERR_INVALID_ARG
+        assert b"overlap its rows" in lib.fa_last_error()
+    # 8 pages x 2 heads x 16 tokens x 128 columns of two bytes
+    for v in (FAKE, FAKE + 65536 - 16, FAKE - 65536 + 16):
+        assert lib.fa_kv_append(ctypes.byref(_kv(fa, v=v)), ctypes.byref(_append(fa)), ws, None) == fa.ERR_INVALID_ARG
+        assert b"k and v overlap" in lib.fa_last_error()
+
+
 def _fwd(fa, **kw):
     a = fa.PagedFwdArgs()
     a.Hq, a.max_q_len = 4, 4
@@ -760,6 +773,44 @@ def test_other_stream_and_repeatability(fa):
         again = fa.fwd_paged(q, *dev, max_q_len=1)
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
     compare(first, reference(bt, bt.queries(8), "causal", 0, 0))
+
+
+@gpu
+def test_outputs_on_another_stream_are_its_own(fa):
+    """What a call on another stream allocates is not memory that the current stream has just given back, and may
+    still be writing."""
+    bt = Batch([3] * 5, [40 + 9 * b for b in range(5)], 2, 64, 16)
+    kc, vc, table, kv, qs = bt.device()
+    q = torch.from_numpy(bt.queries(4)).cuda().to(torch.bfloat16)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for call in (lambda: fa.fwd_paged(q, kc, vc, table, kv, qs, max_q_len=3, stream=s),
+                 lambda: (fa.kv_append(q, q[:, :2], q[:, 2:], kc.clone(), vc.clone(), table, kv, qs, stream=s),)):
+        like = [torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")]
+        freed = {t.data_ptr() for t in like}
+        del like
+        s.wait_stream(torch.cuda.current_stream())
+        got = call()
+        assert not freed & {t.data_ptr() for t in got}
+        torch.cuda.current_stream().wait_stream(s)
+    want = fa.fwd_paged(q, kc, vc, table, kv, qs, max_q_len=3)
+    got = fa.fwd_paged(q, kc, vc, table, kv, qs, max_q_len=3, stream=s)
+    s.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@gpu
+def test_append_head_major_output(fa):
+    """q_out's tokens may lie within the head stride."""
+    bt = Batch([70, 3], [80, 3], 2, 64, 16)
+    kc, vc, table, kv, qs = bt.device()
+    q = torch.from_numpy(bt.queries(4)).cuda().to(torch.bfloat16)
+    angle = torch.rand(100, 32, device="cuda")
+    kw = dict(cos=angle.cos(), sin=angle.sin())
+    want = fa.kv_append(q, q[:, :2], q[:, 2:], kc, vc, table, kv, qs, **kw)
+    out = torch.zeros(4, q.shape[0], 64, dtype=torch.bfloat16, device="cuda").transpose(0, 1)
+    fa.kv_append(q, q[:, :2], q[:, 2:], kc, vc, table, kv, qs, q_out=out, **kw)
+    assert torch.equal(out, want)
 
 
 @gpu

@@ -79,6 +79,15 @@ int main() {
             }
         }
     }
+    // partials: what lies in the slots, row by row
+    for (int it = 0; it < 20000; ++it) {
+        const RowParts a{nullptr, nullptr, pick(0, 4) ? pick(-3, 400) : (pick(0, 1) ? INT_MAX : INT_MIN),
+                         pick(0, 4) ? pick(-2, 9) : (pick(0, 1) ? INT_MAX : INT_MIN), pick(0, 1) ? 16 : 256};
+        const long long rows = pick(1, 12) * 2LL * a.stride;
+        bool in = a.count >= 1;
+        for (int k = 0; in && k < a.count && k < 100; ++k) in = a.at(k) >= 0 && a.at(k) < rows;
+        CHECK(a.within(rows) == in);
+    }
     // the division by the group size
     for (uint32_t d : {1u, 2u, 3u, 5u, 6u, 7u, 8u, 12u, 31u, 64u, 100u, 255u, 65537u, 2147483647u}) {
         const FastDiv f = fast_div(d);
