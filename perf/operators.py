@@ -193,8 +193,8 @@ def _paged_own(s):
     c = s["case"]
     mask = "causal" if c["window"] < 0 else "sink_window"
     return fa.fwd_paged(s["q"], s["k_cache"], s["v_cache"], s["page_table"], s["kv_len"], s["q_start"],
-                        max_q_len=s["max_q"], mask=mask, window=max(c["window"], 0), sinks=c["sinks"],
-                        shared_len=c["shared"])
+                        max_q_len=s["max_q"], mask=mask, window=max(c["window"], 0),
+                        sinks=c["sinks"] if c["window"] >= 0 else 0, shared_len=c["shared"])
 
 
 def _seen(i, j, window, sinks):
