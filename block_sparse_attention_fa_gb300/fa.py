@@ -237,6 +237,14 @@ def _workspace_of(idx: int, raw: int) -> Workspace:
     return ws
 
 
+def _launch(device: torch.device, stream, workspace):
+    """The workspace's address and the stream of a call on tensors of ``device``."""
+    if workspace is None:
+        workspace = default_workspace(device, stream) if stream is not None or device.index != _device_now() else \
+            _workspace_of(device.index, _raw_stream(device.index))
+    return workspace.tensor.data_ptr(), _raw_stream(_device_now()) if stream is None else stream.cuda_stream
+
+
 class _IndexArrays:
     """The two count and two index arrays of a (transposed) BlockMask in one allocation: four would take longer to
     allocate than the arrays of a short sequence take to build.  Each starts on a 16-byte boundary."""
@@ -264,11 +272,10 @@ class BlockMask:
     full_kv_indices = property(lambda self: self._arrays[3])
 
     def __init__(self, B, H, q_len, kv_len, mask, window, prefix_len, seg_ids, device, table=None):
-        lib = load_library()
-        nq, nkv, ne = ctypes.c_int32(), ctypes.c_int32(), ctypes.c_int64()
-        _check(lib.fa_block_mask_shape(B, H, q_len, kv_len, ctypes.byref(nq), ctypes.byref(nkv), ctypes.byref(ne)))
+        if min(B, H, q_len, kv_len) < 1:          # the library says what is wrong
+            _check(load_library().fa_block_mask_shape(B, H, q_len, kv_len, None, None, None))
         self.B, self.H, self.q_len, self.kv_len = B, H, q_len, kv_len
-        self.nq, self.nkv = nq.value, nkv.value
+        self.nq, self.nkv = -(-q_len // BLOCK), -(-kv_len // BLOCK)
         self.mask, self.window, self.prefix_len = mask, window, prefix_len
         self.seg_ids = seg_ids
         self.table = table
@@ -280,23 +287,20 @@ class BlockMask:
         s.block_q = s.block_kv = BLOCK
         s.nq, s.nkv = self.nq, self.nkv
         s.kv_num_blocks, s.kv_indices, s.full_kv_num_blocks, s.full_kv_indices = self._arrays.ptrs
-        s.mask.kind = MASK_KINDS[mask]
-        s.mask.window = window
-        s.mask.prefix_len = prefix_len
+        m = s.mask
+        m.kind, m.window, m.prefix_len = MASK_KINDS[mask], window, prefix_len
         if seg_ids is not None:
-            s.mask.seg_batch = seg_ids.shape[0]
-            s.mask.seg_ids = seg_ids.data_ptr()
+            m.seg_batch, m.seg_ids = seg_ids.shape[0], seg_ids.data_ptr()
         if table is not None:
-            s.mask.table_batch = table.shape[0]
-            s.mask.table = table.data_ptr()
+            m.table_batch, m.table = table.shape[0], table.data_ptr()
         self.struct = s
 
     def rebuild(self, stream=None, workspace: Optional["Workspace"] = None):
         """Run fa_block_mask_build again into this BlockMask's own buffers
         (e.g. after the segment ids changed in place); capturable in a CUDA
         graph since it allocates nothing."""
-        ws = workspace or default_workspace(self.device, stream)
-        _check(load_library().fa_block_mask_build(ctypes.byref(self.struct), ws.ptr, _stream_ptr(stream)))
+        ws, raw = _launch(self.device, stream, workspace)
+        _check(load_library().fa_block_mask_build(ctypes.byref(self.struct), ws, raw))
         return self
 
     def cols(self, stream=None, workspace: Optional["Workspace"] = None, rebuild: bool = False) -> dict:
@@ -310,9 +314,9 @@ class BlockMask:
             if self._cols is None:
                 self._cols = _IndexArrays((self.B, self.H, self.nkv), (self.B, self.H, self.nkv, self.nq), self.device)
                 self._cols_struct = BlockMaskColsStruct(*self._cols.ptrs)
-            ws = workspace or default_workspace(self.device, stream)
+            ws, raw = _launch(self.device, stream, workspace)
             _check(load_library().fa_block_mask_build_cols(ctypes.byref(self.struct), ctypes.byref(self._cols_struct),
-                                                           ws.ptr, _stream_ptr(stream)))
+                                                           ws, raw))
 
     def visited_tiles(self) -> int:
         return int(self.kv_num_blocks.sum().item() + self.full_kv_num_blocks.sum().item())
@@ -354,36 +358,34 @@ def block_mask(mask: str, B: int, H: int, q_len: int, kv_len: int, *, window: in
         if mask != "sink_window" or prefix_len:
             raise ValueError("sinks applies to the sink_window mask (and excludes prefix_len)")
         prefix_len = sinks
-    device = torch.device(device or "cuda")
-    bm = BlockMask(B, H, q_len, kv_len, mask, window, prefix_len, seg_ids, device, table=table)
-    ws = workspace or default_workspace(device, stream)
-    _check(load_library().fa_block_mask_build(ctypes.byref(bm.struct), ws.ptr, _stream_ptr(stream)))
-    return bm
+    bm = BlockMask(B, H, q_len, kv_len, mask, window, prefix_len, seg_ids, device or "cuda", table=table)
+    return bm.rebuild(stream, workspace)
 
 
 def _check_fwd_tensors(q, k, v, out, lse, out_fp32, alibi_slopes, rel_bias, rel_max, bm):
     """The shapes, dtypes and placement fa_fwd / fa_fwd_noalloc read and write
     through raw pointers, which the C ABI cannot see: anything wrong here
     would become an out-of-bounds device access, so it is rejected first."""
-    if q.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"unsupported dtype {q.dtype}")
-    for t in (k, v):
-        if t.dtype != q.dtype:
-            raise ValueError("q, k and v must share a dtype")
+    dtype = q.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+        raise ValueError(f"unsupported dtype {dtype}")
+    if k.dtype is not dtype or v.dtype is not dtype:
+        raise ValueError("q, k and v must share a dtype")
     for t in (q, k, v):
         if not (t.is_cuda and t.is_contiguous() and t.dim() == 4):
             raise ValueError("q, k, v must be contiguous CUDA tensors [B, H, T, D]")
-    B, Hq, Tq, D = q.shape
-    if tuple(k.shape) != tuple(v.shape):
+    shape, kv_shape = q.shape, k.shape
+    B, Hq, Tq, D = shape
+    if kv_shape != v.shape:
         raise ValueError("k and v must have the same shape")
-    if k.shape[0] != B or k.shape[3] != D:
+    if kv_shape[0] != B or kv_shape[3] != D:
         raise ValueError("k and v must be [B, Hkv, kv_len, D] with q's B and D")
-    if out_fp32 and q.dtype != torch.bfloat16:
+    if out_fp32 and dtype is not torch.bfloat16:
         raise ValueError("out_fp32 applies to bf16 inputs only")
-    want = torch.float32 if (out_fp32 or q.dtype == torch.float32) else torch.bfloat16
-    if out.dtype != want or not out.is_cuda or not out.is_contiguous() or tuple(out.shape) != tuple(q.shape):
+    want = torch.float32 if out_fp32 else dtype
+    if out.dtype is not want or not out.is_cuda or not out.is_contiguous() or out.shape != shape:
         raise ValueError(f"out must be a contiguous CUDA {want} tensor of q's shape")
-    if lse.dtype != torch.float32 or not lse.is_cuda or not lse.is_contiguous() or tuple(lse.shape) != (B, Hq, Tq):
+    if lse.dtype is not torch.float32 or not lse.is_cuda or not lse.is_contiguous() or lse.shape != (B, Hq, Tq):
         raise ValueError("lse must be a contiguous CUDA float32 tensor [B, Hq, q_len]")
     if alibi_slopes is not None:
         if alibi_slopes.dtype != torch.float32 or not alibi_slopes.is_cuda or not alibi_slopes.is_contiguous() \
@@ -393,8 +395,8 @@ def _check_fwd_tensors(q, k, v, out, lse, out_fp32, alibi_slopes, rel_bias, rel_
         if rel_bias.dtype != torch.float32 or not rel_bias.is_cuda or not rel_bias.is_contiguous() \
                 or rel_bias.numel() < Hq * (2 * rel_max + 1):
             raise ValueError("rel_bias must be a contiguous CUDA float32 tensor [Hq, 2 rel_max + 1]")
-    if bm.q_len != Tq or bm.kv_len != k.shape[2]:
-        raise ValueError(f"the BlockMask was built for ({bm.q_len}, {bm.kv_len}), not ({Tq}, {k.shape[2]})")
+    if bm.q_len != Tq or bm.kv_len != kv_shape[2]:
+        raise ValueError(f"the BlockMask was built for ({bm.q_len}, {bm.kv_len}), not ({Tq}, {kv_shape[2]})")
 
 
 def fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, bm: BlockMask, *, score: str = "none",
@@ -432,9 +434,8 @@ def fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, bm: BlockMask, *, sco
     if rel_bias is not None:
         sc.rel_bias = rel_bias.data_ptr()
         sc.rel_max = rel_max
-    ws = workspace or default_workspace(q.device, stream)
-    _check(load_library().fa_fwd(ctypes.byref(a), ctypes.byref(bm.struct), ctypes.byref(sc), ws.ptr,
-                                 _stream_ptr(stream)))
+    ws, raw = _launch(q.device, stream, workspace)
+    _check(load_library().fa_fwd(ctypes.byref(a), ctypes.byref(bm.struct), ctypes.byref(sc), ws, raw))
     return out, lse
 
 
@@ -539,10 +540,10 @@ def fwd_decode(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, bm: BlockMask,
     if partials.dtype != torch.float32 or not partials.is_cuda or not partials.is_contiguous():
         raise ValueError("partials must be a contiguous CUDA float32 tensor (see decode_partials)")
     sc = _score_desc(score, softcap, alibi_slopes, rel_bias, rel_max)
-    ws = workspace or default_workspace(q.device, stream)
+    ws, raw = _launch(q.device, stream, workspace)
     _check(lib.fa_fwd_decode(ctypes.byref(a), ctypes.byref(bm.struct), ctypes.byref(sc), num_splits,
                              ctypes.c_void_p(partials.data_ptr()), partials.numel() * partials.element_size(),
-                             ws.ptr, _stream_ptr(stream)))
+                             ws, raw))
     return out, lse
 
 
@@ -563,13 +564,13 @@ def bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor, lse:
     its lse, and the upstream gradient dout; returns fp32 (dq, dk, dv).  The
     BlockMask's transposed lists are built on first use (BlockMask.cols)."""
     for t in (q, k, v, o, dout):
-        if t.dtype != torch.bfloat16 or not (t.is_cuda and t.is_contiguous() and t.dim() == 4):
+        if t.dtype is not torch.bfloat16 or not (t.is_cuda and t.is_contiguous() and t.dim() == 4):
             raise ValueError("q, k, v, o and dout must be contiguous CUDA bf16 tensors [B, H, T, D]")
     B, Hq, Tq, D = q.shape
     Hkv, Tkv = k.shape[1], k.shape[2]
-    if tuple(o.shape) != tuple(q.shape) or tuple(dout.shape) != tuple(q.shape):
+    if o.shape != q.shape or dout.shape != q.shape:
         raise ValueError("o and dout must have q's shape")
-    if tuple(k.shape) != tuple(v.shape) or k.shape[0] != B or k.shape[3] != D:
+    if k.shape != v.shape or k.shape[0] != B or k.shape[3] != D:
         raise ValueError("k and v must be [B, Hkv, kv_len, D] with q's B and D")
     f32 = dict(dtype=torch.float32, device=q.device)
     dq = torch.empty((B, Hq, Tq, D), **f32) if dq is None else dq
@@ -578,7 +579,7 @@ def bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor, lse:
     rowstats = bwd_rowstats(q) if rowstats is None else rowstats
     for name, t, shape in (("lse", lse, (B, Hq, Tq)), ("dq", dq, (B, Hq, Tq, D)), ("dk", dk, (B, Hkv, Tkv, D)),
                            ("dv", dv, (B, Hkv, Tkv, D))):
-        if t.dtype != torch.float32 or not t.is_cuda or not t.is_contiguous() or tuple(t.shape) != shape:
+        if t.dtype is not torch.float32 or not t.is_cuda or not t.is_contiguous() or t.shape != shape:
             raise ValueError(f"{name} must be a contiguous CUDA float32 tensor of shape {shape}")
     need = load_library().fa_bwd_rowstats_bytes(B, Hq, Tq)
     if rowstats.dtype != torch.float32 or not rowstats.is_cuda or not rowstats.is_contiguous() \
@@ -594,10 +595,10 @@ def bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor, lse:
     a.rowstats = rowstats.data_ptr()
     a.timeout_ms = timeout_ms
     sc = _score_desc(score, softcap, alibi_slopes, rel_bias, rel_max)
-    ws = workspace or default_workspace(q.device, stream)
-    bm._build_cols(stream, ws)
+    bm._build_cols(stream, workspace)
+    ws, raw = _launch(q.device, stream, workspace)
     _check(load_library().fa_bwd(ctypes.byref(a), ctypes.byref(bm.struct), ctypes.byref(bm._cols_struct),
-                                 ctypes.byref(sc), ws.ptr, _stream_ptr(stream)))
+                                 ctypes.byref(sc), ws, raw))
     return dq, dk, dv
 
 
