@@ -514,17 +514,25 @@ paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
 // Joins the partials of rows, the parts of `a` and then those of `b`:
 //   M = max m_k, L = sum 2^(m_k - M) l_k, O = sum 2^(m_k - M) O_k / L.
 // Eight lanes to a row, four rows to a warp.  What it costs is the loads'
-// latency, so as many as possible are in flight at once: a lane reads the
-// (m, l) of every eighth part for the weights, then its 4 x D / 32 columns of
-// four parts at a time.  SPLIT: the block's four warps take every fourth part
-// of the same four rows (single tokens and shared prefixes, where a row has
-// tens of parts) and add up through shared memory; otherwise each warp has
-// rows of its own.  Summing is in a fixed order either way.
-constexpr int kJoinWarps = 4;
-template <int D, bool SPLIT>
+// latency, so many are in flight at once: a lane holds the (m, l) of every
+// eighth part for the weights, and reads its 4 x D / 32 columns of several
+// parts at a time.  SHARE warps, the block, take the parts of the same four
+// rows in turn and add up through shared memory (single tokens and shared
+// prefixes, where a row has tens of parts); 1: each of four warps has rows of
+// its own.  With few rows eight warps share (one token, 520 keys, 8 blocks:
+// the call 8.6 us, with four 9.4; 64 rows after a prefix of 5024 keys, 188
+// blocks: 17.5 and 18.9); with many, four that need fewer registers together,
+// for then all blocks run at once (64 chats after a prefix of 16384 keys, 512
+// blocks: 55.5 us, with eight 58.5).  Summing is in a
+// fixed order either way.
+template <int SHARE>
+constexpr int kJoinWarps = SHARE == 1 ? 4 : SHARE;
+template <int D, int SHARE>
 __device__ __forceinline__ void join_rows(const PagedParams& p, const RowParts& a, const RowParts& b, long long row,
                                           bool valid, float4* sums) {
     constexpr int kC = D / 32;                     // float4 columns per lane, 32 apart
+    constexpr bool SPLIT = SHARE > 1;
+    constexpr int kHold = SPLIT ? SHARE / 2 : 1;   // weights per lane: 8 kHold parts per pass
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane & 7;
     const int n = valid ? a.count + b.count : 0;
     auto ml_of = [&](int k) {
@@ -532,9 +540,13 @@ __device__ __forceinline__ void join_rows(const PagedParams& p, const RowParts& 
         return k < a.count ? __ldcg(a.ml + a.at(k)) : __ldcg(b.ml + b.at(k - a.count));
     };
     const int longest = __reduce_max_sync(0xffffffffu, n);
-    const float2 head = ml_of(sub);
-    float m = -CUDART_INF_F;
-    for (int k0 = 0; k0 < longest; k0 += 8) m = fmaxf(m, (k0 ? ml_of(k0 + sub) : head).x);
+    float2 ml[kHold];
+#pragma unroll
+    for (int t = 0; t < kHold; ++t) ml[t] = ml_of(8 * t + sub);
+    float m = ml[0].x;
+#pragma unroll
+    for (int t = 1; t < kHold; ++t) m = fmaxf(m, ml[t].x);
+    for (int k0 = 8 * kHold; k0 < longest; k0 += 8) m = fmaxf(m, ml_of(k0 + sub).x);
 #pragma unroll
     for (int d = 4; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
     const float ref = m == -CUDART_INF_F ? 0.f : m;
@@ -542,16 +554,19 @@ __device__ __forceinline__ void join_rows(const PagedParams& p, const RowParts& 
     float4 o[kC];
 #pragma unroll
     for (int c = 0; c < kC; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = 0; k0 < longest; k0 += 8) {
-        const float2 ml = k0 ? ml_of(k0 + sub) : head;
-        const float w = ml.y == 0.f ? 0.f : ex2_approx(ml.x - ref);    // 0: the part has no visible key for this row
-        l += ml.y * w;
-        const int e0 = SPLIT ? warp : 0;
-        constexpr int kStep = SPLIT ? kJoinWarps : 1;
+    for (int k0 = 0; k0 < longest; k0 += 8 * kHold) {
+        float w[kHold];
 #pragma unroll
-        for (int e = 0; e < 8; e += kStep) {
-            const int k = k0 + e + e0;
-            const float we = __shfl_sync(0xffffffffu, w, (lane & 24) + e + e0);
+        for (int t = 0; t < kHold; ++t) {
+            if (k0) ml[t] = ml_of(k0 + 8 * t + sub);
+            w[t] = ml[t].y == 0.f ? 0.f : ex2_approx(ml[t].x - ref);   // 0: the part has no visible key for this row
+            l += ml[t].y * w[t];
+        }
+        // this warp's parts of the pass
+#pragma unroll
+        for (int e = 0; e < 8 * kHold; e += SHARE) {
+            const int k = k0 + e + (SPLIT ? warp : 0);
+            const float we = __shfl_sync(0xffffffffu, w[e >> 3], (lane & 24) + (e & 7) + (SPLIT ? warp : 0));
             if (k >= n) continue;
             const float4* src = reinterpret_cast<const float4*>(
                 k < a.count ? a.o + a.at(k) * D : b.o + b.at(k - a.count) * D) + sub;
@@ -575,7 +590,7 @@ __device__ __forceinline__ void join_rows(const PagedParams& p, const RowParts& 
         __syncthreads();
         if (warp > 0) return;
 #pragma unroll
-        for (int w = 0; w < kJoinWarps - 1; ++w) {
+        for (int w = 0; w < SHARE - 1; ++w) {
 #pragma unroll
             for (int c = 0; c < kC; ++c) {
                 const float4 v = sums[(w * kC + c) * 32 + lane];
@@ -603,26 +618,27 @@ __device__ __forceinline__ void join_rows(const PagedParams& p, const RowParts& 
 
 // Without a shared prefix: block (c, y) joins rows of the unit that starts in
 // CTA c of the attention kernel and runs on into the next ones.
-template <int D, bool SPLIT>
-__global__ void __launch_bounds__(32 * kJoinWarps) paged_join_units_kernel(const PagedParams p, int rows_per_unit) {
-    __shared__ float4 sums[SPLIT ? (kJoinWarps - 1) * (D / 32) * 32 : 1];
+template <int D, int SHARE>
+__global__ void __launch_bounds__(32 * kJoinWarps<SHARE>) paged_join_units_kernel(const PagedParams p, int rows_per_unit) {
+    __shared__ float4 sums[SHARE > 1 ? (SHARE - 1) * (D / 32) * 32 : 1];
     pdl_launch_next();
     pdl_wait_previous();
     const PagedMeta t = p.meta[blockIdx.x];
-    const int r = (SPLIT ? blockIdx.y : blockIdx.y * kJoinWarps + (threadIdx.x >> 5)) * 4 + ((threadIdx.x & 31) >> 3);
-    if (t.count == 0 || (r & ~3) >= t.rows) return;        // (uniform: four rows to a warp, and to a block if SPLIT)
+    const int r = (SHARE > 1 ? blockIdx.y : blockIdx.y * kJoinWarps<SHARE> + (threadIdx.x >> 5)) * 4 + ((threadIdx.x & 31) >> 3);
+    if (t.count == 0 || (r & ~3) >= t.rows) return;        // (uniform: four rows to a warp, and to a block that shares them)
     const bool valid = r < t.rows;
     const RowParts a{p.parts.slot_o, p.parts.slot_ml, (2LL * blockIdx.x + 1) * rows_per_unit + r, t.count, rows_per_unit};
     const RowParts none{nullptr, nullptr, 0, 0, 0};
     const int R = t.row0 + r, tok = quotient(R, p.by_group);
-    join_rows<D, SPLIT>(p, a, none, (long long)(t.q0 + tok) * p.Hq + t.h * p.group + R - tok * p.group, valid, sums);
+    join_rows<D, SHARE>(p, a, none, (long long)(t.q0 + tok) * p.Hq + t.h * p.group + R - tok * p.group, valid, sums);
 }
 
 // With a shared prefix: block (t, h, y) joins four rows of token t and kv head
 // h, the prefix's partials first, then those of the sequence's own keys.
-template <int D>
-__global__ void __launch_bounds__(32 * kJoinWarps) paged_join_rows_kernel(const PagedJoin j) {
-    __shared__ float4 sums[(kJoinWarps - 1) * (D / 32) * 32];
+template <int D, int SHARE>
+__global__ void __launch_bounds__(32 * SHARE) paged_join_rows_kernel(const PagedJoin j) {
+    constexpr int kThreads = 32 * SHARE;
+    __shared__ float4 sums[(SHARE - 1) * (D / 32) * 32];
     const PagedParams& p = j.own;
     pdl_launch_next();
     pdl_wait_previous();
@@ -633,7 +649,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_rows_kernel(const 
     const long long row = (long long)t * p.Hq + h * p.group + min(gq, p.group - 1);
     const int2 d = __ldcg(p.rowdesc + row);        // (what it says of a row without a unit is not used)
     int b = 0;
-    for (int b0 = 0; b0 < p.c.B; b0 += 32 * kJoinWarps) {
+    for (int b0 = 0; b0 < p.c.B; b0 += kThreads) {
         const int x = b0 + threadIdx.x;
         b += __syncthreads_count(x < p.c.B && __ldg(p.c.q_start + min(x, p.c.B - 1) + 1) <= t);
     }
@@ -649,7 +665,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_rows_kernel(const 
     if (d.x < 0) own = RowParts{p.parts.row_o, p.parts.row_ml, row, 1, 0};
     // (a CTA whose wait ran out leaves its rows' places as the scratch held them)
     if (d.x >= 0 && !own.within(2LL * p.ctas * j.own_rows)) own.count = 0;
-    join_rows<D, true>(p, a, own, row, valid, sums);
+    join_rows<D, SHARE>(p, a, own, row, valid, sums);
 }
 
 template <int D, int SCORE>
@@ -689,22 +705,40 @@ cudaError_t launch_paged_small(const PagedParams& p, const CUtensorMap& tk, cons
     return p.D == 64 ? launch_small_d<64>(p, tk, tv, s) : launch_small_d<128>(p, tk, tv, s);
 }
 
+namespace {
+
+// Eight warps to four rows while that is at most one block per SM and a half.
+bool few_joins(long long blocks) { return 2 * blocks <= 3 * device_sm_count(); }
+
+template <int D>
+cudaError_t launch_join_units(const PagedParams& p, int rows_per_unit, cudaStream_t s) {
+    if (rows_per_unit != kPagedSmallRows)
+        return paged_launch(paged_join_units_kernel<D, 1>, dim3(p.ctas, rows_per_unit / (4 * kJoinWarps<1>)),
+                            32 * kJoinWarps<1>, 0, true, s, p, rows_per_unit);
+    // (the blocks that find something to join)
+    const int per_unit = (std::min(p.max_q * p.group, kPagedSmallRows) + 3) / 4;
+    const dim3 grid(p.ctas, per_unit);
+    return few_joins(std::min<long long>((long long)p.c.B * p.c.Hkv, p.ctas) * per_unit)
+               ? paged_launch(paged_join_units_kernel<D, 8>, grid, 32 * 8, 0, true, s, p, rows_per_unit)
+               : paged_launch(paged_join_units_kernel<D, 4>, grid, 32 * 4, 0, true, s, p, rows_per_unit);
+}
+
+template <int D>
+cudaError_t launch_join_rows(const PagedJoin& j, cudaStream_t s) {
+    const dim3 grid(j.own.c.total_q, j.own.c.Hkv, (j.own.group + 3) / 4);
+    return few_joins((long long)grid.x * grid.y * grid.z)
+               ? paged_launch(paged_join_rows_kernel<D, 8>, grid, 32 * 8, 0, true, s, j)
+               : paged_launch(paged_join_rows_kernel<D, 4>, grid, 32 * 4, 0, true, s, j);
+}
+
+}  // namespace
+
 cudaError_t launch_paged_join_units(const PagedParams& p, int rows_per_unit, cudaStream_t s) {
-    const int threads = 32 * kJoinWarps;
-    if (rows_per_unit == kPagedSmallRows) {
-        const dim3 grid(p.ctas, kPagedSmallRows / 4);
-        return p.D == 64 ? paged_launch(paged_join_units_kernel<64, true>, grid, threads, 0, true, s, p, rows_per_unit)
-                         : paged_launch(paged_join_units_kernel<128, true>, grid, threads, 0, true, s, p, rows_per_unit);
-    }
-    const dim3 grid(p.ctas, rows_per_unit / (4 * kJoinWarps));
-    return p.D == 64 ? paged_launch(paged_join_units_kernel<64, false>, grid, threads, 0, true, s, p, rows_per_unit)
-                     : paged_launch(paged_join_units_kernel<128, false>, grid, threads, 0, true, s, p, rows_per_unit);
+    return p.D == 64 ? launch_join_units<64>(p, rows_per_unit, s) : launch_join_units<128>(p, rows_per_unit, s);
 }
 
 cudaError_t launch_paged_join_rows(const PagedJoin& p, cudaStream_t s) {
-    const dim3 grid(p.own.c.total_q, p.own.c.Hkv, (p.own.group + 3) / 4);
-    return p.own.D == 64 ? paged_launch(paged_join_rows_kernel<64>, grid, 32 * kJoinWarps, 0, true, s, p)
-                         : paged_launch(paged_join_rows_kernel<128>, grid, 32 * kJoinWarps, 0, true, s, p);
+    return p.own.D == 64 ? launch_join_rows<64>(p, s) : launch_join_rows<128>(p, s);
 }
 
 }  // namespace fa
