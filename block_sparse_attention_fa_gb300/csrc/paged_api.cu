@@ -94,8 +94,9 @@ fa_status check_fwd(const fa_paged_kv* c, const fa_paged_fwd_args* a) {
         return fail(FA_ERR_INVALID_ARG, "shared_len (%d) is past max_pages x page_size (%lld)", a->shared_len, cap);
     if (c->Hkv > 65535) return fail(FA_ERR_UNSUPPORTED, "Hkv must be <= 65535");
     // the line of tiles is counted in 32 bits: units (at most one partly
-    // filled one per sequence) x kv heads x tiles
-    const long long group = a->Hq / c->Hkv, tiles = cap / 64 + 2;
+    // filled one per sequence) x kv heads x tiles (of 64 keys, or of 128 and
+    // a few for the unit itself)
+    const long long group = a->Hq / c->Hkv, tiles = cap / 64 + 4;
     const double units = (double)c->B + (double)c->total_q * group / fa::kPagedTileRows + 1;
     if (units * c->Hkv * tiles > 2147483647.0 || (long long)c->total_q * a->Hq > 2147483647LL)
         return fail(FA_ERR_UNSUPPORTED, "too much work for one call (%d rows of %d heads against up to %lld keys)",

@@ -73,11 +73,19 @@ constexpr uint32_t kSegReaders = 11;             // the MMA, clearing and softma
 enum TSite : uint32_t { S_T_Q = 80, S_T_K_FULL, S_T_K_EMPTY, S_T_V_FULL, S_T_V_EMPTY, S_T_V_OK, S_T_S, S_T_P, S_T_O,
                         S_T_UPD, S_T_DRAIN, S_T_SEG, S_T_SEG_EMPTY };
 
+// What a unit's start and end cost (Q, the pipeline's first and last steps, O)
+// beside its tiles, in tiles: its place in the line is that much longer.
+// Without it a CTA whose stretch is all short units ends long after the others
+// (prompts of 4 x 1024 tokens 92 us, one of 4096 tokens 210); with 2 those
+// take 55 and 123, with 4 57 and 126, with 6 61 and 130, and chunks up to 8192
+// keys 376 to 385 with any.  (The units of a shared prefix are all alike.)
+constexpr int kUnitTiles = 2;
+
 // The part of a unit in a CTA's stretch.
 struct TileSeg {
     int b, h, row0, rows, q0, n, kv;
     int jlo, jhi, i0, i1;          // keys of this kernel's part, positions of the unit's rows
-    int tiles, k0, k1, t;          // t: where the part begins in the line
+    int tiles, k0, k1, t;          // t: the place of tile k0 in the line
     Hull hull;
     __device__ __forceinline__ bool begins() const { return k0 == 0; }
     __device__ __forceinline__ bool ends() const { return k1 == tiles; }
@@ -155,6 +163,13 @@ __device__ __forceinline__ void unit_rows(const FastDiv& by_group, int n, int kv
     i1 = kv - n + quotient(r1, by_group);
 }
 
+// The length of one such unit's place in the line.
+__device__ __forceinline__ int unit_length(const PagedParams& p, int n, int kv, int rt) {
+    int i0, i1;
+    unit_rows(p.by_group, n, kv, rt, i0, i1);
+    return make_hull(p.mask, i0, i1, p.shared, kv, 7).tiles + kUnitTiles;
+}
+
 __device__ __forceinline__ bool next_seg(const PagedParams& p, TileLine& ln, TileSeg& s) {
     if (ln.t >= ln.t1) return false;
     int off;
@@ -185,7 +200,7 @@ __device__ __forceinline__ bool next_seg(const PagedParams& p, TileLine& ln, Til
         for (;;) {
             unit_rows(p.by_group, s.n, s.kv, ln.rt, s.i0, s.i1);
             s.hull = make_hull(p.mask, s.i0, s.i1, s.jlo, s.jhi, 7);
-            const int next = ln.start + p.c.Hkv * s.hull.tiles;
+            const int next = ln.start + p.c.Hkv * (s.hull.tiles + kUnitTiles);
             if (ln.t < next) break;
             ln.start = next;
             ++ln.rt;
@@ -195,12 +210,37 @@ __device__ __forceinline__ bool next_seg(const PagedParams& p, TileLine& ln, Til
         s.row0 = ln.rt * kPagedTileRows;
         s.rows = min(kPagedTileRows, s.n * p.group - s.row0);
     }
-    s.h = off / s.tiles;
-    s.k0 = off - s.h * s.tiles;
-    s.k1 = min(s.tiles, s.k0 + (ln.t1 - ln.t));
-    s.t = ln.t;
-    ln.t += s.k1 - s.k0;
-    return true;
+    const int front = p.prefix ? 0 : kUnitTiles, length = s.tiles + front;
+    s.h = off / length;
+    const int a = off - s.h * length, b = min(length, a + (ln.t1 - ln.t));
+    s.k0 = max(a - front, 0);
+    s.k1 = max(b - front, 0);
+    s.t = ln.t + max(front - a, 0);
+    ln.t += b - a;
+    return s.k1 > 0;               // (0: the stretch ends before the unit's first tile)
+}
+
+// Finds the unit group of ln.b in which the stretch begins: a lane to a group
+// of the next 32.
+__device__ __forceinline__ void seek(const PagedParams& p, TileLine& ln, int lane) {
+    const int q0 = ln.q0[ln.b], n = ln.q0[ln.b + 1] - q0, kv = ln.kv[ln.b];
+    for (; ln.rt * kPagedTileRows < n * p.group; ln.rt += 32) {
+        int len = 0;
+        if ((ln.rt + lane) * kPagedTileRows < n * p.group) len = p.c.Hkv * unit_length(p, n, kv, ln.rt + lane);
+        int upto = len;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, upto, d);
+            if (lane >= d) upto += y;
+        }
+        const uint32_t behind = __ballot_sync(0xffffffffu, ln.start + upto > ln.t);
+        const int at = behind ? __ffs(behind) - 1 : 31;
+        ln.start += __shfl_sync(0xffffffffu, behind ? upto - len : upto, at);
+        if (behind) {
+            ln.rt += at;
+            return;
+        }
+    }
 }
 
 // Rows r0 .. r0 + 31 of a unit's Q into their row tile at `tile` (128-byte
@@ -296,19 +336,25 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
             line.prefix_rows ? make_hull(p.mask, line.imin, line.imax, 0, p.shared, 7).tiles : 1;
         total = (line.prefix_rows + kPagedTileRows - 1) / kPagedTileRows * p.c.Hkv * line.prefix_tiles;
     } else {
-        block_prefix<kThreadsT>(p.c.B, pre, reinterpret_cast<int*>(smem + L::kScan), [&](int b) {
-            const SeqInfo s = seq_info(p.c, b, p.max_q, p.shared, cta == 0 ? p.ws : nullptr);
+        // the sequences' lengths: a warp to each of a few sequences (long
+        // prompts have hundreds of units), a thread to each of many
+        const bool few = p.c.B <= kThreadsT / 32;
+        for (int b = few ? warp : threadIdx.x; b < p.c.B; b += few ? kThreadsT / 32 : kThreadsT) {
+            const bool first = !few || lane == 0;
+            const SeqInfo s = seq_info(p.c, b, p.max_q, p.shared, cta == 0 && first ? p.ws : nullptr);
             int sum = 0;
-            for (int rt = 0; rt * kPagedTileRows < s.n * p.group; ++rt) {
-                int i0, i1;
-                unit_rows(p.by_group, s.n, s.kv, rt, i0, i1);
-                sum += make_hull(p.mask, i0, i1, p.shared, s.kv, 7).tiles;
+            for (int rt = few ? lane : 0; rt * kPagedTileRows < s.n * p.group; rt += few ? 32 : 1)
+                sum += unit_length(p, s.n, s.kv, rt);
+            if (few) sum = __reduce_add_sync(0xffffffffu, sum);
+            if (first) {
+                pre[b] = sum;
+                len_s[b] = s.kv;
+                q0_s[b] = s.q0;
+                if (b == p.c.B - 1) q0_s[p.c.B] = s.q0 + s.n;
             }
-            len_s[b] = s.kv;
-            q0_s[b] = s.q0;
-            if (b == p.c.B - 1) q0_s[p.c.B] = s.q0 + s.n;
-            return sum;
-        });
+        }
+        __syncthreads();
+        block_prefix<kThreadsT>(p.c.B, pre, reinterpret_cast<int*>(smem + L::kScan), [&](int b) { return pre[b]; });
         total = p.c.Hkv * pre[p.c.B];
     }
     line.per = max((total + p.ctas - 1) / p.ctas, 1);
@@ -360,6 +406,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         int last_k = -1, last_v = -1;
         bool ok = true;
         TileSeg s{};
+        if (!p.prefix && line.t < line.t1) seek(p, line, lane);
         // the copies of one tile of K or V: `id` the lane's page, `row` its
         // first row within the page
         auto load = [&](const CUtensorMap* tm, uint32_t base, int full, int empty, uint32_t gg, int id, int row,
@@ -559,10 +606,14 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         for (;;) {
             if (have) bring(next);
             if (done) {
-                // the unit's end in this CTA: O / l and lse, or a partial
                 if (!mbar_wait_warp(bar(T_O_DONE + t), uq & 1, wc, S_T_O)) { ok = false; break; }
                 tc_fence_after();
                 ++uq;
+            }
+            // (the next unit's first products may come while O is read: they go to S)
+            if (have) announce(next);
+            if (done) {
+                // the unit's end in this CTA: O / l and lse, or a partial
                 const bool whole = s.begins() && s.ends(), last = whole && !p.join_rows;
                 const long long row = (long long)trow * p.Hq + hq;
                 const long long at = whole ? row : (2LL * cta + (s.begins() ? 1 : 0)) * kPagedTileRows + ur;
@@ -606,7 +657,6 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                 tc_fence_before();
             }
             if (!have) break;
-            announce(next);
             s = next;
             if (s.begins() && !s.ends()) {
                 meta.count = s.count(line.per);
