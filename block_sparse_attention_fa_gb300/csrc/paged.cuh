@@ -9,6 +9,8 @@
 
 namespace fa {
 
+constexpr float kPagedLog2e = 1.4426950408889634f, kPagedLn2 = 0.6931471805599453f;
+
 __host__ __device__ __forceinline__ int imin(int a, int b) { return a < b ? a : b; }
 __host__ __device__ __forceinline__ int imax(int a, int b) { return a > b ? a : b; }
 
@@ -108,20 +110,10 @@ __host__ __device__ __forceinline__ bool tile_open(const PagedMask& m, int kb, i
     return c0 >= jlo && c1 < jhi && (!m.causal || c1 <= i0) && (m.window < 0 || i1 - c0 <= m.window || c1 < m.sinks);
 }
 
-// score_mod on s = scale q.k (natural units), in the reference forms.
-template <int SCORE>
-__device__ __forceinline__ float paged_score(const ScoreParams& sc, float s, int hq, int i, int j) {
-    if (SCORE == FA_SCORE_SOFTCAP) return sc.softcap * tanhf(s / sc.softcap);
-    if (SCORE == FA_SCORE_ALIBI) return s - __ldg(sc.slopes + hq) * fabsf(static_cast<float>(i - j));
-    if (SCORE == FA_SCORE_ALIBI_SOFTCAP) {
-        const float u = s - __ldg(sc.slopes + hq) * fabsf(static_cast<float>(i - j));
-        return sc.softcap * tanhf(u / sc.softcap);
-    }
-    if (SCORE == FA_SCORE_REL_BIAS) {
-        const int R = sc.rel_max;
-        return s + __ldg(sc.rel_bias + (size_t)hq * (2 * R + 1) + min(max(i - j, -R), R) + R);
-    }
-    return s;
+// cap_out tanh(u) through 1 - 2 / (2^(2 log2(e) |u|) + 1).
+__device__ __forceinline__ float softcap_exact(float u, float cap_out) {
+    const float e = ex2_approx(2.f * kPagedLog2e * fabsf(u));
+    return copysignf(cap_out * (1.f - __fdividef(2.f, e + 1.f)), u);
 }
 
 // The loader's share of one tile of KT keys: lane l of the warp stands for the

@@ -315,7 +315,9 @@ paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
     float* const smax = reinterpret_cast<float*>(smem + L::kMax);
     float* const ssum = reinterpret_cast<float*>(smem + L::kSum);
     const uint32_t sP = sbase + L::kP;
-    const float sl2 = SCORE == FA_SCORE_NONE ? p.scale * kLog2eP : kLog2eP;   // to base 2
+    // score_mod, to base 2
+    const float sl2 = p.scale * kLog2eP;
+    const float cap_in = (SCORE == FA_SCORE_SOFTCAP ? p.scale : 1.f) / p.score.softcap, cap_out = p.score.softcap * kLog2eP;
     constexpr int kNT = D / 64;                    // n8 tiles of O per warp
     constexpr int kKW = KT / 8, kNK = kKW / 8;     // keys per warp, n8 tiles of S
     const int col0 = warp * (D / 8);               // the warp's first column of O
@@ -330,11 +332,14 @@ paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         if (s.b < 0) break;
         const int rows = s.n * p.group, i0 = s.kv - s.n;
         int tok[2], hq[2];
+        float slope[2] = {0.f, 0.f};
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int r = min(gr + 8 * e, rows - 1);
             tok[e] = quotient(r, p.by_group);
             hq[e] = s.h * p.group + r - tok[e] * p.group;
+            if (SCORE == FA_SCORE_ALIBI) slope[e] = __ldg(p.score.slopes + hq[e]) * kLog2eP;
+            if (SCORE == FA_SCORE_ALIBI_SOFTCAP) slope[e] = __ldg(p.score.slopes + hq[e]);
         }
         // Q's fragments (what the rows past the unit's hold stays in those rows)
         uint32_t qa[D / 16][4];
@@ -390,8 +395,15 @@ paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                     for (int c = 0; c < 4; ++c) {
                         const int e = c >> 1, j = c0 + kKW * warp + 8 * nt + 2 * tq + (c & 1);
                         float v = x[nt][c];
-                        if (SCORE != FA_SCORE_NONE) v = paged_score<SCORE>(p.score, v * p.scale, hq[e], i0 + tok[e], j);
-                        v *= sl2;
+                        const float far = fabsf(static_cast<float>(i0 + tok[e] - j));
+                        if (SCORE == FA_SCORE_NONE || SCORE == FA_SCORE_REL_BIAS) v *= sl2;
+                        if (SCORE == FA_SCORE_SOFTCAP) v = softcap_exact(v * cap_in, cap_out);
+                        if (SCORE == FA_SCORE_ALIBI) v = fmaf(-slope[e], far, v * sl2);
+                        if (SCORE == FA_SCORE_ALIBI_SOFTCAP) v = softcap_exact(fmaf(-slope[e], far, v * p.scale) * cap_in, cap_out);
+                        if (SCORE == FA_SCORE_REL_BIAS) {
+                            const int R = p.score.rel_max, d = min(max(i0 + tok[e] - j, -R), R);
+                            v = fmaf(__ldg(p.score.rel_bias + (size_t)hq[e] * (2 * R + 1) + d + R), kLog2eP, v);
+                        }
                         if (!open && !paged_visible(p.mask, i0 + tok[e], j, p.shared, s.kv)) v = -CUDART_INF_F;
                         x[nt][c] = v;
                         mx[e] = fmaxf(mx[e], v);
@@ -728,15 +740,16 @@ bool few_joins(long long blocks) { return 2 * blocks <= 3 * device_sm_count(); }
 
 template <int D>
 cudaError_t launch_join_units(const PagedParams& p, int rows_per_unit, cudaStream_t s) {
-    if (rows_per_unit != kPagedSmallRows)
-        return paged_launch(paged_join_units_kernel<D, 1>, dim3(p.ctas, rows_per_unit / (4 * kJoinWarps<1>)),
-                            32 * kJoinWarps<1>, 0, true, s, p, rows_per_unit);
-    // (the blocks that find something to join)
-    const int per_unit = (std::min(p.max_q * p.group, kPagedSmallRows) + 3) / 4;
-    const dim3 grid(p.ctas, per_unit);
-    return few_joins(std::min<long long>((long long)p.c.B * p.c.Hkv, p.ctas) * per_unit)
-               ? paged_launch(paged_join_units_kernel<D, 8>, grid, 32 * 8, 0, true, s, p, rows_per_unit)
-               : paged_launch(paged_join_units_kernel<D, 4>, grid, 32 * 4, 0, true, s, p, rows_per_unit);
+    // the blocks that find something to join: at most the units', or one per CTA
+    const long long rows = std::min((long long)p.max_q * p.group, (long long)rows_per_unit);
+    const long long units = ((long long)p.c.B + (long long)p.c.total_q * p.group / rows_per_unit) * p.c.Hkv;
+    const dim3 grid(p.ctas, (unsigned)((rows + 3) / 4));
+    if (few_joins(std::min<long long>(units, p.ctas) * grid.y))
+        return paged_launch(paged_join_units_kernel<D, 8>, grid, 32 * 8, 0, true, s, p, rows_per_unit);
+    if (rows_per_unit == kPagedSmallRows)
+        return paged_launch(paged_join_units_kernel<D, 4>, grid, 32 * 4, 0, true, s, p, rows_per_unit);
+    return paged_launch(paged_join_units_kernel<D, 1>, dim3(p.ctas, (grid.y + kJoinWarps<1> - 1) / kJoinWarps<1>),
+                        32 * kJoinWarps<1>, 0, true, s, p, rows_per_unit);
 }
 
 template <int D>

@@ -463,6 +463,35 @@ def test_chunk_lengths(fa, new, kv):
 
 
 @gpu
+@pytest.mark.parametrize("new,kv", [([1] * 48, [3] * 24 + [2500] * 24), ([1] * 300, [64 + (b % 7) for b in range(300)]),
+                                    ([2, 1, 2] * 30, [5, 1, 900] * 30)])
+def test_decode_short_beside_long(fa, new, kv):
+    run(fa, Batch(new, kv, 4, 64, 32), 8)
+
+
+@gpu
+@pytest.mark.parametrize("new,kv,Hq,Hkv", [([2100], [2100], 4, 1), ([700] * 3, [700] * 3, 8, 2), ([130] * 15, [130] * 15, 4, 2),
+                                           ([17, 1, 300, 40] * 5, [17, 2000, 300, 3000] * 5, 4, 1)])
+def test_prompts(fa, new, kv, Hq, Hkv):
+    run(fa, Batch(new, kv, Hkv, 64, 64), Hq)
+
+
+@gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,Hq", [(1, 24), (4, 8), (9, 8)])
+def test_few_rows_in_many_parts(fa, n, Hq, D):
+    run(fa, Batch([n], [40000], 1, D, 16), Hq)
+
+
+@gpu
+@pytest.mark.parametrize("q_scale", [0.1, 1.0, 8.0, 60.0])
+@pytest.mark.parametrize("cap", [2.0, 50.0])
+@pytest.mark.parametrize("n", [1, 40])
+def test_softcap_ranges(fa, n, cap, q_scale):
+    run(fa, Batch([n] * 3, [n + 300, n + 90, n + 1000], 2, 64, 32), 8, score="softcap", softcap=cap, q_scale=q_scale)
+
+
+@gpu
 def test_large_scores_rescale(fa):
     """Scores that grow along the keys: the running max rises again and again."""
     for new in ([1], [80]):
