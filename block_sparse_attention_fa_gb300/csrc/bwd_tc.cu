@@ -394,18 +394,86 @@ __device__ __forceinline__ uint32_t chunk_mask(const BwdParams& p, int b, int ro
     return ((0xffffffffu >> (31 - hi)) & (0xffffffffu << lo)) | sinks;
 }
 
+// score_mod of s = scale q.k (natural units), for the few rows below.
+__device__ __forceinline__ float row_score(const ScoreParams& sc, float s, int hq, int i, int j) {
+    const int kind = sc.kind;
+    if (kind == FA_SCORE_ALIBI || kind == FA_SCORE_ALIBI_SOFTCAP)
+        s -= __ldg(sc.slopes + hq) * fabsf(static_cast<float>(i - j));
+    if (kind == FA_SCORE_SOFTCAP || kind == FA_SCORE_ALIBI_SOFTCAP) s = sc.softcap * tanhf(s / sc.softcap);
+    if (kind == FA_SCORE_REL_BIAS) {
+        const int R = sc.rel_max;
+        s += __ldg(sc.rel_bias + (size_t)hq * (2 * R + 1) + min(max(i - j, -R), R) + R);
+    }
+    return s;
+}
+
+// Delta of query row i from its keys, sum_j P_ij dP_ij, where the window with
+// sinks shows it at most kFewKeys.  Delta from O is off by O's rounding to
+// bf16, about 2^-9 |dO| |O|; with a few keys dP - Delta is no larger than dP,
+// or much smaller, and that is what shows in dQ and dK (relative error under a
+// window of two keys 0.0037 instead of 0.0023, in a sequence of two tokens up
+// to 0.03).  One warp, four lanes to a key.  False: left alone.
+constexpr int kFewKeys = 8;
+template <int D>
+__device__ __forceinline__ bool few_keys_delta(const BwdParams& p, long long bh, int i, int lane, float& delta) {
+    const int a = max(i - p.mask.window, 0), n_win = max(min(i, p.kv_len - 1) - a + 1, 0);
+    const int n_sink = min(min(p.mask.prefix_len, a), p.kv_len), n = n_sink + n_win;
+    if (n == 0 || n > kFewKeys) return false;
+    const int b = static_cast<int>(bh / p.Hq), hq = static_cast<int>(bh - (long long)b * p.Hq);
+    const int x = min(lane >> 2, n - 1), j = x < n_sink ? x : a + x - n_sink;
+    const long long row = (bh * p.q_len + i) * (D / 8) + (lane & 3);
+    const long long key = (((long long)b * p.Hkv + hq / p.group) * p.kv_len + j) * (D / 8) + (lane & 3);
+    uint4 q[D / 32], g[D / 32], k[D / 32], v[D / 32];
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+        q[c] = __ldg(static_cast<const uint4*>(p.q) + row + 4 * c);
+        g[c] = __ldg(static_cast<const uint4*>(p.dout) + row + 4 * c);
+        k[c] = __ldg(static_cast<const uint4*>(p.k) + key + 4 * c);
+        v[c] = __ldg(static_cast<const uint4*>(p.v) + key + 4 * c);
+    }
+    float sc = 0.f, dp = 0.f;
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+        const __nv_bfloat16 *qe = reinterpret_cast<const __nv_bfloat16*>(q + c), *ke = reinterpret_cast<const __nv_bfloat16*>(k + c);
+        const __nv_bfloat16 *ge = reinterpret_cast<const __nv_bfloat16*>(g + c), *ve = reinterpret_cast<const __nv_bfloat16*>(v + c);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            sc = fmaf(__bfloat162float(qe[e]), __bfloat162float(ke[e]), sc);
+            dp = fmaf(__bfloat162float(ge[e]), __bfloat162float(ve[e]), dp);
+        }
+    }
+#pragma unroll
+    for (int w = 1; w < 4; w <<= 1) {
+        sc += __shfl_xor_sync(0xffffffffu, sc, w);
+        dp += __shfl_xor_sync(0xffffffffu, dp, w);
+    }
+    sc = (lane >> 2) < n ? row_score(p.score, sc * p.scale, hq, i, j) * kLog2eT : -CUDART_INF_F;
+    float m = sc;
+#pragma unroll
+    for (int w = 4; w < 32; w <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
+    float l = sc == -CUDART_INF_F ? 0.f : ex2_approx(sc - m), d = l == 0.f ? 0.f : l * dp;
+#pragma unroll
+    for (int w = 4; w < 32; w <<= 1) {
+        l += __shfl_xor_sync(0xffffffffu, l, w);
+        d += __shfl_xor_sync(0xffffffffu, d, w);
+    }
+    if (l == 0.f) return false;
+    delta = d / l;
+    return true;
+}
+
 // A warp takes kStatRows padded rows at once.  They come in 16-byte pieces
 // through shared memory (two-byte loads from global memory, a row at a time,
 // took 48 us for 262144 rows of 128 columns instead of 31); every row is
 // summed in one order: lane l takes columns l, l + 32, .., then the lanes add
 // up pairwise.
 constexpr int kStatRows = 8;
-template <int D>
+template <int D, bool SINKS>
 __global__ void __launch_bounds__(256) bwd_rowstats_kernel(const BwdParams p) {
     constexpr int kLanes = D / 8, kPer = 32 / kLanes;     // lanes per row, rows per load
     __shared__ uint4 stage[8][2][kStatRows * kLanes];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long rows_pad = (long long)p.B * p.Hq * p.bm.nq * 128;      // (a multiple of kStatRows)
+    const long long rows_pad = (long long)p.B * p.Hq * p.bm.nq * 128;      // (a multiple of 64: whole blocks)
     const long long prow0 = ((long long)blockIdx.x * 8 + warp) * kStatRows;
     if (prow0 >= rows_pad) return;
     // the rows are of one head: a head has a multiple of 128
@@ -447,6 +515,17 @@ __global__ void __launch_bounds__(256) bwd_rowstats_kernel(const BwdParams p) {
         p.rowstats[prow0 + lane] = -mine;
         p.rowstats[rows_pad + prow0 + lane] =
             i0 + lane < p.q_len && lse > -CUDART_INF_F ? -lse * kLog2eT : -CUDART_INF_F;
+    }
+    if (SINKS) {
+        // the block's 64 rows (of one head) once more, every eighth to a warp:
+        // the first rows of a sequence then go to different warps
+        __syncthreads();
+        const int first = i0 - kStatRows * warp;
+        for (int r = warp; r < 8 * kStatRows && first + r < p.q_len; r += 8) {
+            float delta;
+            if (few_keys_delta<D>(p, bh, first + r, lane, delta) && lane == 0)
+                p.rowstats[prow0 - kStatRows * warp + r] = -delta;
+        }
     }
 }
 
@@ -1057,10 +1136,14 @@ cudaError_t launch_bwd_tc(const BwdParams& p, const CUtensorMap& tq, const CUten
                           const CUtensorMap& tg, cudaStream_t s) {
     const long long rows_pad = (long long)p.B * p.Hq * p.bm.nq * 128;
     const unsigned stat_blocks = (unsigned)((rows_pad + 8 * kStatRows - 1) / (8 * kStatRows));
-    if (p.D == 64)
-        bwd_rowstats_kernel<64><<<stat_blocks, 256, 0, s>>>(p);
-    else
-        bwd_rowstats_kernel<128><<<stat_blocks, 256, 0, s>>>(p);
+    const bool sinks = p.mask.kind == FA_MASK_SINK_WINDOW;
+    if (p.D == 64) {
+        if (sinks) bwd_rowstats_kernel<64, true><<<stat_blocks, 256, 0, s>>>(p);
+        else bwd_rowstats_kernel<64, false><<<stat_blocks, 256, 0, s>>>(p);
+    } else {
+        if (sinks) bwd_rowstats_kernel<128, true><<<stat_blocks, 256, 0, s>>>(p);
+        else bwd_rowstats_kernel<128, false><<<stat_blocks, 256, 0, s>>>(p);
+    }
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     return p.D == 64 ? launch_tc_d<64>(p, tq, tk, tv, tg, s) : launch_tc_d<128>(p, tq, tk, tv, tg, s);

@@ -237,3 +237,64 @@ def test_backward_with_split_sinks(fa, D, B, Hq, Hkv, q_len, kv_len, window, sin
         err = np.abs(got.double().cpu().numpy() - ref)
         assert err.max() <= 2e-2 * max(1.0, np.abs(ref).max()), name
         assert np.linalg.norm(err) <= 1e-2 * np.linalg.norm(ref), name
+
+
+def score_and_slope(x, i, j, score, softcap=1.0, slopes=None, rel_bias=None, rel_max=0):
+    """The modified score and its derivative by the scaled one."""
+    slope = np.ones_like(x)
+    if slopes is not None:
+        x = x - np.asarray(slopes, np.float64)[:, None, None] * np.abs(i - j)
+    if "softcap" in score:
+        t = np.tanh(x / softcap)
+        x, slope = softcap * t, 1 - t * t
+    if rel_bias is not None:
+        x = x + np.asarray(rel_bias, np.float64)[:, np.clip(i - j, -rel_max, rel_max) + rel_max]
+    return x, slope
+
+
+@gpu
+@pytest.mark.parametrize("score,skw", SCORES)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("q_len,kv_len,window,sinks", [(2, 2, 1, 0), (2, 2, 9, 0), (3, 3, 1, 1), (8, 8, 8, 0), (200, 200, 1, 0),
+                                                       (200, 200, 3, 3), (300, 300, 0, 2), (140, 40, 5, 1), (9, 300, 100, 4)])
+def test_backward_of_few_keys(fa, score, skw, D, q_len, kv_len, window, sinks):
+    """With few keys dP - Delta is small beside dP.  What may be off, element by element: the rounding of P and dS to
+    bf16 (half a step, 2^-8 of each; the gradients are fp32); the soft-cap's tanh by 2.3e-5 of itself, which is
+    2^-13 of P at a cap of 5 and 2^-14 of dS before its slope; and, of fp32 sums, 2^-15 of P (|dP| + |Delta|)."""
+    import torch
+    w = _case(B=1, Hq=4, Hkv=2, T=kv_len, D=D, q_len=q_len, score=score, **skw)
+    q, k, v = w.qkv()
+    g = synth.round_to_bf16(synth.standard_normal(80, q.shape))
+    qd, kd, vd = parity.to_device(w, q, k, v)
+    gd = torch.from_numpy(g).cuda().to(torch.bfloat16)
+    bm = fa.block_mask("sink_window", 1, 1, q_len, kv_len, window=window, sinks=sinks)
+    kw = parity.score_kwargs_gpu(w)
+    o, lse = fa.fwd(qd, kd, vd, bm, **kw)
+    grads = fa.bwd(qd, kd, vd, o, lse, gd, bm, **kw)
+    fa.default_workspace("cuda").check()
+    refs = oracle.bwd(q, k, v, g, **_okw(window, sinks), **parity.score_kwargs_oracle(w))
+    # |dS|, P and the rest of the bounds, from the oracle's lse under the same score
+    see, scale = dense(q_len, kv_len, window, sinks), 1 / np.sqrt(D)
+    k2, v2 = (np.repeat(x, 2, 1).astype(np.float64) for x in (k, v))
+    q2, g2 = q.astype(np.float64), g.astype(np.float64)
+    x = q2 @ k2.swapaxes(-1, -2) * scale
+    i, j = np.arange(q_len)[:, None], np.arange(kv_len)[None]
+    x, slope = score_and_slope(x, i, j, **parity.score_kwargs_oracle(w))
+    x = np.where(see, x, -np.inf)
+    m = x.max(-1, keepdims=True)
+    p = np.exp(x - np.where(np.isfinite(m), m, 0))
+    p /= np.maximum(p.sum(-1, keepdims=True), 1e-300)
+    dp = g2 @ v2.swapaxes(-1, -2)
+    delta = (p * dp).sum(-1, keepdims=True)
+    rounding = 2.0 ** -8 + 2.0 ** -13
+    slack = np.abs(p * (dp - delta)) * (slope * rounding + 2.0 ** -14) + p * (np.abs(dp) + np.abs(delta)) * 2.0 ** -15
+    # a row of more than 8 keys has its Delta from the bf16 O: each O_d off by half a step, so Delta by at most
+    # 2^-8 sum_d |dO_d O_d| (row 8 of the nine-row case)
+    many = see.sum(-1)[:, None] > 8
+    slack += np.where(many, p * (np.abs(g2 * (p @ v2)).sum(-1, keepdims=True) * 2.0 ** -8), 0)
+    pair = lambda t: t.reshape(1, 2, 2, *t.shape[2:]).sum(2)                        # noqa: E731
+    bounds = (scale * slack @ np.abs(k2), pair(scale * slack.swapaxes(-1, -2) @ np.abs(q2)),
+              pair((p * rounding).swapaxes(-1, -2) @ np.abs(g2)))
+    for name, got, ref, bound in zip(("dq", "dk", "dv"), grads, refs, bounds):
+        err = np.abs(got.double().cpu().numpy() - ref)
+        assert (err <= bound + 1e-6).all(), f"{name}: {(err / (bound + 1e-6)).max():.2f} of what it may be off"
