@@ -9,16 +9,21 @@
 // every K and V tile) against the keys that some row of them sees.  As in
 // paged_small.cu the 128-key tiles of all units stand in one line, every CTA
 // (one per SM) takes an equal stretch of it, and the units that two CTAs share
-// are joined by a second kernel.
+// are joined by a second kernel.  Chunks of 4 x up to 1024 tokens up to 8192
+// keys (32 heads on 8, 128 columns) take 186 us with the join, a prompt of
+// 4096 tokens 123, one of 16384 1500 (1.47 PFLOP/s).
 //
 // 384 threads:
 //   warps 0-3, 4-7  softmax of row tile 0, 1: thread r owns row r (TMEM lane
-//                   r).  Loads its row of Q into shared memory, then for each
-//                   64-key half reads S, applies score_mod and mask, keeps the
-//                   running max and sum (base 2), writes P (bf16) over S.
-//   warp 8          loader: its lanes stand for the pages of a tile; each
-//                   reads its page's id ahead of time and issues the page's
-//                   TMA boxes (K one step ahead of V).
+//                   r).  A warp brings its 32 rows of Q into shared memory
+//                   (asynchronous copies, while the unit before ends), then
+//                   for each 64-key half reads S, applies score_mod and mask,
+//                   keeps the running max and sum (base 2), writes P (bf16)
+//                   over S.
+//   warp 8          loader: walks the line and hands each unit to the other
+//                   warps; its lanes stand for the pages of a tile: each reads
+//                   its page's id ahead of time and issues the page's TMA
+//                   boxes (K one step ahead of V).
 //   warps 9, 10     MMA of row tile 0, 1: O += P V(k), then S = Q K(k + 1).
 //   warp 11         clears the V rows of keys that no row sees (their P is 0,
 //                   but 0 x NaN is not) before the product may read the tile.
