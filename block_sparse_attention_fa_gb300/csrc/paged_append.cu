@@ -16,8 +16,8 @@
 // Finding a token's slot takes three loads that wait for one another (q_start,
 // the sequence's numbers, its page).  A CTA takes up to four tokens, one warp
 // to a token for that part, and then moves the data of two tokens at a time,
-// so that enough loads are in flight: 107 us for 26418 tokens of 32 + 16 heads
-// of 128 columns (656 MB, 0.90 of the copy rate), 128 us with a CTA per token;
+// so that enough loads are in flight: 107 to 112 us for 26418 tokens of 32 + 16 heads
+// of 128 columns (656 MB, 0.86 to 0.90 of the copy rate), 128 us with a CTA per token;
 // eight tokens took 109 us, sixteen 117.  A step of few tokens gives each a CTA
 // of its own.
 #include <cuda_bf16.h>

@@ -132,7 +132,7 @@ __device__ __forceinline__ bool consumers_all(bool ok) {
 // A CTA's stretch [t, t1) of the line of tiles.  Once every CTA has some tiles
 // a unit counts as one more (`front` places before its first tile): its start
 // and end cost about as much, and a CTA whose stretch is all short units would
-// end long after the others (32 sequences of 64 keys before 32 of 8192: 169 us,
+// end long after the others (32 sequences of 64 keys before 32 of 8192: 166 us,
 // 216 without).  With fewer tiles the units' parts are alike, and the work is
 // best on the first CTAs (16 x 4 rows after a shared prefix of 5024 keys: 17.7
 // us, 20.2 with).
