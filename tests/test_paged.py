@@ -432,6 +432,12 @@ def test_decode_largest_batch(fa):
     run(fa, Batch([1] * 2048, [(i * 37) % 50 + 1 for i in range(2048)], 1, 64, 16), 2)
 
 
+@gpu
+@pytest.mark.parametrize("Hq,shared", [(17, 0), (2, 16), (17, 16)])
+def test_largest_batch_of_the_other_kernels(fa, Hq, shared):
+    run(fa, Batch([1] * 2048, [shared + (i * 37) % 50 + 1 for i in range(2048)], 1, 64, 16, shared=shared), Hq)
+
+
 # ------------------------------------------------------------- GPU: many rows
 @gpu
 @pytest.mark.parametrize("page", [16, 64, 256])
@@ -840,6 +846,32 @@ def test_append_head_major_output(fa):
     out = torch.zeros(4, q.shape[0], 64, dtype=torch.bfloat16, device="cuda").transpose(0, 1)
     fa.kv_append(q, q[:, :2], q[:, 2:], kc, vc, table, kv, qs, q_out=out, **kw)
     assert torch.equal(out, want)
+
+
+@gpu
+@pytest.mark.parametrize("n", [1, 40])
+def test_pages_past_32_bits(fa, n):
+    """A cache whose last pages lie 2^33 bytes (2^32 elements) behind its first: the same step on the same pages in
+    a small cache gives the same bits."""
+    page, Hkv, D, far = 256, 8, 128, 16384 + 8
+    bt = Batch([n, n], [900, 2000], Hkv, D, page)
+    kc, vc, table, kv, qs = bt.device()
+    ids = torch.linspace(0, far - 1, kc.shape[0], device="cuda").round().long().flip(0)
+    big = [torch.empty((far, Hkv, page, D), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    for x, y in zip(big, (kc, vc)):
+        x[ids] = y
+    there = torch.where(table >= 0, ids[table.clamp(min=0).long()], table.long()).to(torch.int32)
+    q = torch.from_numpy(bt.queries(32)).cuda().to(torch.bfloat16)
+    for step in range(2):
+        want = fa.fwd_paged(q, kc, vc, table, kv, qs, max_q_len=n)
+        got = fa.fwd_paged(q, *big, there, kv, qs, max_q_len=n)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        if step == 0:
+            rows = q.flip(0)
+            for k, v, t in ((kc, vc, table), (*big, there)):
+                fa.kv_append(None, rows[:, :Hkv], rows[:, Hkv:2 * Hkv], k, v, t, kv, qs)
+    assert torch.equal(big[0][ids].view(torch.int16), kc.view(torch.int16))
+    fa.default_workspace("cuda").check()
 
 
 @gpu
