@@ -66,6 +66,14 @@ struct SmallSeg {
     __device__ __forceinline__ bool ends() const { return k1 == tiles; }
 };
 
+// The line's index in shared memory has at most 1000 entries, so that two CTAs
+// fit on an SM: one per sequence, or per 2, 4 sequences, within which the loader
+// counts for itself (1024 sequences of 512 keys, 32 heads on 8 of 128 columns,
+// pages of 16: 329 us, 470 with an entry for each and one CTA per SM).
+constexpr int kLineEntries = 1000;
+__host__ __device__ constexpr int group_shift(int B) { return B <= kLineEntries ? 0 : B <= 2 * kLineEntries ? 1 : 2; }
+__host__ __device__ constexpr uint32_t groups_of(int B) { return (B + (1 << group_shift(B)) - 1) >> group_shift(B); }
+
 template <int D>
 struct SmallLayout {
     static constexpr int kStages = 3;
@@ -84,10 +92,9 @@ struct SmallLayout {
     static constexpr uint32_t kBars = (kInfo + 4u * kStages + 7u) & ~7u;  // FULL, EMPTY [stage], Q_FULL, Q_EMPTY [2]
     static constexpr uint32_t kAbort = kBars + 16u * kStages + 32u;
     static constexpr uint32_t kScan = kAbort + 16u;              // warp sums
-    static constexpr uint32_t kPre = kScan + 64u;                // [B + 1] first tile of each sequence
-    static constexpr uint32_t bytes(int B) { return kPre + 4u * (B + 1u) + 1024u; }
-    // two CTAs fit on an SM (228 KB less 1 KB for each) while B <= 1000; with
-    // more sequences one after the other
+    static constexpr uint32_t kPre = kScan + 64u;                // first tile of each group of sequences
+    static constexpr uint32_t bytes(int B) { return kPre + 4u * (groups_of(B) + 1u) + 1024u; }
+    // two CTAs fit on an SM (228 KB less 1 KB for each)
     static_assert(2u * (kPre + 4u * 1001u + 1024u) <= 226u * 1024u, "shared memory budget");
 };
 
@@ -138,16 +145,46 @@ __device__ __forceinline__ bool consumers_all(bool ok) {
 // us, 20.2 with).
 constexpr int kManyTiles = 4;                    // per CTA
 struct Line {
-    const int* pre;
-    int t, t1, per, b, front;
+    const int* pre;                // [groups + 1] first tile of each group of 2^shift sequences
+    int t, t1, per, front, shift;
+    int g, b, base, len;           // group, sequence, its first tile (as in pre) and length
 };
+
+// The length of sequence b's place in the line, for one kv head.
+template <int SHIFT>
+__device__ __forceinline__ int seq_length(const PagedParams& p, int b, int front, uint32_t* ws) {
+    const SeqInfo s = seq_info(p.c, b, p.max_q, p.shared, ws);
+    return s.n == 0 ? 0 : make_hull(p.mask, s.kv - s.n, s.kv - 1, p.shared, s.kv, SHIFT).tiles + front;
+}
+
+// The same out of line, for the calls that only many sequences make (the others
+// need not fetch their code).
+template <int SHIFT>
+__device__ __noinline__ int seq_length_again(const PagedParams& p, int b, int front) {
+    return seq_length<SHIFT>(p, b, front, nullptr);
+}
+
+template <int SHIFT>
+__device__ __forceinline__ void open_group(const PagedParams& p, Line& ln) {
+    ln.b = ln.g << ln.shift;
+    ln.base = ln.pre[ln.g];
+    ln.len = ln.shift ? seq_length_again<SHIFT>(p, ln.b, ln.front) : ln.pre[ln.g + 1] - ln.base;
+}
 
 template <int SHIFT>
 __device__ __forceinline__ bool next_seg(const PagedParams& p, Line& ln, SmallSeg& s) {
     if (ln.t >= ln.t1) return false;
-    while (p.c.Hkv * ln.pre[ln.b + 1] <= ln.t) ++ln.b;
+    while (p.c.Hkv * (ln.base + ln.len) <= ln.t) {
+        if (p.c.Hkv * ln.pre[ln.g + 1] <= ln.t) {
+            do ++ln.g; while (p.c.Hkv * ln.pre[ln.g + 1] <= ln.t);
+            open_group<SHIFT>(p, ln);
+        } else {
+            ln.base += ln.len;
+            ln.len = seq_length_again<SHIFT>(p, ++ln.b, ln.front);
+        }
+    }
     s.b = ln.b;
-    const int length = ln.pre[ln.b + 1] - ln.pre[ln.b], off = ln.t - p.c.Hkv * ln.pre[ln.b];
+    const int length = ln.len, off = ln.t - p.c.Hkv * ln.base;
     s.tiles = length - ln.front;
     s.h = off / length;
     const int a = off - s.h * length, e = min(length, a + (ln.t1 - ln.t));
@@ -200,31 +237,41 @@ paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
     if (!p.join_rows) pdl_wait_previous();
     pdl_launch_next();
     // the line of tiles
-    block_prefix<kThreadsS>(p.c.B, pre, reinterpret_cast<int*>(smem + L::kScan), [&](int b) {
-        const SeqInfo s = seq_info(p.c, b, p.max_q, p.shared, cta == 0 ? p.ws : nullptr);
-        return s.n == 0 ? 0 : make_hull(p.mask, s.kv - s.n, s.kv - 1, p.shared, s.kv, SH).tiles;
-    });
-    Line line;
+    Line line{};
     line.pre = pre;
-    line.front = p.c.Hkv * pre[p.c.B] >= kManyTiles * p.ctas;
+    line.shift = group_shift(p.c.B);
+    const int groups = groups_of(p.c.B);
+    int* const scan = reinterpret_cast<int*>(smem + L::kScan);
+    block_prefix<kThreadsS>(groups, pre, scan, [&](int g) {
+        int sum = 0;
+#pragma unroll 1
+        for (int b = g << line.shift; b < min((g + 1) << line.shift, p.c.B); ++b)
+            sum += seq_length<SH>(p, b, 0, cta == 0 ? p.ws : nullptr);
+        return sum;
+    });
+    line.front = p.c.Hkv * pre[groups] >= kManyTiles * p.ctas;
     if (line.front) {
-        block_prefix<kThreadsS>(p.c.B, pre, reinterpret_cast<int*>(smem + L::kScan), [&](int b) {
-            const int tiles = pre[b + 1] - pre[b];
-            return tiles + (tiles > 0);
+        block_prefix<kThreadsS>(groups, pre, scan, [&](int g) {
+            int sum = pre[g + 1] - pre[g];
+            if (line.shift == 0) return sum + (sum > 0);
+            sum = 0;
+#pragma unroll 1
+            for (int b = g << line.shift; b < min((g + 1) << line.shift, p.c.B); ++b) sum += seq_length_again<SH>(p, b, 1);
+            return sum;
         });
     }
-    const int total = p.c.Hkv * pre[p.c.B];
+    const int total = p.c.Hkv * pre[groups];
     line.per = max((total + p.ctas - 1) / p.ctas, 1);
     line.t = (int)min((long long)cta * line.per, (long long)total);
     line.t1 = (int)min((long long)line.t + line.per, (long long)total);
-    line.b = 0;
     if (line.t < line.t1) {
-        int lo = 0, hi = p.c.B - 1;                // the last sequence that starts at or before t
+        int lo = 0, hi = groups - 1;               // the last group that starts at or before t
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
             if (p.c.Hkv * pre[mid] <= line.t) lo = mid; else hi = mid - 1;
         }
-        line.b = lo;
+        line.g = lo;
+        if (warp == kWarps) open_group<SH>(p, line);
     }
     const WaitCtl wc{abort_flag, p.ws, p.timeout_ns};
 
@@ -701,7 +748,7 @@ cudaError_t launch_small(const PagedParams& p, const CUtensorMap& tk, const CUte
                          cudaStream_t s) {
     auto kern = paged_small_kernel<D, SCORE>;
     using L = SmallLayout<D>;
-    constexpr size_t most = L::bytes(kPagedMaxSeqs);
+    constexpr size_t most = L::bytes(kLineEntries);
     static bool attr_set[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);

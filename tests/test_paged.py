@@ -433,6 +433,15 @@ def test_decode_largest_batch(fa):
 
 
 @gpu
+@pytest.mark.parametrize("B", [1000, 1001, 1999, 2001])
+@pytest.mark.parametrize("lengths", ["short", "mixed"])
+def test_decode_many_sequences(fa, B, lengths):
+    new = [0 if b % 5 == 3 or 300 < b < 340 else 1 for b in range(B)]
+    kv = [(b * 37) % 50 + 1 + (900 if lengths == "mixed" and b % 97 == 5 else 0) for b in range(B)]
+    run(fa, Batch(new, kv, 2, 64, 16), 4)
+
+
+@gpu
 @pytest.mark.parametrize("Hq,shared", [(17, 0), (2, 16), (17, 16)])
 def test_largest_batch_of_the_other_kernels(fa, Hq, shared):
     run(fa, Batch([1] * 2048, [shared + (i * 37) % 50 + 1 for i in range(2048)], 1, 64, 16, shared=shared), Hq)
