@@ -4,6 +4,7 @@ Method: Remez exchange for the minimax *relative* error.
   tanh_poly.h  q(v) ~ tanh(u) / u with v = u^2, u in [0, U], so that
                tanh(u) = u q(u^2) is odd by construction.
   tanh2_poly.h the same on the narrower range |u| <= 1/2 at degree 2.
+  tanh_fine_poly.h the same on |u| <= 3/4, the error a tenth.
 Run: ``python gen_poly.py``; writes the headers next to this file.
 """
 from __future__ import annotations
@@ -20,6 +21,10 @@ TANH_DEGREE = 4        # degree in v = u^2 (u^9)
 # reaches about the same error as degree 4 on |u| <= 1.
 TANH2_RANGE = 0.5
 TANH2_DEGREE = 2
+# The paged kernels' polynomial: a cap far above the scores is one of their
+# inputs, and the polynomial's relative error is then that of the scores.
+TANH_FINE_RANGE = 0.75
+TANH_FINE_DEGREE = 4
 
 
 def remez(func, lo, hi, deg, iters=60, grid_n=200001):
@@ -89,3 +94,9 @@ if __name__ == "__main__":
                           f"constexpr float kTanh2Range = {TANH2_RANGE}f;",
                           f"constexpr float kTanh2MaxRelErr = {e:.3e}f;"])
     print(f"tanh2: {c.tolist()} max rel err {e:.3e}")
+    c, e = tanh_coeffs(TANH_FINE_DEGREE, TANH_FINE_RANGE)
+    _write(os.path.join(HERE, "tanh_fine_poly.h"),
+           f"Remez minimax of tanh(u)/u in v = u^2, |u| <= {TANH_FINE_RANGE}, degree {TANH_FINE_DEGREE} in v, "
+           f"max relative error {e:.3e}",
+           "kTanhFineC", c, [f"constexpr float kTanhFineRange = {TANH_FINE_RANGE}f;"])
+    print(f"tanh fine: {c.tolist()} max rel err {e:.3e}")

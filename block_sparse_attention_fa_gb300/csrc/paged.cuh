@@ -2,10 +2,12 @@
 // check it, the keys a unit of work can see, and the split of the work.
 #pragma once
 
+#include <cfloat>
 #include <climits>
 
 #include "fa_internal.h"
 #include "ptx.cuh"
+#include "tanh_fine_poly.h"
 
 namespace fa {
 
@@ -110,10 +112,45 @@ __host__ __device__ __forceinline__ bool tile_open(const PagedMask& m, int kb, i
     return c0 >= jlo && c1 < jhi && (!m.causal || c1 <= i0) && (m.window < 0 || i1 - c0 <= m.window || c1 < m.sinks);
 }
 
-// cap_out tanh(u) through 1 - 2 / (2^(2 log2(e) |u|) + 1).
-__device__ __forceinline__ float softcap_exact(float u, float cap_out) {
+// A soft-cap: the score x mul (base 2) becomes out tanh(x in).  Two forms: with
+// u = x in, x mul q(u^2) where the polynomial q ~ tanh(u) / u holds, off by 8e-7
+// of the score; and out (1 - 2 / (e^(2 |u|) + 1)), off by 3e-7 of the cap at any
+// u.  Up to a cap of 64 that is 2e-5 in the exponent and the second form does
+// alone; far above the scores it would be all of them, so that beyond 64 (fine)
+// it is taken past the polynomial's range only.
+constexpr float kSoftCapCoarse = 64.f;
+struct SoftCap {
+    float in, out, mul;
+    bool fine;
+};
+__device__ __forceinline__ SoftCap soft_cap(float softcap, float scale) {
+    // (finite for the smallest and the largest caps too, so that 0 stays 0)
+    return {fminf(scale / softcap, FLT_MAX), fminf(softcap * kPagedLog2e, FLT_MAX), scale * kPagedLog2e,
+            softcap > kSoftCapCoarse};
+}
+__device__ __forceinline__ float softcap_inner(float x, float u, const SoftCap& c) {
+    const float w = u * u;
+    float q = fmaf(kTanhFineC4, w, kTanhFineC3);
+    q = fmaf(q, w, kTanhFineC2);
+    q = fmaf(q, w, kTanhFineC1);
+    q = fmaf(q, w, kTanhFineC0);
+    return x * c.mul * q;
+}
+__device__ __forceinline__ float softcap_outer(float u, const SoftCap& c) {
     const float e = ex2_approx(2.f * kPagedLog2e * fabsf(u));
-    return copysignf(cap_out * (1.f - __fdividef(2.f, e + 1.f)), u);
+    return copysignf(c.out * (1.f - __fdividef(2.f, e + 1.f)), u);
+}
+// One form or the other (a selection: a branch costs three times as much).
+__device__ __forceinline__ float softcap_pick(float inner, float u, const SoftCap& c) {
+    float y;
+    asm("{\n\t.reg .pred p;\n\tsetp.le.f32 p, %3, %4;\n\tselp.f32 %0, %1, %2, p;\n\t}"
+        : "=f"(y)
+        : "f"(inner), "f"(softcap_outer(u, c)), "f"(fabsf(u)), "f"(kTanhFineRange));
+    return y;
+}
+__device__ __forceinline__ float softcap_one(float x, const SoftCap& c) {
+    const float u = x * c.in;
+    return c.fine ? softcap_pick(softcap_inner(x, u, c), u, c) : softcap_outer(u, c);
 }
 
 // The loader's share of one tile of KT keys: lane l of the warp stands for the

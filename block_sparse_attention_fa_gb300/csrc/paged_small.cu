@@ -364,7 +364,7 @@ paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
     const uint32_t sP = sbase + L::kP;
     // score_mod, to base 2
     const float sl2 = p.scale * kLog2eP;
-    const float cap_in = (SCORE == FA_SCORE_SOFTCAP ? p.scale : 1.f) / p.score.softcap, cap_out = p.score.softcap * kLog2eP;
+    const SoftCap cap = soft_cap(p.score.softcap, SCORE == FA_SCORE_SOFTCAP ? p.scale : 1.f);
     constexpr int kNT = D / 64;                    // n8 tiles of O per warp
     constexpr int kKW = KT / 8, kNK = kKW / 8;     // keys per warp, n8 tiles of S
     const int col0 = warp * (D / 8);               // the warp's first column of O
@@ -444,9 +444,9 @@ paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                         float v = x[nt][c];
                         const float far = fabsf(static_cast<float>(i0 + tok[e] - j));
                         if (SCORE == FA_SCORE_NONE || SCORE == FA_SCORE_REL_BIAS) v *= sl2;
-                        if (SCORE == FA_SCORE_SOFTCAP) v = softcap_exact(v * cap_in, cap_out);
+                        if (SCORE == FA_SCORE_SOFTCAP) v = softcap_one(v, cap);
                         if (SCORE == FA_SCORE_ALIBI) v = fmaf(-slope[e], far, v * sl2);
-                        if (SCORE == FA_SCORE_ALIBI_SOFTCAP) v = softcap_exact(fmaf(-slope[e], far, v * p.scale) * cap_in, cap_out);
+                        if (SCORE == FA_SCORE_ALIBI_SOFTCAP) v = softcap_one(fmaf(-slope[e], far, v * p.scale), cap);
                         if (SCORE == FA_SCORE_REL_BIAS) {
                             const int R = p.score.rel_max, d = min(max(i0 + tok[e] - j, -R), R);
                             v = fmaf(__ldg(p.score.rel_bias + (size_t)hq[e] * (2 * R + 1) + d + R), kLog2eP, v);

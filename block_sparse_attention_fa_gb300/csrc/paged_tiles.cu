@@ -41,7 +41,6 @@
 #include <math_constants.h>
 
 #include "paged.cuh"
-#include "tanh_poly.h"
 
 namespace fa {
 namespace {
@@ -118,30 +117,54 @@ struct TileLayout {
     static_assert(kPre + 4 * (3 * kPagedMaxSeqs + 2) + 1024 <= 227u * 1024u, "shared memory budget");
 };
 
-// x <- cap_out tanh(x).  While no row of the warp is past the range of the
-// minimax polynomial (relative error 7e-6) by that, two elements to an
-// instruction; exactly otherwise, at two MUFU operations per element (4 x 1024
-// new tokens up to 8192 keys: 588 us, 672 with these).
-__device__ __forceinline__ void softcap_all(float (&x)[64], float cap_out) {
-    float am = 0.f;
+// x <- the soft-capped score, base 2.  TRY: where no element of the warp is past
+// the polynomial's range, two elements to an instruction (4 x 1024 new tokens
+// at 8192 keys, cap 30: 529 us).  Otherwise, and always without TRY, the
+// exponential form, at two MUFU operations per element (cap 2: 747).  A cap far
+// above the scores takes the polynomial where it holds, with or without TRY;
+// a warp that needs both forms evaluates both (ALiBi then a cap of 100: 1134 us,
+// 1e5, where the polynomial alone does: 771; 30, exponential: 792).
+template <bool TRY>
+__device__ __forceinline__ void softcap_all(float (&x)[64], const SoftCap& c) {
+    bool inner = false;
+    if (TRY || c.fine) {
+        float am = 0.f;
 #pragma unroll
-    for (int e = 0; e < 64; e += 2) am = fmax3(am, fabsf(x[e]), fabsf(x[e + 1]));
-    if (!__any_sync(0xffffffffu, !(am <= kTanhRange))) {
-        const float q0 = cap_out * kTanhC0, q1 = cap_out * kTanhC1, q2 = cap_out * kTanhC2, q3 = cap_out * kTanhC3,
-                    q4 = cap_out * kTanhC4;
+        for (int e = 0; e < 64; e += 2) am = fmax3(am, fabsf(x[e]), fabsf(x[e + 1]));
+        inner = !__any_sync(0xffffffffu, !(am * c.in <= kTanhFineRange));
+    }
+    const float q0 = c.mul * kTanhFineC0, q1 = c.mul * kTanhFineC1, q2 = c.mul * kTanhFineC2, q3 = c.mul * kTanhFineC3,
+                q4 = c.mul * kTanhFineC4;
+    // u = x in and x mul q(u^2) of a pair
+    auto pair = [&](int e, float& u0, float& u1, float& y0, float& y1) {
+        float w0, w1;
+        ffma2(u0, u1, x[e], x[e + 1], c.in, c.in, -0.f, -0.f);
+        ffma2(w0, w1, u0, u1, u0, u1, -0.f, -0.f);
+        ffma2(y0, y1, w0, w1, q4, q4, q3, q3);
+        ffma2(y0, y1, y0, y1, w0, w1, q2, q2);
+        ffma2(y0, y1, y0, y1, w0, w1, q1, q1);
+        ffma2(y0, y1, y0, y1, w0, w1, q0, q0);
+        ffma2(y0, y1, x[e], x[e + 1], y0, y1, -0.f, -0.f);
+    };
+    if (inner) {
 #pragma unroll
         for (int e = 0; e < 64; e += 2) {
-            float w0, w1, y0, y1;
-            ffma2(w0, w1, x[e], x[e + 1], x[e], x[e + 1], -0.f, -0.f);
-            ffma2(y0, y1, w0, w1, q4, q4, q3, q3);
-            ffma2(y0, y1, y0, y1, w0, w1, q2, q2);
-            ffma2(y0, y1, y0, y1, w0, w1, q1, q1);
-            ffma2(y0, y1, y0, y1, w0, w1, q0, q0);
-            ffma2(x[e], x[e + 1], x[e], x[e + 1], y0, y1, -0.f, -0.f);
+            float u0, u1, y0, y1;
+            pair(e, u0, u1, y0, y1);
+            x[e] = y0;
+            x[e + 1] = y1;
+        }
+    } else if (c.fine) {
+#pragma unroll
+        for (int e = 0; e < 64; e += 2) {
+            float u0, u1, y0, y1;
+            pair(e, u0, u1, y0, y1);
+            x[e] = softcap_pick(y0, u0, c);
+            x[e + 1] = softcap_pick(y1, u1, c);
         }
     } else {
 #pragma unroll
-        for (int e = 0; e < 64; ++e) x[e] = softcap_exact(x[e], cap_out);
+        for (int e = 0; e < 64; ++e) x[e] = softcap_outer(x[e] * c.in, c);
     }
 }
 
@@ -602,8 +625,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
         const uint32_t tS = tmem + 128u * t + lane_off, tO = tmem + 256u + D * t + lane_off;
         const float sl2 = p.scale * kLog2eQ;
-        const float cap_in = (SCORE == FA_SCORE_SOFTCAP ? p.scale : 1.f) / p.score.softcap;
-        const float cap_out = p.score.softcap * kLog2eQ;
+        const SoftCap cap = soft_cap(p.score.softcap, SCORE == FA_SCORE_SOFTCAP ? p.scale : 1.f);
         const bool out32 = (p.flags & FA_OUT_FP32) != 0;
         const float lazy = out32 ? 0.f : kLazyMaxT;
         uint32_t n = 0, uq = 0;
@@ -740,11 +762,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                         // modified score in base 2 otherwise
                         float sc = 1.f;
                         if (SCORE == FA_SCORE_NONE) sc = sl2;
-                        if (SCORE == FA_SCORE_SOFTCAP) {
-#pragma unroll
-                            for (int e = 0; e < 64; ++e) x[e] *= cap_in;
-                            softcap_all(x, cap_out);
-                        }
+                        if (SCORE == FA_SCORE_SOFTCAP) softcap_all<true>(x, cap);
                         if (SCORE == FA_SCORE_ALIBI || SCORE == FA_SCORE_ALIBI_SOFTCAP) {
                             const float di = static_cast<float>(i - ch), mul = SCORE == FA_SCORE_ALIBI ? sl2 : p.scale;
                             if (__all_sync(0xffffffffu, di >= 63.f)) {     // i - j >= 0: affine in the column
@@ -761,10 +779,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                                     x[e] = fmaf(-slope, fabsf(di - static_cast<float>(e)), x[e] * mul);
                             }
                         }
-                        if (SCORE == FA_SCORE_ALIBI_SOFTCAP) {
-#pragma unroll
-                            for (int e = 0; e < 64; ++e) x[e] = softcap_exact(x[e] * cap_in, cap_out);   // (mostly past the polynomial's range)
-                        }
+                        // (small caps: most distances take the score past the polynomial's range)
+                        if (SCORE == FA_SCORE_ALIBI_SOFTCAP) softcap_all<false>(x, cap);
                         if (SCORE == FA_SCORE_REL_BIAS) {
 #pragma unroll
                             for (int e = 0; e < 64; ++e) {
