@@ -110,12 +110,11 @@ fa::MaskParams mask_params(const fa_block_mask* bm) {
     m.table = bm->mask.table;
     m.table_batch = bm->mask.table_batch;
     m.table_words = (bm->kv_len + 31) / 32;
-    if (m.kind == FA_MASK_SINK_WINDOW) {
-        // no pair is further apart, and no key index larger, than these: the
-        // kernels' i - window and j + window then stay within 32 bits
+    // no pair is further apart, and no key index larger, than these: the
+    // kernels' i - window and j + window then stay within 32 bits
+    if (m.kind == FA_MASK_SLIDING_WINDOW || m.kind == FA_MASK_SINK_WINDOW)
         m.window = std::min(m.window, std::max(bm->q_len, bm->kv_len));
-        m.prefix_len = std::min(m.prefix_len, bm->kv_len);
-    }
+    if (m.kind == FA_MASK_SINK_WINDOW) m.prefix_len = std::min(m.prefix_len, bm->kv_len);
     return m;
 }
 
