@@ -210,7 +210,7 @@ struct PagedParams {
 struct PagedJoin {
     PagedParams own;
     PagedParts pre;
-    int own_rows, pre_rows;   // rows per unit of each kernel
+    int own_rows;             // rows per unit of the sequences' own kernel
 };
 
 // Sets this thread's fa_last_error() message and returns `st`.

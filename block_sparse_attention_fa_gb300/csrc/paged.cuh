@@ -16,8 +16,23 @@ constexpr float kPagedLog2e = 1.4426950408889634f, kPagedLn2 = 0.693147180559945
 __host__ __device__ __forceinline__ int imin(int a, int b) { return a < b ? a : b; }
 __host__ __device__ __forceinline__ int imax(int a, int b) { return a > b ? a : b; }
 
-__device__ __forceinline__ int quotient(int n, const FastDiv& f) {
-    return static_cast<int>((__umulhi(f.m, static_cast<uint32_t>(n)) + static_cast<uint32_t>(n)) >> f.s);
+__host__ __device__ __forceinline__ int quotient(int n, const FastDiv& f) {
+    const uint32_t u = static_cast<uint32_t>(n);
+#ifdef __CUDA_ARCH__
+    return static_cast<int>((__umulhi(f.m, u) + u) >> f.s);
+#else
+    return static_cast<int>((static_cast<uint32_t>((static_cast<uint64_t>(f.m) * u) >> 32) + u) >> f.s);
+#endif
+}
+
+// A number of the step's arrays (the line of tiles is walked on the host too,
+// by its test).
+__host__ __device__ __forceinline__ int load_i32(const int32_t* p) {
+#ifdef __CUDA_ARCH__
+    return __ldg(p);
+#else
+    return *p;
+#endif
 }
 
 // A sequence of the step: its rows of the step's tensors and its length.
@@ -52,10 +67,15 @@ __host__ __device__ __forceinline__ bool check_sequence(const PagedView& c, int 
 
 // Reads and checks sequence b; every kernel takes its numbers from here, so
 // that none of them indexes with numbers that were not checked.
-__device__ __forceinline__ SeqInfo seq_info(const PagedView& c, int b, int max_q, int shared, uint32_t* ws) {
+__host__ __device__ __forceinline__ SeqInfo seq_info(const PagedView& c, int b, int max_q, int shared, uint32_t* ws) {
     SeqInfo s;
-    if (!check_sequence(c, b, __ldg(c.q_start + b), __ldg(c.q_start + b + 1), __ldg(c.kv_len + b), max_q, shared, s) && ws)
-        report_sequence(ws, b);
+    const bool fits = check_sequence(c, b, load_i32(c.q_start + b), load_i32(c.q_start + b + 1), load_i32(c.kv_len + b),
+                                     max_q, shared, s);
+#ifdef __CUDA_ARCH__
+    if (!fits && ws) report_sequence(ws, b);
+#else
+    (void)fits, (void)ws;
+#endif
     return s;
 }
 

@@ -42,7 +42,7 @@
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
-#include "paged.cuh"
+#include "paged_line.cuh"
 
 namespace fa {
 namespace {
@@ -54,25 +54,6 @@ constexpr float kLog2eP = 1.4426950408889634f;
 constexpr float kLn2P = 0.6931471805599453f;
 constexpr int kTileOpen = 1, kTileClear = 2;    // every row sees every key; some key is seen by no row
 enum PagedSite : uint32_t { S_PG_FULL = 64, S_PG_EMPTY, S_PG_DRAIN, S_PG_Q, S_PG_Q_EMPTY };
-
-// The part of one unit that falls into a CTA's stretch: tiles k0 .. k1 - 1 of
-// the unit's list.  The loader finds it, ahead of the consumers, who read it
-// from a slot in shared memory (with its rows of Q).
-struct SmallSeg {
-    int b, h, kv, n, q0;
-    int tiles, k0, k1, count;      // count: CTAs that share the unit from here on
-    Hull hull;
-    __device__ __forceinline__ bool begins() const { return k0 == 0; }
-    __device__ __forceinline__ bool ends() const { return k1 == tiles; }
-};
-
-// The line's index in shared memory has at most 1000 entries, so that two CTAs
-// fit on an SM: one per sequence, or per 2, 4 sequences, within which the loader
-// counts for itself (1024 sequences of 512 keys, 32 heads on 8 of 128 columns,
-// pages of 16: 329 us, 470 with an entry for each and one CTA per SM).
-constexpr int kLineEntries = 1000;
-__host__ __device__ constexpr int group_shift(int B) { return B <= kLineEntries ? 0 : B <= 2 * kLineEntries ? 1 : 2; }
-__host__ __device__ constexpr uint32_t groups_of(int B) { return (B + (1 << group_shift(B)) - 1) >> group_shift(B); }
 
 template <int D>
 struct SmallLayout {
@@ -136,71 +117,6 @@ __device__ __forceinline__ bool consumers_all(bool ok) {
     return r != 0;
 }
 
-// A CTA's stretch [t, t1) of the line of tiles.  Once every CTA has some tiles
-// a unit counts as one more (`front` places before its first tile): its start
-// and end cost about as much, and a CTA whose stretch is all short units would
-// end long after the others (32 sequences of 64 keys before 32 of 8192: 166 us,
-// 216 without).  With fewer tiles the units' parts are alike, and the work is
-// best on the first CTAs (16 x 4 rows after a shared prefix of 5024 keys: 17.7
-// us, 20.2 with).
-constexpr int kManyTiles = 4;                    // per CTA
-struct Line {
-    const int* pre;                // [groups + 1] first tile of each group of 2^shift sequences
-    int t, t1, per, front, shift;
-    int g, b, base, len;           // group, sequence, its first tile (as in pre) and length
-};
-
-// The length of sequence b's place in the line, for one kv head.
-template <int SHIFT>
-__device__ __forceinline__ int seq_length(const PagedParams& p, int b, int front, uint32_t* ws) {
-    const SeqInfo s = seq_info(p.c, b, p.max_q, p.shared, ws);
-    return s.n == 0 ? 0 : make_hull(p.mask, s.kv - s.n, s.kv - 1, p.shared, s.kv, SHIFT).tiles + front;
-}
-
-// The same out of line, for the calls that only many sequences make (the others
-// need not fetch their code).
-template <int SHIFT>
-__device__ __noinline__ int seq_length_again(const PagedParams& p, int b, int front) {
-    return seq_length<SHIFT>(p, b, front, nullptr);
-}
-
-template <int SHIFT>
-__device__ __forceinline__ void open_group(const PagedParams& p, Line& ln) {
-    ln.b = ln.g << ln.shift;
-    ln.base = ln.pre[ln.g];
-    ln.len = ln.shift ? seq_length_again<SHIFT>(p, ln.b, ln.front) : ln.pre[ln.g + 1] - ln.base;
-}
-
-template <int SHIFT>
-__device__ __forceinline__ bool next_seg(const PagedParams& p, Line& ln, SmallSeg& s) {
-    if (ln.t >= ln.t1) return false;
-    while (p.c.Hkv * (ln.base + ln.len) <= ln.t) {
-        if (p.c.Hkv * ln.pre[ln.g + 1] <= ln.t) {
-            do ++ln.g; while (p.c.Hkv * ln.pre[ln.g + 1] <= ln.t);
-            open_group<SHIFT>(p, ln);
-        } else {
-            ln.base += ln.len;
-            ln.len = seq_length_again<SHIFT>(p, ++ln.b, ln.front);
-        }
-    }
-    s.b = ln.b;
-    const int length = ln.len, off = ln.t - p.c.Hkv * ln.base;
-    s.tiles = length - ln.front;
-    s.h = off / length;
-    const int a = off - s.h * length, e = min(length, a + (ln.t1 - ln.t));
-    s.k0 = max(a - ln.front, 0);
-    s.k1 = max(e - ln.front, 0);
-    s.kv = __ldg(p.c.kv_len + ln.b);               // (checked when the line was made)
-    s.q0 = __ldg(p.c.q_start + ln.b);
-    s.n = __ldg(p.c.q_start + ln.b + 1) - s.q0;
-    s.hull = make_hull(p.mask, s.kv - s.n, s.kv - 1, p.shared, s.kv, SHIFT);
-    // the places of tile k0 and of the unit's last one
-    const int here = ln.t + max(ln.front - a, 0), last = here - s.k0 + s.tiles - 1;
-    s.count = last / ln.per - here / ln.per + 1;
-    ln.t += e - a;
-    return s.k1 > 0;               // (0: the stretch ends before the unit's first tile)
-}
-
 template <int D, int SCORE>
 __global__ void __launch_bounds__(kThreadsS, 2)
 paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -243,34 +159,18 @@ paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
     const int groups = groups_of(p.c.B);
     int* const scan = reinterpret_cast<int*>(smem + L::kScan);
     block_prefix<kThreadsS>(groups, pre, scan, [&](int g) {
-        int sum = 0;
-#pragma unroll 1
-        for (int b = g << line.shift; b < min((g + 1) << line.shift, p.c.B); ++b)
-            sum += seq_length<SH>(p, b, 0, cta == 0 ? p.ws : nullptr);
-        return sum;
+        return group_length<SH>(p, line.shift, g, cta == 0 ? p.ws : nullptr);
     });
     line.front = p.c.Hkv * pre[groups] >= kManyTiles * p.ctas;
     if (line.front) {
         block_prefix<kThreadsS>(groups, pre, scan, [&](int g) {
-            int sum = pre[g + 1] - pre[g];
-            if (line.shift == 0) return sum + (sum > 0);
-            sum = 0;
-#pragma unroll 1
-            for (int b = g << line.shift; b < min((g + 1) << line.shift, p.c.B); ++b) sum += seq_length_again<SH>(p, b, 1);
-            return sum;
+            return group_length_front<SH>(p, line.shift, g, pre[g + 1] - pre[g]);
         });
     }
     const int total = p.c.Hkv * pre[groups];
-    line.per = max((total + p.ctas - 1) / p.ctas, 1);
-    line.t = (int)min((long long)cta * line.per, (long long)total);
-    line.t1 = (int)min((long long)line.t + line.per, (long long)total);
+    line_share(total, p.ctas, cta, line.per, line.t, line.t1);
     if (line.t < line.t1) {
-        int lo = 0, hi = groups - 1;               // the last group that starts at or before t
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (p.c.Hkv * pre[mid] <= line.t) lo = mid; else hi = mid - 1;
-        }
-        line.g = lo;
+        line.g = line_find(pre, groups, p.c.Hkv, line.t);
         if (warp == kWarps) open_group<SH>(p, line);
     }
     const WaitCtl wc{abort_flag, p.ws, p.timeout_ns};
@@ -702,7 +602,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps<SHARE>) paged_join_units_kerne
     const int r = (SHARE > 1 ? blockIdx.y : blockIdx.y * kJoinWarps<SHARE> + (threadIdx.x >> 5)) * 4 + ((threadIdx.x & 31) >> 3);
     if (t.count == 0 || (r & ~3) >= t.rows) return;        // (uniform: four rows to a warp, and to a block that shares them)
     const bool valid = r < t.rows;
-    const RowParts a{p.parts.slot_o, p.parts.slot_ml, (2LL * blockIdx.x + 1) * rows_per_unit + r, t.count, rows_per_unit};
+    const RowParts a = unit_parts(p.parts, blockIdx.x, t.count, rows_per_unit, r);
     const RowParts none{nullptr, nullptr, 0, 0, 0};
     const int R = t.row0 + r, tok = quotient(R, p.by_group);
     join_rows<D, SHARE>(p, a, none, (long long)(t.q0 + tok) * p.Hq + t.h * p.group + R - tok * p.group, valid, sums);
@@ -731,11 +631,7 @@ __global__ void __launch_bounds__(32 * SHARE) paged_join_rows_kernel(const Paged
     if (b >= p.c.B) return;
     const SeqInfo s = seq_info(p.c, b, p.max_q, p.shared, nullptr);
     if (s.n == 0 || t < s.q0 || t >= s.q0 + s.n) return;
-    const int tiles = pre.x, per = pre.y;
-    const int R = t * p.group + min(gq, p.group - 1), rt = R / j.pre_rows, r = R - rt * j.pre_rows;
-    const int first = (rt * p.c.Hkv + h) * tiles, ca = first / per, cb = (first + tiles - 1) / per;
-    RowParts a{j.pre.slot_o, j.pre.slot_ml, (2LL * ca + 1) * j.pre_rows + r, cb - ca + 1, j.pre_rows};
-    if (ca == cb) a = RowParts{j.pre.row_o, j.pre.row_ml, row, 1, 0};
+    const RowParts a = prefix_parts(j.pre, pre.x, pre.y, p.c.Hkv, t * p.group + min(gq, p.group - 1), h, row);
     RowParts own{p.parts.slot_o, p.parts.slot_ml, d.x, d.y, j.own_rows};
     if (d.x < 0) own = RowParts{p.parts.row_o, p.parts.row_ml, row, 1, 0};
     // (a CTA whose wait ran out leaves its rows' places as the scratch held them)

@@ -40,7 +40,7 @@
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
-#include "paged.cuh"
+#include "paged_line.cuh"
 
 namespace fa {
 namespace {
@@ -77,26 +77,6 @@ enum TBar {
 constexpr uint32_t kSegReaders = 11;             // the MMA, clearing and softmax warps
 enum TSite : uint32_t { S_T_Q = 80, S_T_K_FULL, S_T_K_EMPTY, S_T_V_FULL, S_T_V_EMPTY, S_T_V_OK, S_T_S, S_T_P, S_T_O,
                         S_T_UPD, S_T_DRAIN, S_T_SEG, S_T_SEG_EMPTY };
-
-// What a unit's start and end cost (Q, the pipeline's first and last steps, O)
-// beside its tiles, in tiles: its place in the line is that much longer.
-// Without it a CTA whose stretch is all short units ends long after the others
-// (prompts of 4 x 1024 tokens 92 us, one of 4096 tokens 210); with 2 those
-// take 55 and 123, with 4 57 and 126, with 6 61 and 130, and chunks up to 8192
-// keys 376 to 385 with any.  (The units of a shared prefix are all alike.)
-constexpr int kUnitTiles = 2;
-
-// The part of a unit in a CTA's stretch.
-struct TileSeg {
-    int b, h, row0, rows, q0, n, kv;
-    int jlo, jhi, i0, i1;          // keys of this kernel's part, positions of the unit's rows
-    int tiles, k0, k1, t;          // t: the place of tile k0 in the line
-    Hull hull;
-    __device__ __forceinline__ bool begins() const { return k0 == 0; }
-    __device__ __forceinline__ bool ends() const { return k1 == tiles; }
-    // CTAs that share the unit, from this part on (per: tiles of a CTA)
-    __device__ __forceinline__ int count(int per) const { return (t - k0 + tiles - 1) / per - t / per + 1; }
-};
 
 template <int D>
 struct TileLayout {
@@ -199,76 +179,6 @@ __device__ __forceinline__ void store8(void* dst, const uint32_t* w, bool wide) 
 // Bits a .. 31, and bits 0 .. a, of a word (any a).
 __device__ __forceinline__ uint32_t bits_from(int a) { return a <= 0 ? 0xffffffffu : a > 31 ? 0u : 0xffffffffu << a; }
 __device__ __forceinline__ uint32_t bits_to(int a) { return a < 0 ? 0u : a >= 31 ? 0xffffffffu : 0xffffffffu >> (31 - a); }
-
-struct TileLine {
-    const int *pre, *kv, *q0;           // [B + 1] first tile, [B] length, [B + 1] first row
-    int t, t1, per, b, rt, start;       // start: where unit group (b, rt), its Hkv units, begins in the line
-    int prefix_tiles, prefix_rows, imin, imax;
-};
-
-// The positions of rows 256 rt .. of a sequence of n new tokens.
-__device__ __forceinline__ void unit_rows(const FastDiv& by_group, int n, int kv, int rt, int& i0, int& i1) {
-    const int r0 = rt * kPagedTileRows, r1 = min(r0 + kPagedTileRows, n * static_cast<int>(by_group.d)) - 1;
-    i0 = kv - n + quotient(r0, by_group);
-    i1 = kv - n + quotient(r1, by_group);
-}
-
-// The length of one such unit's place in the line.
-__device__ __forceinline__ int unit_length(const PagedParams& p, int n, int kv, int rt) {
-    int i0, i1;
-    unit_rows(p.by_group, n, kv, rt, i0, i1);
-    return make_hull(p.mask, i0, i1, p.shared, kv, 7).tiles + kUnitTiles;
-}
-
-__device__ __forceinline__ bool next_seg(const PagedParams& p, TileLine& ln, TileSeg& s) {
-    if (ln.t >= ln.t1) return false;
-    int off;
-    if (p.prefix) {
-        s.tiles = ln.prefix_tiles;
-        const int group_tiles = p.c.Hkv * s.tiles, rt = ln.t / group_tiles;
-        off = ln.t - rt * group_tiles;
-        s.b = s.q0 = s.n = s.kv = 0;
-        s.row0 = rt * kPagedTileRows;
-        s.rows = min(kPagedTileRows, ln.prefix_rows - s.row0);
-        s.jlo = 0;
-        s.jhi = p.shared;
-        s.i0 = ln.imin;
-        s.i1 = ln.imax;
-        s.hull = make_hull(p.mask, s.i0, s.i1, s.jlo, s.jhi, 7);
-    } else {
-        while (p.c.Hkv * ln.pre[ln.b + 1] <= ln.t) {
-            ++ln.b;
-            ln.rt = 0;
-            ln.start = p.c.Hkv * ln.pre[ln.b];
-        }
-        s.b = ln.b;
-        s.q0 = ln.q0[s.b];
-        s.n = ln.q0[s.b + 1] - s.q0;
-        s.kv = ln.kv[s.b];
-        s.jlo = p.shared;
-        s.jhi = s.kv;
-        for (;;) {
-            unit_rows(p.by_group, s.n, s.kv, ln.rt, s.i0, s.i1);
-            s.hull = make_hull(p.mask, s.i0, s.i1, s.jlo, s.jhi, 7);
-            const int next = ln.start + p.c.Hkv * (s.hull.tiles + kUnitTiles);
-            if (ln.t < next) break;
-            ln.start = next;
-            ++ln.rt;
-        }
-        s.tiles = s.hull.tiles;
-        off = ln.t - ln.start;
-        s.row0 = ln.rt * kPagedTileRows;
-        s.rows = min(kPagedTileRows, s.n * p.group - s.row0);
-    }
-    const int front = p.prefix ? 0 : kUnitTiles, length = s.tiles + front;
-    s.h = off / length;
-    const int a = off - s.h * length, b = min(length, a + (ln.t1 - ln.t));
-    s.k0 = max(a - front, 0);
-    s.k1 = max(b - front, 0);
-    s.t = ln.t + max(front - a, 0);
-    ln.t += b - a;
-    return s.k1 > 0;               // (0: the stretch ends before the unit's first tile)
-}
 
 // Finds the unit group of ln.b in which the stretch begins: a lane to a group
 // of the next 32.
@@ -380,11 +290,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         __syncthreads();
         line.imin = minmax[0];
         line.imax = minmax[1];
-        const int rows = min(max(__ldg(p.c.q_start + p.c.B), 0), p.c.total_q) * p.group;
-        line.prefix_rows = line.imin <= line.imax ? rows : 0;      // no sequence has rows: nothing to do
-        line.prefix_tiles =
-            line.prefix_rows ? make_hull(p.mask, line.imin, line.imax, 0, p.shared, 7).tiles : 1;
-        total = (line.prefix_rows + kPagedTileRows - 1) / kPagedTileRows * p.c.Hkv * line.prefix_tiles;
+        total = prefix_line(p, line, __ldg(p.c.q_start + p.c.B));
     } else {
         // the sequences' lengths: a warp to each of a few sequences (long
         // prompts have hundreds of units), a thread to each of many
@@ -407,22 +313,15 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         block_prefix<kThreadsT>(p.c.B, pre, reinterpret_cast<int*>(smem + L::kScan), [&](int b) { return pre[b]; });
         total = p.c.Hkv * pre[p.c.B];
     }
-    line.per = max((total + p.ctas - 1) / p.ctas, 1);
-    line.t = (int)min((long long)cta * line.per, (long long)total);
-    line.t1 = (int)min((long long)line.t + line.per, (long long)total);
+    line_share(total, p.ctas, cta, line.per, line.t, line.t1);
     if (p.prefix) {
         if (cta == 0 && threadIdx.x == 0) {
             p.hdr[0] = line.prefix_tiles;
             p.hdr[1] = line.per;
         }
     } else if (line.t < line.t1) {
-        int lo = 0, hi = p.c.B - 1;                // the last sequence that starts at or before t
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (p.c.Hkv * pre[mid] <= line.t) lo = mid; else hi = mid - 1;
-        }
-        line.b = lo;
-        line.start = p.c.Hkv * pre[lo];
+        line.b = line_find(pre, p.c.B, p.c.Hkv, line.t);
+        line.start = p.c.Hkv * pre[line.b];
     }
 
     // Only the loader walks the line; it passes each unit through a two-slot
