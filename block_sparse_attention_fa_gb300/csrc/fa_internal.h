@@ -211,6 +211,7 @@ struct PagedJoin {
     PagedParams own;
     PagedParts pre;
     int own_rows;             // rows per unit of the sequences' own kernel
+    int pre_ctas;             // CTAs of the prefix's
 };
 
 // Sets this thread's fa_last_error() message and returns `st`.

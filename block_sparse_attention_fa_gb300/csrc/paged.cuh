@@ -37,8 +37,11 @@ __host__ __device__ __forceinline__ int load_i32(const int32_t* p) {
 
 // A sequence of the step: its rows of the step's tensors and its length.
 // n = 0: nothing to do (no new tokens, or numbers that contradict each other).
+// ordered: q_start does not decrease here, and starts at 0; where that holds
+// for every sequence, their rows are disjoint and no more than total_q.
 struct SeqInfo {
     int q0, n, kv;
+    bool ordered;
 };
 
 __device__ __forceinline__ void report_sequence(uint32_t* ws, int b) {
@@ -55,7 +58,8 @@ __host__ __device__ __forceinline__ bool check_sequence(const PagedView& c, int 
     s.q0 = q0;
     s.n = 0;
     s.kv = kv;
-    const bool placed = q0 >= 0 && q0 <= q1 && q1 <= c.total_q && (b > 0 || q0 == 0);
+    s.ordered = q0 <= q1 && (b > 0 || q0 == 0);
+    const bool placed = s.ordered && q0 >= 0 && q1 <= c.total_q;
     if (placed && q0 == q1) return true;
     // (q1 - q0 cannot overflow once placed)
     if (!placed || q1 - q0 > max_q || kv < q1 - q0 || kv < shared ||

@@ -318,6 +318,7 @@ fa_status fa_fwd_paged(const fa_paged_kv* c, const fa_paged_fwd_args* a, const f
         j.own = p;
         j.pre = pre.parts;
         j.own_rows = unit_rows;
+        j.pre_ctas = pre.ctas;
         e = fa::launch_paged_join_rows(j, s);
     } else {
         e = fa::launch_paged_join_units(p, unit_rows, s);

@@ -604,6 +604,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps<SHARE>) paged_join_units_kerne
     const bool valid = r < t.rows;
     const RowParts a = unit_parts(p.parts, blockIdx.x, t.count, rows_per_unit, r);
     const RowParts none{nullptr, nullptr, 0, 0, 0};
+    if (!a.within(2LL * gridDim.x * rows_per_unit)) return;     // (the same for all rows of a unit)
     const int R = t.row0 + r, tok = quotient(R, p.by_group);
     join_rows<D, SHARE>(p, a, none, (long long)(t.q0 + tok) * p.Hq + t.h * p.group + R - tok * p.group, valid, sums);
 }
@@ -631,9 +632,11 @@ __global__ void __launch_bounds__(32 * SHARE) paged_join_rows_kernel(const Paged
     if (b >= p.c.B) return;
     const SeqInfo s = seq_info(p.c, b, p.max_q, p.shared, nullptr);
     if (s.n == 0 || t < s.q0 || t >= s.q0 + s.n) return;
-    const RowParts a = prefix_parts(j.pre, pre.x, pre.y, p.c.Hkv, t * p.group + min(gq, p.group - 1), h, row);
+    RowParts a = prefix_parts(j.pre, pre.x, pre.y, p.c.Hkv, t * p.group + min(gq, p.group - 1), h, row);
     RowParts own{p.parts.slot_o, p.parts.slot_ml, d.x, d.y, j.own_rows};
     if (d.x < 0) own = RowParts{p.parts.row_o, p.parts.row_ml, row, 1, 0};
+    // (a q_start that decreases can name rows past the prefix's line)
+    if (a.stride > 0 && !a.within(2LL * j.pre_ctas * kPagedTileRows)) a.count = 0;
     // (a CTA whose wait ran out leaves its rows' places as the scratch held them)
     if (d.x >= 0 && !own.within(2LL * p.ctas * j.own_rows)) own.count = 0;
     join_rows<D, SHARE>(p, a, own, row, valid, sums);

@@ -295,6 +295,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         // the sequences' lengths: a warp to each of a few sequences (long
         // prompts have hundreds of units), a thread to each of many
         const bool few = p.c.B <= kThreadsT / 32;
+        bool ordered = true;
         for (int b = few ? warp : threadIdx.x; b < p.c.B; b += few ? kThreadsT / 32 : kThreadsT) {
             const bool first = !few || lane == 0;
             const SeqInfo s = seq_info(p.c, b, p.max_q, p.shared, cta == 0 && first ? p.ws : nullptr);
@@ -302,6 +303,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
             for (int rt = few ? lane : 0; rt * kPagedTileRows < s.n * p.group; rt += few ? 32 : 1)
                 sum += unit_length(p, s.n, s.kv, rt);
             if (few) sum = __reduce_add_sync(0xffffffffu, sum);
+            ordered = ordered && s.ordered;
             if (first) {
                 pre[b] = sum;
                 len_s[b] = s.kv;
@@ -309,8 +311,11 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                 if (b == p.c.B - 1) q0_s[p.c.B] = s.q0 + s.n;
             }
         }
-        __syncthreads();
-        block_prefix<kThreadsT>(p.c.B, pre, reinterpret_cast<int*>(smem + L::kScan), [&](int b) { return pre[b]; });
+        // Offsets that decrease (0, T, 0, T, ..) can make of T rows any number, more
+        // than 32 bits count and than the slots hold: such a batch is no work.
+        ordered = __syncthreads_and(ordered);
+        block_prefix<kThreadsT>(p.c.B, pre, reinterpret_cast<int*>(smem + L::kScan),
+                                [&](int b) { return ordered ? pre[b] : 0; });
         total = p.c.Hkv * pre[p.c.B];
     }
     line_share(total, p.ctas, cta, line.per, line.t, line.t1);
