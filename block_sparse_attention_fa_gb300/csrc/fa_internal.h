@@ -200,7 +200,7 @@ struct PagedParams {
     PagedParts parts;
     PagedMeta* meta;      // [ctas] (join_rows = 0)
     int2* rowdesc;        // [total_q][Hq] {first slot row or -1, count} (join_rows = 1, own keys)
-    int* hdr;             // {tiles of a prefix unit, tiles per CTA} of the prefix kernel
+    int* hdr;             // {tiles of a prefix unit, tiles per CTA} of the prefix kernel, its mark (8 bytes)
     uint32_t* ws;
     uint64_t timeout_ns;
     uint32_t flags;

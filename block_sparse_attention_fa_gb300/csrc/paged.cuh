@@ -228,6 +228,33 @@ __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy
 __device__ __forceinline__ void pdl_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// The sequences' own kernel beside a shared prefix's.  It is launched once all
+// of the prefix's CTAs have signalled, reads nothing of theirs, and would lose
+// their overlap by waiting for their end (64 chats after a prefix of 16384
+// keys: 55 us, 62 with the wait; 16 x 4 rows after 5024: 19.4 and 24.5).  What
+// both read was written before the prefix's kernel, which has waited for that;
+// but a launch that was signalled early orders no memory by itself.  So the
+// prefix's kernel, behind its wait, writes a mark (release), and the own kernel
+// reads it (acquire): seeing it, it also sees what the wait made visible.  Not
+// seeing it, it waits after all.  The join clears the mark for the next call.
+constexpr unsigned long long kPrefixMark = 0x9d3ac1f05b7e2468ull;
+__device__ __forceinline__ unsigned long long* prefix_mark(const PagedParams& p) {
+    return reinterpret_cast<unsigned long long*>(p.hdr) + 1;
+}
+__device__ __forceinline__ void mark_prefix(const PagedParams& p) {
+    asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(prefix_mark(p)), "l"(kPrefixMark) : "memory");
+}
+// The whole block; the copies that it starts afterwards see the same memory.
+__device__ __forceinline__ void wait_before_prefix(const PagedParams& p) {
+    if (threadIdx.x == 0) {
+        unsigned long long seen;
+        asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(seen) : "l"(prefix_mark(p)) : "memory");
+        if (seen != kPrefixMark) pdl_wait_previous();
+    }
+    __syncthreads();
+    asm volatile("fence.proxy.async;" ::: "memory");
+}
+
 // A wait that only time ends (it guards copies and products still writing).
 __device__ __forceinline__ bool paged_drain_wait(uint32_t bar, uint32_t parity, const WaitCtl& c, uint32_t site) {
     if (mbar_try_wait(bar, parity)) return true;
@@ -274,8 +301,9 @@ __device__ __forceinline__ void block_prefix(int n, int* pre, int* warp_sums, F 
 
 // A launch; `overlap`: as a programmatic dependent of the kernel before it.  Such
 // a kernel starts (barriers, TMEM) while that one ends, and touches no memory
-// that others write before pdl_wait_previous(); a kernel that signals early
-// itself has waited for its own predecessor first, or does so before it ends.
+// that others write before pdl_wait_previous() or, beside a shared prefix,
+// wait_before_prefix().  Every kernel has waited for the one before it by its
+// own end, so that whoever waits for it has waited for all of them.
 template <class K, class... A>
 cudaError_t paged_launch(K kern, dim3 grid, int threads, size_t smem, bool overlap, cudaStream_t s, A... args) {
     cudaLaunchConfig_t cfg{};

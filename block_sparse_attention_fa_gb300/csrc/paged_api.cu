@@ -104,7 +104,7 @@ fa_status check_fwd(const fa_paged_kv* c, const fa_paged_fwd_args* a) {
     return FA_OK;
 }
 
-// The scratch in order: the prefix's two numbers, the units to join, the two
+// The scratch in order: the prefix's two numbers and mark, the units to join, the two
 // slots per CTA; with a shared prefix the same for it, and partials by row.
 struct Scratch {
     size_t hdr, meta, slot_o, slot_ml, row_o, row_ml, desc, pre_slot_o, pre_slot_ml, pre_row_o, pre_row_ml, bytes;

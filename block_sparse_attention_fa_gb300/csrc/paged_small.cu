@@ -150,7 +150,10 @@ paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         mbar_fence_init();
     }
     // (a shared prefix's kernel is no input of this one: it is waited for at the end)
-    if (!p.join_rows) pdl_wait_previous();
+    if (p.join_rows)
+        wait_before_prefix(p);
+    else
+        pdl_wait_previous();
     pdl_launch_next();
     // the line of tiles
     Line line{};
@@ -620,6 +623,7 @@ __global__ void __launch_bounds__(32 * SHARE) paged_join_rows_kernel(const Paged
     pdl_wait_previous();
     const int t = blockIdx.x, h = blockIdx.y;
     const int2 pre = *reinterpret_cast<const int2*>(p.hdr);
+    if ((blockIdx.x | blockIdx.y | blockIdx.z | threadIdx.x) == 0) *prefix_mark(p) = 0;
     const int gq = blockIdx.z * 4 + ((threadIdx.x & 31) >> 3);
     const bool valid = gq < p.group;
     const long long row = (long long)t * p.Hq + h * p.group + min(gq, p.group - 1);

@@ -269,8 +269,14 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
 
     // (a shared prefix's kernel is no input of the sequences' own: that one
     // waits for it at the end)
-    if (p.prefix || !p.join_rows) pdl_wait_previous();
-    pdl_launch_next();
+    if (p.join_rows && !p.prefix)
+        wait_before_prefix(p);
+    else
+        pdl_wait_previous();
+    if (threadIdx.x == 0) {
+        if (p.prefix && cta == 0) mark_prefix(p);
+        pdl_launch_next();
+    }
     // the line of tiles
     TileLine line{};
     line.pre = pre;
