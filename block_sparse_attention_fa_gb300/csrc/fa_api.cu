@@ -575,6 +575,28 @@ fa_status fa_bwd(const fa_bwd_args* a, const fa_block_mask* bm, const fa_block_m
     return ok();
 }
 
+// For the Python binding's default workspaces; not part of the C ABI.
+// The id of the capture that `stream` takes part in, 0 for none.
+uint64_t fa_internal_capture_id(void* stream) {
+    cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+    unsigned long long id = 0;
+    const cudaError_t e = cudaStreamGetCaptureInfo(static_cast<cudaStream_t>(stream), &status, &id, nullptr, nullptr,
+                                                   nullptr, nullptr);
+    if (e != cudaSuccess) {
+        cudaGetLastError();        // (the legacy stream while another one captures)
+        return 0;
+    }
+    return status == cudaStreamCaptureStatusActive ? id : 0;
+}
+
+// Sets this thread's capture mode and returns the one before (-1: failed): in
+// the relaxed mode memory can be allocated and filled on a stream of its own
+// while another is captured.
+int fa_internal_capture_mode(int mode) {
+    cudaStreamCaptureMode m = static_cast<cudaStreamCaptureMode>(mode);
+    return cudaThreadExchangeStreamCaptureMode(&m) == cudaSuccess ? static_cast<int>(m) : -1;
+}
+
 fa_status fa_workspace_check(void* workspace, void* stream) {
     if (!workspace) return fail(FA_ERR_INVALID_ARG, "workspace is NULL");
     cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -169,6 +169,10 @@ def load_library(path: str = LIB_PATH):
     h.fa_paged_scratch_bytes.argtypes = [ctypes.c_void_p] * 2
     h.fa_fwd_paged.restype = ctypes.c_int
     h.fa_fwd_paged.argtypes = [ctypes.c_void_p] * 5 + [ctypes.c_size_t] + [ctypes.c_void_p] * 2
+    h.fa_internal_capture_id.restype = ctypes.c_uint64
+    h.fa_internal_capture_id.argtypes = [ctypes.c_void_p]
+    h.fa_internal_capture_mode.restype = ctypes.c_int
+    h.fa_internal_capture_mode.argtypes = [ctypes.c_int]
     h.fa_workspace_check.restype = ctypes.c_int
     h.fa_workspace_check.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
     h.fa_last_error.restype = ctypes.c_char_p
@@ -205,9 +209,11 @@ def _ptr(t: Optional[torch.Tensor]):
 class Workspace:
     """fa_workspace_bytes() zero-filled device bytes for status flags."""
 
-    def __init__(self, device=None):
-        n = load_library().fa_workspace_bytes()
-        self.tensor = torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+    def __init__(self, device=None, tensor: Optional[torch.Tensor] = None):
+        if tensor is None:
+            tensor = torch.zeros(load_library().fa_workspace_bytes(), dtype=torch.uint8, device=device or "cuda")
+        self.tensor = tensor
+        self.graphs = []          # a default workspace: those of the graphs captured on its stream
 
     @property
     def ptr(self):
@@ -215,33 +221,83 @@ class Workspace:
 
     def check(self, stream=None):
         """Synchronise and raise FAError if a kernel flagged a device-side failure."""
-        _check(load_library().fa_workspace_check(self.ptr, _stream_ptr(stream)))
+        for ws in (self, *self.graphs):
+            _check(load_library().fa_workspace_check(ws.ptr, _stream_ptr(stream)))
 
 
 _default_ws = {}
+_ws_slots = {}
+_ws_lock = threading.Lock()
+_WS_SLOTS = 64
+_CAPTURE_RELAXED = 2           # cudaStreamCaptureModeRelaxed
 
 
 def default_workspace(device, stream=None) -> Workspace:
     """The binding's workspace for (device, stream).  Launches that may run
     concurrently must not share a workspace (the forward keeps its work
-    queue there), so each stream gets its own."""
+    queue there), so each stream gets its own, and each graph that is captured
+    on it: graphs may be replayed at once.  The stream's check() covers those of
+    its graphs."""
     dev = torch.device(device)
     idx = dev.index if dev.index is not None else torch.cuda.current_device()
-    return _workspace_of(idx, _raw_stream(idx) if stream is None else stream.cuda_stream)
+    raw = _raw_stream(idx) if stream is None else stream.cuda_stream
+    return _workspace_of(idx, raw, _capture_of(idx, raw, stream is not None))
 
 
-def _workspace_of(idx: int, raw: int) -> Workspace:
-    ws = _default_ws.get((idx, raw))
+def _capture_of(idx: int, raw: int, other: bool) -> int:
+    """The capture that a call on the stream becomes part of (0: none).  ``other``: not the current device's current
+    stream."""
+    if not other and not _capturing() and idx == _device_now():
+        return 0
+    return load_library().fa_internal_capture_id(raw)
+
+
+def _workspace_of(idx: int, raw: int, capture: int) -> Workspace:
+    ws = _default_ws.get((idx, raw, capture))
     if ws is None:
-        ws = _default_ws[(idx, raw)] = Workspace(torch.device("cuda", idx))
+        with _ws_lock:
+            ws = _default_ws.get((idx, raw, 0))
+            if ws is None:
+                ws = _default_ws[(idx, raw, 0)] = Workspace(tensor=_ws_slot(idx))
+            if capture:
+                eager, ws = ws, Workspace(tensor=_ws_slot(idx))
+                eager.graphs.append(ws)
+                _default_ws[(idx, raw, capture)] = ws
     return ws
+
+
+def _ws_slot(idx: int) -> torch.Tensor:
+    """A zero-filled piece for one workspace.  They are made several at a time and filled before they are handed out,
+    outside any capture, since no fill on one stream comes before a launch on another."""
+    free = _ws_slots.setdefault(idx, [])
+    if not free:
+        lib = load_library()
+        with torch.cuda.device(idx):
+            while True:                            # (streams come round, and this one might be in a capture)
+                side = torch.cuda.Stream(idx)
+                if not lib.fa_internal_capture_id(side.cuda_stream):
+                    break
+            mode = lib.fa_internal_capture_mode(_CAPTURE_RELAXED)
+            try:
+                with torch.cuda.stream(side):
+                    slab = torch.zeros((_WS_SLOTS, lib.fa_workspace_bytes()), dtype=torch.uint8,
+                                       device=torch.device("cuda", idx))
+                side.synchronize()
+            finally:
+                lib.fa_internal_capture_mode(mode)
+        free.extend(slab.unbind(0))
+    return free.pop()
 
 
 def _launch(device: torch.device, stream, workspace):
     """The workspace's address and the stream of a call on tensors of ``device``."""
+    if stream is None and device.index == _device_now():
+        raw = _raw_stream(device.index)
+        if workspace is None:
+            workspace = _workspace_of(device.index, raw, _capture_of(device.index, raw, False))
+        return workspace.tensor.data_ptr(), raw
     if workspace is None:
-        workspace = default_workspace(device, stream) if stream is not None or device.index != _device_now() else \
-            _workspace_of(device.index, _raw_stream(device.index))
+        workspace = default_workspace(device, stream)
     return workspace.tensor.data_ptr(), _raw_stream(_device_now()) if stream is None else stream.cuda_stream
 
 
@@ -713,7 +769,7 @@ def kv_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, k_cac
     a = _KV_APPEND.pack(Hq, rot, rope_len, 1 if interleaved else 0, qp, k.data_ptr(), v.data_ptr(), op, *qs, *ks, *vs,
                         *os_, cp, sp, pp)
     raw = _raw_stream(dev) if stream is None else stream.cuda_stream
-    ws = workspace or _workspace_of(dev, raw)
+    ws = workspace or _workspace_of(dev, raw, _capture_of(dev, raw, stream is not None))
     st = _call_on(dev, load_library().fa_kv_append, c, a, ws.tensor.data_ptr(), raw)
     if st != OK:
         _check(st)
@@ -770,14 +826,15 @@ def fwd_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, pag
     sc = _SCORE.pack(SCORE_KINDS[score], softcap, sp, bp, rel_max)
     lib = load_library()
     raw = _raw_stream(dev) if stream is None else stream.cuda_stream
-    ws = workspace or _workspace_of(dev, raw)
+    capture = _capture_of(dev, raw, stream is not None)
+    ws = workspace or _workspace_of(dev, raw, capture)
 
     if scratch is not None:
         if scratch.get_device() != dev or not scratch.is_contiguous():
             raise ValueError("scratch must be a contiguous tensor on q's device")
         st = _call_on(dev, lib.fa_fwd_paged, c, a, m, sc, scratch.data_ptr(), scratch.numel() * scratch.element_size(),
                       ws.tensor.data_ptr(), raw)
-    elif stream is not None or _capturing():
+    elif stream is not None or capture:
         # (no bytes: the arguments are wrong, and the call says how)
         scratch = _new(_call_on(dev, lib.fa_paged_scratch_bytes, c, a) or 16, torch.uint8, q.device, stream)
         st = _call_on(dev, lib.fa_fwd_paged, c, a, m, sc, scratch.data_ptr(), scratch.numel(), ws.tensor.data_ptr(), raw)
