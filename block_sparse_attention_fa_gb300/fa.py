@@ -301,17 +301,29 @@ def _launch(device: torch.device, stream, workspace):
     return workspace.tensor.data_ptr(), _raw_stream(_device_now()) if stream is None else stream.cuda_stream
 
 
+def _new(shape, dtype, device, stream):
+    """An output or scratch of a call on ``stream`` (None: the current one).  Memory of another stream is that
+    stream's: what the current one still does with the block's last tenant must not reach it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    now = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(now)                          # where the caller goes on with it
+    return t
+
+
 class _IndexArrays:
     """The two count and two index arrays of a (transposed) BlockMask in one allocation: four would take longer to
     allocate than the arrays of a short sequence take to build.  Each starts on a 16-byte boundary."""
 
-    def __init__(self, counts, indices, device):
+    def __init__(self, counts, indices, device, stream):
         self.shapes = (counts, indices, counts, indices)
         at = [0]
         for s in self.shapes:
             at.append(at[-1] + (math.prod(s) + 3) // 4 * 4)
         self.at = at
-        self.buf = torch.empty(at[-1], dtype=torch.int32, device=device)
+        self.buf = _new((at[-1],), torch.int32, device, stream)
         base = self.buf.data_ptr()
         self.ptrs = [base + 4 * x for x in at[:-1]]
 
@@ -327,7 +339,7 @@ class BlockMask:
     full_kv_num_blocks = property(lambda self: self._arrays[2])
     full_kv_indices = property(lambda self: self._arrays[3])
 
-    def __init__(self, B, H, q_len, kv_len, mask, window, prefix_len, seg_ids, device, table=None):
+    def __init__(self, B, H, q_len, kv_len, mask, window, prefix_len, seg_ids, device, table=None, stream=None):
         if min(B, H, q_len, kv_len) < 1:          # the library says what is wrong
             _check(load_library().fa_block_mask_shape(B, H, q_len, kv_len, None, None, None))
         self.B, self.H, self.q_len, self.kv_len = B, H, q_len, kv_len
@@ -335,7 +347,7 @@ class BlockMask:
         self.mask, self.window, self.prefix_len = mask, window, prefix_len
         self.seg_ids = seg_ids
         self.table = table
-        self._arrays = _IndexArrays((B, H, self.nq), (B, H, self.nq, self.nkv), device)
+        self._arrays = _IndexArrays((B, H, self.nq), (B, H, self.nq, self.nkv), device, stream)
         self.device = self._arrays.buf.device
         self._cols = None
         s = BlockMaskStruct()
@@ -368,7 +380,8 @@ class BlockMask:
     def _build_cols(self, stream, workspace, rebuild=False):
         if self._cols is None or rebuild:
             if self._cols is None:
-                self._cols = _IndexArrays((self.B, self.H, self.nkv), (self.B, self.H, self.nkv, self.nq), self.device)
+                self._cols = _IndexArrays((self.B, self.H, self.nkv), (self.B, self.H, self.nkv, self.nq), self.device,
+                                          stream)
                 self._cols_struct = BlockMaskColsStruct(*self._cols.ptrs)
             ws, raw = _launch(self.device, stream, workspace)
             _check(load_library().fa_block_mask_build_cols(ctypes.byref(self.struct), ctypes.byref(self._cols_struct),
@@ -414,7 +427,7 @@ def block_mask(mask: str, B: int, H: int, q_len: int, kv_len: int, *, window: in
         if mask != "sink_window" or prefix_len:
             raise ValueError("sinks applies to the sink_window mask (and excludes prefix_len)")
         prefix_len = sinks
-    bm = BlockMask(B, H, q_len, kv_len, mask, window, prefix_len, seg_ids, device or "cuda", table=table)
+    bm = BlockMask(B, H, q_len, kv_len, mask, window, prefix_len, seg_ids, device or "cuda", table=table, stream=stream)
     return bm.rebuild(stream, workspace)
 
 
@@ -472,9 +485,9 @@ def fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, bm: BlockMask, *, sco
     B, Hq, Tq, D = q.shape
     Hkv, Tkv = k.shape[1], k.shape[2]
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.float32 if out_fp32 else q.dtype, device=q.device)
+        out = _new(q.shape, torch.float32 if out_fp32 else q.dtype, q.device, stream)
     if lse is None:
-        lse = torch.empty((B, Hq, Tq), dtype=torch.float32, device=q.device)
+        lse = _new((B, Hq, Tq), torch.float32, q.device, stream)
     _check_fwd_tensors(q, k, v, out, lse, out_fp32, alibi_slopes, rel_bias, rel_max, bm)
     a = FwdArgs()
     a.dtype, a.B, a.Hq, a.Hkv, a.q_len, a.kv_len, a.D = dt, B, Hq, Hkv, Tq, Tkv, D
@@ -556,10 +569,10 @@ def decode_splits(q: torch.Tensor, k: torch.Tensor, bm: BlockMask) -> int:
     return int(load_library().fa_decode_splits(ctypes.byref(a), ctypes.byref(bm.struct)))
 
 
-def decode_partials(q: torch.Tensor, num_splits: int) -> torch.Tensor:
+def decode_partials(q: torch.Tensor, num_splits: int, stream=None) -> torch.Tensor:
     """fp32 scratch for fa_fwd_decode: [B, Hq, q_len, num_splits, D + 2]."""
     B, Hq, Tq, D = q.shape
-    return torch.empty((B, Hq, Tq, num_splits, D + 2), dtype=torch.float32, device=q.device)
+    return _new((B, Hq, Tq, num_splits, D + 2), torch.float32, q.device, stream)
 
 
 def fwd_decode(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, bm: BlockMask, *, score: str = "none",
@@ -578,9 +591,9 @@ def fwd_decode(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, bm: BlockMask,
             raise ValueError("q, k, v must be contiguous CUDA tensors [B, H, T, D]")
     B, Hq, Tq, D = q.shape
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.float32 if out_fp32 else q.dtype, device=q.device)
+        out = _new(q.shape, torch.float32 if out_fp32 else q.dtype, q.device, stream)
     if lse is None:
-        lse = torch.empty((B, Hq, Tq), dtype=torch.float32, device=q.device)
+        lse = _new((B, Hq, Tq), torch.float32, q.device, stream)
     want = torch.float32 if out_fp32 else torch.bfloat16
     if out.dtype != want or not out.is_cuda or not out.is_contiguous() or tuple(out.shape) != tuple(q.shape):
         raise ValueError(f"out must be a contiguous CUDA {want} tensor of q's shape")
@@ -592,7 +605,7 @@ def fwd_decode(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, bm: BlockMask,
     if num_splits == 0:
         num_splits = int(lib.fa_decode_splits(ctypes.byref(a), ctypes.byref(bm.struct))) or 1
     if partials is None:
-        partials = decode_partials(q, num_splits)
+        partials = decode_partials(q, num_splits, stream)
     if partials.dtype != torch.float32 or not partials.is_cuda or not partials.is_contiguous():
         raise ValueError("partials must be a contiguous CUDA float32 tensor (see decode_partials)")
     sc = _score_desc(score, softcap, alibi_slopes, rel_bias, rel_max)
@@ -603,11 +616,11 @@ def fwd_decode(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, bm: BlockMask,
     return out, lse
 
 
-def bwd_rowstats(q: torch.Tensor) -> torch.Tensor:
+def bwd_rowstats(q: torch.Tensor, stream=None) -> torch.Tensor:
     """fp32 scratch for fa_bwd: fa_bwd_rowstats_bytes() bytes as a flat tensor."""
     B, Hq, Tq, _ = q.shape
     n = load_library().fa_bwd_rowstats_bytes(B, Hq, Tq) // 4
-    return torch.empty(n, dtype=torch.float32, device=q.device)
+    return _new((n,), torch.float32, q.device, stream)
 
 
 def bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor, lse: torch.Tensor,
@@ -628,11 +641,10 @@ def bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor, lse:
         raise ValueError("o and dout must have q's shape")
     if k.shape != v.shape or k.shape[0] != B or k.shape[3] != D:
         raise ValueError("k and v must be [B, Hkv, kv_len, D] with q's B and D")
-    f32 = dict(dtype=torch.float32, device=q.device)
-    dq = torch.empty((B, Hq, Tq, D), **f32) if dq is None else dq
-    dk = torch.empty((B, Hkv, Tkv, D), **f32) if dk is None else dk
-    dv = torch.empty((B, Hkv, Tkv, D), **f32) if dv is None else dv
-    rowstats = bwd_rowstats(q) if rowstats is None else rowstats
+    dq = _new((B, Hq, Tq, D), torch.float32, q.device, stream) if dq is None else dq
+    dk = _new((B, Hkv, Tkv, D), torch.float32, q.device, stream) if dk is None else dk
+    dv = _new((B, Hkv, Tkv, D), torch.float32, q.device, stream) if dv is None else dv
+    rowstats = bwd_rowstats(q, stream) if rowstats is None else rowstats
     for name, t, shape in (("lse", lse, (B, Hq, Tq)), ("dq", dq, (B, Hq, Tq, D)), ("dk", dk, (B, Hkv, Tkv, D)),
                            ("dv", dv, (B, Hkv, Tkv, D))):
         if t.dtype is not torch.float32 or not t.is_cuda or not t.is_contiguous() or t.shape != shape:
@@ -691,18 +703,6 @@ def _rows(name, t, total, H, D, dev):
         raise ValueError(f"{name}'s last dimension must be contiguous")
     # the stride of a dimension of one entry says nothing
     return ts if n > 1 else D, hs if h > 1 else D
-
-
-def _new(shape, dtype, device, stream):
-    """An output or scratch of a call on ``stream`` (None: the current one).  Memory of another stream is that
-    stream's: what the current one still does with the block's last tenant must not reach it."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    now = torch.cuda.current_stream(device)
-    with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
-    t.record_stream(now)                          # where the caller goes on with it
-    return t
 
 
 def _call_on(dev, fn, *args):
