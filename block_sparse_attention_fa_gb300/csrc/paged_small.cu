@@ -50,8 +50,6 @@ namespace {
 constexpr int kWarps = 8;                        // consumers; warp 8 loads
 constexpr int kThreadsS = 32 * (kWarps + 1);
 constexpr int kRows = kPagedSmallRows;
-constexpr float kLog2eP = 1.4426950408889634f;
-constexpr float kLn2P = 0.6931471805599453f;
 constexpr int kTileOpen = 1, kTileClear = 2;    // every row sees every key; some key is seen by no row
 enum PagedSite : uint32_t { S_PG_FULL = 64, S_PG_EMPTY, S_PG_DRAIN, S_PG_Q, S_PG_Q_EMPTY };
 
@@ -266,7 +264,7 @@ paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
     float* const ssum = reinterpret_cast<float*>(smem + L::kSum);
     const uint32_t sP = sbase + L::kP;
     // score_mod, to base 2
-    const float sl2 = p.scale * kLog2eP;
+    const float sl2 = p.scale * kPagedLog2e;
     const SoftCap cap = soft_cap(p.score.softcap, SCORE == FA_SCORE_SOFTCAP ? p.scale : 1.f);
     constexpr int kNT = D / 64;                    // n8 tiles of O per warp
     constexpr int kKW = KT / 8, kNK = kKW / 8;     // keys per warp, n8 tiles of S
@@ -288,7 +286,7 @@ paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
             const int r = min(gr + 8 * e, rows - 1);
             tok[e] = quotient(r, p.by_group);
             hq[e] = s.h * p.group + r - tok[e] * p.group;
-            if (SCORE == FA_SCORE_ALIBI) slope[e] = __ldg(p.score.slopes + hq[e]) * kLog2eP;
+            if (SCORE == FA_SCORE_ALIBI) slope[e] = __ldg(p.score.slopes + hq[e]) * kPagedLog2e;
             if (SCORE == FA_SCORE_ALIBI_SOFTCAP) slope[e] = __ldg(p.score.slopes + hq[e]);
         }
         // Q's fragments (what the rows past the unit's hold stays in those rows)
@@ -352,7 +350,7 @@ paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                         if (SCORE == FA_SCORE_ALIBI_SOFTCAP) v = softcap_one(fmaf(-slope[e], far, v * p.scale), cap);
                         if (SCORE == FA_SCORE_REL_BIAS) {
                             const int R = p.score.rel_max, d = min(max(i0 + tok[e] - j, -R), R);
-                            v = fmaf(__ldg(p.score.rel_bias + (size_t)hq[e] * (2 * R + 1) + d + R), kLog2eP, v);
+                            v = fmaf(__ldg(p.score.rel_bias + (size_t)hq[e] * (2 * R + 1) + d + R), kPagedLog2e, v);
                         }
                         if (!open && !paged_visible(p.mask, i0 + tok[e], j, p.shared, s.kv)) v = -CUDART_INF_F;
                         x[nt][c] = v;
@@ -463,7 +461,7 @@ paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                     else
                         *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + at) = pack_bf16x2(y0, y1);
                 }
-                if (warp == 0 && tq == 0) p.lse[row] = sum == 0.f ? -CUDART_INF_F : (m[e] + log2f(sum)) * kLn2P;
+                if (warp == 0 && tq == 0) p.lse[row] = sum == 0.f ? -CUDART_INF_F : (m[e] + log2f(sum)) * kPagedLn2;
             } else {
                 const long long slot = whole ? row : (2LL * cta + (s.begins() ? 1 : 0)) * kRows + r;
                 float* dst = (whole ? p.parts.row_o : p.parts.slot_o) + slot * D + col0 + 2 * tq;
@@ -591,7 +589,7 @@ __device__ __forceinline__ void join_rows(const PagedParams& p, const RowParts& 
             *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + at) =
                 make_uint2(pack_bf16x2(o[c].x * inv, o[c].y * inv), pack_bf16x2(o[c].z * inv, o[c].w * inv));
     }
-    if (sub == 0) p.lse[row] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * kLn2P;
+    if (sub == 0) p.lse[row] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * kPagedLn2;
 }
 
 // Without a shared prefix: block (c, y) joins rows of the unit that starts in

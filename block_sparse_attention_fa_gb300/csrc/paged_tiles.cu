@@ -52,8 +52,6 @@ constexpr int kThreadsT = 384;
 constexpr uint32_t kRegsSoftmaxT = 184, kRegsOtherT = 136;
 static_assert(2 * kRegsSoftmaxT + kRegsOtherT == 3 * 168, "register split must match the launch");
 constexpr uint32_t kTmemColsT = 512;
-constexpr float kLog2eQ = 1.4426950408889634f;
-constexpr float kLn2Q = 0.6931471805599453f;
 constexpr int kMaxRing = 4;
 // With bf16 output the running max is raised (and O, l rescaled) only when it
 // grows by more than 2^8; with fp32 output it follows every increase, so that
@@ -534,7 +532,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         const int t = warp >> 2, wq = warp & 3, r = wq * 32 + lane;
         const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
         const uint32_t tS = tmem + 128u * t + lane_off, tO = tmem + 256u + D * t + lane_off;
-        const float sl2 = p.scale * kLog2eQ;
+        const float sl2 = p.scale * kPagedLog2e;
         const SoftCap cap = soft_cap(p.score.softcap, SCORE == FA_SCORE_SOFTCAP ? p.scale : 1.f);
         const bool out32 = (p.flags & FA_OUT_FP32) != 0;
         const float lazy = out32 ? 0.f : kLazyMaxT;
@@ -606,7 +604,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                 }
                 if (valid) {
                     if (last) {
-                        p.lse[row] = l == 0.f ? -CUDART_INF_F : (m_use + log2f(l)) * kLn2Q;
+                        p.lse[row] = l == 0.f ? -CUDART_INF_F : (m_use + log2f(l)) * kPagedLn2;
                     } else {
                         (whole ? p.parts.row_ml : p.parts.slot_ml)[at] = make_float2(m_use, l);
                         if (p.join_rows && !p.prefix && s.begins())
@@ -642,7 +640,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                     i = max(len_s[lo] - q0_s[lo + 1] + trow, -1);
                 }
                 float slope = 0.f;
-                if (SCORE == FA_SCORE_ALIBI) slope = __ldg(p.score.slopes + hq) * kLog2eQ;
+                if (SCORE == FA_SCORE_ALIBI) slope = __ldg(p.score.slopes + hq) * kPagedLog2e;
                 if (SCORE == FA_SCORE_ALIBI_SOFTCAP) slope = __ldg(p.score.slopes + hq);
                 const float* rb = nullptr;
                 if (SCORE == FA_SCORE_REL_BIAS) rb = p.score.rel_bias + (size_t)hq * (2 * p.score.rel_max + 1);
@@ -695,7 +693,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
 #pragma unroll
                             for (int e = 0; e < 64; ++e) {
                                 const int rr = min(max(i - ch - e, -p.score.rel_max), p.score.rel_max);
-                                x[e] = fmaf(__ldg(rb + rr + p.score.rel_max), kLog2eQ, x[e] * sl2);
+                                x[e] = fmaf(__ldg(rb + rr + p.score.rel_max), kPagedLog2e, x[e] * sl2);
                             }
                         }
                         if (!open) {

@@ -79,7 +79,8 @@ typedef struct fa_paged_kv {
  *               other two strides given in elements (multiples of 8); 16-byte
  *               aligned.  Slices of one fused projection are the usual case.
  *   q_out       device bf16, as q with its own strides; may be q itself (the
- *               same pointer and strides), but must not overlap it otherwise.
+ *               same pointer and strides), but must not overlap it otherwise, nor
+ *               k or v.
  *               Its rows must not overlap: heads lie within the token stride,
  *               or tokens within the head stride.
  *               Hq = 0: no queries (q and q_out are ignored).
