@@ -427,6 +427,10 @@ def block_mask(mask: str, B: int, H: int, q_len: int, kv_len: int, *, window: in
         if mask != "sink_window" or prefix_len:
             raise ValueError("sinks applies to the sink_window mask (and excludes prefix_len)")
         prefix_len = sinks
+    # (a field of a ctypes structure would take the low 32 bits of a larger number)
+    for name, x in (("window", window), ("sinks" if sinks else "prefix_len", prefix_len)):
+        if not -2**31 <= x < 2**31:
+            raise ValueError(f"{name} must be a 32-bit integer (got {x})")
     bm = BlockMask(B, H, q_len, kv_len, mask, window, prefix_len, seg_ids, device or "cuda", table=table, stream=stream)
     return bm.rebuild(stream, workspace)
 
@@ -687,8 +691,8 @@ def _paged_kv(k_cache, v_cache, page_table, kv_len, q_start, total_q, dev):
         raise ValueError(f"page_table has {B} rows: kv_len must hold {B} lengths and q_start {B + 1} offsets "
                          f"(got {kv_len.numel()}, {q_start.numel()})")
     num_pages, Hkv, page, D = shape
-    return _PAGED_KV.pack(B, Hkv, D, num_pages, page, max_pages, total_q, k_cache.data_ptr(), v_cache.data_ptr(),
-                          page_table.data_ptr(), kv_len.data_ptr(), q_start.data_ptr()), Hkv, D
+    return _packed(_PAGED_KV, "the paged cache", B, Hkv, D, num_pages, page, max_pages, total_q, k_cache.data_ptr(),
+                   v_cache.data_ptr(), page_table.data_ptr(), kv_len.data_ptr(), q_start.data_ptr()), Hkv, D
 
 
 def _rows(name, t, total, H, D, dev):
@@ -703,6 +707,14 @@ def _rows(name, t, total, H, D, dev):
         raise ValueError(f"{name}'s last dimension must be contiguous")
     # the stride of a dimension of one entry says nothing
     return ts if n > 1 else D, hs if h > 1 else D
+
+
+def _packed(layout, what, *values):
+    """The packed struct of a paged call; numbers that its fields do not hold are refused like the other arguments."""
+    try:
+        return layout.pack(*values)
+    except (struct.error, OverflowError):
+        raise ValueError(f"{what}: a number is past the 32 bits of its field (got {values})") from None
 
 
 def _call_on(dev, fn, *args):
@@ -766,8 +778,8 @@ def kv_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, k_cac
                 or positions.numel() != total:
             raise ValueError("positions must be a contiguous int32 tensor with one entry per row")
         pp = positions.data_ptr()
-    a = _KV_APPEND.pack(Hq, rot, rope_len, 1 if interleaved else 0, qp, k.data_ptr(), v.data_ptr(), op, *qs, *ks, *vs,
-                        *os_, cp, sp, pp)
+    a = _packed(_KV_APPEND, "kv_append", Hq, rot, rope_len, 1 if interleaved else 0, qp, k.data_ptr(), v.data_ptr(), op,
+                *qs, *ks, *vs, *os_, cp, sp, pp)
     raw = _raw_stream(dev) if stream is None else stream.cuda_stream
     ws = workspace or _workspace_of(dev, raw, _capture_of(dev, raw, stream is not None))
     st = _call_on(dev, load_library().fa_kv_append, c, a, ws.tensor.data_ptr(), raw)
@@ -819,11 +831,11 @@ def fwd_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, pag
         raise ValueError(f"unknown mask {mask!r} or score {score!r}")
     if sinks and mask != "sink_window":
         raise ValueError("sinks applies to the sink_window mask")
-    a = _PAGED_FWD.pack(Hq, (total or 1) if max_q_len is None else max_q_len, shared_len,
-                        0.0 if scale is None else scale, q.data_ptr(), *qs, out.data_ptr(), lse.data_ptr(), timeout_ms,
-                        OUT_FP32 if out_fp32 else 0)
-    m = _MASK.pack(MASK_KINDS[mask], window, sinks, 0, 0, 0, 0)
-    sc = _SCORE.pack(SCORE_KINDS[score], softcap, sp, bp, rel_max)
+    a = _packed(_PAGED_FWD, "fwd_paged", Hq, (total or 1) if max_q_len is None else max_q_len, shared_len,
+                0.0 if scale is None else scale, q.data_ptr(), *qs, out.data_ptr(), lse.data_ptr(), timeout_ms,
+                OUT_FP32 if out_fp32 else 0)
+    m = _packed(_MASK, "the mask", MASK_KINDS[mask], window, sinks, 0, 0, 0, 0)
+    sc = _packed(_SCORE, "the score", SCORE_KINDS[score], softcap, sp, bp, rel_max)
     lib = load_library()
     raw = _raw_stream(dev) if stream is None else stream.cuda_stream
     capture = _capture_of(dev, raw, stream is not None)
@@ -860,8 +872,8 @@ def paged_scratch(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     """Scratch for fwd_paged calls of these shapes, for callers that keep their own."""
     with torch.cuda.device(q.device):
         c, _, _ = _paged_kv(k_cache, v_cache, page_table, kv_len, q_start, q.shape[0], q.get_device())
-        a = _PAGED_FWD.pack(q.shape[1], max(q.shape[0], 1) if max_q_len is None else max_q_len, shared_len, 0.0, 0, 0, 0,
-                            0, 0, 0, 0)
+        a = _packed(_PAGED_FWD, "paged_scratch", q.shape[1], max(q.shape[0], 1) if max_q_len is None else max_q_len,
+                    shared_len, 0.0, 0, 0, 0, 0, 0, 0, 0)
         n = load_library().fa_paged_scratch_bytes(c, a)
         if n == 0:
             raise FAError(ERR_INVALID_ARG, load_library().fa_last_error().decode())

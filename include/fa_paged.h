@@ -120,7 +120,9 @@ fa_status fa_kv_append(const fa_paged_kv *c, const fa_kv_append_args *a, void *w
  *   q           device bf16 [total_q][Hq][D] with D contiguous, the other
  *               strides in elements (multiples of 8); 16-byte aligned.
  *   o           device [total_q][Hq][D] contiguous, 16-byte aligned, bf16 (or
- *               fp32 with FA_OUT_FP32); lse device fp32 [total_q][Hq].
+ *               fp32 with FA_OUT_FP32); lse device fp32 [total_q][Hq].  o may be
+ *               q itself where that is contiguous; the two must not overlap
+ *               otherwise.
  *   max_q_len   at least the new tokens of every sequence: a longer sequence
  *               is reported like the contradictions above.
  *   shared_len  0, or the length of a prefix that all sequences have in
