@@ -25,15 +25,9 @@ __host__ __device__ __forceinline__ int quotient(int n, const FastDiv& f) {
 #endif
 }
 
-// A number of the step's arrays (the line of tiles is walked on the host too,
-// by its test).
-__host__ __device__ __forceinline__ int load_i32(const int32_t* p) {
-#ifdef __CUDA_ARCH__
-    return __ldg(p);
-#else
-    return *p;
-#endif
-}
+// A number of the step's arrays.  A plain load: the non-coherent one takes no
+// part in the order that wait_before_prefix() below gives.
+__host__ __device__ __forceinline__ int load_i32(const int32_t* p) { return *p; }
 
 // A sequence of the step: its rows of the step's tensors and its length.
 // n = 0: nothing to do (no new tokens, or numbers that contradict each other).
@@ -185,7 +179,7 @@ __device__ __forceinline__ int tile_page(const PagedView& c, const int32_t* tabl
                                          int b, uint32_t* ws) {
     const int span = min(c.page_size, KT), a = kb * KT + lane * span;
     if (lane * span >= KT || !u.any(a, a + span)) return -1;
-    const int id = __ldg(table + (a >> c.page_shift));
+    const int id = load_i32(table + (a >> c.page_shift));
     if (id < 0 || id >= c.num_pages) {
         report_sequence(ws, b);
         return 0;                                  // reported; read something that exists

@@ -286,8 +286,8 @@ paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
             const int r = min(gr + 8 * e, rows - 1);
             tok[e] = quotient(r, p.by_group);
             hq[e] = s.h * p.group + r - tok[e] * p.group;
-            if (SCORE == FA_SCORE_ALIBI) slope[e] = __ldg(p.score.slopes + hq[e]) * kPagedLog2e;
-            if (SCORE == FA_SCORE_ALIBI_SOFTCAP) slope[e] = __ldg(p.score.slopes + hq[e]);
+            if (SCORE == FA_SCORE_ALIBI) slope[e] = p.score.slopes[hq[e]] * kPagedLog2e;
+            if (SCORE == FA_SCORE_ALIBI_SOFTCAP) slope[e] = p.score.slopes[hq[e]];
         }
         // Q's fragments (what the rows past the unit's hold stays in those rows)
         uint32_t qa[D / 16][4];
@@ -350,7 +350,7 @@ paged_small_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                         if (SCORE == FA_SCORE_ALIBI_SOFTCAP) v = softcap_one(fmaf(-slope[e], far, v * p.scale), cap);
                         if (SCORE == FA_SCORE_REL_BIAS) {
                             const int R = p.score.rel_max, d = min(max(i0 + tok[e] - j, -R), R);
-                            v = fmaf(__ldg(p.score.rel_bias + (size_t)hq[e] * (2 * R + 1) + d + R), kPagedLog2e, v);
+                            v = fmaf(p.score.rel_bias[(size_t)hq[e] * (2 * R + 1) + d + R], kPagedLog2e, v);
                         }
                         if (!open && !paged_visible(p.mask, i0 + tok[e], j, p.shared, s.kv)) v = -CUDART_INF_F;
                         x[nt][c] = v;

@@ -285,7 +285,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         for (int b = threadIdx.x; b < p.c.B; b += kThreadsT) {
             const SeqInfo s = seq_info(p.c, b, p.max_q, p.shared, cta == 0 ? p.ws : nullptr);
             len_s[b] = s.kv;
-            q0_s[b + 1] = __ldg(p.c.q_start + b + 1);
+            q0_s[b + 1] = load_i32(p.c.q_start + b + 1);
             if (s.n > 0) {
                 atomicMin(minmax, s.kv - s.n);
                 atomicMax(minmax + 1, s.kv - 1);
@@ -294,7 +294,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         __syncthreads();
         line.imin = minmax[0];
         line.imax = minmax[1];
-        total = prefix_line(p, line, __ldg(p.c.q_start + p.c.B));
+        total = prefix_line(p, line, load_i32(p.c.q_start + p.c.B));
     } else {
         // the sequences' lengths: a warp to each of a few sequences (long
         // prompts have hundreds of units), a thread to each of many
@@ -640,8 +640,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                     i = max(len_s[lo] - q0_s[lo + 1] + trow, -1);
                 }
                 float slope = 0.f;
-                if (SCORE == FA_SCORE_ALIBI) slope = __ldg(p.score.slopes + hq) * kPagedLog2e;
-                if (SCORE == FA_SCORE_ALIBI_SOFTCAP) slope = __ldg(p.score.slopes + hq);
+                if (SCORE == FA_SCORE_ALIBI) slope = p.score.slopes[hq] * kPagedLog2e;
+                if (SCORE == FA_SCORE_ALIBI_SOFTCAP) slope = p.score.slopes[hq];
                 const float* rb = nullptr;
                 if (SCORE == FA_SCORE_REL_BIAS) rb = p.score.rel_bias + (size_t)hq * (2 * p.score.rel_max + 1);
                 // the row's keys: [vlo, vhi] and the sinks from jlo on
@@ -693,7 +693,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
 #pragma unroll
                             for (int e = 0; e < 64; ++e) {
                                 const int rr = min(max(i - ch - e, -p.score.rel_max), p.score.rel_max);
-                                x[e] = fmaf(__ldg(rb + rr + p.score.rel_max), kPagedLog2e, x[e] * sl2);
+                                x[e] = fmaf(rb[rr + p.score.rel_max], kPagedLog2e, x[e] * sl2);
                             }
                         }
                         if (!open) {
