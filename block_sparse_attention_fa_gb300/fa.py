@@ -260,9 +260,10 @@ def _workspace_of(idx: int, raw: int, capture: int) -> Workspace:
             if ws is None:
                 ws = _default_ws[(idx, raw, 0)] = Workspace(tensor=_ws_slot(idx))
             if capture:
-                eager, ws = ws, Workspace(tensor=_ws_slot(idx))
-                eager.graphs.append(ws)
-                _default_ws[(idx, raw, capture)] = ws
+                eager, ws = ws, _default_ws.get((idx, raw, capture))
+                if ws is None:
+                    ws = _default_ws[(idx, raw, capture)] = Workspace(tensor=_ws_slot(idx))
+                    eager.graphs.append(ws)
     return ws
 
 
