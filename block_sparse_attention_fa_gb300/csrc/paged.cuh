@@ -5,7 +5,7 @@
 #include <cfloat>
 #include <climits>
 
-#include "fa_internal.h"
+#include "paged_internal.h"
 #include "ptx.cuh"
 #include "tanh_fine_poly.h"
 
@@ -185,6 +185,11 @@ __device__ __forceinline__ int tile_page(const PagedView& c, const int32_t* tabl
         return 0;                                  // reported; read something that exists
     }
     return id;
+}
+
+// Expect `bytes` more in the barrier's current phase, without an arrival.
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 
 // 3-d tiled load into shared memory (as tma_load_4d).

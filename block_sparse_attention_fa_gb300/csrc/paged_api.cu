@@ -5,8 +5,10 @@
 #include <cstdarg>
 #include <cstdio>
 
+#include <cudaTypedefs.h>
+
 #include "../../include/fa_paged.h"
-#include "fa_internal.h"
+#include "paged_internal.h"
 #include "ptx.cuh"
 
 namespace {
@@ -26,18 +28,30 @@ fa_status cuda_fail(cudaError_t e, const char* what) {
 
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
+int page_shift(int page_size) {
+    int shift = 4;
+    while ((1 << shift) < page_size) ++shift;
+    return shift;
+}
+
+fa_status check_pages(int page_size, int max_pages) {
+    if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1)))
+        return fail(FA_ERR_UNSUPPORTED, "page size %d not supported (16, 32, 64, 128 or 256)", page_size);
+    if ((long long)max_pages * page_size > 2147483647LL - 1024)
+        return fail(FA_ERR_UNSUPPORTED, "max_pages x page_size must be below 2^31 - 1024");
+    return FA_OK;
+}
+
 fa_status check_cache(const fa_paged_kv* c) {
     if (!c) return fail(FA_ERR_INVALID_ARG, "the paged cache is NULL");
     if (c->B < 1 || c->Hkv < 1 || c->num_pages < 1 || c->max_pages < 1 || c->total_q < 0)
         return fail(FA_ERR_INVALID_ARG, "B, Hkv, num_pages and max_pages must be >= 1 and total_q >= 0 "
                     "(got %d, %d, %d, %d, %d)", c->B, c->Hkv, c->num_pages, c->max_pages, c->total_q);
     if (c->D != 64 && c->D != 128) return fail(FA_ERR_UNSUPPORTED, "head dim %d not supported (64 or 128)", c->D);
-    if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1)))
-        return fail(FA_ERR_UNSUPPORTED, "page size %d not supported (16, 32, 64, 128 or 256)", c->page_size);
+    const fa_status st = check_pages(c->page_size, c->max_pages);
+    if (st != FA_OK) return st;
     if ((long long)c->num_pages * c->Hkv > 2147483647LL)
         return fail(FA_ERR_UNSUPPORTED, "num_pages x Hkv must be below 2^31");
-    if ((long long)c->max_pages * c->page_size > 2147483647LL - 1024)
-        return fail(FA_ERR_UNSUPPORTED, "max_pages x page_size must be below 2^31 - 1024");
     if (!c->k || !c->v || !c->page_table || !c->kv_len || !c->q_start)
         return fail(FA_ERR_INVALID_ARG, "k, v, page_table, kv_len and q_start must be non-NULL");
     if (!aligned(c->k, 16) || !aligned(c->v, 16))
@@ -64,7 +78,7 @@ fa::PagedView view(const fa_paged_kv* c) {
     v.Hkv = c->Hkv;
     v.num_pages = c->num_pages;
     v.page_size = c->page_size;
-    for (v.page_shift = 4; (1 << v.page_shift) < c->page_size; ++v.page_shift) {}
+    v.page_shift = page_shift(c->page_size);
     v.max_pages = c->max_pages;
     v.total_q = c->total_q;
     v.page_table = c->page_table;
@@ -147,13 +161,36 @@ Scratch layout(const fa_paged_kv* c, const fa_paged_fwd_args* a) {
     return s;
 }
 
-}  // namespace
+// cuTensorMapEncodeTiled, through the runtime (the library does not link the driver's).
+PFN_cuTensorMapEncodeTiled_v12000 encode_tiled() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found);
+        return e == cudaSuccess && found == cudaDriverEntryPointSuccess
+                   ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p)
+                   : nullptr;
+    }();
+    return fn;
+}
 
-extern "C" {
+// The scales of a cache held in 8 bits (s may be what a call got from its caller).
+fa_status check_scales(const fa_paged_kv* c, const fa_paged_scales* s) {
+    if (!s) return fail(FA_ERR_INVALID_ARG, "the scales are NULL");
+    if (!s->k_scale || !s->v_scale || !aligned(s->k_scale, 4) || !aligned(s->v_scale, 4))
+        return fail(FA_ERR_INVALID_ARG, "k_scale and v_scale must be non-NULL and 4-byte aligned");
+    const uintptr_t k = reinterpret_cast<uintptr_t>(s->k_scale), v = reinterpret_cast<uintptr_t>(s->v_scale);
+    if ((double)(k > v ? k - v : v - k) < 4.0 * c->num_pages * c->Hkv)
+        return fail(FA_ERR_INVALID_ARG, "k_scale and v_scale overlap");
+    return FA_OK;
+}
 
-fa_status fa_kv_append(const fa_paged_kv* c, const fa_kv_append_args* a, void* workspace, void* stream) {
+// fa_kv_append, or with `scaled` fa_kv_append_scaled.
+fa_status append(const fa_paged_kv* c, bool scaled, const fa_paged_scales* scales, const fa_kv_append_args* a,
+                 void* workspace, void* stream) {
     fa_status st = check_cache(c);
     if (st != FA_OK) return st;
+    if (scaled && (st = check_scales(c, scales)) != FA_OK) return st;
     if (!a) return fail(FA_ERR_INVALID_ARG, "the append's args are NULL");
     if (!workspace) return fail(FA_ERR_INVALID_ARG, "workspace is NULL");
     if (a->Hq < 0) return fail(FA_ERR_INVALID_ARG, "Hq must be >= 0 (got %d)", a->Hq);
@@ -184,10 +221,10 @@ fa_status fa_kv_append(const fa_paged_kv* c, const fa_kv_append_args* a, void* w
     }
     if (!aligned(a->positions, 4)) return fail(FA_ERR_INVALID_ARG, "positions must be 4-byte aligned");
     const uintptr_t kc = reinterpret_cast<uintptr_t>(c->k), vc = reinterpret_cast<uintptr_t>(c->v);
-    if ((double)(kc > vc ? kc - vc : vc - kc) < 2.0 * c->num_pages * c->Hkv * c->page_size * c->D)
+    if ((double)(kc > vc ? kc - vc : vc - kc) < (scaled ? 1.0 : 2.0) * c->num_pages * c->Hkv * c->page_size * c->D)
         return fail(FA_ERR_INVALID_ARG, "the cache's k and v overlap");
 
-    fa::AppendParams p{};
+    fa::AppendScaledParams p{};
     p.c = view(c);
     p.Hq = a->Hq;
     p.D = c->D;
@@ -198,8 +235,15 @@ fa_status fa_kv_append(const fa_paged_kv* c, const fa_kv_append_args* a, void* w
     p.k = static_cast<const uint16_t*>(a->k);
     p.v = static_cast<const uint16_t*>(a->v);
     p.q_out = static_cast<uint16_t*>(a->q_out);
-    p.kc = static_cast<uint16_t*>(c->k);
-    p.vc = static_cast<uint16_t*>(c->v);
+    if (scaled) {
+        p.k8 = static_cast<uint8_t*>(c->k);
+        p.v8 = static_cast<uint8_t*>(c->v);
+        p.k_scale = scales->k_scale;
+        p.v_scale = scales->v_scale;
+    } else {
+        p.kc = static_cast<uint16_t*>(c->k);
+        p.vc = static_cast<uint16_t*>(c->v);
+    }
     for (int e = 0; e < 2; ++e) {
         p.qs[e] = a->q_stride[e];
         p.ks[e] = a->k_stride[e];
@@ -210,21 +254,19 @@ fa_status fa_kv_append(const fa_paged_kv* c, const fa_kv_append_args* a, void* w
     p.sin = a->sin;
     p.positions = a->positions;
     p.ws = static_cast<uint32_t*>(workspace);
-    cudaError_t e = fa::launch_kv_append(p, static_cast<cudaStream_t>(stream));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = scaled ? fa::launch_kv_append_scaled(p, s) : fa::launch_kv_append(p, s);
     if (e != cudaSuccess) return cuda_fail(e, "append launch");
     return fa::report(FA_OK, "");
 }
 
-size_t fa_paged_scratch_bytes(const fa_paged_kv* c, const fa_paged_fwd_args* a) {
-    if (check_fwd(c, a) != FA_OK) return 0;
-    fa::report(FA_OK, "");
-    return layout(c, a).bytes;
-}
-
-fa_status fa_fwd_paged(const fa_paged_kv* c, const fa_paged_fwd_args* a, const fa_mask_desc* mask,
-                       const fa_score_desc* sc, void* scratch, size_t scratch_bytes, void* workspace, void* stream) {
+// fa_fwd_paged, or with `scaled` fa_fwd_paged_scaled.
+fa_status forward(const fa_paged_kv* c, bool scaled, const fa_paged_scales* scales, const fa_paged_fwd_args* a,
+                  const fa_mask_desc* mask, const fa_score_desc* sc, void* scratch, size_t scratch_bytes,
+                  void* workspace, void* stream) {
     fa_status st = check_fwd(c, a);
     if (st != FA_OK) return st;
+    if (scaled && (st = check_scales(c, scales)) != FA_OK) return st;
     if (!mask) return fail(FA_ERR_INVALID_ARG, "the mask is NULL");
     fa::PagedMask m{0, -1, 0};
     switch (mask->kind) {
@@ -261,7 +303,7 @@ fa_status fa_fwd_paged(const fa_paged_kv* c, const fa_paged_fwd_args* a, const f
         return fail(FA_ERR_INVALID_ARG, "scratch holds %zu bytes, %zu needed", scratch_bytes, lay.bytes);
 
     uint8_t* base = static_cast<uint8_t*>(scratch);
-    fa::PagedParams p{};
+    fa::PagedScaledParams p{};
     p.c = view(c);
     p.mask = m;
     p.Hq = a->Hq;
@@ -291,30 +333,42 @@ fa_status fa_fwd_paged(const fa_paged_kv* c, const fa_paged_fwd_args* a, const f
     p.ws = static_cast<uint32_t*>(workspace);
     p.timeout_ns = (uint64_t)(a->timeout_ms ? a->timeout_ms : 2000u) * 1000000ull;
     p.flags = a->flags;
+    if (scaled) {
+        p.k_scale = scales->k_scale;
+        p.v_scale = scales->v_scale;
+    }
 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool small = small_rows(c, a);
     const long long blocks = (long long)c->num_pages * c->Hkv;
+    const auto map_of = scaled ? fa::page_tensor_map_scaled : fa::page_tensor_map;
     alignas(64) CUtensorMap tk, tv, sk, sv;       // boxes of the tile kernel, of the small one
     if (!small || p.join_rows) {
-        if ((st = fa::page_tensor_map(&tk, c->k, blocks, c->page_size, c->D, fa::kPagedTileKeys)) != FA_OK) return st;
-        if ((st = fa::page_tensor_map(&tv, c->v, blocks, c->page_size, c->D, fa::kPagedTileKeys)) != FA_OK) return st;
+        const int keys = fa::kPagedTileKeys;
+        if ((st = map_of(&tk, c->k, blocks, c->page_size, c->D, keys)) != FA_OK) return st;
+        if ((st = map_of(&tv, c->v, blocks, c->page_size, c->D, keys)) != FA_OK) return st;
     }
     if (small) {
-        const int keys = fa::paged_small_keys(c->D);
-        if ((st = fa::page_tensor_map(&sk, c->k, blocks, c->page_size, c->D, keys)) != FA_OK) return st;
-        if ((st = fa::page_tensor_map(&sv, c->v, blocks, c->page_size, c->D, keys)) != FA_OK) return st;
+        const int keys = scaled ? fa::kPagedSmallScaledKeys : fa::paged_small_keys(c->D);
+        if ((st = map_of(&sk, c->k, blocks, c->page_size, c->D, keys)) != FA_OK) return st;
+        if ((st = map_of(&sv, c->v, blocks, c->page_size, c->D, keys)) != FA_OK) return st;
     }
-    fa::PagedParams pre = p;
+    auto tile_kernel = [&](const fa::PagedScaledParams& x) {
+        return scaled ? fa::launch_paged_tiles_scaled(x, tk, tv, s) : fa::launch_paged_tiles(x, tk, tv, s);
+    };
+    auto small_kernel = [&](const fa::PagedScaledParams& x) {
+        return scaled ? fa::launch_paged_small_scaled(x, sk, sv, s) : fa::launch_paged_small(x, sk, sv, s);
+    };
+    fa::PagedScaledParams pre = p;
     if (p.join_rows) {
         pre.prefix = 1;
         pre.ctas = fa::device_sm_count();
         pre.parts = {reinterpret_cast<float*>(base + lay.pre_slot_o), reinterpret_cast<float2*>(base + lay.pre_slot_ml),
                      reinterpret_cast<float*>(base + lay.pre_row_o), reinterpret_cast<float2*>(base + lay.pre_row_ml)};
-        cudaError_t e = fa::launch_paged_tiles(pre, tk, tv, s);
+        cudaError_t e = tile_kernel(pre);
         if (e != cudaSuccess) return cuda_fail(e, "shared prefix launch");
     }
-    cudaError_t e = small ? fa::launch_paged_small(p, sk, sv, s) : fa::launch_paged_tiles(p, tk, tv, s);
+    cudaError_t e = small ? small_kernel(p) : tile_kernel(p);
     if (e != cudaSuccess) return cuda_fail(e, "paged forward launch");
     const int unit_rows = small ? fa::kPagedSmallRows : fa::kPagedTileRows;
     if (p.join_rows) {
@@ -329,6 +383,120 @@ fa_status fa_fwd_paged(const fa_paged_kv* c, const fa_paged_fwd_args* a, const f
     }
     if (e != cudaSuccess) return cuda_fail(e, "joining launch");
     return fa::report(FA_OK, "");
+}
+
+}  // namespace
+
+fa_status fa::page_tensor_map_scaled(CUtensorMap* map, const void* base, long long blocks, int page_size, int D,
+                                     int tile_keys) {
+    const auto fn = encode_tiled();
+    if (!fn) return fail(FA_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+    const int rows = page_size * D / 128, box_rows = std::min(page_size, tile_keys) * D / 128;
+    const cuuint64_t dims[3] = {128, (cuuint64_t)rows, (cuuint64_t)blocks};
+    const cuuint64_t strides[2] = {128, (cuuint64_t)rows * 128};
+    const cuuint32_t box[3] = {128, (cuuint32_t)box_rows, 1}, estr[3] = {1, 1, 1};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(FA_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);
+    return FA_OK;
+}
+
+extern "C" {
+
+fa_status fa_kv_append(const fa_paged_kv* c, const fa_kv_append_args* a, void* workspace, void* stream) {
+    return append(c, false, nullptr, a, workspace, stream);
+}
+
+fa_status fa_kv_append_scaled(const fa_paged_kv* c, const fa_paged_scales* scales, const fa_kv_append_args* a,
+                              void* workspace, void* stream) {
+    return append(c, true, scales, a, workspace, stream);
+}
+
+fa_status fa_paged_step(const fa_paged_step_args* a, void* workspace, void* stream) {
+    if (!a) return fail(FA_ERR_INVALID_ARG, "the step's args are NULL");
+    if (!workspace) return fail(FA_ERR_INVALID_ARG, "workspace is NULL");
+    if (a->B < 1 || a->num_pages < 1 || a->max_pages < 1 || a->total_q < 0)
+        return fail(FA_ERR_INVALID_ARG, "B, num_pages and max_pages must be >= 1 and total_q >= 0 (got %d, %d, %d, %d)",
+                    a->B, a->num_pages, a->max_pages, a->total_q);
+    if (a->B > fa::kPagedMaxSeqs)
+        return fail(FA_ERR_UNSUPPORTED, "at most %d sequences per call (got %d)", fa::kPagedMaxSeqs, a->B);
+    fa_status st = check_pages(a->page_size, a->max_pages);
+    if (st != FA_OK) return st;
+    if (a->shared_pages < 0 || a->shared_pages > a->max_pages)
+        return fail(FA_ERR_INVALID_ARG, "shared_pages must be 0 .. max_pages (got %d)", a->shared_pages);
+    // every array, the written ones first
+    const size_t B = a->B, rows = a->total_q;
+    const struct {
+        const char* name;
+        const void* p;
+        size_t bytes, align;
+        bool optional;
+    } arrays[] = {{"kv_len_out", a->kv_len_out, 4 * B, 4, false},
+                  {"free_count_out", a->free_count_out, 4, 4, false},
+                  {"page_table", a->page_table, 4 * B * a->max_pages, 4, false},
+                  {"free_pages", a->free_pages, 4 * (size_t)a->num_pages, 4, false},
+                  {"q_start", a->q_start, 4 * (B + 1), 4, false},
+                  {"slots", a->slots, 8 * rows, 8, true},
+                  {"positions", a->positions, 4 * rows, 4, true},
+                  {"kv_len", a->kv_len, 4 * B, 4, false},
+                  {"keep_len", a->keep_len, 4 * B, 4, true},
+                  {"new_len", a->new_len, 4 * B, 4, false},
+                  {"free_count", a->free_count, 4, 4, false}};
+    constexpr int kWritten = 7, kArrays = sizeof(arrays) / sizeof(arrays[0]);
+    for (const auto& x : arrays) {
+        if (!x.p && !x.optional) return fail(FA_ERR_INVALID_ARG, "%s must be non-NULL", x.name);
+        if (!aligned(x.p, x.align)) return fail(FA_ERR_INVALID_ARG, "%s must be %zu-byte aligned", x.name, x.align);
+    }
+    for (int i = 0; i < kWritten; ++i) {
+        for (int j = i + 1; j < kArrays; ++j) {
+            const uintptr_t x = reinterpret_cast<uintptr_t>(arrays[i].p), y = reinterpret_cast<uintptr_t>(arrays[j].p);
+            if (!x || !y || arrays[i].bytes == 0 || arrays[j].bytes == 0) continue;
+            if (x == y && ((i == 0 && (j == 7 || j == 8)) || (i == 1 && j == 10))) continue;     // in place
+            if (x < y + arrays[j].bytes && y < x + arrays[i].bytes)
+                return fail(FA_ERR_INVALID_ARG, "%s and %s overlap", arrays[i].name, arrays[j].name);
+        }
+    }
+    fa::StepParams p{};
+    p.B = a->B;
+    p.num_pages = a->num_pages;
+    p.page_size = a->page_size;
+    p.page_shift = page_shift(a->page_size);
+    p.max_pages = a->max_pages;
+    p.shared_pages = a->shared_pages;
+    p.total_q = a->total_q;
+    p.new_len = a->new_len;
+    p.keep_len = a->keep_len ? a->keep_len : a->kv_len;
+    p.kv_len = a->kv_len;
+    p.page_table = a->page_table;
+    p.free_pages = a->free_pages;
+    p.free_count = a->free_count;
+    p.kv_len_out = a->kv_len_out;
+    p.free_count_out = a->free_count_out;
+    p.q_start = a->q_start;
+    p.slots = a->slots;
+    p.positions = a->positions;
+    p.ws = static_cast<uint32_t*>(workspace);
+    cudaError_t e = fa::launch_paged_step(p, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "step launch");
+    return fa::report(FA_OK, "");
+}
+
+size_t fa_paged_scratch_bytes(const fa_paged_kv* c, const fa_paged_fwd_args* a) {
+    if (check_fwd(c, a) != FA_OK) return 0;
+    fa::report(FA_OK, "");
+    return layout(c, a).bytes;
+}
+
+fa_status fa_fwd_paged(const fa_paged_kv* c, const fa_paged_fwd_args* a, const fa_mask_desc* mask,
+                       const fa_score_desc* sc, void* scratch, size_t scratch_bytes, void* workspace, void* stream) {
+    return forward(c, false, nullptr, a, mask, sc, scratch, scratch_bytes, workspace, stream);
+}
+
+fa_status fa_fwd_paged_scaled(const fa_paged_kv* c, const fa_paged_scales* scales, const fa_paged_fwd_args* a,
+                              const fa_mask_desc* mask, const fa_score_desc* sc, void* scratch, size_t scratch_bytes,
+                              void* workspace, void* stream) {
+    return forward(c, true, scales, a, mask, sc, scratch, scratch_bytes, workspace, stream);
 }
 
 }  // extern "C"

@@ -47,8 +47,14 @@ struct SmallSeg {
 // counts for itself (1024 sequences of 512 keys, 32 heads on 8 of 128 columns,
 // pages of 16: 329 us, 470 with an entry for each and one CTA per SM).
 constexpr int kLineEntries = 1000;
-__host__ __device__ constexpr int group_shift(int B) { return B <= kLineEntries ? 0 : B <= 2 * kLineEntries ? 1 : 2; }
-__host__ __device__ constexpr uint32_t groups_of(int B) { return (B + (1 << group_shift(B)) - 1) >> group_shift(B); }
+__host__ __device__ constexpr int group_shift(int B, int entries = kLineEntries) {
+    int shift = 0;
+    while (B > entries << shift) ++shift;
+    return shift;
+}
+__host__ __device__ constexpr uint32_t groups_of(int B, int entries = kLineEntries) {
+    return (B + (1 << group_shift(B, entries)) - 1) >> group_shift(B, entries);
+}
 
 // A CTA's stretch [t, t1) of the line of tiles.  Once every CTA has some tiles
 // a unit counts as one more (`front` places before its first tile): its start

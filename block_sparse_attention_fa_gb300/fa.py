@@ -33,7 +33,8 @@ SYMBOLS = ("fa_workspace_bytes", "fa_block_mask_shape", "fa_block_mask_size", "f
            "fa_fwd_noalloc", "fa_fwd_decode", "fa_decode_partials_bytes", "fa_decode_splits", "fa_bwd",
            "fa_block_mask_build_cols", "fa_bwd_rowstats_bytes", "fa_workspace_check", "fa_last_error", "fa_version")
 
-PAGED_SYMBOLS = ("fa_kv_append", "fa_fwd_paged", "fa_paged_scratch_bytes")
+PAGED_SYMBOLS = ("fa_kv_append", "fa_fwd_paged", "fa_paged_scratch_bytes", "fa_kv_append_scaled", "fa_fwd_paged_scaled",
+                 "fa_paged_step")
 
 
 class FAError(RuntimeError):
@@ -91,6 +92,8 @@ class BlockMaskColsStruct(ctypes.Structure):
 _PAGED_KV = struct.Struct("7i5P")
 _KV_APPEND = struct.Struct("4i4P8q3P")
 _PAGED_FWD = struct.Struct("3ifP2q2P2I")
+_PAGED_SCALES = struct.Struct("2P")
+_PAGED_STEP = struct.Struct("6i11P")
 _MASK = struct.Struct("4i2Pi0P")
 _SCORE = struct.Struct("if2Pi0P")
 
@@ -116,6 +119,19 @@ class PagedFwdArgs(ctypes.Structure):
                 ("scale", ctypes.c_float), ("q", ctypes.c_void_p), ("q_stride", ctypes.c_int64 * 2),
                 ("o", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("timeout_ms", ctypes.c_uint32),
                 ("flags", ctypes.c_uint32)]
+
+
+class PagedScales(ctypes.Structure):
+    _fields_ = [("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
+class PagedStepArgs(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("shared_pages", ctypes.c_int32), ("total_q", ctypes.c_int32),
+                ("new_len", ctypes.c_void_p), ("keep_len", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p), ("free_pages", ctypes.c_void_p), ("free_count", ctypes.c_void_p),
+                ("kv_len_out", ctypes.c_void_p), ("free_count_out", ctypes.c_void_p), ("q_start", ctypes.c_void_p),
+                ("slots", ctypes.c_void_p), ("positions", ctypes.c_void_p)]
 
 
 _lib = None
@@ -169,6 +185,12 @@ def load_library(path: str = LIB_PATH):
     h.fa_paged_scratch_bytes.argtypes = [ctypes.c_void_p] * 2
     h.fa_fwd_paged.restype = ctypes.c_int
     h.fa_fwd_paged.argtypes = [ctypes.c_void_p] * 5 + [ctypes.c_size_t] + [ctypes.c_void_p] * 2
+    h.fa_kv_append_scaled.restype = ctypes.c_int
+    h.fa_kv_append_scaled.argtypes = [ctypes.c_void_p] * 5
+    h.fa_fwd_paged_scaled.restype = ctypes.c_int
+    h.fa_fwd_paged_scaled.argtypes = [ctypes.c_void_p] * 6 + [ctypes.c_size_t] + [ctypes.c_void_p] * 2
+    h.fa_paged_step.restype = ctypes.c_int
+    h.fa_paged_step.argtypes = [ctypes.c_void_p] * 3
     h.fa_internal_capture_id.restype = ctypes.c_uint64
     h.fa_internal_capture_id.argtypes = [ctypes.c_void_p]
     h.fa_internal_capture_mode.restype = ctypes.c_int
@@ -675,15 +697,15 @@ def bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor, lse:
     return dq, dk, dv
 
 
-def _paged_kv(k_cache, v_cache, page_table, kv_len, q_start, total_q, dev):
+def _paged_kv(k_cache, v_cache, page_table, kv_len, q_start, total_q, dev, scaled=False):
     """The packed fa_paged_kv of these tensors and the cache's shape.  The C ABI reads them through raw pointers:
     everything it cannot see is checked here."""
-    shape = k_cache.shape
-    if len(shape) != 4 or k_cache.dtype is not torch.bfloat16 or v_cache.dtype is not torch.bfloat16 \
+    shape, dtype = k_cache.shape, torch.float8_e4m3fn if scaled else torch.bfloat16
+    if len(shape) != 4 or k_cache.dtype is not dtype or v_cache.dtype is not dtype \
             or v_cache.shape != shape or not k_cache.is_contiguous() or not v_cache.is_contiguous() \
             or k_cache.get_device() != dev or v_cache.get_device() != dev:
         raise ValueError("k_cache and v_cache must be contiguous CUDA bf16 tensors [num_pages, Hkv, page_size, D] "
-                         "on the rows' device")
+                         "on the rows' device (float8_e4m3fn where k_scale and v_scale are given)")
     for name, t, dims in (("page_table", page_table, 2), ("kv_len", kv_len, 1), ("q_start", q_start, 1)):
         if t.dtype is not torch.int32 or t.dim() != dims or t.get_device() != dev or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous int32 tensor of {dims} dimensions on the rows' device")
@@ -694,6 +716,19 @@ def _paged_kv(k_cache, v_cache, page_table, kv_len, q_start, total_q, dev):
     num_pages, Hkv, page, D = shape
     return _packed(_PAGED_KV, "the paged cache", B, Hkv, D, num_pages, page, max_pages, total_q, k_cache.data_ptr(),
                    v_cache.data_ptr(), page_table.data_ptr(), kv_len.data_ptr(), q_start.data_ptr()), Hkv, D
+
+
+def _scales(k_scale, v_scale, k_cache, dev):
+    """The packed fa_paged_scales; None for a cache without scales (bf16)."""
+    if k_scale is None and v_scale is None:
+        return None
+    want = k_cache.shape[:2]
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if t is None or t.dtype is not torch.float32 or t.shape != want or t.get_device() != dev \
+                or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous float32 tensor [num_pages, Hkv] = {tuple(want)} on the "
+                             "cache's device (k_scale and v_scale come together)")
+    return _PAGED_SCALES.pack(k_scale.data_ptr(), v_scale.data_ptr())
 
 
 def _rows(name, t, total, H, D, dev):
@@ -737,6 +772,7 @@ _paged_lock = threading.Lock()
 
 def kv_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
               v_cache: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tensor, q_start: torch.Tensor, *,
+              k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
               cos: Optional[torch.Tensor] = None, sin: Optional[torch.Tensor] = None, interleaved: bool = False,
               positions: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
               workspace: Optional[Workspace] = None, stream=None):
@@ -747,12 +783,17 @@ def kv_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, k_cac
     of a fused projection); q may be None.  k_cache and v_cache [num_pages, Hkv, page_size, D]; page_table int32
     [B, max_pages]; kv_len int32 [B] counts the new tokens; sequence b's rows are q_start[b] .. q_start[b + 1] - 1,
     rows from q_start[B] on are left as they were.  cos and sin: fp32 [positions, rot_dim / 2], both or neither.
-    q_out may be q."""
+    q_out may be q.
+
+    With k_scale and v_scale, float32 [num_pages, Hkv], the cache is held in 8 bits (fa_kv_append_scaled): k_cache and
+    v_cache are float8_e4m3fn, and every page that receives tokens gets, per kv head, the power of two that its largest
+    value needs, or keeps a larger one that its earlier tokens have."""
     dev = k.get_device()
     if dev < 0 or k.dim() != 3:
         raise ValueError("k must be a CUDA bf16 tensor [tokens, Hkv, D]")
     total = k.shape[0]
-    c, Hkv, D = _paged_kv(k_cache, v_cache, page_table, kv_len, q_start, total, dev)
+    scales = _scales(k_scale, v_scale, k_cache, dev)
+    c, Hkv, D = _paged_kv(k_cache, v_cache, page_table, kv_len, q_start, total, dev, scales is not None)
     ks, vs = _rows("k", k, total, Hkv, D, dev), _rows("v", v, total, Hkv, D, dev)
     Hq, qp, op, qs, os_ = 0, 0, 0, (0, 0), (0, 0)
     if q is not None:
@@ -783,14 +824,19 @@ def kv_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, k_cac
                 *qs, *ks, *vs, *os_, cp, sp, pp)
     raw = _raw_stream(dev) if stream is None else stream.cuda_stream
     ws = workspace or _workspace_of(dev, raw, _capture_of(dev, raw, stream is not None))
-    st = _call_on(dev, load_library().fa_kv_append, c, a, ws.tensor.data_ptr(), raw)
+    lib = load_library()
+    if scales is None:
+        st = _call_on(dev, lib.fa_kv_append, c, a, ws.tensor.data_ptr(), raw)
+    else:
+        st = _call_on(dev, lib.fa_kv_append_scaled, c, scales, a, ws.tensor.data_ptr(), raw)
     if st != OK:
         _check(st)
     return q_out
 
 
 def fwd_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
-              kv_len: torch.Tensor, q_start: torch.Tensor, *, max_q_len: Optional[int] = None, mask: str = "causal",
+              kv_len: torch.Tensor, q_start: torch.Tensor, *, k_scale: Optional[torch.Tensor] = None,
+              v_scale: Optional[torch.Tensor] = None, max_q_len: Optional[int] = None, mask: str = "causal",
               window: int = 0, sinks: int = 0, shared_len: int = 0, score: str = "none", softcap: float = 0.0,
               alibi_slopes: Optional[torch.Tensor] = None, rel_bias: Optional[torch.Tensor] = None, rel_max: int = 0,
               scale: Optional[float] = None, out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
@@ -803,12 +849,16 @@ def fwd_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, pag
     ``max_q_len`` bounds the new tokens of a sequence (default: all of q's rows; a tight bound lets single tokens take
     the decoding kernel: 64 x 512 keys 31 us, 41 without, 8 x 32768 keys 165 and 176).  mask: "full", "causal", "sliding_window" (``window``) or "sink_window" (``window`` and
     ``sinks``), by position.  ``shared_len``: length of a prefix all sequences share, read once through page_table[0].
-    Rows behind the last sequence are left as they were; ``scratch`` is allocated when not given."""
+    Rows behind the last sequence are left as they were; ``scratch`` is allocated when not given.
+
+    With k_scale and v_scale, float32 [num_pages, Hkv], the cache is held in 8 bits (fa_fwd_paged_scaled): k_cache and
+    v_cache are float8_e4m3fn codes, whose values are code x scale of the code's page and kv head."""
     dev = q.get_device()
     if dev < 0 or q.dim() != 3:
         raise ValueError("q must be a CUDA bf16 tensor [tokens, Hq, D]")
     total, Hq, _ = q.shape
-    c, _, D = _paged_kv(k_cache, v_cache, page_table, kv_len, q_start, total, dev)
+    scales = _scales(k_scale, v_scale, k_cache, dev)
+    c, _, D = _paged_kv(k_cache, v_cache, page_table, kv_len, q_start, total, dev, scales is not None)
     qs = _rows("q", q, total, None, D, dev)
     want = torch.float32 if out_fp32 else torch.bfloat16
     if out is None:
@@ -841,25 +891,27 @@ def fwd_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, pag
     raw = _raw_stream(dev) if stream is None else stream.cuda_stream
     capture = _capture_of(dev, raw, stream is not None)
     ws = workspace or _workspace_of(dev, raw, capture)
+    # the calls on the cache (and its scales, in 8 bits)
+    head, call = ((c,), lib.fa_fwd_paged) if scales is None else ((c, scales), lib.fa_fwd_paged_scaled)
 
     if scratch is not None:
         if scratch.get_device() != dev or not scratch.is_contiguous():
             raise ValueError("scratch must be a contiguous tensor on q's device")
-        st = _call_on(dev, lib.fa_fwd_paged, c, a, m, sc, scratch.data_ptr(), scratch.numel() * scratch.element_size(),
+        st = _call_on(dev, call, *head, a, m, sc, scratch.data_ptr(), scratch.numel() * scratch.element_size(),
                       ws.tensor.data_ptr(), raw)
     elif stream is not None or capture:
         # (no bytes: the arguments are wrong, and the call says how)
         scratch = _new(_call_on(dev, lib.fa_paged_scratch_bytes, c, a) or 16, torch.uint8, q.device, stream)
-        st = _call_on(dev, lib.fa_fwd_paged, c, a, m, sc, scratch.data_ptr(), scratch.numel(), ws.tensor.data_ptr(), raw)
+        st = _call_on(dev, call, *head, a, m, sc, scratch.data_ptr(), scratch.numel(), ws.tensor.data_ptr(), raw)
     else:
         with _paged_lock:
             kept = _paged_scratch.get((dev, raw))
             st = ERR_INVALID_ARG if kept is None else \
-                _call_on(dev, lib.fa_fwd_paged, c, a, m, sc, kept.data_ptr(), kept.numel(), ws.tensor.data_ptr(), raw)
+                _call_on(dev, call, *head, a, m, sc, kept.data_ptr(), kept.numel(), ws.tensor.data_ptr(), raw)
             if st == ERR_INVALID_ARG:              # none yet, or too small (or wrong arguments: the call says so again)
                 kept = torch.empty(_call_on(dev, lib.fa_paged_scratch_bytes, c, a) or 16, dtype=torch.uint8,
                                    device=q.device)
-                st = _call_on(dev, lib.fa_fwd_paged, c, a, m, sc, kept.data_ptr(), kept.numel(), ws.tensor.data_ptr(), raw)
+                st = _call_on(dev, call, *head, a, m, sc, kept.data_ptr(), kept.numel(), ws.tensor.data_ptr(), raw)
                 if st == OK and kept.numel() <= _PAGED_KEEP:
                     _paged_scratch[(dev, raw)] = kept
     if st != OK:
@@ -870,15 +922,70 @@ def fwd_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, pag
 def paged_scratch(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
                   kv_len: torch.Tensor, q_start: torch.Tensor, *, max_q_len: Optional[int] = None,
                   shared_len: int = 0) -> torch.Tensor:
-    """Scratch for fwd_paged calls of these shapes, for callers that keep their own."""
+    """Scratch for fwd_paged calls of these shapes (of a bf16 cache or one held in 8 bits), for callers that keep their
+    own."""
     with torch.cuda.device(q.device):
-        c, _, _ = _paged_kv(k_cache, v_cache, page_table, kv_len, q_start, q.shape[0], q.get_device())
+        c, _, _ = _paged_kv(k_cache, v_cache, page_table, kv_len, q_start, q.shape[0], q.get_device(),
+                            k_cache.dtype is torch.float8_e4m3fn)
         a = _packed(_PAGED_FWD, "paged_scratch", q.shape[1], max(q.shape[0], 1) if max_q_len is None else max_q_len,
                     shared_len, 0.0, 0, 0, 0, 0, 0, 0, 0)
         n = load_library().fa_paged_scratch_bytes(c, a)
         if n == 0:
             raise FAError(ERR_INVALID_ARG, load_library().fa_last_error().decode())
         return torch.empty(n, dtype=torch.uint8, device=q.device)
+
+
+def paged_step(new_len: torch.Tensor, kv_len: torch.Tensor, page_table: torch.Tensor, free_pages: torch.Tensor,
+               free_count: torch.Tensor, *, page_size: int, total_q: int, keep_len: Optional[torch.Tensor] = None,
+               shared_pages: int = 0, kv_len_out: Optional[torch.Tensor] = None,
+               free_count_out: Optional[torch.Tensor] = None, q_start: Optional[torch.Tensor] = None,
+               slots: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+               workspace: Optional[Workspace] = None, stream=None):
+    """A step's pages, offsets and slots from its sequences' lengths, on the device (fa_paged_step); returns
+    (q_start, slots, positions): int32 [B + 1], int64 [total_q] (page x page_size + place, -1 behind the last sequence)
+    and int32 [total_q].
+
+    Sequence b had kv_len[b] tokens in the cache, of which it keeps keep_len[b] (default: all), and brings new_len[b]
+    new ones.  Its row of page_table [B, max_pages] gets the pages that it needs from the stack free_pages [num_pages],
+    of which the first free_count[0] are free, or gives back those that it no longer needs; the first shared_pages
+    entries stay.  kv_len and free_count are brought up to date in place, or into kv_len_out and free_count_out.  All are
+    int32 on one device.  A step that cannot be made (contradicting lengths, too few free pages) becomes an empty one,
+    and the workspace's check() says so."""
+    dev = kv_len.get_device()
+    if dev < 0 or kv_len.dim() != 1 or page_table.dim() != 2 or page_table.shape[0] != kv_len.shape[0]:
+        raise ValueError("kv_len must be a CUDA int32 tensor [B] and page_table one of [B, max_pages]")
+    B, max_pages = page_table.shape
+    if total_q < 0 or total_q > 2147483647:
+        raise ValueError(f"total_q must be 0 .. 2^31 - 1 (got {total_q})")
+    if q_start is None:
+        q_start = _new((B + 1,), torch.int32, kv_len.device, stream)
+    if slots is None:
+        slots = _new((total_q,), torch.int64, kv_len.device, stream)
+    if positions is None:
+        positions = _new((total_q,), torch.int32, kv_len.device, stream)
+    kv_out = kv_len if kv_len_out is None else kv_len_out
+    count_out = free_count if free_count_out is None else free_count_out
+    for name, t, n in (("new_len", new_len, B), ("kv_len", kv_len, B), ("keep_len", keep_len, B),
+                       ("page_table", page_table, B * max_pages), ("free_pages", free_pages, None),
+                       ("free_count", free_count, 1), ("kv_len_out", kv_out, B), ("free_count_out", count_out, 1),
+                       ("q_start", q_start, B + 1), ("positions", positions, total_q)):
+        if t is not None and (t.dtype is not torch.int32 or t.get_device() != dev or not t.is_contiguous()
+                              or (n is not None and t.numel() != n)):
+            raise ValueError(f"{name} must be a contiguous int32 tensor{'' if n is None else f' of {n} entries'} on "
+                             "kv_len's device")
+    if slots.dtype is not torch.int64 or slots.get_device() != dev or not slots.is_contiguous() \
+            or slots.numel() != total_q:
+        raise ValueError(f"slots must be a contiguous int64 tensor of {total_q} entries on kv_len's device")
+    a = _packed(_PAGED_STEP, "paged_step", B, free_pages.numel(), page_size, max_pages, shared_pages, total_q,
+                new_len.data_ptr(), 0 if keep_len is None else keep_len.data_ptr(), kv_len.data_ptr(),
+                page_table.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), kv_out.data_ptr(),
+                count_out.data_ptr(), q_start.data_ptr(), slots.data_ptr(), positions.data_ptr())
+    raw = _raw_stream(dev) if stream is None else stream.cuda_stream
+    ws = workspace or _workspace_of(dev, raw, _capture_of(dev, raw, stream is not None))
+    st = _call_on(dev, load_library().fa_paged_step, a, ws.tensor.data_ptr(), raw)
+    if st != OK:
+        _check(st)
+    return q_start, slots, positions
 
 
 def version() -> str:

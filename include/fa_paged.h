@@ -10,11 +10,14 @@
  * uses without giving one; the layout below is this library's own.
  *
  * A step of a serving loop:
- *   1. the caller gives every sequence the pages its new tokens need and sets
- *      kv_len and q_start for the step;
+ *   1. every sequence gets the pages its new tokens need, and kv_len and
+ *      q_start are set for the step: by the caller, or by fa_paged_step from
+ *      the sequences' lengths;
  *   2. fa_kv_append rotates the step's queries and keys and writes the keys
  *      and values to their slots;
  *   3. fa_fwd_paged attends from the step's queries to the cache.
+ * fa_kv_append_scaled and fa_fwd_paged_scaled do 2 and 3 on a cache held in 8
+ * bits, half the memory and half the bytes that attention reads.
  */
 #ifndef FA_GB300_PAGED_H
 #define FA_GB300_PAGED_H
@@ -154,6 +157,111 @@ size_t fa_paged_scratch_bytes(const fa_paged_kv *c, const fa_paged_fwd_args *a);
 
 fa_status fa_fwd_paged(const fa_paged_kv *c, const fa_paged_fwd_args *a, const fa_mask_desc *mask,
                        const fa_score_desc *sc, void *scratch, size_t scratch_bytes, void *workspace, void *stream);
+
+/* The scales of a cache held in 8 bits.  The cache's k and v (fa_paged_kv) are
+ * then e4m3 codes, one byte each, laid out as the bf16 elements are; the value
+ * of a code is
+ *     code x scale[page][head],
+ * one scale for the tokens of a page and a kv head, k's and v's apart.
+ *   k_scale, v_scale   device fp32 [num_pages][Hkv], 4-byte aligned.  Any
+ *               finite numbers that are not negative; those of pages that are
+ *               not read may be anything.
+ * A page that receives a token in a step belongs to one sequence of the step
+ * (its earlier codes change with its scale): no other sequence's table names
+ * it, except behind what that sequence reads.                                */
+typedef struct fa_paged_scales {
+    float *k_scale;
+    float *v_scale;
+} fa_paged_scales;
+
+/* fa_kv_append into a cache held in 8 bits.  q's part is the same.  For every
+ * page that receives tokens, and every kv head, of k (rotated, in fp32) and of
+ * v each:
+ *     amax   the largest finite magnitude among the page's new tokens,
+ *     need   2^e with the smallest e for which amax <= 448 2^e, e within
+ *            -100 .. 119,
+ *     scale  need, or where the page holds earlier tokens of the sequence
+ *            max(need, its scale before), in which case their codes are
+ *            rounded again to the new scale;
+ *     code   x / scale rounded to e4m3 (to the nearest, ties to even); beyond
+ *            448 it is +-448, and infinities and NaN become NaN.
+ * A scale grows by factors of two, so that rounding again changes nothing but
+ * codes that run out of exponents (below 2^-6 of their unit).  For scales before
+ * that are no powers of two, x / scale is x (1 / scale) in fp32.
+ * Tokens whose position is outside 0 .. rope_len - 1 are reported, not written,
+ * and do not count in amax.  One kernel launch.                             */
+fa_status fa_kv_append_scaled(const fa_paged_kv *c, const fa_paged_scales *scales, const fa_kv_append_args *a,
+                              void *workspace, void *stream);
+
+/* fa_fwd_paged over a cache held in 8 bits: the same softmax over the values
+ * that the codes stand for.  Products, sums and scales are exact up to fp32; P
+ * is rounded to 11 significant bits for up to 16 rows per sequence and kv head,
+ * to 8 (bf16) beyond.  scratch: fa_paged_scratch_bytes().                   */
+fa_status fa_fwd_paged_scaled(const fa_paged_kv *c, const fa_paged_scales *scales, const fa_paged_fwd_args *a,
+                              const fa_mask_desc *mask, const fa_score_desc *sc, void *scratch, size_t scratch_bytes,
+                              void *workspace, void *stream);
+
+/* A step's pages, offsets and slots from its sequences' lengths, on the device:
+ * what fa_kv_append and fa_fwd_paged need for the step, without a copy to the
+ * host.  Sequence b had kv_len[b] tokens in the cache; the step keeps the first
+ * keep_len[b] of them (fewer where drafts were rejected; 0, with new_len 0,
+ * where it has ended) and brings new_len[b] new ones.  With P = page_size and
+ * S = shared_pages:
+ *     kv_len_out[b] = keep_len[b] + new_len[b]
+ *     before = max(ceil(kv_len[b] / P), S), after = max(ceil(kv_len_out[b] / P), S)
+ * Entries after .. before - 1 of its row of the page table are given back,
+ * entries before .. after - 1 are filled.  The free pages are a stack: those
+ * given back go on top, the last sequence's last entry first, and then the
+ * entries to fill take their pages from the top, the first sequence's first
+ * entry first.  (So a step that gives pages back undoes the one that took
+ * them.)  The first S entries of every row are a prefix's that all sequences
+ * share and stay as they are; keep_len may reach up to S x P there.
+ *   new_len, keep_len, kv_len   device int32 [B]; keep_len may be NULL: all are
+ *               kept.
+ *   page_table  device int32 [B][max_pages], in and out.  Entries that are
+ *               given back stay there, and mean nothing.
+ *   free_pages  device int32 [num_pages], in and out: the stack, its bottom first.
+ *   free_count  device int32 [1]: pages on the stack.
+ *   kv_len_out, free_count_out   device int32 [B], [1]; may be kv_len and
+ *               free_count.  Where they are not, the call may be repeated: it
+ *               writes the same again.
+ *   q_start     device int32 [B + 1], out: sums of new_len.
+ *   slots       device int64 [total_q], out, or NULL: for each row of the step
+ *               page x P + place within the page, -1 behind the last sequence.
+ *   positions   device int32 [total_q], out, or NULL: the row's place in its
+ *               sequence (fa_kv_append's positions), 0 behind the last one.
+ *   total_q     rows of the step's tensors, at least the sum of new_len.
+ * A step that cannot be made changes nothing but its outputs, which are those
+ * of an empty step (kv_len_out = kv_len, free_count_out = free_count, q_start
+ * all 0), and is reported by fa_workspace_check as FA_ERR_DEVICE_CHECK: numbers
+ * that contradict each other (a negative length, keep_len past kv_len and the
+ * shared pages, more than max_pages x P tokens, new_len adding up to more than
+ * total_q, free_count or a page that moves outside 0 .. num_pages), or too few
+ * free pages.
+ * B <= 2048; page_size as for fa_paged_kv.  No two arrays overlap, apart from
+ * kv_len_out and free_count_out as said.  One kernel launch, or two for many
+ * rows.                                                                     */
+typedef struct fa_paged_step_args {
+    int32_t B;
+    int32_t num_pages;
+    int32_t page_size;
+    int32_t max_pages;
+    int32_t shared_pages;
+    int32_t total_q;
+    const int32_t *new_len;
+    const int32_t *keep_len;
+    const int32_t *kv_len;
+    int32_t *page_table;
+    int32_t *free_pages;
+    const int32_t *free_count;
+    int32_t *kv_len_out;
+    int32_t *free_count_out;
+    int32_t *q_start;
+    int64_t *slots;
+    int32_t *positions;
+} fa_paged_step_args;
+
+fa_status fa_paged_step(const fa_paged_step_args *a, void *workspace, void *stream);
 
 #ifdef __cplusplus
 }
