@@ -54,7 +54,8 @@ def up_to_date() -> bool:
 # they hand out add up to a fixed per-thread launch count, so the compiled
 # kernel must be launched with exactly that many registers (a smaller launch
 # allocation would leave a setmaxnreg.inc waiting for registers forever).
-LAUNCH_REGISTERS = {"fwd_bf16.cu": ("fwd_bf16_kernel", 168), "paged_tiles.cu": ("paged_tiles_kernel", 168)}
+LAUNCH_REGISTERS = {"fwd_bf16.cu": ("fwd_bf16_kernel", 168), "paged_tiles.cu": ("paged_tiles_kernel", 168),
+                    "paged_tiles_scaled.cu": ("paged_tiles_kernel", 128)}
 
 
 def check_launch_registers(src: str, ptxas_log: str) -> None:

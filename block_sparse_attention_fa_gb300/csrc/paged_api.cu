@@ -344,7 +344,7 @@ fa_status forward(const fa_paged_kv* c, bool scaled, const fa_paged_scales* scal
     const auto map_of = scaled ? fa::page_tensor_map_scaled : fa::page_tensor_map;
     alignas(64) CUtensorMap tk, tv, sk, sv;       // boxes of the tile kernel, of the small one
     if (!small || p.join_rows) {
-        const int keys = fa::kPagedTileKeys;
+        const int keys = scaled ? fa::kPagedTileScaledKeys : fa::kPagedTileKeys;
         if ((st = map_of(&tk, c->k, blocks, c->page_size, c->D, keys)) != FA_OK) return st;
         if ((st = map_of(&tv, c->v, blocks, c->page_size, c->D, keys)) != FA_OK) return st;
     }

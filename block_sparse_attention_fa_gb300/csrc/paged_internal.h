@@ -33,6 +33,8 @@ struct StepParams {
 // Keys of a tile of the small kernel over codes: 32 KB of K and V (16 KB for 64
 // columns, where 32 would be 256 keys).
 constexpr int kPagedSmallScaledKeys = 128;
+// Keys that the tile kernel converts at a time, and so of a copy.
+constexpr int kPagedTileScaledKeys = 64;
 
 cudaError_t launch_kv_append_scaled(const AppendScaledParams& p, cudaStream_t s);
 cudaError_t launch_paged_step(const StepParams& p, cudaStream_t s);

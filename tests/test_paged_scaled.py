@@ -71,6 +71,9 @@ class Batch8(Batch):
             scale = 2.0 ** np.round(r.normal(-6.5, spread, n))
             if kind == "any":
                 scale = scale * r.uniform(0.7, 1.4, n)
+            if self.shared % self.page:          # the prefix's last keys, in common as values: copied with their scale
+                last = self.table[:, self.shared // self.page]
+                scale[last[last >= 0]] = scale[self.table[0, self.shared // self.page]]
             scale = np.where(owned[:, None], scale, np.nan).astype(np.float32)
             with np.errstate(invalid="ignore"):
                 y = values / scale[:, :, None, None]
@@ -381,3 +384,49 @@ def test_decode_scales_far_apart(fa, D):  # noqa: F811
     run8(fa, Batch8([1, 2], [300, 500], 2, D, 16, kind="any", spread=3.0), 4, q_scale=0.01)
     run8(fa, Batch8([1, 2], [300, 500], 2, D, 16), 4, q_scale=1e-30)
     run8(fa, Batch8([1, 2], [300, 500], 2, D, 16), 4, q_scale=1e6, scale=1e-7)
+
+
+# ---------------------------------------------------------------- GPU: many rows
+@gpu
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("mask,window,sinks", MASKS)
+def test_chunk_masks(fa, page, D, mask, window, sinks):  # noqa: F811
+    run8(fa, Batch8([100, 1, 40, 0, 130], [100, 700, 129, 10, 300], 2, D, page, pad=2), 8, mask, window, sinks)
+
+
+@gpu
+@pytest.mark.parametrize("score", SCORES)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("out_fp32", [False, True])
+def test_chunk_scores(fa, score, D, out_fp32):  # noqa: F811
+    run8(fa, Batch8([60, 1, 0, 33], [500, 40, 10, 333], 2, D, 32, kind="any"), 6, "sink_window", 200, 3, score=score,
+         out_fp32=out_fp32, **score_kw(score, 6))
+
+
+@gpu
+@pytest.mark.parametrize("Hq,Hkv,n", [(1, 1, 17), (1, 1, 300), (3, 1, 90), (4, 4, 129), (16, 2, 7), (14, 2, 300)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_chunk_groups(fa, Hq, Hkv, n, D):  # noqa: F811
+    r = np.random.default_rng(Hq)
+    kv = list(r.integers(n, n + 1200, 5))
+    run8(fa, Batch8([n] * 4 + [n - 1], kv, Hkv, D, 64, kind="any", spread=2.0), Hq)
+
+
+@gpu
+@pytest.mark.parametrize("D", [64, 128])
+def test_chunk_long_and_many(fa, D):  # noqa: F811
+    run8(fa, Batch8([600, 40], [3000, 5000], 1, D, 128, kind="any"), 2)
+    r = np.random.default_rng(2)
+    run8(fa, Batch8([1] * 299 + [20], list(r.integers(20, 90, 300)), 1, D, 16), 2)
+
+
+@gpu
+@pytest.mark.parametrize("shared", [16, 64, 1000, 3000])
+@pytest.mark.parametrize("n,Hq", [(1, 8), (3, 4), (40, 4)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_shared_prefix(fa, shared, n, Hq, D):  # noqa: F811
+    kv = [shared + x for x in (n, n + 5, n + 300, n + 64, n)]
+    page = 16 if shared < 1000 else 64
+    for mask in (("causal", 0, 0), ("sink_window", 400, 7)):
+        run8(fa, Batch8([n, n, n, max(n - 1, 0), n], kv, 2, D, page, shared=shared, kind="any"), Hq, *mask)
