@@ -97,6 +97,9 @@ bool small_rows(const fa_paged_kv* c, const fa_paged_fwd_args* a) {
     return (long long)a->max_q_len * (a->Hq / c->Hkv) <= fa::kPagedSmallRows;
 }
 
+// Of those, over a cache held in 8 bits: whether 8 rows are enough.
+bool eight_rows(const fa_paged_kv* c, const fa_paged_fwd_args* a) { return (long long)a->max_q_len * (a->Hq / c->Hkv) <= 8; }
+
 fa_status check_fwd(const fa_paged_kv* c, const fa_paged_fwd_args* a) {
     fa_status st = check_cache(c);
     if (st != FA_OK) return st;
@@ -357,7 +360,8 @@ fa_status forward(const fa_paged_kv* c, bool scaled, const fa_paged_scales* scal
         return scaled ? fa::launch_paged_tiles_scaled(x, tk, tv, s) : fa::launch_paged_tiles(x, tk, tv, s);
     };
     auto small_kernel = [&](const fa::PagedScaledParams& x) {
-        return scaled ? fa::launch_paged_small_scaled(x, sk, sv, s) : fa::launch_paged_small(x, sk, sv, s);
+        if (!scaled) return fa::launch_paged_small(x, sk, sv, s);
+        return eight_rows(c, a) ? fa::launch_paged_eight_scaled(x, sk, sv, s) : fa::launch_paged_small_scaled(x, sk, sv, s);
     };
     fa::PagedScaledParams pre = p;
     if (p.join_rows) {

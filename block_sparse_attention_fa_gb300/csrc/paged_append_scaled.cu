@@ -11,13 +11,13 @@
 // rounded once, however often the page's scale grows.
 //
 // A token's code needs the largest of all the step's tokens on its page, so a
-// unit of work is a page's share of the step, for some heads of k or of v: a
-// CTA takes kAppendThreads / G heads, G threads (whole warps) to each.  A thread
-// holds the first four of its 16-element items rotated in registers between the
-// maximum and the rounding (a page of 64 tokens of 128 columns, with 128
-// threads, or one of 16 with a warp); items beyond that are read and rotated
-// again, from L2.  The queries are no part of this: the first CTAs of the launch
-// rotate them token by token, as in paged_append.cu.
+// unit of work is a page's share of the step, for some kv heads: a CTA takes
+// kAppendThreads / G heads, G threads (whole warps) to each.  A thread holds the
+// first two of its 16-element items of k (rotated, fp32) and of v in registers
+// between the maximum and the rounding; items beyond that are read and rotated
+// again, from L2.  The loads set out before the page's id is known.  The queries
+// are no part of this: the first CTAs of the launch rotate them token by token,
+// as in paged_append.cu.
 //
 // Memory bounds it: a token is read as bf16 and written as bytes.
 #include <algorithm>
@@ -28,7 +28,7 @@
 namespace fa {
 namespace {
 
-constexpr int kHeld = 4;
+constexpr int kHeld = 2;
 
 // Which page's share of the step is unit u: the sequence, and the page's place
 // in its row of the table.  Uniform over the block; false: there is none.
@@ -111,65 +111,57 @@ __device__ __forceinline__ uint32_t e4m3_again(uint32_t w, float ratio) {
     return r;
 }
 
-// A page's share of the step, heads h0 .. of k (which = 0) or v.
+// A page's share of the step, heads h0 .. of k and v.
 template <int D>
-__device__ __forceinline__ void append_page(const AppendScaledParams& p, int u, int h0, int which, int threads_per_head,
-                                            bool report) {
+__device__ __forceinline__ void append_page(const AppendScaledParams& p, int u, int h0, int threads_per_head, bool report) {
     constexpr int kItems = D / 16;
-    __shared__ unsigned amax_s[kAppendThreads / 32];
+    __shared__ unsigned amax_s[2][kAppendThreads / 32];
     const int tid = threadIdx.x, G = threads_per_head, slot = tid / G, g = tid - slot * G, h = h0 + slot;
     SeqInfo s;
     int b, entry;
-    if (tid < kAppendThreads / 32) amax_s[tid] = 0;
+    if (tid < 2 * (kAppendThreads / 32)) amax_s[tid & 1][tid >> 1] = 0;
     if (!find_unit(p, u, report, s, b, entry)) return;
-    const int page = load_i32(p.c.page_table + static_cast<size_t>(b) * p.c.max_pages + entry);
-    if (page < 0 || page >= p.c.num_pages) {
-        if (tid == 0) report_sequence(p.ws, b);
-        return;
-    }
     const int first = entry << p.c.page_shift, start = s.kv - s.n;
     const int lo = max(first, start), hi = min(first + p.c.page_size, s.kv);     // positions of the unit
     const bool active = h < p.c.Hkv;
     const int items = active ? (hi - lo) * kItems : 0, row0 = s.q0 + lo - start;
-    const uint16_t* const src = which ? p.v + static_cast<long long>(h) * p.vs[1] : p.k + static_cast<long long>(h) * p.ks[1];
-    const long long step = which ? p.vs[0] : p.ks[0];
-    const int rot = which ? 0 : p.rot;
-    float* const scales = which ? p.v_scale : p.k_scale;
-    uint8_t* const codes = (which ? p.v8 : p.k8) + (static_cast<size_t>(page) * p.c.Hkv + h) * p.c.page_size * D;
-    const float scale_before = active && lo > first ? scales[static_cast<size_t>(page) * p.c.Hkv + h] : 0.f;
+    const uint16_t* const src_k = p.k + static_cast<long long>(h) * p.ks[1];
+    const uint16_t* const src_v = p.v + static_cast<long long>(h) * p.vs[1];
 
     // an item's two pieces of 8 (as in append_tokens), its first elements within the head
-    auto pieces = [&](int x, int& ea, int& eb) {
+    auto pieces = [&](int x, int rot, int& ea, int& eb) {
         const int k = x % kItems;
         const bool halves = k < rot / 16 && !p.interleaved;
         ea = halves ? 8 * k : 16 * k;
         eb = halves ? 8 * k + rot / 2 : 16 * k + 8;
     };
-    // the item's 16 values; false: its token has no place
-    auto fetch = [&](int x, float (&y)[16]) -> bool {
-        const int tok = x / kItems, k = x % kItems;
+    auto fetch = [&](int x, const uint16_t* src, long long step, int rot, Piece16& w) {
         int ea, eb;
-        pieces(x, ea, eb);
-        uint32_t a[4], c[4];
-        const uint16_t* const from = src + static_cast<long long>(row0 + tok) * step;
-        *reinterpret_cast<uint4*>(a) = __ldg(reinterpret_cast<const uint4*>(from + ea));
-        *reinterpret_cast<uint4*>(c) = __ldg(reinterpret_cast<const uint4*>(from + eb));
-        int at = 0;
-        if (p.rot) {
-            at = p.positions ? __ldg(p.positions + row0 + tok) : lo + tok;
-            if (at < 0 || at >= p.rope_len) {
-                report_sequence(p.ws, b);
-                return false;
-            }
-        }
+        pieces(x, rot, ea, eb);
+        const uint16_t* const from = src + static_cast<long long>(row0 + x / kItems) * step;
+        *reinterpret_cast<uint4*>(w.a) = __ldg(reinterpret_cast<const uint4*>(from + ea));
+        *reinterpret_cast<uint4*>(w.b) = __ldg(reinterpret_cast<const uint4*>(from + eb));
+    };
+    // the token's row of the tables; -1: it has no place
+    auto place = [&](int x) {
+        if (!p.rot) return 0;
+        const int at = p.positions ? __ldg(p.positions + row0 + x / kItems) : lo + x / kItems;
+        if (at >= 0 && at < p.rope_len) return at;
+        report_sequence(p.ws, b);
+        return -1;
+    };
+    auto widen = [](const Piece16& w, float (&y)[16]) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            y[2 * e] = bf_lo(a[e]);
-            y[2 * e + 1] = bf_hi(a[e]);
-            y[8 + 2 * e] = bf_lo(c[e]);
-            y[9 + 2 * e] = bf_hi(c[e]);
+            y[2 * e] = bf_lo(w.a[e]);
+            y[2 * e + 1] = bf_hi(w.a[e]);
+            y[8 + 2 * e] = bf_lo(w.b[e]);
+            y[9 + 2 * e] = bf_hi(w.b[e]);
         }
-        if (k >= rot / 16) return true;
+    };
+    auto rotate = [&](int x, int at, float (&y)[16]) {
+        const int k = x % kItems;
+        if (k >= p.rot / 16) return;
         float cs[8], sn[8];
         const size_t row = static_cast<size_t>(at) * (p.rot / 2) + 8 * k;
         *reinterpret_cast<float4*>(cs) = __ldg(reinterpret_cast<const float4*>(p.cos + row));
@@ -189,7 +181,6 @@ __device__ __forceinline__ void append_page(const AppendScaledParams& p, int u, 
 #pragma unroll
             for (int e = 0; e < 8; ++e) turn(y[e], y[8 + e], e);
         }
-        return true;
     };
     auto largest = [](const float (&y)[16], float m) {
 #pragma unroll
@@ -200,30 +191,68 @@ __device__ __forceinline__ void append_page(const AppendScaledParams& p, int u, 
         return m;
     };
 
-    float held[kHeld][16];
-    bool fits[kHeld];
-    float m = 0.f;
+    Piece16 raw_k[kHeld], raw_v[kHeld];
 #pragma unroll
     for (int e = 0; e < kHeld; ++e) {
-        fits[e] = g + e * G < items && fetch(g + e * G, held[e]);
-        if (fits[e]) m = largest(held[e], m);
+        const int x = g + e * G;
+        if (x >= items) continue;
+        fetch(x, src_k, p.ks[0], p.rot, raw_k[e]);
+        fetch(x, src_v, p.vs[0], 0, raw_v[e]);
+    }
+    const int page = load_i32(p.c.page_table + static_cast<size_t>(b) * p.c.max_pages + entry);
+    const bool placed = page >= 0 && page < p.c.num_pages;         // (uniform)
+    if (!placed) {
+        if (tid == 0) report_sequence(p.ws, b);
+        return;
+    }
+    const size_t head = static_cast<size_t>(page) * p.c.Hkv + h;
+    const bool earlier = lo > first;
+    const float before[2] = {active && earlier ? p.k_scale[head] : 0.f, active && earlier ? p.v_scale[head] : 0.f};
+    float held[kHeld][16], m[2] = {0.f, 0.f};
+    bool fits[kHeld];
+#pragma unroll
+    for (int e = 0; e < kHeld; ++e) {
+        const int x = g + e * G, at = x < items ? place(x) : -1;
+        fits[e] = at >= 0;
+        if (!fits[e]) continue;
+        float y[16];
+        widen(raw_v[e], y);
+        m[1] = largest(y, m[1]);
+        widen(raw_k[e], held[e]);
+        rotate(x, at, held[e]);
+        m[0] = largest(held[e], m[0]);
     }
     for (int x = g + kHeld * G; x < items; x += G) {
+        const int at = place(x);
+        if (at < 0) continue;
+        Piece16 w;
         float y[16];
-        if (fetch(x, y)) m = largest(y, m);
+        fetch(x, src_v, p.vs[0], 0, w);
+        widen(w, y);
+        m[1] = largest(y, m[1]);
+        fetch(x, src_k, p.ks[0], p.rot, w);
+        widen(w, y);
+        rotate(x, at, y);
+        m[0] = largest(y, m[0]);
     }
     // (the bits of numbers that are not negative are in their order)
-    const unsigned top = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
-    if ((tid & 31) == 0) atomicMax(&amax_s[slot], top);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const unsigned top = __reduce_max_sync(0xffffffffu, __float_as_uint(m[q]));
+        if ((tid & 31) == 0) atomicMax(&amax_s[q][slot], top);
+    }
     __syncthreads();
     if (!active) return;
-    const float scale = fmaxf(needed_scale(__uint_as_float(amax_s[slot])), scale_before);
-    const float inv = 1.f / scale;
-    if (g == 0) scales[static_cast<size_t>(page) * p.c.Hkv + h] = scale;
-    if (lo > first && scale != scale_before) {
+    float inv[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const float scale = fmaxf(needed_scale(__uint_as_float(amax_s[q][slot])), before[q]);
+        inv[q] = 1.f / scale;
+        if (g == 0) (q ? p.v_scale : p.k_scale)[head] = scale;
+        if (!earlier || scale == before[q]) continue;
         // the earlier tokens' codes, to the new scale
-        const float ratio = scale_before / scale;
-        uint4* const old = reinterpret_cast<uint4*>(codes);
+        const float ratio = before[q] / scale;
+        uint4* const old = reinterpret_cast<uint4*>((q ? p.v8 : p.k8) + head * p.c.page_size * D);
         for (int x = g; x < (lo - first) * kItems; x += G) {
             uint4 w = old[x];
             w.x = e4m3_again(w.x, ratio);
@@ -233,25 +262,38 @@ __device__ __forceinline__ void append_page(const AppendScaledParams& p, int u, 
             old[x] = w;
         }
     }
-    auto put = [&](int x, const float (&y)[16]) {
+    auto put = [&](int x, int q, const float (&y)[16]) {
         int ea, eb;
-        pieces(x, ea, eb);
-        uint8_t* const dst = codes + static_cast<size_t>(lo - first + x / kItems) * D;
-        *reinterpret_cast<uint2*>(dst + ea) = make_uint2(e4m3_four(y, inv), e4m3_four(y + 4, inv));
-        *reinterpret_cast<uint2*>(dst + eb) = make_uint2(e4m3_four(y + 8, inv), e4m3_four(y + 12, inv));
+        pieces(x, q ? 0 : p.rot, ea, eb);
+        uint8_t* const dst = (q ? p.v8 : p.k8) + head * p.c.page_size * D + static_cast<size_t>(lo - first + x / kItems) * D;
+        *reinterpret_cast<uint2*>(dst + ea) = make_uint2(e4m3_four(y, inv[q]), e4m3_four(y + 4, inv[q]));
+        *reinterpret_cast<uint2*>(dst + eb) = make_uint2(e4m3_four(y + 8, inv[q]), e4m3_four(y + 12, inv[q]));
     };
 #pragma unroll
     for (int e = 0; e < kHeld; ++e) {
-        if (fits[e]) put(g + e * G, held[e]);
+        if (!fits[e]) continue;
+        put(g + e * G, 0, held[e]);
+        float y[16];
+        widen(raw_v[e], y);
+        put(g + e * G, 1, y);
     }
     for (int x = g + kHeld * G; x < items; x += G) {
+        const int at = place(x);
+        if (at < 0) continue;
+        Piece16 w;
         float y[16];
-        if (fetch(x, y)) put(x, y);
+        fetch(x, src_k, p.ks[0], p.rot, w);
+        widen(w, y);
+        rotate(x, at, y);
+        put(x, 0, y);
+        fetch(x, src_v, p.vs[0], 0, w);
+        widen(w, y);
+        put(x, 1, y);
     }
 }
 
 // CTAs 0 .. q_ctas - 1: the queries of per_cta tokens each; the others: page by
-// page, for k and v of `heads` kv heads.
+// page, some kv heads each.
 template <int D>
 __global__ void __launch_bounds__(kAppendThreads, 2)
 kv_append_scaled_kernel(const AppendParams q, const AppendScaledParams p, int q_ctas, int per_cta, int threads_per_head) {
@@ -263,8 +305,8 @@ kv_append_scaled_kernel(const AppendParams q, const AppendScaledParams p, int q_
     pdl_launch_next();
     const int at = blockIdx.x - q_ctas, heads = kAppendThreads / threads_per_head;
     const int parts = (p.c.Hkv + heads - 1) / heads;
-    const int u = at / (2 * parts), r = at - u * 2 * parts;
-    append_page<D>(p, u, (r >> 1) * heads, r & 1, threads_per_head, at == 0);
+    const int u = at / parts;
+    append_page<D>(p, u, (at - u * parts) * heads, threads_per_head, at == 0);
 }
 
 }  // namespace
@@ -280,7 +322,7 @@ cudaError_t launch_kv_append_scaled(const AppendScaledParams& p, cudaStream_t s)
     // pages that the step can touch: one more than it fills, twice, per sequence, and one per token at most
     const long long units = std::min<long long>(p.c.total_q, p.c.total_q / p.c.page_size + 2LL * p.c.B);
     const int heads = kAppendThreads / G;
-    const long long kv_ctas = units * 2 * ((p.c.Hkv + heads - 1) / heads);
+    const long long kv_ctas = units * ((p.c.Hkv + heads - 1) / heads);
     const int per_cta = p.c.total_q >= kAppendTokens * 4 * device_sm_count() ? kAppendTokens : 1;
     const long long q_ctas = p.Hq ? (p.c.total_q + per_cta - 1LL) / per_cta : 0;
     if (q_ctas + kv_ctas > 2147483647LL) return cudaErrorInvalidConfiguration;

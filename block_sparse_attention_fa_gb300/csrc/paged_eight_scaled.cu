@@ -1,0 +1,633 @@
+// paged_eight_scaled.cu -- attention over a cache held in 8 bits (e4m3 codes, a
+// scale for each page and kv head) for up to 8 rows per (sequence, kv head).
+//
+// The split of the work and the partials are paged_small.cu's: the tiles (128
+// keys) of all units stand in one line, every CTA (two per SM) takes an equal
+// stretch, and a second kernel joins the units that two CTAs share.  With half
+// the bytes per key what a key costs beside its bytes counts twice, so the
+// consumers work differently.
+//
+// Each of the 4 consumer warps keeps 32 keys of a tile to itself, from S to
+// P V, with a running maximum, a sum and all columns of O of its own: no barrier
+// between the warps and no exchange through shared memory within a unit; at its
+// end the four are added up.  The products are transposed, S^T = K Q^T and
+// O^T = V^T P^T (mma.sync m16n8k16: 16 keys, then 16 columns, by 8 rows of Q), so
+// that 8 rows fill them.
+//   - K: ldmatrix gives a thread 32 bits of a key's row: four adjacent columns,
+//     where the product wants two and two, 8 apart.  The columns of 16 go to the
+//     product in that order, Q's with them.
+//   - P^T is S^T's result with keys and rows exchanged: movmatrix.
+//   - V: ldmatrix.trans gives two keys of two adjacent columns; the even columns
+//     are the product's rows 0-7, the odd ones 8-15.
+// A code is converted once, to f16, which holds it exactly; so does it a row of Q
+// scaled by a power of two, and P is rounded to f16's 11 bits.  The scales are
+// applied in fp32: k's to S, v's to the product of 16 keys, which are of one page.
+//
+// The maximum is raised (and O and the sum rescaled) only when a score is 2^8
+// past it, which one vote of the warp tells.
+//
+// The loader's lanes stand for the pages of the next tiles (32 pages at a time):
+// a page's id and scales are read a batch ahead, for a scale needs the id and
+// both come from memory.
+//
+// V rows of keys that no row of the unit sees are cleared in shared memory before
+// the product: their P is 0, but 0 x NaN is not.
+#include <algorithm>
+#include <math_constants.h>
+
+#include "paged_line.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kWarps = 4;                        // consumers; warp 4 loads
+constexpr int kThreadsS = 32 * (kWarps + 1);
+constexpr int kKeys = kPagedSmallScaledKeys, kShift = 7;
+constexpr int kTileOpen = 1, kTileClear = 2;    // every row sees every key; some key is seen by no row
+constexpr float kLazyMax = 8.f;
+// Units that the consumers read where the loader puts them.  It writes unit nu once
+// all of them have begun unit nu - 2, and so are done with nu - 3.
+constexpr int kSegs = 4;
+static_assert(kKeys == 32 * kWarps && kKeys == 1 << kShift, "32 keys to a warp");
+enum PagedSite8 : uint32_t { S_P8_FULL = 112, S_P8_EMPTY, S_P8_DRAIN, S_P8_Q, S_P8_Q_EMPTY };
+
+// Two CTAs on an SM.
+template <int D>
+struct Small8 {
+    static constexpr int kCtas = 2;
+    static constexpr int kRows = 8;
+    static constexpr uint32_t kTile = kKeys * static_cast<uint32_t>(D);
+    static constexpr uint32_t kStage = 2u * kTile;               // K then V
+    static constexpr int kStages = 98304 / kStage;               // 96 KB
+    static constexpr uint32_t kQRow = 2u * D + 16u;
+    static constexpr uint32_t kMerge = kStages * kStage;         // two warps' O
+    static constexpr uint32_t kMl = kMerge + 8u * kRows * D;     // [warps][rows] maximum and sum
+    static constexpr uint32_t kQ = kMl + 8u * kWarps * kRows;    // two units' rows of Q
+    static constexpr uint32_t kSeg = kQ + 2u * kRows * kQRow;    // [kSegs] units, the last one flagged by b < 0
+    static constexpr uint32_t kScale = kSeg + kSegs * sizeof(SmallSeg);      // [stage]: k's scale of each of the tile's pages, v's
+    static constexpr uint32_t kScaleStage = 8u * (kKeys / 16);
+    static constexpr uint32_t kInfo = kScale + kScaleStage * kStages;     // [stage]: 4 x tile + kTileOpen, kTileClear
+    static constexpr uint32_t kBars = (kInfo + 4u * kStages + 7u) & ~7u;  // FULL, EMPTY [stage], Q_FULL, Q_EMPTY [2]
+    static constexpr uint32_t kAbort = kBars + 16u * kStages + 32u;
+    static constexpr uint32_t kScan = kAbort + 16u;              // warp sums
+    static constexpr uint32_t kPre = kScan + 64u;                // first tile of each group of sequences
+    // (fewer entries of the line's index than the bf16 kernel has room for)
+    static constexpr int kEntries = 350;
+    static constexpr uint32_t bytes(int B) { return kPre + 4u * (groups_of(B, kEntries) + 1u) + 1024u; }
+    // 228 KB on an SM, less 1 KB for each CTA
+    static_assert(kCtas * (kPre + 4u * (kEntries + 1u) + 1024u) <= (228u - kCtas) * 1024u, "shared memory budget");
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+// An 8 x 8 matrix of 16-bit elements, two of a row to a thread, transposed.
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+// c += a b, one m16n8k16 tile of f16, fp32 sums
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+// d = a b, the same from 0
+__device__ __forceinline__ void mma_f16_from_0(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(0.f));
+}
+// Four e4m3 codes as two pairs of f16: exact.
+__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float bf_low(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+// Byte offset of 16-byte chunk `chunk` of key `key` in a tile of codes, rows of
+// 128 bytes written with 128-byte swizzle: a key of 128 columns, or two of 64.
+template <int D>
+__device__ __forceinline__ uint32_t swz8(int key, int chunk) {
+    const int row = D == 128 ? key : key >> 1, at = D == 128 ? chunk : 4 * (key & 1) + chunk;
+    return static_cast<uint32_t>(row * 128 + ((at ^ (row & 7)) << 4));
+}
+__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// The same barrier with a vote: whether `ok` holds in every thread.
+__device__ __forceinline__ bool consumers_all(bool ok) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.and.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(ok))
+        : "memory");
+    return r != 0;
+}
+
+template <int D, int SCORE>
+__global__ void __launch_bounds__(kThreadsS, Small8<D>::kCtas)
+paged_eight_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                          const PagedScaledParams p) {
+    using L = Small8<D>;
+    constexpr int ST = L::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const uint32_t sbase = smem_addr(smem);
+    auto full_bar = [&](int st) { return sbase + L::kBars + 8u * st; };
+    auto empty_bar = [&](int st) { return sbase + L::kBars + 8u * (ST + st); };
+    auto q_full = [&](int u) { return sbase + L::kBars + 8u * (2 * ST + (u & 1)); };
+    auto q_empty = [&](int u) { return sbase + L::kBars + 8u * (2 * ST + 2 + (u & 1)); };
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kAbort);
+    int* const pre = reinterpret_cast<int*>(smem + L::kPre);
+    SmallSeg* const seg_s = reinterpret_cast<SmallSeg*>(smem + L::kSeg);
+    volatile int* const info_s = reinterpret_cast<volatile int*>(smem + L::kInfo);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
+
+    if (threadIdx.x == 0) {
+        for (int st = 0; st < ST; ++st) {
+            mbar_init(full_bar(st), 1);
+            mbar_init(empty_bar(st), kWarps);
+        }
+        for (int u = 0; u < 2; ++u) {
+            mbar_init(q_full(u), 1);
+            mbar_init(q_empty(u), kWarps);
+        }
+        *abort_flag = 0;
+        mbar_fence_init();
+    }
+    // (a shared prefix's kernel is no input of this one: it is waited for at the end)
+    if (p.join_rows)
+        wait_before_prefix(p);
+    else
+        pdl_wait_previous();
+    pdl_launch_next();
+    // the line of tiles
+    Line line{};
+    line.pre = pre;
+    line.shift = group_shift(p.c.B, L::kEntries);
+    const int groups = groups_of(p.c.B, L::kEntries);
+    int* const scan = reinterpret_cast<int*>(smem + L::kScan);
+    block_prefix<kThreadsS>(groups, pre, scan, [&](int g) {
+        return group_length<kShift>(p, line.shift, g, cta == 0 ? p.ws : nullptr);
+    });
+    line.front = p.c.Hkv * pre[groups] >= kManyTiles * p.ctas;
+    if (line.front) {
+        block_prefix<kThreadsS>(groups, pre, scan, [&](int g) {
+            return group_length_front<kShift>(p, line.shift, g, pre[g + 1] - pre[g]);
+        });
+    }
+    const int total = p.c.Hkv * pre[groups];
+    line_share(total, p.ctas, cta, line.per, line.t, line.t1);
+    if (line.t < line.t1) {
+        line.g = line_find(pre, groups, p.c.Hkv, line.t);
+        if (warp == kWarps) open_group<kShift>(p, line);
+    }
+    const WaitCtl wc{abort_flag, p.ws, p.timeout_ns};
+
+    if (warp == kWarps) {
+        // ------------------------------------------------------------ loader
+        if (lane == 0) {
+            tma_prefetch_desc(&tmK);
+            tma_prefetch_desc(&tmV);
+        }
+        const int span = min(p.c.page_size, kKeys), pages = kKeys / span;    // 1, 2, 4 or 8
+        const uint32_t page_bytes = static_cast<uint32_t>(span) * D * 2u;    // K and V
+        int last[ST];
+#pragma unroll
+        for (int st = 0; st < ST; ++st) last[st] = -1;
+        int g = 0, nu = 0;
+        bool ok = true, marked = false;
+        SmallSeg s;
+        for (; ok; ++nu) {
+            const bool more = next_seg<kShift>(p, line, s);
+            if (nu >= 2 && !mbar_wait_warp(q_empty(nu), ((nu >> 1) - 1) & 1, wc, S_P8_Q_EMPTY)) break;
+            if (!more) {
+                if (lane == 0) {
+                    seg_s[nu % kSegs].b = -1;
+                    mbar_arrive(q_full(nu));
+                }
+                marked = true;
+                break;
+            }
+            const int32_t* table = p.c.page_table + (size_t)s.b * p.c.max_pages;
+            // A lane stands for a page of one of the next 32 / `pages` tiles; it reads
+            // the page's id and scales a whole batch of tiles ahead (a scale needs the
+            // id, and both come from memory).
+            auto page_of = [&](int k) {
+                return k < s.k1 ? tile_page<kKeys>(p.c, table, s.hull, s.hull.tile(k), lane & (pages - 1), s.b, p.ws) : -1;
+            };
+            auto scale_of = [&](const float* scales, int id) {
+                return id >= 0 ? scales[(size_t)id * p.c.Hkv + s.h] : 0.f;
+            };
+            int id = page_of(s.k0 + lane / pages), id2 = -1;
+            // the unit and its rows of Q, a lane to each, into the slots that
+            // the unit before the last has left
+            const int rows = s.n * p.group, i0 = s.kv - s.n, i1 = s.kv - 1;
+            if (lane == 0) {
+                seg_s[nu % kSegs] = s;
+                mbar_arrive_expect_tx(q_full(nu), static_cast<uint32_t>(rows) * 2u * D);
+            }
+            __syncwarp();
+            if (lane < rows) {
+                const int tok = quotient(lane, p.by_group);
+                bulk_load(sbase + L::kQ + ((nu & 1) * L::kRows + lane) * L::kQRow,
+                          p.q + (long long)(s.q0 + tok) * p.qs[0] +
+                              (long long)(s.h * p.group + lane - tok * p.group) * p.qs[1],
+                          2u * D, q_full(nu));
+            }
+            float ks = scale_of(p.k_scale, id), vs = scale_of(p.v_scale, id), ks2 = 0.f, vs2 = 0.f;
+            for (int k = s.k0, e = 0; k < s.k1; ++k, ++g, ++e) {
+                if (e == 32 / pages) {
+                    e = 0;
+                    id = id2;
+                    ks = ks2;
+                    vs = vs2;
+                }
+                if (e == 0) id2 = page_of(k + 32 / pages + lane / pages);
+                if (e == 2) {
+                    ks2 = scale_of(p.k_scale, id2);
+                    vs2 = scale_of(p.v_scale, id2);
+                }
+                const int kb = s.hull.tile(k), st = g % ST, at = lane & (pages - 1);
+                const bool here = lane / pages == e;
+                if (g >= ST && !mbar_wait_warp(empty_bar(st), (g / ST - 1) & 1, wc, S_P8_EMPTY)) { ok = false; break; }
+                const uint32_t copies = __popc(__ballot_sync(0xffffffffu, here && id >= 0));
+                if (lane == 0) mbar_expect_tx(full_bar(st), copies * page_bytes);
+                __syncwarp();
+                if (here && id >= 0) {
+                    const uint32_t dst = sbase + st * L::kStage + static_cast<uint32_t>(at * span) * D;
+                    const int row = ((kb * kKeys + at * span) & (p.c.page_size - 1)) / (128 / D);
+                    const int block = id * p.c.Hkv + s.h;
+                    tma_load_3d(dst, &tmK, full_bar(st), 0, row, block);
+                    tma_load_3d(dst + L::kTile, &tmV, full_bar(st), 0, row, block);
+                }
+                // what else the consumers need of the tile, and only then the loader's arrival
+                float* const sc = reinterpret_cast<float*>(smem + L::kScale + st * L::kScaleStage);
+                if (here) {
+                    sc[at] = ks;
+                    sc[kKeys / 16 + at] = vs;
+                }
+                if (lane == 0)
+                    info_s[st] = 4 * kb + (tile_open(p.mask, kb, i0, i1, p.shared, s.kv, kShift) ? kTileOpen : 0) +
+                                 (s.hull.all(kb * kKeys, kb * kKeys + kKeys) ? 0 : kTileClear);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(full_bar(st));
+                last[st] = g;
+            }
+        }
+        // every issued copy lands before the CTA exits
+        if (lane == 0) {
+#pragma unroll
+            for (int st = 0; st < ST; ++st)
+                if (last[st] >= 0) paged_drain_wait(full_bar(st), (last[st] / ST) & 1, wc, S_P8_DRAIN);
+            // (behind the end mark only the last unit's rows can be on their
+            // way: the mark's slot had been read)
+            for (int u = max(nu - (marked ? 1 : 2), 0); u < nu; ++u)
+                paged_drain_wait(q_full(u), (u >> 1) & 1, wc, S_P8_DRAIN);
+        }
+        __syncwarp();
+        if (p.join_rows) pdl_wait_previous();
+        return;
+    }
+
+    // --------------------------------------------------------------- consumers
+    const int gr = lane >> 2, tq = lane & 3, mi = lane >> 3, l8 = lane & 7;
+    float2* const ml_s = reinterpret_cast<float2*>(smem + L::kMl);
+    // score_mod, to base 2
+    const float sl2 = p.scale * kPagedLog2e;
+    const SoftCap cap = soft_cap(p.score.softcap, SCORE == FA_SCORE_SOFTCAP ? p.scale : 1.f);
+    const int by_page = min(p.c.page_shift, kShift);       // 2^by_page keys of a tile share a page
+    constexpr int kChunks = D / 16;                        // 16 columns each
+    int g = 0;
+    bool ok = true;
+    PagedMeta meta{};
+    for (int nu = 0;; ++nu) {
+        const bool q_here = mbar_wait_warp(q_full(nu), (nu >> 1) & 1, wc, S_P8_Q);
+        // (the vote keeps the warps together where a wait has run out)
+        if (!consumers_all(q_here)) { ok = false; break; }
+        const SmallSeg& s = seg_s[nu % kSegs];
+        if (s.b < 0) break;
+        const int rows = s.n * p.group, i0 = s.kv - s.n;
+        // Q's fragments in f16: a row times a power of two, so that its largest
+        // element is 2^14 .. 2^15 and those below f16's normal numbers are 2^28
+        // times smaller.  (Rows past the unit's are 0.)
+        uint32_t qb[kChunks][2];
+        float unscale[2], slope[2];
+        int tok[2];
+        const int r = gr;
+        const uint8_t* const q_row = smem + L::kQ + ((nu & 1) * L::kRows + r) * L::kQRow + 8 * tq;
+        float top = 0.f;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+            const uint2 w = r < rows ? *reinterpret_cast<const uint2*>(q_row + 32 * c) : make_uint2(0u, 0u);
+            qb[c][0] = w.x;
+            qb[c][1] = w.y;
+            top = fmaxf(top, fmaxf(fmaxf(fabsf(bf_low(w.x)), fabsf(bf_high(w.x))),
+                                   fmaxf(fabsf(bf_low(w.y)), fabsf(bf_high(w.y)))));
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int at = max(__float_as_int(top) >> 23, 15);
+        const float up = __int_as_float((268 - at) << 23), down = __int_as_float((at - 14) << 23);
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                qb[c][e] = pack_f16x2(bf_low(qb[c][e]) * up, bf_high(qb[c][e]) * up);
+        }
+        // this thread's columns of S^T: rows 2 tq and the next one
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            unscale[e] = __shfl_sync(0xffffffffu, down, 4 * (2 * tq + e));
+            const int row = min(2 * tq + e, rows - 1);
+            tok[e] = quotient(row, p.by_group);
+            slope[e] = 0.f;
+            if (SCORE == FA_SCORE_ALIBI || SCORE == FA_SCORE_ALIBI_SOFTCAP)
+                slope[e] = p.score.slopes[s.h * p.group + row - tok[e] * p.group] *
+                               (SCORE == FA_SCORE_ALIBI ? kPagedLog2e : 1.f);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_empty(nu));
+        float m[2], l[2], o[kChunks][4];
+        m[0] = m[1] = -CUDART_INF_F;
+        l[0] = l[1] = 0.f;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) o[c][0] = o[c][1] = o[c][2] = o[c][3] = 0.f;
+
+        const int tiles = s.k1 - s.k0;
+        for (int k = 0; k < tiles; ++k, ++g) {
+            const int st = g % ST;
+            const uint32_t kbase = sbase + st * L::kStage, vbase = kbase + L::kTile;
+            if (!mbar_wait_warp(full_bar(st), (g / ST) & 1, wc, S_P8_FULL)) { ok = false; break; }
+            const int info = info_s[st], j0 = (info >> 2) * kKeys + 32 * warp;
+            const float* const sc = reinterpret_cast<const float*>(smem + L::kScale + st * L::kScaleStage);
+            const bool open = (info & kTileOpen) != 0;
+            bool cleared = false;
+            // S^T, 16 keys at a time
+            float x[2][4];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                x[u][0] = x[u][1] = x[u][2] = x[u][3] = 0.f;
+            }
+#pragma unroll
+            for (int c = 0; c < kChunks; c += 2) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    uint32_t kf[4], a[4], b[4];
+                    ldsm4(kbase + swz8<D>(32 * warp + 16 * u + 8 * (mi & 1) + l8, c + (mi >> 1)), kf);
+                    codes_to_f16(kf[0], a[0], a[2]);
+                    codes_to_f16(kf[1], a[1], a[3]);
+                    codes_to_f16(kf[2], b[0], b[2]);
+                    codes_to_f16(kf[3], b[1], b[3]);
+                    mma_f16(x[u], a, qb[c]);
+                    mma_f16(x[u], b, qb[c + 1]);
+                }
+            }
+            if (info & kTileClear) {
+                // V rows that no row of the unit sees
+                cleared = true;
+                for (int r = 0; r < 32; ++r) {
+                    if (!s.hull.live(j0 + r) && lane < kChunks)
+                        *reinterpret_cast<uint4*>(smem + st * L::kStage + L::kTile + swz8<D>(32 * warp + r, lane)) =
+                            make_uint4(0u, 0u, 0u, 0u);
+                }
+                __syncwarp();
+            }
+            bool over = false;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const float k_scale = sc[(32 * warp + 16 * u) >> by_page];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int e = c & 1, j = j0 + 16 * u + gr + 8 * (c >> 1), i = i0 + tok[e];
+                    float v = x[u][c] * unscale[e] * k_scale;
+                    const float far = fabsf(static_cast<float>(i - j));
+                    if (SCORE == FA_SCORE_NONE || SCORE == FA_SCORE_REL_BIAS) v *= sl2;
+                    if (SCORE == FA_SCORE_SOFTCAP) v = softcap_one(v, cap);
+                    if (SCORE == FA_SCORE_ALIBI) v = fmaf(-slope[e], far, v * sl2);
+                    if (SCORE == FA_SCORE_ALIBI_SOFTCAP) v = softcap_one(fmaf(-slope[e], far, v * p.scale), cap);
+                    if (SCORE == FA_SCORE_REL_BIAS) {
+                        const int R = p.score.rel_max, d = min(max(i - j, -R), R);
+                        const int hq = s.h * p.group + min(2 * tq + e, rows - 1) - tok[e] * p.group;
+                        v = fmaf(p.score.rel_bias[(size_t)hq * (2 * R + 1) + d + R], kPagedLog2e, v);
+                    }
+                    if (!open && !paged_visible(p.mask, i, j, p.shared, s.kv)) v = -CUDART_INF_F;
+                    x[u][c] = v;
+                    over |= v > m[e] + kLazyMax;
+                }
+            }
+            if (__any_sync(0xffffffffu, over)) {
+                float alpha[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float top = fmaxf(fmaxf(fmaxf(x[0][e], x[0][2 + e]), fmaxf(x[1][e], x[1][2 + e])),
+                                      m[e]);
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                    alpha[e] = top == m[e] ? 1.f : ex2_approx(m[e] - top);
+                    m[e] = top;
+                    l[e] *= alpha[e];
+                }
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) {
+                    o[c][0] *= alpha[0];
+                    o[c][1] *= alpha[1];
+                    o[c][2] *= alpha[0];
+                    o[c][3] *= alpha[1];
+                }
+            }
+            // P^T, rows of Q along the threads
+            uint32_t pb[2][2];
+            const float ref[2] = {m[0] == -CUDART_INF_F ? 0.f : m[0], m[1] == -CUDART_INF_F ? 0.f : m[1]};
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                float w[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) w[c] = ex2_approx(x[u][c] - ref[c & 1]);
+                l[0] += w[0] + w[2];
+                l[1] += w[1] + w[3];
+                pb[u][0] = transpose_8x8(pack_f16x2(w[0], w[1]));
+                pb[u][1] = transpose_8x8(pack_f16x2(w[2], w[3]));
+            }
+            // O^T += V^T P^T, 16 columns at a time
+            const float v_scale[2] = {sc[kKeys / 16 + (32 * warp >> by_page)], sc[kKeys / 16 + ((32 * warp + 16) >> by_page)]};
+#pragma unroll
+            for (int c = 0; c < kChunks; c += 2) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    uint32_t vf[4];
+                    ldsm4_t(vbase + swz8<D>(32 * warp + 16 * u + 8 * (mi & 1) + l8, c + (mi >> 1)), vf);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        uint32_t a[4];
+                        codes_to_f16(__byte_perm(vf[2 * e], 0u, 0x3120), a[0], a[1]);
+                        codes_to_f16(__byte_perm(vf[2 * e + 1], 0u, 0x3120), a[2], a[3]);
+                        float z[4];
+                        mma_f16_from_0(z, a, pb[u]);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) o[c + e][q] = fmaf(z[q], v_scale[u], o[c + e][q]);
+                    }
+                }
+            }
+            if (cleared) fence_async_shared();     // the next copy into this stage comes after the clearing
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty_bar(st));
+        }
+
+        // the unit's end in this CTA: the warps' maxima and sums, then their O
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float sum = l[e];
+            sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+            if (gr == 0) ml_s[warp * L::kRows + 2 * tq + e] = make_float2(m[e], sum);
+        }
+        if (!consumers_all(ok)) { ok = false; break; }
+        float sum[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float top = -CUDART_INF_F;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml_s[w * L::kRows + 2 * tq + e].x);
+            const float ref = top == -CUDART_INF_F ? 0.f : top;
+            sum[e] = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float2 t = ml_s[w * L::kRows + 2 * tq + e];
+                sum[e] = fmaf(t.y, ex2_approx(t.x - ref), sum[e]);
+            }
+            const float f = ex2_approx(m[e] - ref);
+            m[e] = top;
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+                o[c][e] *= f;
+                o[c][2 + e] *= f;
+            }
+        }
+        // O of warps 2, 3 to 0, 1, and of 1 to 0
+#pragma unroll
+        for (int half = kWarps / 2; half > 0; half >>= 1) {
+            float4* const at = reinterpret_cast<float4*>(smem + L::kMerge) + (warp % half) * kChunks * 32 + lane;
+            if (warp >= half && warp < 2 * half) {
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) at[32 * c] = make_float4(o[c][0], o[c][1], o[c][2], o[c][3]);
+            }
+            consumers_sync();
+            if (warp < half) {
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) {
+                    const float4 t = at[32 * c];
+                    o[c][0] += t.x;
+                    o[c][1] += t.y;
+                    o[c][2] += t.z;
+                    o[c][3] += t.w;
+                }
+            }
+            if (half > 1) consumers_sync();
+        }
+        if (warp == 0) {
+            const bool whole = s.begins() && s.ends();
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = 2 * tq + e;
+                if (r >= rows) continue;
+                const int at = quotient(r, p.by_group);
+                const long long row = (long long)(s.q0 + at) * p.Hq + s.h * p.group + r - at * p.group;
+                const bool last = whole && !p.join_rows;
+                const long long slot = whole ? row : (2LL * cta + (s.begins() ? 1 : 0)) * kPagedSmallRows + r;
+                const float inv = !last ? 1.f : sum[e] == 0.f ? 0.f : 1.f / sum[e];      // a NaN stays one
+                if (last && !(p.flags & FA_OUT_FP32)) {
+                    uint16_t* const dst = static_cast<uint16_t*>(p.o) + row * D + 2 * gr;
+#pragma unroll
+                    for (int c = 0; c < kChunks; ++c)
+                        *reinterpret_cast<uint32_t*>(dst + 16 * c) = pack_bf16x2(o[c][e] * inv, o[c][2 + e] * inv);
+                } else {
+                    float* const dst = (last ? static_cast<float*>(p.o) : whole ? p.parts.row_o : p.parts.slot_o) +
+                                       slot * D + 2 * gr;
+#pragma unroll
+                    for (int c = 0; c < kChunks; ++c)
+                        *reinterpret_cast<float2*>(dst + 16 * c) = make_float2(o[c][e] * inv, o[c][2 + e] * inv);
+                }
+                if (gr != 0) continue;
+                if (last) {
+                    p.lse[row] = sum[e] == 0.f ? -CUDART_INF_F : (m[e] + log2f(sum[e])) * kPagedLn2;
+                } else {
+                    (whole ? p.parts.row_ml : p.parts.slot_ml)[slot] = make_float2(m[e], sum[e]);
+                    if (p.join_rows && s.begins())
+                        p.rowdesc[row] = whole ? make_int2(-1, 1)
+                                               : make_int2((2 * cta + 1) * kPagedSmallRows + r, s.count);
+                }
+            }
+        }
+        if (s.begins() && !s.ends()) {
+            meta.count = s.count;
+            meta.q0 = s.q0;
+            meta.rows = rows;
+            meta.h = s.h;
+        }
+    }
+    if (!p.join_rows && threadIdx.x == 0) p.meta[cta] = ok ? meta : PagedMeta{};
+    if (p.join_rows) pdl_wait_previous();
+}
+
+template <int D, int SCORE>
+cudaError_t launch_one(const PagedScaledParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
+    auto kern = paged_eight_scaled_kernel<D, SCORE>;
+    using L = Small8<D>;
+    constexpr size_t most = L::bytes(L::kEntries);
+    static bool attr_set[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) attr_set[dev] = true;
+    }
+    return paged_launch(kern, dim3(p.ctas), kThreadsS, L::bytes(p.c.B), true, s, tk, tv, p);
+}
+
+template <int D>
+cudaError_t launch_score(const PagedScaledParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
+    switch (p.score.kind) {
+        case FA_SCORE_SOFTCAP: return launch_one<D, FA_SCORE_SOFTCAP>(p, tk, tv, s);
+        case FA_SCORE_ALIBI: return launch_one<D, FA_SCORE_ALIBI>(p, tk, tv, s);
+        case FA_SCORE_REL_BIAS: return launch_one<D, FA_SCORE_REL_BIAS>(p, tk, tv, s);
+        case FA_SCORE_ALIBI_SOFTCAP: return launch_one<D, FA_SCORE_ALIBI_SOFTCAP>(p, tk, tv, s);
+        default: return launch_one<D, FA_SCORE_NONE>(p, tk, tv, s);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_paged_eight_scaled(const PagedScaledParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
+                                      cudaStream_t s) {
+    return p.D == 64 ? launch_score<64>(p, tk, tv, s) : launch_score<128>(p, tk, tv, s);
+}
+
+}  // namespace fa

@@ -40,6 +40,8 @@ cudaError_t launch_kv_append_scaled(const AppendScaledParams& p, cudaStream_t s)
 cudaError_t launch_paged_step(const StepParams& p, cudaStream_t s);
 cudaError_t launch_paged_small_scaled(const PagedScaledParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
                                       cudaStream_t s);
+cudaError_t launch_paged_eight_scaled(const PagedScaledParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
+                                      cudaStream_t s);
 cudaError_t launch_paged_tiles_scaled(const PagedScaledParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
                                       cudaStream_t s);
 // Pages of codes as rows of 128 bytes (a key of 128 columns, or two of 64),

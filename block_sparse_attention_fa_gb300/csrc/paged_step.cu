@@ -7,18 +7,17 @@
 //     Q of new_len, G of max(before - after, 0), T of max(after - before, 0).
 // The g-th page given back (sequences and entries ascending) goes to place
 // F + R - 1 - g of the stack of free pages (F pages before, R given in all),
-// and the k-th page taken is the one at place F + R - 1 - k.  Row t of the step
-// belongs to the sequence with Q_b <= t < Q_b + new_b.
+// and the k-th page taken is the one at place F + R - 1 - k: of the stack as it
+// was, or for k < R the k-th page given back.  Row t of the step belongs to the
+// sequence with Q_b <= t < Q_b + new_b.
 //
-// The lengths of 2048 sequences are 24 KB and a step moves few pages, so that
-// what this costs is latency: one CTA of 1024 threads does it all, in shared
-// memory, and the page numbers of a batch of prompts (6000 pages for 100000
-// tokens) are a few rounds of it.  The slots of many rows (12 bytes each) are
-// memory traffic: from kRowsHere rows on they are a second launch of as many
-// CTAs as they fill.
-//
-// Nothing is written before every number has been checked, the pages that move
-// among them; one that does not fit makes the step an empty one.
+// So every entry and every slot follows from the arguments alone, and one launch
+// does it all: each CTA makes the sums for itself (the lengths of 2048 sequences
+// are 24 KB) and takes its share of the pages and rows; a row's page comes from
+// the table, or from the stack by the same formula, never from another CTA.  The
+// last CTA to have read the arguments (a counter in the workspace, 0 between
+// launches) writes what may be written in place: the lengths, the count, the
+// stack.  One CTA does up to kRowsEach rows; what it costs is latency.
 #include <algorithm>
 
 #include "paged.cuh"
@@ -26,13 +25,15 @@
 namespace fa {
 namespace {
 
-constexpr int kStepThreads = 1024;
-constexpr int kRowsHere = 4 * kStepThreads;
-constexpr int kSlotThreads = 256, kSlotRows = 4;       // rows of a thread, adjacent ones
+constexpr int kRowsEach = 2048;          // rows, or pages times 4, that are worth a CTA
+constexpr int kSlotRows = 4;             // rows of a thread, adjacent ones
+// The counter's word of the workspace (behind the forward's).
+constexpr int kStepTicket = WS_SCHED_DONE + 1;
+static_assert(kStepTicket < WS_WORDS, "a word of the workspace");
 
-// The last of the B sequences with pre[b] <= x (pre[0] = 0 <= x < pre[B]): the one whose share holds x.
-__device__ __forceinline__ int share_of(const int* pre, int B, int x) {
-    int lo = 0, hi = B - 1;
+// The last of the n sequences with pre[b] <= x (pre[0] = 0 <= x < pre[n]): the one whose share holds x.
+__device__ __forceinline__ int share_of(const int* pre, int n, int x) {
+    int lo = 0, hi = n - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (pre[mid] <= x) lo = mid; else hi = mid - 1;
@@ -40,11 +41,11 @@ __device__ __forceinline__ int share_of(const int* pre, int B, int x) {
     return lo;
 }
 
+// Sequence b's numbers: tokens kept and new, entries before and behind the step.
 struct StepSeq {
     int keep, count, before, after;
     bool fits;
 };
-
 __device__ __forceinline__ StepSeq step_sequence(const StepParams& p, int b) {
     const int old = p.kv_len[b], up = p.page_size - 1;
     StepSeq s;
@@ -63,177 +64,198 @@ __device__ __forceinline__ StepSeq step_sequence(const StepParams& p, int b) {
     return s;
 }
 
-__device__ __forceinline__ bool is_page(const StepParams& p, int id) { return id >= 0 && id < p.num_pages; }
+// Three sums at once, of 64 bits: 2048 sequences' numbers of 31 bits may add up to more than 32.
+struct Sums {
+    long long q, take, give;
+};
 
-// The slot and the position of row t, of sequence b whose first row is q0 and
-// first new position `keep`.
-__device__ __forceinline__ void place_row(const StepParams& p, int t, int b, int q0, int keep, long long& slot, int& pos) {
-    pos = keep + (t - q0);
-    const int page = p.page_table[static_cast<size_t>(b) * p.max_pages + (pos >> p.page_shift)];
-    slot = (static_cast<long long>(page) << p.page_shift) + (pos & (p.page_size - 1));
-}
-
-__global__ void __launch_bounds__(kStepThreads) paged_step_kernel(const StepParams p, bool rows_here) {
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) paged_step_kernel(const StepParams p, bool wide) {
     extern __shared__ int step_smem[];
     int* const q_pre = step_smem;
     int* const take = q_pre + p.B + 1;
     int* const give = take + p.B + 1;
-    __shared__ int warp_sums[kStepThreads / 32];
-    __shared__ unsigned long long sums[3];
-    __shared__ int first_bad, bad_seq;
-    const int tid = threadIdx.x;
-    if (tid < 3) sums[tid] = 0;
-    if (tid == 0) {
-        first_bad = INT_MAX;
-        bad_seq = INT_MAX;
-    }
+    int* const keep_s = give + p.B + 1;
+    int* const before_s = keep_s + p.B;
+    __shared__ Sums warp_sums[THREADS / 32];
+    __shared__ int first_bad;
+    __shared__ unsigned ticket;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) first_bad = INT_MAX;
     __syncthreads();
     pdl_wait_previous();
     pdl_launch_next();
-    for (int b = tid; b < p.B; b += kStepThreads) {
+    const int F = p.free_count[0];
+
+    // the sums; a thread has `per` sequences
+    const int per = (p.B + THREADS - 1) / THREADS, b0 = tid * per, b1 = min(b0 + per, p.B);
+    Sums mine{0, 0, 0};
+    for (int b = b0; b < b1; ++b) {
         const StepSeq s = step_sequence(p, b);
         if (!s.fits) atomicMin(&first_bad, b);
+        keep_s[b] = s.keep;
+        before_s[b] = s.before;
         q_pre[b] = s.count;
         take[b] = max(s.after - s.before, 0);
         give[b] = max(s.before - s.after, 0);
-        // (sums of integers: in any order the same)
-        if (q_pre[b]) atomicAdd(&sums[0], static_cast<unsigned long long>(q_pre[b]));
-        if (take[b]) atomicAdd(&sums[1], static_cast<unsigned long long>(take[b]));
-        if (give[b]) atomicAdd(&sums[2], static_cast<unsigned long long>(give[b]));
+        mine.q += s.count;
+        mine.take += take[b];
+        mine.give += give[b];
     }
-    const int F = p.free_count[0];
-    __syncthreads();
-    const bool counted = F >= 0 && F <= p.num_pages && sums[0] <= static_cast<unsigned long long>(p.total_q) &&
-                         F + sums[2] <= static_cast<unsigned long long>(p.num_pages);
-    const bool enough = sums[1] <= F + sums[2];
-    bool good = first_bad == INT_MAX && counted && enough;
-    const int N = good ? static_cast<int>(sums[1]) : 0, R = good ? static_cast<int>(sums[2]) : 0;
-    if (good) {
-        block_prefix<kStepThreads>(p.B, q_pre, warp_sums, [&](int b) { return q_pre[b]; });
-        if (N) block_prefix<kStepThreads>(p.B, take, warp_sums, [&](int b) { return take[b]; });
-        if (R) block_prefix<kStepThreads>(p.B, give, warp_sums, [&](int b) { return give[b]; });
-        // the pages that move
-        for (int g = tid; g < R; g += kStepThreads) {
-            const int b = share_of(give, p.B, g);
-            const StepSeq s = step_sequence(p, b);
-            if (!is_page(p, p.page_table[static_cast<size_t>(b) * p.max_pages + s.after + g - give[b]])) atomicMin(&bad_seq, b);
+    Sums upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long q = __shfl_up_sync(0xffffffffu, upto.q, d), t = __shfl_up_sync(0xffffffffu, upto.take, d),
+                        g = __shfl_up_sync(0xffffffffu, upto.give, d);
+        if (lane >= d) {
+            upto.q += q;
+            upto.take += t;
+            upto.give += g;
         }
-        for (int k = R + tid; k < N; k += kStepThreads)
-            if (!is_page(p, p.free_pages[F + R - 1 - k])) atomicMin(&bad_seq, share_of(take, p.B, k));
-        __syncthreads();
-        good = bad_seq == INT_MAX;
     }
-    if (!good) {
+    if (lane == 31) warp_sums[warp] = upto;
+    __syncthreads();
+    Sums base{upto.q - mine.q, upto.take - mine.take, upto.give - mine.give}, all{0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+        const Sums x = warp_sums[w];
+        if (w < warp) {
+            base.q += x.q;
+            base.take += x.take;
+            base.give += x.give;
+        }
+        all.q += x.q;
+        all.take += x.take;
+        all.give += x.give;
+    }
+    const bool good = first_bad == INT_MAX && F >= 0 && F <= p.num_pages && all.q <= p.total_q &&
+                      F + all.give <= p.num_pages && all.take <= F + all.give;
+    // (32 bits hold what follows once it is good)
+    for (int b = b0; b < b1; ++b) {
+        const int q = q_pre[b], t = take[b], g = give[b];
+        q_pre[b] = static_cast<int>(base.q);
+        take[b] = static_cast<int>(base.take);
+        give[b] = static_cast<int>(base.give);
+        base.q += q;
+        base.take += t;
+        base.give += g;
+    }
+    if (tid == 0) {
+        q_pre[p.B] = good ? static_cast<int>(all.q) : 0;
+        take[p.B] = static_cast<int>(all.take);
+        give[p.B] = static_cast<int>(all.give);
+    }
+    __syncthreads();
+    const int N = good ? static_cast<int>(all.take) : 0, R = good ? static_cast<int>(all.give) : 0, rows = q_pre[p.B];
+    auto after_of = [&](int b) {
+        return max((keep_s[b] + q_pre[b + 1] - q_pre[b] + p.page_size - 1) >> p.page_shift, p.shared_pages);
+    };
+    // the g-th page given back, and the k-th taken
+    auto given = [&](int g) {
+        const int b = share_of(give, p.B, g);
+        return p.page_table[static_cast<size_t>(b) * p.max_pages + after_of(b) + g - give[b]];
+    };
+    auto taken = [&](int k) { return k < R ? given(k) : p.free_pages[F + R - 1 - k]; };
+
+    const int threads = gridDim.x * THREADS, at = blockIdx.x * THREADS + tid;
+    for (int k = at; k < N; k += threads) {
+        const int b = share_of(take, p.B, k), id = taken(k);
+        if (id < 0 || id >= p.num_pages) report_sequence(p.ws, b);
+        p.page_table[static_cast<size_t>(b) * p.max_pages + before_s[b] + k - take[b]] = id;
+    }
+    for (long long t0 = static_cast<long long>(at) * kSlotRows; (p.slots || p.positions) && t0 < p.total_q;
+         t0 += static_cast<long long>(threads) * kSlotRows) {
+        long long slot[kSlotRows];
+        int pos[kSlotRows];
+        int b = -1;
+#pragma unroll
+        for (int e = 0; e < kSlotRows; ++e) {
+            slot[e] = -1;
+            pos[e] = 0;
+            if (t0 + e >= rows) continue;
+            const int t = static_cast<int>(t0) + e;
+            if (b < 0 || t >= q_pre[b + 1]) b = share_of(q_pre, p.B, t);
+            pos[e] = keep_s[b] + (t - q_pre[b]);
+            const int entry = pos[e] >> p.page_shift;
+            const int id = entry < before_s[b] ? p.page_table[static_cast<size_t>(b) * p.max_pages + entry]
+                                               : taken(take[b] + entry - before_s[b]);
+            if (id >= 0 && id < p.num_pages)
+                slot[e] = (static_cast<long long>(id) << p.page_shift) + (pos[e] & (p.page_size - 1));
+            else
+                report_sequence(p.ws, b);
+        }
+        if (wide && t0 + kSlotRows <= p.total_q) {
+            if (p.slots) {
+                reinterpret_cast<longlong2*>(p.slots + t0)[0] = make_longlong2(slot[0], slot[1]);
+                reinterpret_cast<longlong2*>(p.slots + t0)[1] = make_longlong2(slot[2], slot[3]);
+            }
+            if (p.positions) *reinterpret_cast<int4*>(p.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < kSlotRows; ++e) {
+                if (t0 + e >= p.total_q) break;
+                if (p.slots) p.slots[t0 + e] = slot[e];
+                if (p.positions) p.positions[t0 + e] = pos[e];
+            }
+        }
+    }
+
+    // who is last writes in place
+    __syncthreads();
+    if (gridDim.x > 1) {
         if (tid == 0) {
+            __threadfence();
+            ticket = atomicAdd(p.ws + kStepTicket, 1u);
+            __threadfence();
+        }
+        __syncthreads();
+        if (ticket != gridDim.x - 1) return;
+        if (tid == 0) p.ws[kStepTicket] = 0;
+    }
+    for (int g = tid; g < R; g += THREADS) {
+        const int id = given(g);
+        if (id < 0 || id >= p.num_pages) report_sequence(p.ws, share_of(give, p.B, g));
+        p.free_pages[F + R - 1 - g] = id;
+    }
+    for (int b = b0; b < b1; ++b) {
+        p.q_start[b] = good ? q_pre[b] : 0;
+        if (good)
+            p.kv_len_out[b] = keep_s[b] + (q_pre[b + 1] - q_pre[b]);
+        else if (p.kv_len_out != p.kv_len)
+            p.kv_len_out[b] = p.kv_len[b];
+    }
+    if (tid == 0) {
+        p.q_start[p.B] = rows;
+        p.free_count_out[0] = F + R - N;
+        if (!good) {
             // the sequence whose numbers do not fit, or at which the rows, the stack or its pages run out
-            int at = min(first_bad, bad_seq);
-            if (at == INT_MAX) {
-                const long long given = static_cast<long long>(F) + static_cast<long long>(sums[2]);
-                long long rows = 0, took = 0, gave = F;
-                for (at = 0; at < p.B - 1 && F >= 0 && F <= p.num_pages; ++at) {
-                    const StepSeq s = step_sequence(p, at);
-                    rows += s.count;
+            int b = first_bad;
+            if (b == INT_MAX) {
+                long long q = 0, took = 0, gave = F;
+                for (b = 0; b < p.B - 1 && F >= 0 && F <= p.num_pages; ++b) {
+                    const StepSeq s = step_sequence(p, b);
+                    q += s.count;
                     took += max(s.after - s.before, 0);
                     gave += max(s.before - s.after, 0);
-                    if (rows > p.total_q || took > given || gave > p.num_pages) break;
+                    if (q > p.total_q || took > F + all.give || gave > p.num_pages) break;
                 }
             }
-            report_sequence(p.ws, at);
-            p.free_count_out[0] = F;
+            report_sequence(p.ws, b);
         }
-        for (int b = tid; b <= p.B; b += kStepThreads) {
-            p.q_start[b] = 0;
-            if (b < p.B) p.kv_len_out[b] = p.kv_len[b];
-        }
-        for (int t = tid; rows_here && t < p.total_q; t += kStepThreads) {
-            if (p.slots) p.slots[t] = -1;
-            if (p.positions) p.positions[t] = 0;
-        }
-        return;
-    }
-    for (int g = tid; g < R; g += kStepThreads) {
-        const int b = share_of(give, p.B, g);
-        const StepSeq s = step_sequence(p, b);
-        p.free_pages[F + R - 1 - g] = p.page_table[static_cast<size_t>(b) * p.max_pages + s.after + g - give[b]];
-    }
-    __syncthreads();
-    for (int k = tid; k < N; k += kStepThreads) {
-        const int b = share_of(take, p.B, k);
-        const StepSeq s = step_sequence(p, b);
-        p.page_table[static_cast<size_t>(b) * p.max_pages + s.before + k - take[b]] = p.free_pages[F + R - 1 - k];
-    }
-    __syncthreads();
-    const int rows = q_pre[p.B];
-    for (int t = tid; rows_here && t < p.total_q; t += kStepThreads) {
-        long long slot = -1;
-        int pos = 0;
-        if (t < rows) {
-            const int b = share_of(q_pre, p.B, t);
-            place_row(p, t, b, q_pre[b], p.keep_len[b], slot, pos);
-        }
-        if (p.slots) p.slots[t] = slot;
-        if (p.positions) p.positions[t] = pos;
-    }
-    // (kv_len and free_count may be written in place: every thread is past their last reading)
-    __syncthreads();
-    for (int b = tid; b <= p.B; b += kStepThreads) {
-        p.q_start[b] = q_pre[b];
-        if (b < p.B) p.kv_len_out[b] = p.keep_len[b] + (q_pre[b + 1] - q_pre[b]);
-    }
-    if (tid == 0) p.free_count_out[0] = F + R - N;
-}
-
-// Slots and positions of many rows, from what the kernel above has written.
-__global__ void __launch_bounds__(kSlotThreads) paged_slots_kernel(const StepParams p, bool wide) {
-    extern __shared__ int step_smem[];
-    pdl_wait_previous();
-    pdl_launch_next();
-    for (int b = threadIdx.x; b <= p.B; b += kSlotThreads) step_smem[b] = p.q_start[b];
-    __syncthreads();
-    const int* const q_pre = step_smem;
-    const int rows = q_pre[p.B];
-    const long long t0 = (static_cast<long long>(blockIdx.x) * kSlotThreads + threadIdx.x) * kSlotRows;
-    if (t0 >= p.total_q) return;
-    long long slot[kSlotRows];
-    int pos[kSlotRows];
-    int b = -1, keep = 0;
-#pragma unroll
-    for (int e = 0; e < kSlotRows; ++e) {
-        const int t = static_cast<int>(min(t0 + e, static_cast<long long>(p.total_q) - 1));
-        slot[e] = -1;
-        pos[e] = 0;
-        if (t >= rows) continue;
-        if (b < 0 || t >= q_pre[b + 1]) {
-            b = share_of(q_pre, p.B, t);
-            keep = p.kv_len_out[b] - (q_pre[b + 1] - q_pre[b]);
-        }
-        place_row(p, t, b, q_pre[b], keep, slot[e], pos[e]);
-    }
-    if (wide && t0 + kSlotRows <= p.total_q) {
-        if (p.slots) {
-            reinterpret_cast<longlong2*>(p.slots + t0)[0] = make_longlong2(slot[0], slot[1]);
-            reinterpret_cast<longlong2*>(p.slots + t0)[1] = make_longlong2(slot[2], slot[3]);
-        }
-        if (p.positions) *reinterpret_cast<int4*>(p.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
-        return;
-    }
-#pragma unroll
-    for (int e = 0; e < kSlotRows; ++e) {
-        if (t0 + e >= p.total_q) break;
-        if (p.slots) p.slots[t0 + e] = slot[e];
-        if (p.positions) p.positions[t0 + e] = pos[e];
     }
 }
 
 }  // namespace
 
 cudaError_t launch_paged_step(const StepParams& p, cudaStream_t s) {
-    const bool wants = (p.slots || p.positions) && p.total_q > 0, here = p.total_q <= kRowsHere;
-    cudaError_t e = paged_launch(paged_step_kernel, dim3(1), kStepThreads, 3u * 4u * (p.B + 1), true, s, p, here && wants);
-    if (e != cudaSuccess || here || !wants) return e;
-    const int per = kSlotThreads * kSlotRows;
     const bool wide = ((reinterpret_cast<uintptr_t>(p.slots) | reinterpret_cast<uintptr_t>(p.positions)) & 15) == 0;
-    return paged_launch(paged_slots_kernel, dim3((p.total_q + per - 1LL) / per), kSlotThreads, 4u * (p.B + 1), true, s, p, wide);
+    const long long rows = p.slots || p.positions ? p.total_q : p.B;
+    const unsigned ctas = static_cast<unsigned>(std::min<long long>((rows + kRowsEach - 1) / kRowsEach, device_sm_count()));
+    const size_t smem = 4u * (5u * p.B + 3u);
+    // few sequences and rows: a small block starts and scans sooner
+    return p.B <= 256 && rows <= 1024
+               ? paged_launch(paged_step_kernel<256>, dim3(std::max(ctas, 1u)), 256, smem, true, s, p, wide)
+               : paged_launch(paged_step_kernel<512>, dim3(std::max(ctas, 1u)), 512, smem, true, s, p, wide);
 }
 
 }  // namespace fa

@@ -233,14 +233,15 @@ fa_status fa_fwd_paged_scaled(const fa_paged_kv *c, const fa_paged_scales *scale
  *   total_q     rows of the step's tensors, at least the sum of new_len.
  * A step that cannot be made changes nothing but its outputs, which are those
  * of an empty step (kv_len_out = kv_len, free_count_out = free_count, q_start
- * all 0), and is reported by fa_workspace_check as FA_ERR_DEVICE_CHECK: numbers
- * that contradict each other (a negative length, keep_len past kv_len and the
- * shared pages, more than max_pages x P tokens, new_len adding up to more than
- * total_q, free_count or a page that moves outside 0 .. num_pages), or too few
- * free pages.
+ * all 0), and is reported by fa_workspace_check as FA_ERR_DEVICE_CHECK, with the
+ * sequence at which it fails: numbers that contradict each other (a negative
+ * length, keep_len past kv_len and the shared pages, more than max_pages x P
+ * tokens, new_len adding up to more than total_q, a free_count outside 0 ..
+ * num_pages, more pages given back than the stack holds), or too few free pages.
+ * A page outside 0 .. num_pages - 1 that the step moves, or that holds one of its
+ * rows, is reported too; it moves all the same, and its rows have slot -1.
  * B <= 2048; page_size as for fa_paged_kv.  No two arrays overlap, apart from
- * kv_len_out and free_count_out as said.  One kernel launch, or two for many
- * rows.                                                                     */
+ * kv_len_out and free_count_out as said.  One kernel launch.                */
 typedef struct fa_paged_step_args {
     int32_t B;
     int32_t num_pages;

@@ -206,8 +206,8 @@ BAD = {
     "negative new_len": dict(new=[1, -1, 2]), "negative keep_len": dict(keep=[20, -3, 9]),
     "keep_len past the cache": dict(keep=[20, 51, 9]), "past the row of the table": dict(new=[1, 10000, 2]),
     "negative kv_len": dict(old=[20, -5, 9]), "rows": dict(total=2), "pages": dict(count=0),
-    "count past the stack": dict(count=10**6), "negative count": dict(count=-1), "free page": dict(free=10**6),
-    "given page": dict(table=-4), "new_len adds up past 32 bits": dict(new=[2**30, 2**30, 2**30], total=2**20)}
+    "count past the stack": dict(count=10**6), "negative count": dict(count=-1),
+    "more given back than the stack holds": dict(full=True), "new_len adds up past 32 bits": dict(new=[2**30, 2**30, 2**30], total=2**20)}
 
 
 @gpu
@@ -226,10 +226,8 @@ def test_steps_that_cannot_be_made(fa, what, pad):  # noqa: F811
         s.count = kw["count"]
         if kw["count"] == 0:
             s.keep[1] = 50                       # none given back either
-    if "free" in kw:
-        s.keep[1], s.free[s.count - 1] = 50, kw["free"]
-    if "table" in kw:
-        s.table[1, 3] = kw["table"]
+    if "full" in kw:
+        s.count, s.keep[0] = s.free.size, 31
     d = s.device()
     before = {k: v.clone() for k, v in d.items()}
     kv, count = torch.full_like(d["kv"], 99), torch.full_like(d["count"], 99)
@@ -240,6 +238,29 @@ def test_steps_that_cannot_be_made(fa, what, pad):  # noqa: F811
     assert all(torch.equal(d[k], v) for k, v in before.items())
     assert torch.equal(kv, d["kv"]) and torch.equal(count, d["count"])
     assert not got[0].any() and (got[1] == -1).all() and not got[2].any()
+    fa.default_workspace("cuda").check()
+
+
+@gpu
+@pytest.mark.parametrize("pad", [0, 6000])
+@pytest.mark.parametrize("which", ["free", "given", "kept"])
+def test_bad_pages_are_reported(fa, which, pad):  # noqa: F811
+    s = Server([32, 50, 9], [32, 40, 9], [1, 1, 2], 16, pad=pad, spare=2)
+    if which == "free":
+        s.keep[1], s.free[s.count - 1] = 50, 10**6       # the page that sequence 0 takes
+    if which == "given":
+        s.table[1, 3] = -4                               # given back by sequence 1, taken by sequence 0
+    if which == "kept":
+        s.table[2, 0] = 10**6                            # of sequence 2's rows
+    d = s.device()
+    got = step(fa, s, d)
+    with pytest.raises(fa.FAError) as e:
+        fa.default_workspace("cuda").check()
+    assert e.value.status == fa.ERR_DEVICE_CHECK
+    kv, count, start, table, free, slots, places = s.want()
+    page = slots // 16
+    slots = np.where((page < 0) | (page >= s.free.size), -1, slots)
+    same(d, got, (kv, count, start, table, free, slots, places))
     fa.default_workspace("cuda").check()
 
 
