@@ -214,89 +214,112 @@ paged_eight_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
             tma_prefetch_desc(&tmV);
         }
         const int span = min(p.c.page_size, kKeys), pages = kKeys / span;    // 1, 2, 4 or 8
+        const int most = 32 / pages, mine = lane / pages, at = lane & (pages - 1);
         const uint32_t page_bytes = static_cast<uint32_t>(span) * D * 2u;    // K and V
         int last[ST];
 #pragma unroll
         for (int st = 0; st < ST; ++st) last[st] = -1;
+        // Up to `most` tiles of a unit, a lane to each of their pages.  Three batches
+        // are on their way: the copies of one are issued, the next one's scales
+        // come, and the page ids, which those need, of the one behind.
+        struct Batch {
+            SmallSeg s;
+            int k, tiles, id;
+        };
+        SmallSeg unit;
+        int at_k = 0;
+        bool in_unit = false;
+        auto next_batch = [&](Batch& b) {
+            b.tiles = 0;
+            b.id = -1;
+            if (!in_unit) {
+                if (!next_seg<kShift>(p, line, unit)) return;
+                at_k = unit.k0;
+            }
+            b.s = unit;
+            b.k = at_k;
+            b.tiles = min(most, unit.k1 - at_k);
+            at_k += b.tiles;
+            in_unit = at_k < unit.k1;
+            if (mine < b.tiles)
+                b.id = tile_page<kKeys>(p.c, p.c.page_table + (size_t)unit.b * p.c.max_pages, unit.hull,
+                                        unit.hull.tile(b.k + mine), at, unit.b, p.ws);
+        };
+        auto scales_of = [&](const Batch& b) {
+            const size_t x = (size_t)max(b.id, 0) * p.c.Hkv + b.s.h;
+            return b.id >= 0 ? make_float2(p.k_scale[x], p.v_scale[x]) : make_float2(0.f, 0.f);
+        };
         int g = 0, nu = 0;
         bool ok = true, marked = false;
-        SmallSeg s;
-        for (; ok; ++nu) {
-            const bool more = next_seg<kShift>(p, line, s);
-            if (nu >= 2 && !mbar_wait_warp(q_empty(nu), ((nu >> 1) - 1) & 1, wc, S_P8_Q_EMPTY)) break;
-            if (!more) {
+        Batch now, next, then;
+        next_batch(now);
+        float2 scales = make_float2(0.f, 0.f);
+        if (now.tiles > 0) scales = scales_of(now);
+        next_batch(next);
+        for (;;) {
+            const bool fresh = now.tiles == 0 || now.k == now.s.k0;
+            if (fresh) {
+                if (nu >= 2 && !mbar_wait_warp(q_empty(nu), ((nu >> 1) - 1) & 1, wc, S_P8_Q_EMPTY)) break;
+                if (now.tiles == 0) {
+                    if (lane == 0) {
+                        seg_s[nu % kSegs].b = -1;
+                        mbar_arrive(q_full(nu));
+                    }
+                    marked = true;
+                    break;
+                }
+                // the unit and its rows of Q, a lane to each, into the slots that
+                // the unit before the last has left
+                const SmallSeg& s = now.s;
+                const int rows = s.n * p.group;
                 if (lane == 0) {
-                    seg_s[nu % kSegs].b = -1;
-                    mbar_arrive(q_full(nu));
+                    seg_s[nu % kSegs] = s;
+                    mbar_arrive_expect_tx(q_full(nu), static_cast<uint32_t>(rows) * 2u * D);
                 }
-                marked = true;
-                break;
-            }
-            const int32_t* table = p.c.page_table + (size_t)s.b * p.c.max_pages;
-            // A lane stands for a page of one of the next 32 / `pages` tiles; it reads
-            // the page's id and scales a whole batch of tiles ahead (a scale needs the
-            // id, and both come from memory).
-            auto page_of = [&](int k) {
-                return k < s.k1 ? tile_page<kKeys>(p.c, table, s.hull, s.hull.tile(k), lane & (pages - 1), s.b, p.ws) : -1;
-            };
-            auto scale_of = [&](const float* scales, int id) {
-                return id >= 0 ? scales[(size_t)id * p.c.Hkv + s.h] : 0.f;
-            };
-            int id = page_of(s.k0 + lane / pages), id2 = -1;
-            // the unit and its rows of Q, a lane to each, into the slots that
-            // the unit before the last has left
-            const int rows = s.n * p.group, i0 = s.kv - s.n, i1 = s.kv - 1;
-            if (lane == 0) {
-                seg_s[nu % kSegs] = s;
-                mbar_arrive_expect_tx(q_full(nu), static_cast<uint32_t>(rows) * 2u * D);
-            }
-            __syncwarp();
-            if (lane < rows) {
-                const int tok = quotient(lane, p.by_group);
-                bulk_load(sbase + L::kQ + ((nu & 1) * L::kRows + lane) * L::kQRow,
-                          p.q + (long long)(s.q0 + tok) * p.qs[0] +
-                              (long long)(s.h * p.group + lane - tok * p.group) * p.qs[1],
-                          2u * D, q_full(nu));
-            }
-            float ks = scale_of(p.k_scale, id), vs = scale_of(p.v_scale, id), ks2 = 0.f, vs2 = 0.f;
-            for (int k = s.k0, e = 0; k < s.k1; ++k, ++g, ++e) {
-                if (e == 32 / pages) {
-                    e = 0;
-                    id = id2;
-                    ks = ks2;
-                    vs = vs2;
+                __syncwarp();
+                if (lane < rows) {
+                    const int tok = quotient(lane, p.by_group);
+                    bulk_load(sbase + L::kQ + ((nu & 1) * L::kRows + lane) * L::kQRow,
+                              p.q + (long long)(s.q0 + tok) * p.qs[0] +
+                                  (long long)(s.h * p.group + lane - tok * p.group) * p.qs[1],
+                              2u * D, q_full(nu));
                 }
-                if (e == 0) id2 = page_of(k + 32 / pages + lane / pages);
-                if (e == 2) {
-                    ks2 = scale_of(p.k_scale, id2);
-                    vs2 = scale_of(p.v_scale, id2);
-                }
-                const int kb = s.hull.tile(k), st = g % ST, at = lane & (pages - 1);
-                const bool here = lane / pages == e;
+                ++nu;
+            }
+            const float2 scales_next = next.tiles > 0 ? scales_of(next) : make_float2(0.f, 0.f);
+            for (int e = 0; e < now.tiles; ++e, ++g) {
+                const int kb = now.s.hull.tile(now.k + e), st = g % ST;
+                const bool here = mine == e;
                 if (g >= ST && !mbar_wait_warp(empty_bar(st), (g / ST - 1) & 1, wc, S_P8_EMPTY)) { ok = false; break; }
-                const uint32_t copies = __popc(__ballot_sync(0xffffffffu, here && id >= 0));
+                const uint32_t copies = __popc(__ballot_sync(0xffffffffu, here && now.id >= 0));
                 if (lane == 0) mbar_expect_tx(full_bar(st), copies * page_bytes);
                 __syncwarp();
-                if (here && id >= 0) {
+                if (here && now.id >= 0) {
                     const uint32_t dst = sbase + st * L::kStage + static_cast<uint32_t>(at * span) * D;
                     const int row = ((kb * kKeys + at * span) & (p.c.page_size - 1)) / (128 / D);
-                    const int block = id * p.c.Hkv + s.h;
+                    const int block = now.id * p.c.Hkv + now.s.h;
                     tma_load_3d(dst, &tmK, full_bar(st), 0, row, block);
                     tma_load_3d(dst + L::kTile, &tmV, full_bar(st), 0, row, block);
                 }
                 // what else the consumers need of the tile, and only then the loader's arrival
                 float* const sc = reinterpret_cast<float*>(smem + L::kScale + st * L::kScaleStage);
                 if (here) {
-                    sc[at] = ks;
-                    sc[kKeys / 16 + at] = vs;
+                    sc[at] = scales.x;
+                    sc[kKeys / 16 + at] = scales.y;
                 }
                 if (lane == 0)
-                    info_s[st] = 4 * kb + (tile_open(p.mask, kb, i0, i1, p.shared, s.kv, kShift) ? kTileOpen : 0) +
-                                 (s.hull.all(kb * kKeys, kb * kKeys + kKeys) ? 0 : kTileClear);
+                    info_s[st] = 4 * kb +
+                                 (tile_open(p.mask, kb, now.s.kv - now.s.n, now.s.kv - 1, p.shared, now.s.kv, kShift) ? kTileOpen : 0) +
+                                 (now.s.hull.all(kb * kKeys, kb * kKeys + kKeys) ? 0 : kTileClear);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(full_bar(st));
                 last[st] = g;
             }
+            if (!ok) break;
+            next_batch(then);
+            now = next;
+            next = then;
+            scales = scales_next;
         }
         // every issued copy lands before the CTA exits
         if (lane == 0) {
@@ -409,9 +432,12 @@ paged_eight_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
             if (info & kTileClear) {
                 // V rows that no row of the unit sees
                 cleared = true;
-                for (int r = 0; r < 32; ++r) {
-                    if (!s.hull.live(j0 + r) && lane < kChunks)
-                        *reinterpret_cast<uint4*>(smem + st * L::kStage + L::kTile + swz8<D>(32 * warp + r, lane)) =
+                const uint32_t live = __ballot_sync(0xffffffffu, s.hull.live(j0 + lane));
+#pragma unroll
+                for (int e = 0; e < kChunks; ++e) {
+                    const int r = (32 * e + lane) / kChunks;
+                    if (!((live >> r) & 1u))
+                        *reinterpret_cast<uint4*>(smem + st * L::kStage + L::kTile + swz8<D>(32 * warp + r, lane % kChunks)) =
                             make_uint4(0u, 0u, 0u, 0u);
                 }
                 __syncwarp();

@@ -16,8 +16,7 @@
 // are 24 KB) and takes its share of the pages and rows; a row's page comes from
 // the table, or from the stack by the same formula, never from another CTA.  The
 // last CTA to have read the arguments (a counter in the workspace, 0 between
-// launches) writes what may be written in place: the lengths, the count, the
-// stack.  One CTA does up to kRowsEach rows; what it costs is latency.
+// launches) writes what may be written in place: the lengths and the count.  One CTA does up to kRowsEach rows; what it costs is latency.
 #include <algorithm>
 
 #include "paged.cuh"
@@ -158,6 +157,11 @@ __global__ void __launch_bounds__(THREADS) paged_step_kernel(const StepParams p,
     auto taken = [&](int k) { return k < R ? given(k) : p.free_pages[F + R - 1 - k]; };
 
     const int threads = gridDim.x * THREADS, at = blockIdx.x * THREADS + tid;
+    for (int g = at; g < R; g += threads) {      // (nobody reads the stack past F)
+        const int id = given(g);
+        if (id < 0 || id >= p.num_pages) report_sequence(p.ws, share_of(give, p.B, g));
+        p.free_pages[F + R - 1 - g] = id;
+    }
     for (int k = at; k < N; k += threads) {
         const int b = share_of(take, p.B, k), id = taken(k);
         if (id < 0 || id >= p.num_pages) report_sequence(p.ws, b);
@@ -212,11 +216,6 @@ __global__ void __launch_bounds__(THREADS) paged_step_kernel(const StepParams p,
         if (ticket != gridDim.x - 1) return;
         if (tid == 0) p.ws[kStepTicket] = 0;
     }
-    for (int g = tid; g < R; g += THREADS) {
-        const int id = given(g);
-        if (id < 0 || id >= p.num_pages) report_sequence(p.ws, share_of(give, p.B, g));
-        p.free_pages[F + R - 1 - g] = id;
-    }
     for (int b = b0; b < b1; ++b) {
         p.q_start[b] = good ? q_pre[b] : 0;
         if (good)
@@ -250,7 +249,7 @@ __global__ void __launch_bounds__(THREADS) paged_step_kernel(const StepParams p,
 cudaError_t launch_paged_step(const StepParams& p, cudaStream_t s) {
     const bool wide = ((reinterpret_cast<uintptr_t>(p.slots) | reinterpret_cast<uintptr_t>(p.positions)) & 15) == 0;
     const long long rows = p.slots || p.positions ? p.total_q : p.B;
-    const unsigned ctas = static_cast<unsigned>(std::min<long long>((rows + kRowsEach - 1) / kRowsEach, device_sm_count()));
+    const unsigned ctas = static_cast<unsigned>(std::min<long long>((rows + kRowsEach - 1) / kRowsEach, 4 * device_sm_count()));
     const size_t smem = 4u * (5u * p.B + 3u);
     // few sequences and rows: a small block starts and scans sooner
     return p.B <= 256 && rows <= 1024
