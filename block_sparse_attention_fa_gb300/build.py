@@ -55,7 +55,7 @@ def up_to_date() -> bool:
 # kernel must be launched with exactly that many registers (a smaller launch
 # allocation would leave a setmaxnreg.inc waiting for registers forever).
 LAUNCH_REGISTERS = {"fwd_bf16.cu": ("fwd_bf16_kernel", 168), "paged_tiles.cu": ("paged_tiles_kernel", 168),
-                    "paged_tiles_scaled.cu": ("paged_tiles_kernel", 128)}
+                    "paged_tiles_scaled.cu": ("paged_tiles_scaled_kernel", 128)}
 
 
 def check_launch_registers(src: str, ptxas_log: str) -> None:

@@ -344,17 +344,19 @@ fa_status forward(const fa_paged_kv* c, bool scaled, const fa_paged_scales* scal
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool small = small_rows(c, a);
     const long long blocks = (long long)c->num_pages * c->Hkv;
-    const auto map_of = scaled ? fa::page_tensor_map_scaled : fa::page_tensor_map;
+    auto map_of = [&](CUtensorMap* map, const void* base, int keys, bool by_key) {
+        return scaled ? fa::page_tensor_map_scaled(map, base, blocks, c->page_size, c->D, keys, by_key)
+                      : fa::page_tensor_map(map, base, blocks, c->page_size, c->D, keys);
+    };
     alignas(64) CUtensorMap tk, tv, sk, sv;       // boxes of the tile kernel, of the small one
     if (!small || p.join_rows) {
-        const int keys = scaled ? fa::kPagedTileScaledKeys : fa::kPagedTileKeys;
-        if ((st = map_of(&tk, c->k, blocks, c->page_size, c->D, keys)) != FA_OK) return st;
-        if ((st = map_of(&tv, c->v, blocks, c->page_size, c->D, keys)) != FA_OK) return st;
+        if ((st = map_of(&tk, c->k, fa::kPagedTileKeys, true)) != FA_OK) return st;
+        if ((st = map_of(&tv, c->v, fa::kPagedTileKeys, true)) != FA_OK) return st;
     }
     if (small) {
         const int keys = scaled ? fa::kPagedSmallScaledKeys : fa::paged_small_keys(c->D);
-        if ((st = map_of(&sk, c->k, blocks, c->page_size, c->D, keys)) != FA_OK) return st;
-        if ((st = map_of(&sv, c->v, blocks, c->page_size, c->D, keys)) != FA_OK) return st;
+        if ((st = map_of(&sk, c->k, keys, false)) != FA_OK) return st;
+        if ((st = map_of(&sv, c->v, keys, false)) != FA_OK) return st;
     }
     auto tile_kernel = [&](const fa::PagedScaledParams& x) {
         return scaled ? fa::launch_paged_tiles_scaled(x, tk, tv, s) : fa::launch_paged_tiles(x, tk, tv, s);
@@ -392,15 +394,16 @@ fa_status forward(const fa_paged_kv* c, bool scaled, const fa_paged_scales* scal
 }  // namespace
 
 fa_status fa::page_tensor_map_scaled(CUtensorMap* map, const void* base, long long blocks, int page_size, int D,
-                                     int tile_keys) {
+                                     int tile_keys, bool by_key) {
     const auto fn = encode_tiled();
     if (!fn) return fail(FA_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
-    const int rows = page_size * D / 128, box_rows = std::min(page_size, tile_keys) * D / 128;
-    const cuuint64_t dims[3] = {128, (cuuint64_t)rows, (cuuint64_t)blocks};
-    const cuuint64_t strides[2] = {128, (cuuint64_t)rows * 128};
-    const cuuint32_t box[3] = {128, (cuuint32_t)box_rows, 1}, estr[3] = {1, 1, 1};
+    const int width = by_key ? D : 128, rows = page_size * D / width, box_rows = std::min(page_size, tile_keys) * D / width;
+    const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)rows, (cuuint64_t)blocks};
+    const cuuint64_t strides[2] = {(cuuint64_t)width, (cuuint64_t)rows * width};
+    const cuuint32_t box[3] = {(cuuint32_t)width, (cuuint32_t)box_rows, 1}, estr[3] = {1, 1, 1};
     const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, width == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(FA_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);
     return FA_OK;

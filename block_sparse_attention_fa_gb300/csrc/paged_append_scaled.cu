@@ -13,11 +13,15 @@
 // A token's code needs the largest of all the step's tokens on its page, so a
 // unit of work is a page's share of the step, for some kv heads: a CTA takes
 // kAppendThreads / G heads, G threads (whole warps) to each.  A thread holds the
-// first two of its 16-element items of k (rotated, fp32) and of v in registers
-// between the maximum and the rounding; items beyond that are read and rotated
-// again, from L2.  The loads set out before the page's id is known.  The queries
-// are no part of this: the first CTAs of the launch rotate them token by token,
-// as in paged_append.cu.
+// first of its 16-element items of k and of v in registers between the maximum
+// and the rounding (k as it came, and rotated for both); items beyond that are
+// read again, from L2.  What a unit costs is latency (its sequence, its page,
+// its rows, the barrier), so warps count more than items held: 26418 tokens of
+// 32 + 16 heads take 124 us with four CTAs per SM and one item, 135 with two,
+// 149 and 163 with three and two CTAs and two items, 177 with k in fp32 as well.
+// The loads set out before the page's id is known.  The queries are no part of
+// this: the first CTAs of the launch rotate them token by token, as in
+// paged_append.cu.
 //
 // Memory bounds it: a token is read as bf16 and written as bytes.
 #include <algorithm>
@@ -28,7 +32,7 @@
 namespace fa {
 namespace {
 
-constexpr int kHeld = 2;
+constexpr int kHeld = 1;
 
 // Which page's share of the step is unit u: the sequence, and the page's place
 // in its row of the table.  Uniform over the block; false: there is none.
@@ -208,19 +212,19 @@ __device__ __forceinline__ void append_page(const AppendScaledParams& p, int u, 
     const size_t head = static_cast<size_t>(page) * p.c.Hkv + h;
     const bool earlier = lo > first;
     const float before[2] = {active && earlier ? p.k_scale[head] : 0.f, active && earlier ? p.v_scale[head] : 0.f};
-    float held[kHeld][16], m[2] = {0.f, 0.f};
-    bool fits[kHeld];
+    float m[2] = {0.f, 0.f};
+    int at[kHeld];
 #pragma unroll
     for (int e = 0; e < kHeld; ++e) {
-        const int x = g + e * G, at = x < items ? place(x) : -1;
-        fits[e] = at >= 0;
-        if (!fits[e]) continue;
+        const int x = g + e * G;
+        at[e] = x < items ? place(x) : -1;
+        if (at[e] < 0) continue;
         float y[16];
         widen(raw_v[e], y);
         m[1] = largest(y, m[1]);
-        widen(raw_k[e], held[e]);
-        rotate(x, at, held[e]);
-        m[0] = largest(held[e], m[0]);
+        widen(raw_k[e], y);
+        rotate(x, at[e], y);
+        m[0] = largest(y, m[0]);
     }
     for (int x = g + kHeld * G; x < items; x += G) {
         const int at = place(x);
@@ -271,11 +275,14 @@ __device__ __forceinline__ void append_page(const AppendScaledParams& p, int u, 
     };
 #pragma unroll
     for (int e = 0; e < kHeld; ++e) {
-        if (!fits[e]) continue;
-        put(g + e * G, 0, held[e]);
+        if (at[e] < 0) continue;
+        const int x = g + e * G;
         float y[16];
         widen(raw_v[e], y);
-        put(g + e * G, 1, y);
+        put(x, 1, y);
+        widen(raw_k[e], y);
+        rotate(x, at[e], y);
+        put(x, 0, y);
     }
     for (int x = g + kHeld * G; x < items; x += G) {
         const int at = place(x);
@@ -295,7 +302,7 @@ __device__ __forceinline__ void append_page(const AppendScaledParams& p, int u, 
 // CTAs 0 .. q_ctas - 1: the queries of per_cta tokens each; the others: page by
 // page, some kv heads each.
 template <int D>
-__global__ void __launch_bounds__(kAppendThreads, 2)
+__global__ void __launch_bounds__(kAppendThreads, 4)
 kv_append_scaled_kernel(const AppendParams q, const AppendScaledParams p, int q_ctas, int per_cta, int threads_per_head) {
     if (static_cast<int>(blockIdx.x) < q_ctas) {
         append_tokens<D>(q, blockIdx.x, per_cta);

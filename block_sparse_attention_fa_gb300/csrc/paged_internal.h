@@ -33,8 +33,6 @@ struct StepParams {
 // Keys of a tile of the small kernel over codes: 32 KB of K and V (16 KB for 64
 // columns, where 32 would be 256 keys).
 constexpr int kPagedSmallScaledKeys = 128;
-// Keys that the tile kernel converts at a time, and so of a copy.
-constexpr int kPagedTileScaledKeys = 64;
 
 cudaError_t launch_kv_append_scaled(const AppendScaledParams& p, cudaStream_t s);
 cudaError_t launch_paged_step(const StepParams& p, cudaStream_t s);
@@ -44,9 +42,10 @@ cudaError_t launch_paged_eight_scaled(const PagedScaledParams& p, const CUtensor
                                       cudaStream_t s);
 cudaError_t launch_paged_tiles_scaled(const PagedScaledParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
                                       cudaStream_t s);
-// Pages of codes as rows of 128 bytes (a key of 128 columns, or two of 64),
-// boxes of min(page_size, tile_keys) keys with 128-byte swizzle.
+// Pages of codes, boxes of min(page_size, tile_keys) keys: as rows of 128 bytes
+// with 128-byte swizzle (a key of 128 columns, or two of 64), or with `by_key` a
+// row to each key, in the swizzle of its width.
 fa_status page_tensor_map_scaled(CUtensorMap* map, const void* base, long long blocks, int page_size, int D,
-                                 int tile_keys);
+                                 int tile_keys, bool by_key);
 
 }  // namespace fa
