@@ -17,15 +17,15 @@
 // P V keeps P at 11 bits, in f16.  V's codes become f16, which holds them exactly:
 // four more warps (12-15) convert 64-key halves from a ring of codes to one of
 // operands.  v's scales cannot stay out of P, for a product adds up keys of many
-// pages: with w = 2^(x - m), x the score in base 2 and m its running maximum,
-//     P = w 2^(m + lv - M),   lv = log2(v's scale),   M the running maximum of x + lv,
-// so that P is at most 1 (2^8 before the maxima are raised) and its roundings are
-// relative to the largest share that any key has in O; O comes in units of 2^M,
-// the sum of w in units of 2^m.  lv is the same for 16 columns (of one page), so
-// both sums come from one exponential: P = 2^(x + lv - M), and the sum of w is that
-// of P times 2^(M - lv - m), 16 columns at a time.  Where that factor is past 2^60
-// (scales that far apart), w is taken apart, so that nothing that counts in the sum
-// is lost to P's smallness.  k's scale and the row's stay with S.
+// pages: with x the score in base 2, lv = log2(v's scale) and M the running maximum
+// of x + lv,
+//     P = 2^(x + lv - M),   l = sum of P / (v's scale),
+// so that P is at most 1 (2^8 before M is raised), its roundings are relative to
+// the largest share that any key has in O, and one exponential serves both sums;
+// O / l and M + log2 l are what they are without scales.  The scale is the same for
+// 16 columns (of one page).  A scale below 2^-80 of the largest so far in the unit,
+// or below 2^-100, counts as that: what such a page adds to O is nothing beside the
+// others, and l keeps all of its keys.  k's scale and the row's stay with S.
 //
 // Shared memory bounds the pair of products together with the conversion (2700
 // cycles of a step of 128 keys against 256 rows at 128 columns, 2560 over bf16).
@@ -44,7 +44,8 @@ constexpr int kThreads8 = 512;
 constexpr uint32_t kRegsSoftmax8 = 184, kRegsOther8 = 88, kRegsConvert8 = 56;
 static_assert(2 * kRegsSoftmax8 + kRegsOther8 + kRegsConvert8 == 4 * 128, "register split must match the launch");
 constexpr float kLazyMax8 = 8.f;               // (0 with fp32 output)
-constexpr float kFarScale = 60.f;
+constexpr float kLeastRatio = 8.271806125530277e-25f;      // 2^-80
+constexpr float kLeastScale = 7.888609052210118e-31f;      // 2^-100
 constexpr int kMaxRing8 = 4;
 // Tiles whose scales are kept.  K(g) is loaded once S of tile g - stages is done,
 // which came after P of the tile before that: the loader is at most five tiles
@@ -85,8 +86,8 @@ struct TileLayout8 {
     static constexpr uint32_t kTmemSlot = kBars + 8 * T_COUNT;
     static constexpr uint32_t kAbort = kTmemSlot + 4;
     static constexpr uint32_t kMinMax = kAbort + 4;          // positions of the batch (shared prefix)
-    static constexpr uint32_t kScales = kMinMax + 8;         // [tile]: k's scale of its (up to 8) pages, log2 of v's
-    static constexpr uint32_t kSeg = kScales + 64 * kScaleRing;    // two units
+    static constexpr uint32_t kScales = (kMinMax + 8 + 15) & ~15u;   // [tile][k's scale, log2 of v's, 1 / v's][8 x 16 keys]
+    static constexpr uint32_t kSeg = kScales + 96 * kScaleRing;    // two units
     static constexpr uint32_t kScan = kSeg + 2 * sizeof(TileSeg);
     static constexpr uint32_t kPre = kScan + 4 * (kThreads8 / 32);   // TileLine's arrays
     static constexpr uint32_t bytes(int B) { return kPre + 4u * (3u * B + 2u) + 1024u; }
@@ -132,17 +133,18 @@ __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t&
         : "=r"(lo), "=r"(hi)
         : "r"(w));
 }
-// Two numbers to e4m3 (16 bits), and what is left of them.
-__device__ __forceinline__ uint32_t split_pair(float& a, float& b) {
+// Two f16 numbers to e4m3 (16 bits), and what is left of them (exact).
+__device__ __forceinline__ uint32_t split_pair(uint32_t& w) {
     uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
-    float x, y;
-    asm("{\n\t.reg .b32 w;\n\t.reg .b16 lo, hi;\n\tcvt.rn.f16x2.e4m3x2 w, %2;\n\tmov.b32 {lo, hi}, w;\n\t"
-        "cvt.f32.f16 %0, lo;\n\tcvt.f32.f16 %1, hi;\n\t}"
-        : "=f"(x), "=f"(y)
-        : "h"(r));
-    a -= x;
-    b -= y;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(w));
+    uint32_t x;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(x) : "h"(r));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(w) : "r"(w), "r"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t to_e4m3(uint32_t w) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(w));
     return r;
 }
 
@@ -152,38 +154,42 @@ template <int D>
 __device__ __forceinline__ float split_row(uint8_t* tile, int row) {
     constexpr int kPieces = D / 8;               // 16 bytes of bf16 each
     auto at = [&](int c) { return tile + (c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4); };
-    uint4 w[kPieces];
+    constexpr int kHold = kPieces / 2;           // the later pieces, in whose place lo comes
+    uint4 held[kHold];
     float top = 0.f;
 #pragma unroll
     for (int c = 0; c < kPieces; ++c) {
-        w[c] = *reinterpret_cast<const uint4*>(at(c));
-        top = fmax3(top, fmax3(fabsf(bf_low(w[c].x)), fabsf(bf_high(w[c].x)), fabsf(bf_low(w[c].y))),
-                    fmax3(fabsf(bf_high(w[c].y)), fabsf(bf_low(w[c].z)), fabsf(bf_high(w[c].z))));
-        top = fmax3(top, fabsf(bf_low(w[c].w)), fabsf(bf_high(w[c].w)));
+        const uint4 w = *reinterpret_cast<const uint4*>(at(c));
+        if (c >= kHold) held[c - kHold] = w;
+        top = fmax3(top, fmax3(fabsf(bf_low(w.x)), fabsf(bf_high(w.x)), fabsf(bf_low(w.y))),
+                    fmax3(fabsf(bf_high(w.y)), fabsf(bf_low(w.z)), fabsf(bf_high(w.z))));
+        top = fmax3(top, fabsf(bf_low(w.w)), fabsf(bf_high(w.w)));
     }
     // top = 1.f 2^x: times 2^(8 - x), or 2^(7 - x) where 1.f is past 7/4
     const int bits = __float_as_int(top), x = max((bits >> 23) + ((bits & 0x7fffff) > 0x600000 ? 1 : 0), 10);
     const float up = __int_as_float((262 - x) << 23);
     // (an infinity would become 448: it makes all of the row's scores NaN instead)
     const float down = top < CUDART_INF_F ? __int_as_float((x - 8) << 23) : CUDART_NAN_F;
-#pragma unroll
-    for (int c = 0; c < kPieces; c += 2) {
+    // pieces c and c + 1: 16 codes, a piece of hi and one of lo
+    auto split = [&](int c, const uint4& v0, const uint4& v1) {
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const uint4 v = w[c + (e >> 1)];
+            const uint4& v = e < 2 ? v0 : v1;
             const uint32_t p = (e & 1) ? v.z : v.x, q = (e & 1) ? v.w : v.y;
-            float f0 = bf_low(p) * up, f1 = bf_high(p) * up, f2 = bf_low(q) * up, f3 = bf_high(q) * up;
-            hi[e] = split_pair(f0, f1);
-            hi[e] |= split_pair(f2, f3) << 16;
-            lo[e] = split_pair(f0, f1);
-            lo[e] |= split_pair(f2, f3) << 16;
+            uint32_t a = pack_f16x2(bf_low(p) * up, bf_high(p) * up), b = pack_f16x2(bf_low(q) * up, bf_high(q) * up);
+            const uint32_t ha = split_pair(a), hb = split_pair(b);
+            hi[e] = __byte_perm(ha, hb, 0x5410);
+            lo[e] = __byte_perm(to_e4m3(a), to_e4m3(b), 0x5410);
         }
-        // 16 codes: piece c / 2 of the row of hi, and of the row of lo
-        const int to_hi = c / 2, to_lo = D == 128 ? 8 + c / 2 : 4 + c / 2;
-        *reinterpret_cast<uint4*>(at(to_hi)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(at(to_lo)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-    }
+        *reinterpret_cast<uint4*>(at(c / 2)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(at(kHold + c / 2)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    };
+#pragma unroll
+    for (int c = 0; c < kHold; c += 2)
+        split(c, *reinterpret_cast<const uint4*>(at(c)), *reinterpret_cast<const uint4*>(at(c + 1)));
+#pragma unroll
+    for (int c = 0; c < kHold; c += 2) split(kHold + c, held[c], held[c + 1]);
     return down;
 }
 
@@ -423,7 +429,7 @@ paged_tiles_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
                 return id >= 0 ? scales[(size_t)id * p.c.Hkv + s.h] : 0.f;
             };
             int page = page_of(s.k0), page2 = page_of(s.k0 + 1), id_v = -1, row_v = 0;
-            float ks = scale_of(p.k_scale, page), vs = scale_of(p.v_scale, page);
+            float ks = scale_of(p.k_scale, page), vs = scale_of(p.v_scale, page), largest = 0.f;
             for (int k = s.k0; k < s.k1; ++k) {
                 const int id = page, row = (s.hull.tile(k) * kBlock + lane * span) & (p.c.page_size - 1);
                 const float ks_now = ks, vs_now = vs;
@@ -433,10 +439,19 @@ paged_tiles_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
                 page2 = page_of(k + 2);
                 if (!load(&tmK, L::kK, L::kKStages, T_K_FULL, T_K_EMPTY, g, id, row, S_T_K_EMPTY)) { ok = false; break; }
                 last_k = static_cast<int>(g);
-                float* const sc = reinterpret_cast<float*>(smem + L::kScales + 64 * (g % kScaleRing));
+                // (bits of numbers that are not negative are in their order)
+                largest = fmaxf(largest, __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(vs_now, 0.f)))));
+                float v_scale = fmaxf(fmaxf(vs_now, largest * kLeastRatio), kLeastScale);
+                if (vs_now != vs_now) v_scale = vs_now;
+                const float lv = log2f(v_scale), iv = 1.f / v_scale;
+                float* const sc = reinterpret_cast<float*>(smem + L::kScales + 96 * (g % kScaleRing));
+                const int from = (16 * lane / span) & 31;      // the page of 16 keys
+                const float ks_at = __shfl_sync(0xffffffffu, ks_now, from), lv_at = __shfl_sync(0xffffffffu, lv, from),
+                            iv_at = __shfl_sync(0xffffffffu, iv, from);
                 if (lane < 8) {
-                    sc[lane] = ks_now;
-                    sc[8 + lane] = log2f(vs_now);
+                    sc[lane] = ks_at;
+                    sc[8 + lane] = lv_at;
+                    sc[16 + lane] = iv_at;
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(T_SCALES + g % kScaleRing));
@@ -541,7 +556,6 @@ paged_tiles_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
         const SoftCap cap = soft_cap(p.score.softcap, SCORE == FA_SCORE_SOFTCAP ? p.scale : 1.f);
         const bool out32 = (p.flags & FA_OUT_FP32) != 0;
         const float lazy = out32 ? 0.f : kLazyMax8;
-        const int by_page = min(p.c.page_shift, 7);    // 2^by_page keys of a tile share a page
         uint32_t n = 0, uq = 0, g = 0;                 // g: tiles of all units
         bool ok = true;
         PagedMeta meta{};
@@ -566,8 +580,7 @@ paged_tiles_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
         bool have = take(next), done = false;      // done: s has an O to write out
         bool valid = false;
         int ur = 0, hq = 0, trow = 0;
-        // running maxima of x and of x + lv, the sum of 2^(x - m)
-        float m = -CUDART_INF_F, M = -CUDART_INF_F, l = 0.f;
+        float m = -CUDART_INF_F, l = 0.f;          // M, l
         for (;;) {
             if (have) bring(next);
             // (the next unit's first products may come while O is read: they go to S)
@@ -576,7 +589,7 @@ paged_tiles_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
                 if (!mbar_wait_warp(bar(T_O_DONE + t), uq & 1, wc, S_T_O)) { ok = false; break; }
                 tc_fence_after();
                 ++uq;
-                // the unit's end in this CTA: O / l and lse, or a partial in units of 2^m
+                // the unit's end in this CTA: O / l and lse, or a partial
                 const bool whole = s.begins() && s.ends(), last = whole && !p.join_rows;
                 const long long row = (long long)trow * p.Hq + hq;
                 const long long at = whole ? row : (2LL * cta + (s.begins() ? 1 : 0)) * kPagedTileRows + ur;
@@ -584,8 +597,7 @@ paged_tiles_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
                 uint8_t* const dst = static_cast<uint8_t*>(last ? p.o : static_cast<void*>(whole ? p.parts.row_o : p.parts.slot_o)) +
                                      at * (D * (f32 ? 4 : 2));
                 const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31u) == 0;
-                const float unit = M == -CUDART_INF_F ? 0.f : ex2_approx(M - m);
-                const float inv = !last ? unit : l == 0.f ? 0.f : unit / l;
+                const float inv = !last ? 1.f : l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t o[32];
@@ -652,13 +664,14 @@ paged_tiles_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
                 const int vhi = p.mask.causal ? min(s.jhi - 1, i) : s.jhi - 1;
                 const int vlo = p.mask.window >= 0 ? max(s.jlo, i - p.mask.window) : s.jlo;
 
-                m = M = -CUDART_INF_F;
+                m = -CUDART_INF_F;
                 l = 0.f;
+                const float row_scale = SCORE == FA_SCORE_NONE ? down * sl2 : down;
                 for (int k = s.k0; ok && k < s.k1; ++k, ++n) {
                     const int kb = s.hull.tile(k);
                     const bool open = tile_open(p.mask, kb, s.i0, s.i1, s.jlo, s.jhi, 7);
                     const uint32_t gt = g + (k - s.k0);
-                    const float* const scales = reinterpret_cast<const float*>(smem + L::kScales + 64 * (gt % kScaleRing));
+                    const float* const scales = reinterpret_cast<const float*>(smem + L::kScales + 96 * (gt % kScaleRing));
                     if (!mbar_wait_warp(bar(T_SCALES + gt % kScaleRing), (gt / kScaleRing) & 1, wc, S_T_SCALES)) { ok = false; break; }
 #pragma unroll 1
                     for (int h = 0; h < 2; ++h) {
@@ -677,18 +690,17 @@ paged_tiles_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
                         // score_mod x becomes q.k here and the modified score in base
                         // 2 below; without one it stays as it is, to be multiplied by
                         // sc (which is no 0, so that -inf stays what it is)
-                        float sc[4], lv[4];
+                        float sc[4];
+                        const float4 ks = *reinterpret_cast<const float4*>(scales + 4 * h);
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
-                            sc[c] = down * scales[(64 * h + 16 * c) >> by_page];
-                            lv[c] = scales[8 + ((64 * h + 16 * c) >> by_page)];
+                            const float f = row_scale * (c == 0 ? ks.x : c == 1 ? ks.y : c == 2 ? ks.z : ks.w);
                             if (SCORE == FA_SCORE_NONE) {
-                                sc[c] *= sl2;
-                                if (sc[c] == 0.f) sc[c] = FLT_MIN;
+                                asm("max.NaN.f32 %0, %1, %2;" : "=f"(sc[c]) : "f"(f), "f"(FLT_MIN));
                             } else {
 #pragma unroll
                                 for (int e = 16 * c; e < 16 * c + 16; e += 2)
-                                    ffma2(x[e], x[e + 1], x[e], x[e + 1], sc[c], sc[c], -0.f, -0.f);
+                                    ffma2(x[e], x[e + 1], x[e], x[e + 1], f, f, -0.f, -0.f);
                                 sc[c] = 1.f;
                             }
                         }
@@ -729,7 +741,10 @@ paged_tiles_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
                                 for (int e = 0; e < 32; ++e) x[32 * c + e] = (see >> e) & 1u ? x[32 * c + e] : -CUDART_INF_F;
                             }
                         }
-                        float m_new = m, M_new = M;
+                        const float4 lv4 = *reinterpret_cast<const float4*>(scales + 8 + 4 * h);
+                        const float4 iv4 = *reinterpret_cast<const float4*>(scales + 16 + 4 * h);
+                        const float lv[4] = {lv4.x, lv4.y, lv4.z, lv4.w}, iv[4] = {iv4.x, iv4.y, iv4.z, iv4.w};
+                        float m_new = m;
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
                             const float* const y = x + 16 * c;
@@ -738,66 +753,33 @@ paged_tiles_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
                             b = fmax3(b, y[8], y[9]);
                             a = fmax3(a, y[10], y[11]);
                             b = fmax3(b, y[12], y[13]);
-                            const float top = fmax3(fmaxf(a, b), y[14], y[15]) * sc[c];
-                            m_new = fmaxf(m_new, top);
-                            // (nothing seen, or a scale of 0: -inf, also beside a scale past the largest number)
-                            M_new = fmaxf(M_new, top == -CUDART_INF_F ? top : top + lv[c]);
+                            m_new = fmaxf(m_new, fmaf(fmax3(fmaxf(a, b), y[14], y[15]), sc[c], lv[c]));
                         }
-                        if (m == -CUDART_INF_F || m_new > m + lazy) {
-                            l *= m_new == -CUDART_INF_F ? 1.f : ex2_approx(m - m_new);
-                            m = m_new;
-                        }
-                        const bool need = M != -CUDART_INF_F && M_new > M + lazy;
-                        const float alpha = need ? ex2_approx(M - M_new) : 1.f;
-                        if (need || M == -CUDART_INF_F) M = M_new;
-                        const float m0 = m == -CUDART_INF_F ? 0.f : m, M0 = M == -CUDART_INF_F ? 0.f : M;
-                        // P = w 2^far, far = m + lv - M
-                        float far[4];
-                        bool near = true;
+                        const bool unset = m == -CUDART_INF_F;
+                        const bool need = !unset && m_new > m + lazy;
+                        const float alpha = need ? ex2_approx(m - m_new) : 1.f;
+                        if (need) l *= alpha;
+                        if (unset || need) m = m_new;
+                        const float m0 = m == -CUDART_INF_F ? 0.f : m;
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            far[c] = m0 + lv[c] - M0;
-                            near = near && fabsf(far[c]) <= kFarScale;
-                        }
-                        if (__all_sync(0xffffffffu, near || m == -CUDART_INF_F)) {
+                        for (int c = 0; c < 2; ++c) {
+                            uint32_t pk[16];
 #pragma unroll
-                            for (int c = 0; c < 2; ++c) {
-                                uint32_t pk[16];
+                            for (int u = 0; u < 2; ++u) {
+                                const int q = 2 * c + u;
+                                const float nm = lv[q] - m0;
+                                float rs[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                                for (int u = 0; u < 2; ++u) {
-                                    const int q = 2 * c + u;
-                                    const float nm = m == -CUDART_INF_F ? 0.f : lv[q] - M0;
-                                    float rs[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                                    for (int e = 0; e < 8; ++e) {
-                                        float p0, p1;
-                                        exp2_pair(p0, p1, x[16 * q + 2 * e], x[16 * q + 2 * e + 1], sc[q], nm);
-                                        const int a2 = (e & 1) * 2;
-                                        fadd2(rs[a2], rs[a2 + 1], rs[a2], rs[a2 + 1], p0, p1);
-                                        pk[8 * u + e] = pack_f16x2(p0, p1);
-                                    }
-                                    l = fmaf((rs[0] + rs[1]) + (rs[2] + rs[3]), m == -CUDART_INF_F ? 1.f : ex2_approx(-far[q]), l);
+                                for (int e = 0; e < 8; ++e) {
+                                    float p0, p1;
+                                    exp2_pair(p0, p1, x[16 * q + 2 * e], x[16 * q + 2 * e + 1], sc[q], nm);
+                                    const int a2 = (e & 1) * 2;
+                                    fadd2(rs[a2], rs[a2 + 1], rs[a2], rs[a2 + 1], p0, p1);
+                                    pk[8 * u + e] = pack_f16x2(p0, p1);
                                 }
-                                tmem_st16_nowait(tSh + 16u * c, pk);
+                                l = fmaf((rs[0] + rs[1]) + (rs[2] + rs[3]), iv[q], l);
                             }
-                        } else {
-#pragma unroll
-                            for (int c = 0; c < 2; ++c) {
-                                uint32_t pk[16];
-#pragma unroll
-                                for (int u = 0; u < 2; ++u) {
-                                    const int q = 2 * c + u;
-                                    const float f = ex2_approx(fminf(far[q], 126.f));
-#pragma unroll
-                                    for (int e = 0; e < 8; ++e) {
-                                        float p0, p1;
-                                        exp2_pair(p0, p1, x[16 * q + 2 * e], x[16 * q + 2 * e + 1], sc[q], -m0);
-                                        l += p0 + p1;
-                                        pk[8 * u + e] = pack_f16x2(p0 == 0.f ? 0.f : p0 * f, p1 == 0.f ? 0.f : p1 * f);
-                                    }
-                                }
-                                tmem_st16_nowait(tSh + 16u * c, pk);
-                            }
+                            tmem_st16_nowait(tSh + 16u * c, pk);
                         }
                         // O holds the products of the unit's earlier halves; wait
                         // for the last of them and scale
