@@ -26,70 +26,24 @@
 // The maximum is raised (and O and the sum rescaled) only when a score is 2^8
 // past it, which one vote of the warp tells.
 //
-// The loader's lanes stand for the pages of the next tiles (32 pages at a time):
-// a page's id and scales are read a batch ahead, for a scale needs the id and
-// both come from memory.
-//
 // V rows of keys that no row of the unit sees are cleared in shared memory before
 // the product: their P is 0, but 0 x NaN is not.
-#include <algorithm>
-#include <math_constants.h>
-
-#include "paged_line.cuh"
+#include "paged_codes.cuh"
 
 namespace fa {
 namespace {
 
-constexpr int kWarps = 4;                        // consumers; warp 4 loads
-constexpr int kThreadsS = 32 * (kWarps + 1);
-constexpr int kKeys = kPagedSmallScaledKeys, kShift = 7;
-constexpr int kTileOpen = 1, kTileClear = 2;    // every row sees every key; some key is seen by no row
+constexpr int kWarps = 4;                        // consumers, 32 keys each; warp 4 loads
+constexpr int kRows = 8;
 constexpr float kLazyMax = 8.f;
-// Units that the consumers read where the loader puts them.  It writes unit nu once
-// all of them have begun unit nu - 2, and so are done with nu - 3.
-constexpr int kSegs = 4;
-static_assert(kKeys == 32 * kWarps && kKeys == 1 << kShift, "32 keys to a warp");
-enum PagedSite8 : uint32_t { S_P8_FULL = 112, S_P8_EMPTY, S_P8_DRAIN, S_P8_Q, S_P8_Q_EMPTY };
+static_assert(kKeys == 32 * kWarps, "32 keys to a warp");
 
-// Two CTAs on an SM.
+// Beside the ring and the queues: two warps' O, every warp's [rows] maximum and sum.
 template <int D>
-struct Small8 {
-    static constexpr int kCtas = 2;
-    static constexpr int kRows = 8;
-    static constexpr uint32_t kTile = kKeys * static_cast<uint32_t>(D);
-    static constexpr uint32_t kStage = 2u * kTile;               // K then V
-    static constexpr int kStages = 98304 / kStage;               // 96 KB
-    static constexpr uint32_t kQRow = 2u * D + 16u;
-    static constexpr uint32_t kMerge = kStages * kStage;         // two warps' O
-    static constexpr uint32_t kMl = kMerge + 8u * kRows * D;     // [warps][rows] maximum and sum
-    static constexpr uint32_t kQ = kMl + 8u * kWarps * kRows;    // two units' rows of Q
-    static constexpr uint32_t kSeg = kQ + 2u * kRows * kQRow;    // [kSegs] units, the last one flagged by b < 0
-    static constexpr uint32_t kScale = kSeg + kSegs * sizeof(SmallSeg);      // [stage]: k's scale of each of the tile's pages, v's
-    static constexpr uint32_t kScaleStage = 8u * (kKeys / 16);
-    static constexpr uint32_t kInfo = kScale + kScaleStage * kStages;     // [stage]: 4 x tile + kTileOpen, kTileClear
-    static constexpr uint32_t kBars = (kInfo + 4u * kStages + 7u) & ~7u;  // FULL, EMPTY [stage], Q_FULL, Q_EMPTY [2]
-    static constexpr uint32_t kAbort = kBars + 16u * kStages + 32u;
-    static constexpr uint32_t kScan = kAbort + 16u;              // warp sums
-    static constexpr uint32_t kPre = kScan + 64u;                // first tile of each group of sequences
-    // (fewer entries of the line's index than the bf16 kernel has room for)
-    static constexpr int kEntries = 350;
-    static constexpr uint32_t bytes(int B) { return kPre + 4u * (groups_of(B, kEntries) + 1u) + 1024u; }
-    // 228 KB on an SM, less 1 KB for each CTA
-    static_assert(kCtas * (kPre + 4u * (kEntries + 1u) + 1024u) <= (228u - kCtas) * 1024u, "shared memory budget");
+struct Eight : CodeLayout<D, kWarps, kRows, 8u * kRows * D + 8u * kWarps * kRows> {
+    static constexpr uint32_t kMerge = Eight::kExtra, kMl = kMerge + 8u * kRows * D;
 };
 
-__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
 // An 8 x 8 matrix of 16-bit elements, two of a row to a thread, transposed.
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
     uint32_t r;
@@ -112,27 +66,6 @@ __device__ __forceinline__ void mma_f16_from_0(float (&d)[4], const uint32_t (&a
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(0.f));
 }
-// Four e4m3 codes as two pairs of f16: exact.
-__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(w));
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ float bf_low(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf_high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-// Byte offset of 16-byte chunk `chunk` of key `key` in a tile of codes, rows of
-// 128 bytes written with 128-byte swizzle: a key of 128 columns, or two of 64.
-template <int D>
-__device__ __forceinline__ uint32_t swz8(int key, int chunk) {
-    const int row = D == 128 ? key : key >> 1, at = D == 128 ? chunk : 4 * (key & 1) + chunk;
-    return static_cast<uint32_t>(row * 128 + ((at ^ (row & 7)) << 4));
-}
 __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 // The same barrier with a vote: whether `ok` holds in every thread.
 __device__ __forceinline__ bool consumers_all(bool ok) {
@@ -147,34 +80,22 @@ __device__ __forceinline__ bool consumers_all(bool ok) {
 }
 
 template <int D, int SCORE>
-__global__ void __launch_bounds__(kThreadsS, Small8<D>::kCtas)
+__global__ void __launch_bounds__(Eight<D>::kThreads, 2)
 paged_eight_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                           const PagedScaledParams p) {
-    using L = Small8<D>;
+    using L = Eight<D>;
     constexpr int ST = L::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const uint32_t sbase = smem_addr(smem);
-    auto full_bar = [&](int st) { return sbase + L::kBars + 8u * st; };
-    auto empty_bar = [&](int st) { return sbase + L::kBars + 8u * (ST + st); };
-    auto q_full = [&](int u) { return sbase + L::kBars + 8u * (2 * ST + (u & 1)); };
-    auto q_empty = [&](int u) { return sbase + L::kBars + 8u * (2 * ST + 2 + (u & 1)); };
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kAbort);
-    int* const pre = reinterpret_cast<int*>(smem + L::kPre);
     SmallSeg* const seg_s = reinterpret_cast<SmallSeg*>(smem + L::kSeg);
     volatile int* const info_s = reinterpret_cast<volatile int*>(smem + L::kInfo);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
 
     if (threadIdx.x == 0) {
-        for (int st = 0; st < ST; ++st) {
-            mbar_init(full_bar(st), 1);
-            mbar_init(empty_bar(st), kWarps);
-        }
-        for (int u = 0; u < 2; ++u) {
-            mbar_init(q_full(u), 1);
-            mbar_init(q_empty(u), kWarps);
-        }
+        L::init(sbase);
         *abort_flag = 0;
         mbar_fence_init();
     }
@@ -184,154 +105,11 @@ paged_eight_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
     else
         pdl_wait_previous();
     pdl_launch_next();
-    // the line of tiles
-    Line line{};
-    line.pre = pre;
-    line.shift = group_shift(p.c.B, L::kEntries);
-    const int groups = groups_of(p.c.B, L::kEntries);
-    int* const scan = reinterpret_cast<int*>(smem + L::kScan);
-    block_prefix<kThreadsS>(groups, pre, scan, [&](int g) {
-        return group_length<kShift>(p, line.shift, g, cta == 0 ? p.ws : nullptr);
-    });
-    line.front = p.c.Hkv * pre[groups] >= kManyTiles * p.ctas;
-    if (line.front) {
-        block_prefix<kThreadsS>(groups, pre, scan, [&](int g) {
-            return group_length_front<kShift>(p, line.shift, g, pre[g + 1] - pre[g]);
-        });
-    }
-    const int total = p.c.Hkv * pre[groups];
-    line_share(total, p.ctas, cta, line.per, line.t, line.t1);
-    if (line.t < line.t1) {
-        line.g = line_find(pre, groups, p.c.Hkv, line.t);
-        if (warp == kWarps) open_group<kShift>(p, line);
-    }
+    const Line line = code_line<L>(p, smem, cta, warp == kWarps);
     const WaitCtl wc{abort_flag, p.ws, p.timeout_ns};
 
     if (warp == kWarps) {
-        // ------------------------------------------------------------ loader
-        if (lane == 0) {
-            tma_prefetch_desc(&tmK);
-            tma_prefetch_desc(&tmV);
-        }
-        const int span = min(p.c.page_size, kKeys), pages = kKeys / span;    // 1, 2, 4 or 8
-        const int most = 32 / pages, mine = lane / pages, at = lane & (pages - 1);
-        const uint32_t page_bytes = static_cast<uint32_t>(span) * D * 2u;    // K and V
-        int last[ST];
-#pragma unroll
-        for (int st = 0; st < ST; ++st) last[st] = -1;
-        // Up to `most` tiles of a unit, a lane to each of their pages.  Three batches
-        // are on their way: the copies of one are issued, the next one's scales
-        // come, and the page ids, which those need, of the one behind.
-        struct Batch {
-            SmallSeg s;
-            int k, tiles, id;
-        };
-        SmallSeg unit;
-        int at_k = 0;
-        bool in_unit = false;
-        auto next_batch = [&](Batch& b) {
-            b.tiles = 0;
-            b.id = -1;
-            if (!in_unit) {
-                if (!next_seg<kShift>(p, line, unit)) return;
-                at_k = unit.k0;
-            }
-            b.s = unit;
-            b.k = at_k;
-            b.tiles = min(most, unit.k1 - at_k);
-            at_k += b.tiles;
-            in_unit = at_k < unit.k1;
-            if (mine < b.tiles)
-                b.id = tile_page<kKeys>(p.c, p.c.page_table + (size_t)unit.b * p.c.max_pages, unit.hull,
-                                        unit.hull.tile(b.k + mine), at, unit.b, p.ws);
-        };
-        auto scales_of = [&](const Batch& b) {
-            const size_t x = (size_t)max(b.id, 0) * p.c.Hkv + b.s.h;
-            return b.id >= 0 ? make_float2(p.k_scale[x], p.v_scale[x]) : make_float2(0.f, 0.f);
-        };
-        int g = 0, nu = 0;
-        bool ok = true, marked = false;
-        Batch now, next, then;
-        next_batch(now);
-        float2 scales = make_float2(0.f, 0.f);
-        if (now.tiles > 0) scales = scales_of(now);
-        next_batch(next);
-        for (;;) {
-            const bool fresh = now.tiles == 0 || now.k == now.s.k0;
-            if (fresh) {
-                if (nu >= 2 && !mbar_wait_warp(q_empty(nu), ((nu >> 1) - 1) & 1, wc, S_P8_Q_EMPTY)) break;
-                if (now.tiles == 0) {
-                    if (lane == 0) {
-                        seg_s[nu % kSegs].b = -1;
-                        mbar_arrive(q_full(nu));
-                    }
-                    marked = true;
-                    break;
-                }
-                // the unit and its rows of Q, a lane to each, into the slots that
-                // the unit before the last has left
-                const SmallSeg& s = now.s;
-                const int rows = s.n * p.group;
-                if (lane == 0) {
-                    seg_s[nu % kSegs] = s;
-                    mbar_arrive_expect_tx(q_full(nu), static_cast<uint32_t>(rows) * 2u * D);
-                }
-                __syncwarp();
-                if (lane < rows) {
-                    const int tok = quotient(lane, p.by_group);
-                    bulk_load(sbase + L::kQ + ((nu & 1) * L::kRows + lane) * L::kQRow,
-                              p.q + (long long)(s.q0 + tok) * p.qs[0] +
-                                  (long long)(s.h * p.group + lane - tok * p.group) * p.qs[1],
-                              2u * D, q_full(nu));
-                }
-                ++nu;
-            }
-            const float2 scales_next = next.tiles > 0 ? scales_of(next) : make_float2(0.f, 0.f);
-            for (int e = 0; e < now.tiles; ++e, ++g) {
-                const int kb = now.s.hull.tile(now.k + e), st = g % ST;
-                const bool here = mine == e;
-                if (g >= ST && !mbar_wait_warp(empty_bar(st), (g / ST - 1) & 1, wc, S_P8_EMPTY)) { ok = false; break; }
-                const uint32_t copies = __popc(__ballot_sync(0xffffffffu, here && now.id >= 0));
-                if (lane == 0) mbar_expect_tx(full_bar(st), copies * page_bytes);
-                __syncwarp();
-                if (here && now.id >= 0) {
-                    const uint32_t dst = sbase + st * L::kStage + static_cast<uint32_t>(at * span) * D;
-                    const int row = ((kb * kKeys + at * span) & (p.c.page_size - 1)) / (128 / D);
-                    const int block = now.id * p.c.Hkv + now.s.h;
-                    tma_load_3d(dst, &tmK, full_bar(st), 0, row, block);
-                    tma_load_3d(dst + L::kTile, &tmV, full_bar(st), 0, row, block);
-                }
-                // what else the consumers need of the tile, and only then the loader's arrival
-                float* const sc = reinterpret_cast<float*>(smem + L::kScale + st * L::kScaleStage);
-                if (here) {
-                    sc[at] = scales.x;
-                    sc[kKeys / 16 + at] = scales.y;
-                }
-                if (lane == 0)
-                    info_s[st] = 4 * kb +
-                                 (tile_open(p.mask, kb, now.s.kv - now.s.n, now.s.kv - 1, p.shared, now.s.kv, kShift) ? kTileOpen : 0) +
-                                 (now.s.hull.all(kb * kKeys, kb * kKeys + kKeys) ? 0 : kTileClear);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(full_bar(st));
-                last[st] = g;
-            }
-            if (!ok) break;
-            next_batch(then);
-            now = next;
-            next = then;
-            scales = scales_next;
-        }
-        // every issued copy lands before the CTA exits
-        if (lane == 0) {
-#pragma unroll
-            for (int st = 0; st < ST; ++st)
-                if (last[st] >= 0) paged_drain_wait(full_bar(st), (last[st] / ST) & 1, wc, S_P8_DRAIN);
-            // (behind the end mark only the last unit's rows can be on their
-            // way: the mark's slot had been read)
-            for (int u = max(nu - (marked ? 1 : 2), 0); u < nu; ++u)
-                paged_drain_wait(q_full(u), (u >> 1) & 1, wc, S_P8_DRAIN);
-        }
-        __syncwarp();
+        load_codes<L>(p, tmK, tmV, line, smem, sbase, wc, lane);
         if (p.join_rows) pdl_wait_previous();
         return;
     }
@@ -348,7 +126,7 @@ paged_eight_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
     bool ok = true;
     PagedMeta meta{};
     for (int nu = 0;; ++nu) {
-        const bool q_here = mbar_wait_warp(q_full(nu), (nu >> 1) & 1, wc, S_P8_Q);
+        const bool q_here = mbar_wait_warp(L::q_full(sbase, nu), (nu >> 1) & 1, wc, S_PC_Q);
         // (the vote keeps the warps together where a wait has run out)
         if (!consumers_all(q_here)) { ok = false; break; }
         const SmallSeg& s = seg_s[nu % kSegs];
@@ -393,7 +171,7 @@ paged_eight_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
                                (SCORE == FA_SCORE_ALIBI ? kPagedLog2e : 1.f);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(q_empty(nu));
+        if (lane == 0) mbar_arrive(L::q_empty(sbase, nu));
         float m[2], l[2], o[kChunks][4];
         m[0] = m[1] = -CUDART_INF_F;
         l[0] = l[1] = 0.f;
@@ -404,7 +182,7 @@ paged_eight_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
         for (int k = 0; k < tiles; ++k, ++g) {
             const int st = g % ST;
             const uint32_t kbase = sbase + st * L::kStage, vbase = kbase + L::kTile;
-            if (!mbar_wait_warp(full_bar(st), (g / ST) & 1, wc, S_P8_FULL)) { ok = false; break; }
+            if (!mbar_wait_warp(L::full(sbase, st), (g / ST) & 1, wc, S_PC_FULL)) { ok = false; break; }
             const int info = info_s[st], j0 = (info >> 2) * kKeys + 32 * warp;
             const float* const sc = reinterpret_cast<const float*>(smem + L::kScale + st * L::kScaleStage);
             const bool open = (info & kTileOpen) != 0;
@@ -521,7 +299,7 @@ paged_eight_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
             }
             if (cleared) fence_async_shared();     // the next copy into this stage comes after the clearing
             __syncwarp();
-            if (lane == 0) mbar_arrive(empty_bar(st));
+            if (lane == 0) mbar_arrive(L::empty(sbase, st));
         }
 
         // the unit's end in this CTA: the warps' maxima and sums, then their O
@@ -624,8 +402,8 @@ paged_eight_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
 template <int D, int SCORE>
 cudaError_t launch_one(const PagedScaledParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
     auto kern = paged_eight_scaled_kernel<D, SCORE>;
-    using L = Small8<D>;
-    constexpr size_t most = L::bytes(L::kEntries);
+    using L = Eight<D>;
+    constexpr size_t most = L::bytes(kCodeEntries);
     static bool attr_set[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -635,7 +413,7 @@ cudaError_t launch_one(const PagedScaledParams& p, const CUtensorMap& tk, const 
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) attr_set[dev] = true;
     }
-    return paged_launch(kern, dim3(p.ctas), kThreadsS, L::bytes(p.c.B), true, s, tk, tv, p);
+    return paged_launch(kern, dim3(p.ctas), L::kThreads, L::bytes(p.c.B), true, s, tk, tv, p);
 }
 
 template <int D>

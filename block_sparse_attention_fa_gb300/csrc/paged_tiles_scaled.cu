@@ -65,7 +65,8 @@ enum TBar8 {
     T_DRAIN = T_O_UPD + 2,                       // two
     T_SEG_FULL = T_DRAIN + 2,                    // two slots
     T_SEG_EMPTY = T_SEG_FULL + 2,
-    T_COUNT = T_SEG_EMPTY + 2
+    T_Q_HERE = T_SEG_EMPTY + 2,                  // the first unit's rows of tile 0, before they are split
+    T_COUNT = T_Q_HERE + 1
 };
 constexpr uint32_t kSegReaders = 14;             // the MMA, softmax and converting warps
 enum TSite8 : uint32_t { S_T_Q = 128, S_T_K_FULL, S_T_K_EMPTY, S_T_RAW_FULL, S_T_RAW_EMPTY, S_T_V_FULL, S_T_V_EMPTY,
@@ -241,6 +242,7 @@ paged_tiles_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
             uint32_t cnt = 1;
             if (k < T_K_FULL) cnt = 4;
             if (k >= T_P_FULL && k < T_P_FULL + 4) cnt = 4;
+            if (k == T_Q_HERE) cnt = 4;
             if (k >= T_RAW_EMPTY && k < T_RAW_EMPTY + kMaxRing8) cnt = 4;     // the converting warps
             if (k >= T_V_FULL && k < T_V_FULL + kMaxRing8) cnt = 4;
             if (k >= T_K_EMPTY && k < T_K_EMPTY + kMaxRing8) cnt = 2;         // both MMA warps
@@ -457,7 +459,7 @@ paged_tiles_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
                 if (lane == 0) mbar_arrive(bar(T_SCALES + g % kScaleRing));
                 // the first unit's rows of Q come before the rest of the ring:
                 // behind it they would wait for all of it to arrive
-                if (g == 0 && !mbar_wait_warp(bar(T_Q_FULL), 0, wc, S_T_Q)) { ok = false; break; }
+                if (g == 0 && !mbar_wait_warp(bar(T_Q_HERE), 0, wc, S_T_Q)) { ok = false; break; }
                 if (k > s.k0 && !load_v(g - 1, id_v, row_v)) { ok = false; break; }
                 id_v = id;
                 row_v = row;
@@ -562,6 +564,7 @@ paged_tiles_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
         // The warp's 32 rows of a unit's Q, as in paged_tiles.cu, and their split
         // (a thread's row; the copies of all lanes are waited for first).
         float down_next = 1.f;
+        bool q_here = false;
         auto bring = [&](const TileSeg& u) {
             if (u.rows > 128 * t) load_rows<D>(p, u, 128 * t + 32 * wq, sbase + L::kQ + t * L::kTile, lane);
         };
@@ -569,6 +572,8 @@ paged_tiles_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
             if (u.rows <= 128 * t) return;
             copies_wait();
             __syncwarp();
+            if (t == 0 && !q_here && lane == 0) mbar_arrive(bar(T_Q_HERE));
+            q_here = true;
             down_next = split_row<D>(smem + L::kQ + t * L::kTile, r);
             fence_async_shared();
             __syncwarp();
