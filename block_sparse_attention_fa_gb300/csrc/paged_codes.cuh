@@ -23,12 +23,12 @@ enum CodeSite : uint32_t { S_PC_FULL = 112, S_PC_EMPTY, S_PC_DRAIN, S_PC_Q, S_PC
 
 // Shared memory of such a kernel: the ring of tiles, `EXTRA` bytes of the
 // kernel's own, two units' rows of Q, units, scales, barriers, the line's index.
-template <int D, int WARPS, int ROWS, uint32_t EXTRA>
+template <int D, int CTAS, int WARPS, int ROWS, uint32_t EXTRA>
 struct CodeLayout {
-    static constexpr int kD = D, kWarps = WARPS, kThreads = 32 * (WARPS + 1), kRows = ROWS;
+    static constexpr int kCtas = CTAS, kD = D, kWarps = WARPS, kThreads = 32 * (WARPS + 1), kRows = ROWS;
     static constexpr uint32_t kTile = kKeys * static_cast<uint32_t>(D);
     static constexpr uint32_t kStage = 2u * kTile;               // K then V
-    static constexpr int kStages = 98304 / kStage;               // 96 KB
+    static constexpr int kStages = (CTAS == 2 ? 98304 : 65536) / kStage;  // 192 KB of an SM
     static constexpr uint32_t kExtra = kStages * kStage;
     static constexpr uint32_t kQRow = 2u * D + 16u;              // rows on distinct banks
     static constexpr uint32_t kQ = (kExtra + EXTRA + 15u) & ~15u;
@@ -41,17 +41,17 @@ struct CodeLayout {
     static constexpr uint32_t kScan = kAbort + 16u;              // warp sums
     static constexpr uint32_t kPre = kScan + 64u;                // first tile of each group of sequences
     static constexpr uint32_t bytes(int B) { return kPre + 4u * (groups_of(B, kCodeEntries) + 1u) + 1024u; }
-    // two CTAs fit on an SM (228 KB less 1 KB for each)
-    static_assert(2u * (kPre + 4u * (kCodeEntries + 1u) + 1024u) <= 226u * 1024u, "shared memory budget");
+    // the CTAs fit on an SM (228 KB less 1 KB for each)
+    static_assert(CTAS * (kPre + 4u * (kCodeEntries + 1u) + 1024u) <= (228u - CTAS) * 1024u, "shared memory budget");
     static __device__ __forceinline__ uint32_t full(uint32_t sbase, int st) { return sbase + kBars + 8u * st; }
     static __device__ __forceinline__ uint32_t empty(uint32_t sbase, int st) { return sbase + kBars + 8u * (kStages + st); }
     static __device__ __forceinline__ uint32_t q_full(uint32_t sbase, int u) { return sbase + kBars + 8u * (2 * kStages + (u & 1)); }
     static __device__ __forceinline__ uint32_t q_empty(uint32_t sbase, int u) {
         return sbase + kBars + 8u * (2 * kStages + 2 + (u & 1));
     }
-    static __device__ __forceinline__ void init(uint32_t sbase) {
+    static __device__ __forceinline__ void init(uint32_t sbase, bool by_lane) {
         for (int st = 0; st < kStages; ++st) {
-            mbar_init(full(sbase, st), 1);
+            mbar_init(full(sbase, st), by_lane ? 33 : 1);
             mbar_init(empty(sbase, st), kWarps);
         }
         for (int u = 0; u < 2; ++u) {
@@ -94,6 +94,21 @@ __device__ __forceinline__ uint32_t swz8(int key, int chunk) {
     const int row = D == 128 ? key : key >> 1, at = D == 128 ? chunk : 4 * (key & 1) + chunk;
     return static_cast<uint32_t>(row * 128 + ((at ^ (row & 7)) << 4));
 }
+// Pages of 1 KB (16 keys of 64 columns) come by 16-byte copies of the loader's
+// lanes: in boxes of that size the copy engine brings 22 a microsecond and SM,
+// half of what HBM gives (128 ragged chats: 82 us with it, 71 with pages of 2 KB).
+template <int D>
+__device__ __forceinline__ bool copy_by_lane(const PagedParams& p) { return D == 64 && p.c.page_size == 16; }
+
+// 16 bytes from global into shared memory, and this thread's arrival once all
+// of its copies so far are there (which the barrier's count includes).
+__device__ __forceinline__ void copy_piece(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void arrive_with_copies(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
 // The CTA's stretch of the line of tiles (the whole block).
 template <class L>
 __device__ __forceinline__ Line code_line(const PagedParams& p, uint8_t* smem, int cta, bool loads) {
@@ -144,6 +159,7 @@ __device__ __forceinline__ void load_codes(const PagedScaledParams& p, const CUt
         tma_prefetch_desc(&tmV);
     }
     const int span = min(p.c.page_size, kKeys), pages = kKeys / span;    // 1, 2, 4 or 8
+    const bool by_lane = copy_by_lane<D>(p);
     const int most = 32 / pages, mine = lane / pages, at = lane & (pages - 1);
     const uint32_t page_bytes = static_cast<uint32_t>(span) * D * 2u;    // K and V
     int last[ST];
@@ -217,10 +233,28 @@ __device__ __forceinline__ void load_codes(const PagedScaledParams& p, const CUt
             const int kb = now.s.hull.tile(now.k + e), st = g % ST;
             const bool here = mine == e;
             if (g >= ST && !mbar_wait_warp(empty_bar(st), (g / ST - 1) & 1, wc, S_PC_EMPTY)) { ok = false; break; }
-            const uint32_t copies = __popc(__ballot_sync(0xffffffffu, here && now.id >= 0));
-            if (lane == 0) mbar_expect_tx(full_bar(st), copies * page_bytes);
+            if (by_lane) {
+                constexpr int kPages = kKeys / 16, kPage = 16 * D;       // pages of the tile, bytes of one
+#pragma unroll
+                for (int i = 0; i < kPages; ++i) {
+                    const int id = __shfl_sync(0xffffffffu, now.id, (e * kPages + i) & 31);
+                    if (id < 0) continue;
+                    const size_t from = ((size_t)id * p.c.Hkv + now.s.h) * kPage + 16 * lane;
+#pragma unroll
+                    for (int x = 0; x < kPage; x += 512) {
+                        const uint32_t row = (x + 16 * lane) >> 7;
+                        const uint32_t dst = sbase + st * L::kStage + i * kPage + row * 128 + ((lane ^ row) & 7) * 16;
+                        copy_piece(dst, p.k8 + from + x);
+                        copy_piece(dst + L::kTile, p.v8 + from + x);
+                    }
+                }
+                arrive_with_copies(full_bar(st));
+            } else {
+                const uint32_t copies = __popc(__ballot_sync(0xffffffffu, here && now.id >= 0));
+                if (lane == 0) mbar_expect_tx(full_bar(st), copies * page_bytes);
+            }
             __syncwarp();
-            if (here && now.id >= 0) {
+            if (!by_lane && here && now.id >= 0) {
                 const uint32_t dst = sbase + st * L::kStage + static_cast<uint32_t>(at * span) * D;
                 const int row = ((kb * kKeys + at * span) & (p.c.page_size - 1)) / (128 / D);
                 const int block = now.id * p.c.Hkv + now.s.h;

@@ -40,7 +40,7 @@ static_assert(kKeys == 32 * kWarps, "32 keys to a warp");
 
 // Beside the ring and the queues: two warps' O, every warp's [rows] maximum and sum.
 template <int D>
-struct Eight : CodeLayout<D, kWarps, kRows, 8u * kRows * D + 8u * kWarps * kRows> {
+struct Eight : CodeLayout<D, paged_eight_ctas(D), kWarps, kRows, 8u * kRows * D + 8u * kWarps * kRows> {
     static constexpr uint32_t kMerge = Eight::kExtra, kMl = kMerge + 8u * kRows * D;
 };
 
@@ -80,7 +80,7 @@ __device__ __forceinline__ bool consumers_all(bool ok) {
 }
 
 template <int D, int SCORE>
-__global__ void __launch_bounds__(Eight<D>::kThreads, 2)
+__global__ void __launch_bounds__(Eight<D>::kThreads, paged_eight_ctas(D))
 paged_eight_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                           const PagedScaledParams p) {
     using L = Eight<D>;
@@ -95,7 +95,7 @@ paged_eight_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
 
     if (threadIdx.x == 0) {
-        L::init(sbase);
+        L::init(sbase, copy_by_lane<D>(p));
         *abort_flag = 0;
         mbar_fence_init();
     }
