@@ -132,9 +132,8 @@ struct Scratch {
 };
 
 // CTAs that share the work of a call's own keys.
-int own_ctas(const fa_paged_kv* c, const fa_paged_fwd_args* a, bool scaled) {
-    const int each = !small_rows(c, a) ? 1 : scaled && eight_rows(c, a) ? fa::paged_eight_ctas(c->D) : fa::kPagedSmallCtasPerSm;
-    return fa::device_sm_count() * each;
+int own_ctas(const fa_paged_kv* c, const fa_paged_fwd_args* a) {
+    return fa::device_sm_count() * (small_rows(c, a) ? fa::kPagedSmallCtasPerSm : 1);
 }
 
 Scratch layout(const fa_paged_kv* c, const fa_paged_fwd_args* a) {
@@ -145,8 +144,7 @@ Scratch layout(const fa_paged_kv* c, const fa_paged_fwd_args* a) {
         at += (bytes + 255) & ~(size_t)255;
         return here;
     };
-    // (the most that any kernel takes: a cache held in 8 bits has the same scratch)
-    const size_t ctas = fa::device_sm_count() * (small_rows(c, a) ? fa::kPagedMostCtasPerSm : 1), D = c->D;
+    const size_t ctas = own_ctas(c, a), D = c->D;
     const size_t own = 2 * ctas * (small_rows(c, a) ? fa::kPagedSmallRows : fa::kPagedTileRows);
     s.hdr = take(256);
     s.meta = take(ctas * sizeof(fa::PagedMeta));
@@ -318,7 +316,7 @@ fa_status forward(const fa_paged_kv* c, bool scaled, const fa_paged_scales* scal
     p.max_q = a->max_q_len;
     p.shared = a->shared_len;
     p.join_rows = a->shared_len > 0;
-    p.ctas = own_ctas(c, a, scaled);
+    p.ctas = own_ctas(c, a);
     p.scale = a->scale > 0.f ? a->scale : 1.0f / std::sqrt((float)c->D);
     p.score = {score.kind, score.softcap, score.alibi_slopes, score.rel_bias, score.rel_max};
     p.q = static_cast<const uint16_t*>(a->q);
@@ -341,8 +339,6 @@ fa_status forward(const fa_paged_kv* c, bool scaled, const fa_paged_scales* scal
     if (scaled) {
         p.k_scale = scales->k_scale;
         p.v_scale = scales->v_scale;
-        p.k8 = static_cast<const uint8_t*>(c->k);
-        p.v8 = static_cast<const uint8_t*>(c->v);
     }
 
     cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -18,40 +18,44 @@ static_assert(kKeys == 1 << kShift, "keys of a tile");
 // all of them have begun unit nu - 2, and so are done with nu - 3.
 constexpr int kSegs = 4;
 // Entries of the line's index: fewer than the bf16 kernel has room for.
-constexpr int kCodeEntries = 350;
+constexpr int kCodeEntries = 300;
+// v's scales as exponents (log2 and reciprocal): one below 2^-80 of the largest so
+// far in the unit, or below 2^-100, counts as that.
+constexpr float kLeastRatio = 8.271806125530277e-25f, kLeastScale = 7.888609052210118e-31f;
 enum CodeSite : uint32_t { S_PC_FULL = 112, S_PC_EMPTY, S_PC_DRAIN, S_PC_Q, S_PC_Q_EMPTY };
 
 // Shared memory of such a kernel: the ring of tiles, `EXTRA` bytes of the
 // kernel's own, two units' rows of Q, units, scales, barriers, the line's index.
-template <int D, int CTAS, int WARPS, int ROWS, uint32_t EXTRA>
+template <int D, int WARPS, int LOADERS, int ROWS, uint32_t EXTRA>
 struct CodeLayout {
-    static constexpr int kCtas = CTAS, kD = D, kWarps = WARPS, kThreads = 32 * (WARPS + 1), kRows = ROWS;
+    static constexpr int kD = D, kWarps = WARPS, kThreads = 32 * (WARPS + LOADERS), kRows = ROWS;
     static constexpr uint32_t kTile = kKeys * static_cast<uint32_t>(D);
     static constexpr uint32_t kStage = 2u * kTile;               // K then V
-    static constexpr int kStages = (CTAS == 2 ? 98304 : 65536) / kStage;  // 192 KB of an SM
+    static constexpr int kStages = 98304 / kStage;               // 96 KB
     static constexpr uint32_t kExtra = kStages * kStage;
     static constexpr uint32_t kQRow = 2u * D + 16u;              // rows on distinct banks
     static constexpr uint32_t kQ = (kExtra + EXTRA + 15u) & ~15u;
     static constexpr uint32_t kSeg = kQ + 2u * kRows * kQRow;    // [kSegs], the one behind the last flagged by b < 0
-    static constexpr uint32_t kScale = kSeg + kSegs * sizeof(SmallSeg);   // [stage]: k's scale of each of the tile's pages, v's
-    static constexpr uint32_t kScaleStage = 8u * (kKeys / 16);
+    // [stage][k's scale, v's, its log2, 1 / it][the tile's pages]
+    static constexpr uint32_t kScale = kSeg + kSegs * sizeof(SmallSeg);
+    static constexpr uint32_t kScaleStage = 16u * (kKeys / 16);
     static constexpr uint32_t kInfo = kScale + kScaleStage * kStages;     // [stage]: 4 x tile + kTileOpen, kTileClear
     static constexpr uint32_t kBars = (kInfo + 4u * kStages + 7u) & ~7u;  // FULL, EMPTY [stage], Q_FULL, Q_EMPTY [2]
     static constexpr uint32_t kAbort = kBars + 16u * kStages + 32u;
     static constexpr uint32_t kScan = kAbort + 16u;              // warp sums
     static constexpr uint32_t kPre = kScan + 64u;                // first tile of each group of sequences
     static constexpr uint32_t bytes(int B) { return kPre + 4u * (groups_of(B, kCodeEntries) + 1u) + 1024u; }
-    // the CTAs fit on an SM (228 KB less 1 KB for each)
-    static_assert(CTAS * (kPre + 4u * (kCodeEntries + 1u) + 1024u) <= (228u - CTAS) * 1024u, "shared memory budget");
+    // two CTAs fit on an SM (228 KB less 1 KB for each)
+    static_assert(2u * (kPre + 4u * (kCodeEntries + 1u) + 1024u) <= 226u * 1024u, "shared memory budget");
     static __device__ __forceinline__ uint32_t full(uint32_t sbase, int st) { return sbase + kBars + 8u * st; }
     static __device__ __forceinline__ uint32_t empty(uint32_t sbase, int st) { return sbase + kBars + 8u * (kStages + st); }
     static __device__ __forceinline__ uint32_t q_full(uint32_t sbase, int u) { return sbase + kBars + 8u * (2 * kStages + (u & 1)); }
     static __device__ __forceinline__ uint32_t q_empty(uint32_t sbase, int u) {
         return sbase + kBars + 8u * (2 * kStages + 2 + (u & 1));
     }
-    static __device__ __forceinline__ void init(uint32_t sbase, bool by_lane) {
+    static __device__ __forceinline__ void init(uint32_t sbase) {
         for (int st = 0; st < kStages; ++st) {
-            mbar_init(full(sbase, st), by_lane ? 33 : 1);
+            mbar_init(full(sbase, st), LOADERS);
             mbar_init(empty(sbase, st), kWarps);
         }
         for (int u = 0; u < 2; ++u) {
@@ -94,20 +98,6 @@ __device__ __forceinline__ uint32_t swz8(int key, int chunk) {
     const int row = D == 128 ? key : key >> 1, at = D == 128 ? chunk : 4 * (key & 1) + chunk;
     return static_cast<uint32_t>(row * 128 + ((at ^ (row & 7)) << 4));
 }
-// Pages of 1 KB (16 keys of 64 columns) come by 16-byte copies of the loader's
-// lanes: in boxes of that size the copy engine brings 22 a microsecond and SM,
-// half of what HBM gives (128 ragged chats: 82 us with it, 71 with pages of 2 KB).
-template <int D>
-__device__ __forceinline__ bool copy_by_lane(const PagedParams& p) { return D == 64 && p.c.page_size == 16; }
-
-// 16 bytes from global into shared memory, and this thread's arrival once all
-// of its copies so far are there (which the barrier's count includes).
-__device__ __forceinline__ void copy_piece(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void arrive_with_copies(uint32_t bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
 
 // The CTA's stretch of the line of tiles (the whole block).
 template <class L>
@@ -143,8 +133,15 @@ __device__ __forceinline__ Line code_line(const PagedParams& p, uint8_t* smem, i
 // Up to 32 pages, a lane to each, are a batch of a unit's tiles.  Three batches
 // are on their way: the copies of one are issued, the next one's scales come, and
 // the page ids, which those need, of the one behind (128 ragged chats of 64
-// columns: 66 us, 95 with ids and scales a tile or two ahead within a unit).
-template <class L>
+// columns: a quarter less time than with ids and scales a tile or two ahead
+// within a unit).
+//
+// Pages of 16 keys are 16 copies a tile, which a warp issues one lane after the
+// other.  Two warps may share them, one for K and all else, one for V: 76.6 us for
+// those chats instead of 83.4, 9.9 for a single one instead of 9.1.  Copies of 16
+// bytes by every lane, which a page of 1 KB is still small enough for: 88.8.
+enum LoadPart { kLoadBoth, kLoadK, kLoadV };
+template <class L, int PART>
 __device__ __forceinline__ void load_codes(const PagedScaledParams& p, const CUtensorMap& tmK, const CUtensorMap& tmV, Line line,
                                            uint8_t* smem, uint32_t sbase, const WaitCtl& wc, int lane) {
     constexpr int D = L::kD, ST = L::kStages;
@@ -159,9 +156,8 @@ __device__ __forceinline__ void load_codes(const PagedScaledParams& p, const CUt
         tma_prefetch_desc(&tmV);
     }
     const int span = min(p.c.page_size, kKeys), pages = kKeys / span;    // 1, 2, 4 or 8
-    const bool by_lane = copy_by_lane<D>(p);
     const int most = 32 / pages, mine = lane / pages, at = lane & (pages - 1);
-    const uint32_t page_bytes = static_cast<uint32_t>(span) * D * 2u;    // K and V
+    const uint32_t page_bytes = static_cast<uint32_t>(span) * D * (PART == kLoadBoth ? 2u : 1u);
     int last[ST];
 #pragma unroll
     for (int st = 0; st < ST; ++st) last[st] = -1;
@@ -189,7 +185,7 @@ __device__ __forceinline__ void load_codes(const PagedScaledParams& p, const CUt
     };
     auto scales_of = [&](const Batch& b) {
         const size_t x = (size_t)max(b.id, 0) * p.c.Hkv + b.s.h;
-        return b.id >= 0 ? make_float2(p.k_scale[x], p.v_scale[x]) : make_float2(0.f, 0.f);
+        return PART != kLoadV && b.id >= 0 ? make_float2(p.k_scale[x], p.v_scale[x]) : make_float2(0.f, 0.f);
     };
     int g = 0, nu = 0;
     bool ok = true, marked = false;
@@ -197,10 +193,13 @@ __device__ __forceinline__ void load_codes(const PagedScaledParams& p, const CUt
     next_batch(next);
     now = next;
     float2 scales = now.tiles > 0 ? scales_of(now) : make_float2(0.f, 0.f);
+    float largest = 0.f;                           // of v's scales in the unit
     next_batch(next);
     for (;;) {
         const bool fresh = now.tiles == 0 || now.k == now.s.k0;
-        if (fresh) {
+        if (PART == kLoadV) {
+            if (now.tiles == 0) break;
+        } else if (fresh) {
             if (nu >= 2 && !mbar_wait_warp(q_empty(nu), ((nu >> 1) - 1) & 1, wc, S_PC_Q_EMPTY)) break;
             if (now.tiles == 0) {
                 if (lane == 0) {
@@ -212,6 +211,7 @@ __device__ __forceinline__ void load_codes(const PagedScaledParams& p, const CUt
             }
             // the unit and its rows of Q, a lane to each, into the slots that
             // the unit before the last has left
+            largest = 0.f;
             const SmallSeg& s = now.s;
             const int rows = s.n * p.group;
             if (lane == 0) {
@@ -229,43 +229,39 @@ __device__ __forceinline__ void load_codes(const PagedScaledParams& p, const CUt
             ++nu;
         }
         const float2 scales_next = next.tiles > 0 ? scales_of(next) : make_float2(0.f, 0.f);
+        // (bits of numbers that are not negative are in their order)
+        largest = fmaxf(largest, __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(scales.y, 0.f)))));
+        float least = fmaxf(fmaxf(scales.y, largest * kLeastRatio), kLeastScale);
+        if (scales.y != scales.y) least = scales.y;
+        const float lv = log2f(least), iv = 1.f / least;
         for (int e = 0; e < now.tiles; ++e, ++g) {
             const int kb = now.s.hull.tile(now.k + e), st = g % ST;
             const bool here = mine == e;
             if (g >= ST && !mbar_wait_warp(empty_bar(st), (g / ST - 1) & 1, wc, S_PC_EMPTY)) { ok = false; break; }
-            if (by_lane) {
-                constexpr int kPages = kKeys / 16, kPage = 16 * D;       // pages of the tile, bytes of one
-#pragma unroll
-                for (int i = 0; i < kPages; ++i) {
-                    const int id = __shfl_sync(0xffffffffu, now.id, (e * kPages + i) & 31);
-                    if (id < 0) continue;
-                    const size_t from = ((size_t)id * p.c.Hkv + now.s.h) * kPage + 16 * lane;
-#pragma unroll
-                    for (int x = 0; x < kPage; x += 512) {
-                        const uint32_t row = (x + 16 * lane) >> 7;
-                        const uint32_t dst = sbase + st * L::kStage + i * kPage + row * 128 + ((lane ^ row) & 7) * 16;
-                        copy_piece(dst, p.k8 + from + x);
-                        copy_piece(dst + L::kTile, p.v8 + from + x);
-                    }
-                }
-                arrive_with_copies(full_bar(st));
-            } else {
-                const uint32_t copies = __popc(__ballot_sync(0xffffffffu, here && now.id >= 0));
-                if (lane == 0) mbar_expect_tx(full_bar(st), copies * page_bytes);
+            const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, here && now.id >= 0)) * page_bytes;
+            if (lane == 0) {
+                if (PART == kLoadV)
+                    mbar_arrive_expect_tx(full_bar(st), bytes);
+                else
+                    mbar_expect_tx(full_bar(st), bytes);
             }
             __syncwarp();
-            if (!by_lane && here && now.id >= 0) {
+            if (here && now.id >= 0) {
                 const uint32_t dst = sbase + st * L::kStage + static_cast<uint32_t>(at * span) * D;
                 const int row = ((kb * kKeys + at * span) & (p.c.page_size - 1)) / (128 / D);
                 const int block = now.id * p.c.Hkv + now.s.h;
-                tma_load_3d(dst, &tmK, full_bar(st), 0, row, block);
-                tma_load_3d(dst + L::kTile, &tmV, full_bar(st), 0, row, block);
+                if (PART != kLoadV) tma_load_3d(dst, &tmK, full_bar(st), 0, row, block);
+                if (PART != kLoadK) tma_load_3d(dst + L::kTile, &tmV, full_bar(st), 0, row, block);
             }
+            last[st] = g;
+            if (PART == kLoadV) continue;
             // what else the consumers need of the tile, and only then the loader's arrival
             float* const sc = reinterpret_cast<float*>(smem + L::kScale + st * L::kScaleStage);
             if (here) {
                 sc[at] = scales.x;
                 sc[kKeys / 16 + at] = scales.y;
+                sc[2 * (kKeys / 16) + at] = lv;
+                sc[3 * (kKeys / 16) + at] = iv;
             }
             if (lane == 0)
                 info_s[st] = 4 * kb +
@@ -273,7 +269,6 @@ __device__ __forceinline__ void load_codes(const PagedScaledParams& p, const CUt
                              (now.s.hull.all(kb * kKeys, kb * kKeys + kKeys) ? 0 : kTileClear);
             __syncwarp();
             if (lane == 0) mbar_arrive(full_bar(st));
-            last[st] = g;
         }
         if (!ok) break;
         now = next;
@@ -287,7 +282,7 @@ __device__ __forceinline__ void load_codes(const PagedScaledParams& p, const CUt
             if (last[st] >= 0) paged_drain_wait(full_bar(st), (last[st] / ST) & 1, wc, S_PC_DRAIN);
         // (behind the end mark only the last unit's rows can be on their
         // way: the mark's slot had been read)
-        for (int u = max(nu - (marked ? 1 : 2), 0); u < nu; ++u)
+        for (int u = max(nu - (marked ? 1 : 2), 0); u < nu; ++u)         // (kLoadV has none)
             paged_drain_wait(q_full(u), (u >> 1) & 1, wc, S_PC_DRAIN);
     }
     __syncwarp();

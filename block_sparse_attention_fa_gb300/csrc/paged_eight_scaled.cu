@@ -20,11 +20,20 @@
 //   - V: ldmatrix.trans gives two keys of two adjacent columns; the even columns
 //     are the product's rows 0-7, the odd ones 8-15.
 // A code is converted once, to f16, which holds it exactly; so does it a row of Q
-// scaled by a power of two, and P is rounded to f16's 11 bits.  The scales are
-// applied in fp32: k's to S, v's to the product of 16 keys, which are of one page.
-//
-// The maximum is raised (and O and the sum rescaled) only when a score is 2^8
+// scaled by a power of two, and P is rounded to f16's 11 bits.  k's scale is applied
+// to S in fp32.  v's is part of P's exponent: with x the score in base 2 and
+// lv = log2(v's scale), one for 16 keys (of a page), M the running maximum of x + lv,
+//     P = 2^(x + lv - M),   l = sum of P / (v's scale),
+// so that O accumulates in the products, P's roundings are relative to the largest
+// share that any key has in O, and O / l and M + log2 l are what they are without
+// scales.  The maximum is raised (and O and l rescaled) only when a score is 2^8
 // past it, which one vote of the warp tells.
+//
+// Two warps load (paged_codes.cuh); their issue of pages of 16 keys bounds ragged
+// batches, DRAM the long ones.  8 sequences of 32768 tokens, 8 kv heads of 128
+// columns: 90.4 us, 79.1 at the copy rate (bf16 cache: 163).  128 of up to 4096, 8
+// kv heads of 64 columns, pages of 16: 76.6 us, 41.0 at the copy rate.  One of 520
+// tokens: 9.9.
 //
 // V rows of keys that no row of the unit sees are cleared in shared memory before
 // the product: their P is 0, but 0 x NaN is not.
@@ -33,14 +42,14 @@
 namespace fa {
 namespace {
 
-constexpr int kWarps = 4;                        // consumers, 32 keys each; warp 4 loads
+constexpr int kWarps = 4;                        // consumers, 32 keys each; warps 4 and 5 load
 constexpr int kRows = 8;
 constexpr float kLazyMax = 8.f;
 static_assert(kKeys == 32 * kWarps, "32 keys to a warp");
 
 // Beside the ring and the queues: two warps' O, every warp's [rows] maximum and sum.
 template <int D>
-struct Eight : CodeLayout<D, paged_eight_ctas(D), kWarps, kRows, 8u * kRows * D + 8u * kWarps * kRows> {
+struct Eight : CodeLayout<D, kWarps, 2, kRows, 8u * kRows * D + 8u * kWarps * kRows> {
     static constexpr uint32_t kMerge = Eight::kExtra, kMl = kMerge + 8u * kRows * D;
 };
 
@@ -58,14 +67,6 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], c
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
-// d = a b, the same from 0
-__device__ __forceinline__ void mma_f16_from_0(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
-        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(0.f));
-}
 __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 // The same barrier with a vote: whether `ok` holds in every thread.
 __device__ __forceinline__ bool consumers_all(bool ok) {
@@ -79,8 +80,12 @@ __device__ __forceinline__ bool consumers_all(bool ok) {
     return r != 0;
 }
 
+// Two CTAs per SM, at no more registers than 128: an SM's quarters hold 16384
+// each, and four warps where each of the CTAs has put two there.  (Three CTAs of
+// five warps, of which that left room for only by chance: 66 us or 110 for the
+// chats, depending on what ran before.)
 template <int D, int SCORE>
-__global__ void __launch_bounds__(Eight<D>::kThreads, paged_eight_ctas(D))
+__global__ void __maxnreg__(128)
 paged_eight_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                           const PagedScaledParams p) {
     using L = Eight<D>;
@@ -95,7 +100,7 @@ paged_eight_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
 
     if (threadIdx.x == 0) {
-        L::init(sbase, copy_by_lane<D>(p));
+        L::init(sbase);
         *abort_flag = 0;
         mbar_fence_init();
     }
@@ -105,11 +110,14 @@ paged_eight_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
     else
         pdl_wait_previous();
     pdl_launch_next();
-    const Line line = code_line<L>(p, smem, cta, warp == kWarps);
+    const Line line = code_line<L>(p, smem, cta, warp >= kWarps);
     const WaitCtl wc{abort_flag, p.ws, p.timeout_ns};
 
-    if (warp == kWarps) {
-        load_codes<L>(p, tmK, tmV, line, smem, sbase, wc, lane);
+    if (warp >= kWarps) {
+        if (warp == kWarps)
+            load_codes<L, kLoadK>(p, tmK, tmV, line, smem, sbase, wc, lane);
+        else
+            load_codes<L, kLoadV>(p, tmK, tmV, line, smem, sbase, wc, lane);
         if (p.join_rows) pdl_wait_previous();
         return;
     }
@@ -185,6 +193,8 @@ paged_eight_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
             if (!mbar_wait_warp(L::full(sbase, st), (g / ST) & 1, wc, S_PC_FULL)) { ok = false; break; }
             const int info = info_s[st], j0 = (info >> 2) * kKeys + 32 * warp;
             const float* const sc = reinterpret_cast<const float*>(smem + L::kScale + st * L::kScaleStage);
+            const int page[2] = {32 * warp >> by_page, (32 * warp + 16) >> by_page};
+            const float lv[2] = {sc[2 * (kKeys / 16) + page[0]], sc[2 * (kKeys / 16) + page[1]]};
             const bool open = (info & kTileOpen) != 0;
             bool cleared = false;
             // S^T, 16 keys at a time
@@ -220,16 +230,16 @@ paged_eight_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
                 }
                 __syncwarp();
             }
-            bool over = false;
+            // x: the score in base 2, and log2 of v's scale
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const float k_scale = sc[(32 * warp + 16 * u) >> by_page];
+                const float k_scale = sc[page[u]] * (SCORE == FA_SCORE_NONE || SCORE == FA_SCORE_REL_BIAS ? sl2 : 1.f);
+                const float f[2] = {unscale[0] * k_scale, unscale[1] * k_scale};
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     const int e = c & 1, j = j0 + 16 * u + gr + 8 * (c >> 1), i = i0 + tok[e];
-                    float v = x[u][c] * unscale[e] * k_scale;
+                    float v = SCORE == FA_SCORE_NONE ? fmaf(x[u][c], f[e], lv[u]) : x[u][c] * f[e];
                     const float far = fabsf(static_cast<float>(i - j));
-                    if (SCORE == FA_SCORE_NONE || SCORE == FA_SCORE_REL_BIAS) v *= sl2;
                     if (SCORE == FA_SCORE_SOFTCAP) v = softcap_one(v, cap);
                     if (SCORE == FA_SCORE_ALIBI) v = fmaf(-slope[e], far, v * sl2);
                     if (SCORE == FA_SCORE_ALIBI_SOFTCAP) v = softcap_one(fmaf(-slope[e], far, v * p.scale), cap);
@@ -239,21 +249,20 @@ paged_eight_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
                         v = fmaf(p.score.rel_bias[(size_t)hq * (2 * R + 1) + d + R], kPagedLog2e, v);
                     }
                     if (!open && !paged_visible(p.mask, i, j, p.shared, s.kv)) v = -CUDART_INF_F;
-                    x[u][c] = v;
-                    over |= v > m[e] + kLazyMax;
+                    x[u][c] = SCORE == FA_SCORE_NONE ? v : v + lv[u];
                 }
             }
-            if (__any_sync(0xffffffffu, over)) {
+            const float top[2] = {fmaxf(fmax3(x[0][0], x[0][2], x[1][0]), x[1][2]), fmaxf(fmax3(x[0][1], x[0][3], x[1][1]), x[1][3])};
+            if (__any_sync(0xffffffffu, top[0] > m[0] + kLazyMax || top[1] > m[1] + kLazyMax)) {
                 float alpha[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float top = fmaxf(fmaxf(fmaxf(x[0][e], x[0][2 + e]), fmaxf(x[1][e], x[1][2 + e])),
-                                      m[e]);
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                    alpha[e] = top == m[e] ? 1.f : ex2_approx(m[e] - top);
-                    m[e] = top;
+                    float to = fmaxf(top[e], m[e]);
+                    to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, 4));
+                    to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, 8));
+                    to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, 16));
+                    alpha[e] = to == m[e] ? 1.f : ex2_approx(m[e] - to);
+                    m[e] = to;
                     l[e] *= alpha[e];
                 }
 #pragma unroll
@@ -272,13 +281,13 @@ paged_eight_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
                 float w[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) w[c] = ex2_approx(x[u][c] - ref[c & 1]);
-                l[0] += w[0] + w[2];
-                l[1] += w[1] + w[3];
+                const float iv = sc[3 * (kKeys / 16) + page[u]];
+                l[0] = fmaf(w[0] + w[2], iv, l[0]);
+                l[1] = fmaf(w[1] + w[3], iv, l[1]);
                 pb[u][0] = transpose_8x8(pack_f16x2(w[0], w[1]));
                 pb[u][1] = transpose_8x8(pack_f16x2(w[2], w[3]));
             }
             // O^T += V^T P^T, 16 columns at a time
-            const float v_scale[2] = {sc[kKeys / 16 + (32 * warp >> by_page)], sc[kKeys / 16 + ((32 * warp + 16) >> by_page)]};
 #pragma unroll
             for (int c = 0; c < kChunks; c += 2) {
 #pragma unroll
@@ -290,10 +299,7 @@ paged_eight_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
                         uint32_t a[4];
                         codes_to_f16(__byte_perm(vf[2 * e], 0u, 0x3120), a[0], a[1]);
                         codes_to_f16(__byte_perm(vf[2 * e + 1], 0u, 0x3120), a[2], a[3]);
-                        float z[4];
-                        mma_f16_from_0(z, a, pb[u]);
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) o[c + e][q] = fmaf(z[q], v_scale[u], o[c + e][q]);
+                        mma_f16(o[c + e], a, pb[u]);
                     }
                 }
             }

@@ -10,7 +10,6 @@ namespace fa {
 // The paged forward over a cache held in 8 bits.
 struct PagedScaledParams : PagedParams {
     const float *k_scale, *v_scale;   // [num_pages][Hkv]
-    const uint8_t *k8, *v8;           // the codes
 };
 
 // The append to one (kc and vc are not used).
@@ -41,10 +40,6 @@ cudaError_t launch_paged_small_scaled(const PagedScaledParams& p, const CUtensor
                                       cudaStream_t s);
 cudaError_t launch_paged_eight_scaled(const PagedScaledParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
                                       cudaStream_t s);
-// CTAs per SM of the kernel for up to 8 rows over codes: what a CTA of 64 columns
-// waits for (its products, one after the other) a third one covers.
-constexpr int paged_eight_ctas(int D) { return D == 64 ? 3 : 2; }
-constexpr int kPagedMostCtasPerSm = 3;
 cudaError_t launch_paged_tiles_scaled(const PagedScaledParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
                                       cudaStream_t s);
 // Pages of codes, boxes of min(page_size, tile_keys) keys: as rows of 128 bytes

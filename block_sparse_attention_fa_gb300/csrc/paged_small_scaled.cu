@@ -28,7 +28,7 @@ static_assert(kKeys == 16 * kWarps, "16 keys to a warp");
 // Beside the ring and the queues: P, and every warp's [rows] maximum and sum.
 constexpr uint32_t kPRow = 2u * kKeys + 16u;     // 16 bytes of padding: rows on distinct banks
 template <int D>
-struct Sixteen : CodeLayout<D, 2, kWarps, kRows, kRows * kPRow + 8u * kRows * kWarps> {
+struct Sixteen : CodeLayout<D, kWarps, 1, kRows, kRows * kPRow + 8u * kRows * kWarps> {
     static constexpr uint32_t kP = Sixteen::kExtra, kMax = kP + kRows * kPRow, kSum = kMax + 4u * kRows * kWarps;
 };
 
@@ -109,7 +109,7 @@ paged_small_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
 
     if (threadIdx.x == 0) {
-        L::init(sbase, copy_by_lane<D>(p));
+        L::init(sbase);
         *abort_flag = 0;
         mbar_fence_init();
     }
@@ -123,7 +123,7 @@ paged_small_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
     const WaitCtl wc{abort_flag, p.ws, p.timeout_ns};
 
     if (warp == kWarps) {
-        load_codes<L>(p, tmK, tmV, line, smem, sbase, wc, lane);
+        load_codes<L, kLoadBoth>(p, tmK, tmV, line, smem, sbase, wc, lane);
         if (p.join_rows) pdl_wait_previous();
         return;
     }
