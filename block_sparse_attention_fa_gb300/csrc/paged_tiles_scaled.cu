@@ -24,7 +24,7 @@
 // the largest share that any key has in O, and one exponential serves both sums;
 // O / l and M + log2 l are what they are without scales.  The scale is the same for
 // 16 columns (of one page).  A scale below 2^-80 of the largest so far in the unit,
-// or below 2^-100, counts as that: what such a page adds to O is nothing beside the
+// or below 2^-90, counts as that: what such a page adds to O is nothing beside the
 // others, and l keeps all of its keys.  k's scale and the row's stay with S.
 //
 // Shared memory bounds the pair of products together with the conversion (2700
@@ -45,7 +45,7 @@ constexpr uint32_t kRegsSoftmax8 = 184, kRegsOther8 = 88, kRegsConvert8 = 56;
 static_assert(2 * kRegsSoftmax8 + kRegsOther8 + kRegsConvert8 == 4 * 128, "register split must match the launch");
 constexpr float kLazyMax8 = 8.f;               // (0 with fp32 output)
 constexpr float kLeastRatio = 8.271806125530277e-25f;      // 2^-80
-constexpr float kLeastScale = 7.888609052210118e-31f;      // 2^-100
+constexpr float kLeastScale = 8.077935669463161e-28f;      // 2^-90
 constexpr int kMaxRing8 = 4;
 // Tiles whose scales are kept.  K(g) is loaded once S of tile g - stages is done,
 // which came after P of the tile before that: the loader is at most five tiles

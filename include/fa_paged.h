@@ -199,7 +199,7 @@ fa_status fa_kv_append_scaled(const fa_paged_kv *c, const fa_paged_scales *scale
  * error of 2^-18 of that below (where more than 16 rows go per sequence and kv
  * head; exactly otherwise); P is rounded to 11 significant bits.  Except for 9 to
  * 16 rows, a v scale below 2^-80 of the largest one that the rows have seen, or
- * below 2^-100, counts as that.
+ * below 2^-90, counts as that.
  * scratch: fa_paged_scratch_bytes().                                        */
 fa_status fa_fwd_paged_scaled(const fa_paged_kv *c, const fa_paged_scales *scales, const fa_paged_fwd_args *a,
                               const fa_mask_desc *mask, const fa_score_desc *sc, void *scratch, size_t scratch_bytes,
