@@ -682,6 +682,13 @@ paged_tiles_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
                     for (int h = 0; h < 2; ++h) {
                         const uint32_t tSh = tS + 64u * h;
                         const int ch = kb * kBlock + 64 * h;
+                        // of 16 columns each: what S is to be multiplied by (k's scale
+                        // and the row's), v's scale
+                        const float4 ks4 = *reinterpret_cast<const float4*>(scales + 4 * h);
+                        const float4 lv4 = *reinterpret_cast<const float4*>(scales + 8 + 4 * h);
+                        const float4 iv4 = *reinterpret_cast<const float4*>(scales + 16 + 4 * h);
+                        const float lv[4] = {lv4.x, lv4.y, lv4.z, lv4.w}, iv[4] = {iv4.x, iv4.y, iv4.z, iv4.w};
+                        float sc[4] = {row_scale * ks4.x, row_scale * ks4.y, row_scale * ks4.z, row_scale * ks4.w};
                         if (!mbar_wait_warp(bar(T_S_FULL + 2 * t + h), n & 1, wc, S_T_S)) { ok = false; break; }
                         tc_fence_after();
                         float x[64];
@@ -691,15 +698,13 @@ paged_tiles_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
 #pragma unroll
                             for (int e = 0; e < 64; ++e) x[e] = __uint_as_float(raw[e]);
                         }
-                        // k's scale and the row's, of 16 columns at a time: with a
-                        // score_mod x becomes q.k here and the modified score in base
-                        // 2 below; without one it stays as it is, to be multiplied by
-                        // sc (which is no 0, so that -inf stays what it is)
-                        float sc[4];
-                        const float4 ks = *reinterpret_cast<const float4*>(scales + 4 * h);
+                        // with a score_mod x becomes q.k here and the modified score
+                        // in base 2 below; without one it stays as it is, to be
+                        // multiplied by sc (which is no 0, so that -inf stays what it
+                        // is)
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
-                            const float f = row_scale * (c == 0 ? ks.x : c == 1 ? ks.y : c == 2 ? ks.z : ks.w);
+                            const float f = sc[c];
                             if (SCORE == FA_SCORE_NONE) {
                                 asm("max.NaN.f32 %0, %1, %2;" : "=f"(sc[c]) : "f"(f), "f"(FLT_MIN));
                             } else {
@@ -746,9 +751,6 @@ paged_tiles_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
                                 for (int e = 0; e < 32; ++e) x[32 * c + e] = (see >> e) & 1u ? x[32 * c + e] : -CUDART_INF_F;
                             }
                         }
-                        const float4 lv4 = *reinterpret_cast<const float4*>(scales + 8 + 4 * h);
-                        const float4 iv4 = *reinterpret_cast<const float4*>(scales + 16 + 4 * h);
-                        const float lv[4] = {lv4.x, lv4.y, lv4.z, lv4.w}, iv[4] = {iv4.x, iv4.y, iv4.z, iv4.w};
                         float m_new = m;
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
