@@ -68,6 +68,7 @@ enum TBar8 {
     T_Q_HERE = T_SEG_EMPTY + 2,                  // the first unit's rows of tile 0, before they are split
     T_COUNT = T_Q_HERE + 1
 };
+static_assert(T_COUNT <= kThreads8, "a thread to a barrier");
 constexpr uint32_t kSegReaders = 14;             // the MMA, softmax and converting warps
 enum TSite8 : uint32_t { S_T_Q = 128, S_T_K_FULL, S_T_K_EMPTY, S_T_RAW_FULL, S_T_RAW_EMPTY, S_T_V_FULL, S_T_V_EMPTY,
                          S_T_SCALES, S_T_S, S_T_P, S_T_O, S_T_UPD, S_T_DRAIN, S_T_SEG, S_T_SEG_EMPTY };
@@ -149,49 +150,47 @@ __device__ __forceinline__ uint32_t to_e4m3(uint32_t w) {
     return r;
 }
 
-// A row of Q, bf16 in its row tile at `tile`, into hi and lo in its place.
-// Returns what S is to be multiplied by.
+// A warp's 32 rows of Q, bf16 in their row tile at `tile` from row `first` on, into
+// hi and lo in their place.  Returns what S of row first + lane is to be multiplied
+// by.  A row is its lanes' (16 columns each), some rows at a time: a thread to a row
+// would take six times the instructions, which a CTA's first unit has to wait for.
 template <int D>
-__device__ __forceinline__ float split_row(uint8_t* tile, int row) {
-    constexpr int kPieces = D / 8;               // 16 bytes of bf16 each
-    auto at = [&](int c) { return tile + (c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4); };
-    constexpr int kHold = kPieces / 2;           // the later pieces, in whose place lo comes
-    uint4 held[kHold];
-    float top = 0.f;
+__device__ __forceinline__ float split_rows(uint8_t* tile, int first, int lane) {
+    constexpr int kLanes = D / 16, kAtOnce = 32 / kLanes;
+    const int c = lane % kLanes;
+    float mine = 1.f;
+#pragma unroll 1
+    for (int r0 = 0; r0 < 32; r0 += kAtOnce) {
+        const int row = first + r0 + lane / kLanes;
+        auto at = [&](int k) { return tile + (k >> 3) * 16384 + row * 128 + (((k & 7) ^ (row & 7)) << 4); };
+        const uint4 v0 = *reinterpret_cast<const uint4*>(at(2 * c)), v1 = *reinterpret_cast<const uint4*>(at(2 * c + 1));
+        const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+        float top = 0.f;
 #pragma unroll
-    for (int c = 0; c < kPieces; ++c) {
-        const uint4 w = *reinterpret_cast<const uint4*>(at(c));
-        if (c >= kHold) held[c - kHold] = w;
-        top = fmax3(top, fmax3(fabsf(bf_low(w.x)), fabsf(bf_high(w.x)), fabsf(bf_low(w.y))),
-                    fmax3(fabsf(bf_high(w.y)), fabsf(bf_low(w.z)), fabsf(bf_high(w.z))));
-        top = fmax3(top, fabsf(bf_low(w.w)), fabsf(bf_high(w.w)));
-    }
-    // top = 1.f 2^x: times 2^(8 - x), or 2^(7 - x) where 1.f is past 7/4
-    const int bits = __float_as_int(top), x = max((bits >> 23) + ((bits & 0x7fffff) > 0x600000 ? 1 : 0), 10);
-    const float up = __int_as_float((262 - x) << 23);
-    // (an infinity would become 448: it makes all of the row's scores NaN instead)
-    const float down = top < CUDART_INF_F ? __int_as_float((x - 8) << 23) : CUDART_NAN_F;
-    // pieces c and c + 1: 16 codes, a piece of hi and one of lo
-    auto split = [&](int c, const uint4& v0, const uint4& v1) {
+        for (int e = 0; e < 8; ++e) top = fmax3(top, fabsf(bf_low(w[e])), fabsf(bf_high(w[e])));
+#pragma unroll
+        for (int d = 1; d < kLanes; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        // top = 1.f 2^x: times 2^(8 - x), or 2^(7 - x) where 1.f is past 7/4
+        const int bits = __float_as_int(top), x = max((bits >> 23) + ((bits & 0x7fffff) > 0x600000 ? 1 : 0), 10);
+        const float up = __int_as_float((262 - x) << 23);
+        // (an infinity would become 448: it makes all of the row's scores NaN instead)
+        const float down = top < CUDART_INF_F ? __int_as_float((x - 8) << 23) : CUDART_NAN_F;
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const uint4& v = e < 2 ? v0 : v1;
-            const uint32_t p = (e & 1) ? v.z : v.x, q = (e & 1) ? v.w : v.y;
+            const uint32_t p = w[2 * e], q = w[2 * e + 1];
             uint32_t a = pack_f16x2(bf_low(p) * up, bf_high(p) * up), b = pack_f16x2(bf_low(q) * up, bf_high(q) * up);
             const uint32_t ha = split_pair(a), hb = split_pair(b);
             hi[e] = __byte_perm(ha, hb, 0x5410);
             lo[e] = __byte_perm(to_e4m3(a), to_e4m3(b), 0x5410);
         }
-        *reinterpret_cast<uint4*>(at(c / 2)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(at(kHold + c / 2)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-    };
-#pragma unroll
-    for (int c = 0; c < kHold; c += 2)
-        split(c, *reinterpret_cast<const uint4*>(at(c)), *reinterpret_cast<const uint4*>(at(c + 1)));
-#pragma unroll
-    for (int c = 0; c < kHold; c += 2) split(kHold + c, held[c], held[c + 1]);
-    return down;
+        // (the shuffles above: all of the rows' pieces have been read)
+        *reinterpret_cast<uint4*>(at(c)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(at(kLanes + c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        const float theirs = __shfl_sync(0xffffffffu, down, kLanes * (lane % kAtOnce));
+        if (lane / kAtOnce == r0 / kAtOnce) mine = theirs;
+    }
+    return mine;
 }
 
 // A converting warp's 16 keys (of 64, from 16 w on) of a half of V: codes at
@@ -237,22 +236,23 @@ paged_tiles_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
     int* const len_s = q0_s + p.c.B + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
 
-    if (threadIdx.x == 0) {
-        for (int k = 0; k < T_COUNT; ++k) {
-            uint32_t cnt = 1;
-            if (k < T_K_FULL) cnt = 4;
-            if (k >= T_P_FULL && k < T_P_FULL + 4) cnt = 4;
-            if (k == T_Q_HERE) cnt = 4;
-            if (k >= T_RAW_EMPTY && k < T_RAW_EMPTY + kMaxRing8) cnt = 4;     // the converting warps
-            if (k >= T_V_FULL && k < T_V_FULL + kMaxRing8) cnt = 4;
-            if (k >= T_K_EMPTY && k < T_K_EMPTY + kMaxRing8) cnt = 2;         // both MMA warps
-            if (k >= T_V_EMPTY && k < T_V_EMPTY + kMaxRing8) cnt = 2;
-            if (k >= T_SEG_EMPTY && k < T_SEG_EMPTY + 2) cnt = kSegReaders;
-            mbar_init(bar(k), cnt);
+    if (threadIdx.x < T_COUNT) {
+        const int k = threadIdx.x;
+        uint32_t cnt = 1;
+        if (k < T_K_FULL) cnt = 4;
+        if (k >= T_P_FULL && k < T_P_FULL + 4) cnt = 4;
+        if (k == T_Q_HERE) cnt = 4;
+        if (k >= T_RAW_EMPTY && k < T_RAW_EMPTY + kMaxRing8) cnt = 4;         // the converting warps
+        if (k >= T_V_FULL && k < T_V_FULL + kMaxRing8) cnt = 4;
+        if (k >= T_K_EMPTY && k < T_K_EMPTY + kMaxRing8) cnt = 2;             // both MMA warps
+        if (k >= T_V_EMPTY && k < T_V_EMPTY + kMaxRing8) cnt = 2;
+        if (k >= T_SEG_EMPTY && k < T_SEG_EMPTY + 2) cnt = kSegReaders;
+        mbar_init(bar(k), cnt);
+        if (k == 0) {
+            *abort_flag = 0;
+            minmax[0] = INT_MAX;
+            minmax[1] = INT_MIN;
         }
-        *abort_flag = 0;
-        minmax[0] = INT_MAX;
-        minmax[1] = INT_MIN;
         mbar_fence_init();
     }
     if (warp == 9) {
@@ -562,7 +562,7 @@ paged_tiles_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
         bool ok = true;
         PagedMeta meta{};
         // The warp's 32 rows of a unit's Q, as in paged_tiles.cu, and their split
-        // (a thread's row; the copies of all lanes are waited for first).
+        // (the copies of all lanes are waited for first).
         float down_next = 1.f;
         bool q_here = false;
         auto bring = [&](const TileSeg& u) {
@@ -574,7 +574,7 @@ paged_tiles_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
             __syncwarp();
             if (t == 0 && !q_here && lane == 0) mbar_arrive(bar(T_Q_HERE));
             q_here = true;
-            down_next = split_row<D>(smem + L::kQ + t * L::kTile, r);
+            down_next = split_rows<D>(smem + L::kQ + t * L::kTile, 32 * wq, lane);
             fence_async_shared();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(T_Q_FULL + t));
