@@ -15,8 +15,9 @@
 // does it all: each CTA makes the sums for itself (the lengths of 2048 sequences
 // are 24 KB) and takes its share of the pages and rows; a row's page comes from
 // the table, or from the stack by the same formula, never from another CTA.  The
-// last CTA to have read the arguments (a counter in the workspace, 0 between
-// launches) writes what may be written in place: the lengths and the count.  One CTA does up to kRowsEach rows; what it costs is latency.
+// last CTA to have read the lengths (a counter in the workspace, 0 between
+// launches) writes what may be written in place: the lengths and the count.  One
+// CTA does up to kRowsEach rows; what it costs is latency.
 #include <algorithm>
 
 #include "paged.cuh"
@@ -145,6 +146,13 @@ __global__ void __launch_bounds__(THREADS) paged_step_kernel(const StepParams p,
         give[p.B] = static_cast<int>(all.give);
     }
     __syncthreads();
+    // (drawn as soon as the whole CTA has used the lengths and the count; the answer
+    // takes a while)
+    unsigned drawn = 0;
+    if (gridDim.x > 1 && tid == 0) {
+        __threadfence();
+        drawn = atomicAdd(p.ws + kStepTicket, 1u);
+    }
     const int N = good ? static_cast<int>(all.take) : 0, R = good ? static_cast<int>(all.give) : 0, rows = q_pre[p.B];
     auto after_of = [&](int b) {
         return max((keep_s[b] + q_pre[b + 1] - q_pre[b] + p.page_size - 1) >> p.page_shift, p.shared_pages);
@@ -171,18 +179,23 @@ __global__ void __launch_bounds__(THREADS) paged_step_kernel(const StepParams p,
          t0 += static_cast<long long>(threads) * kSlotRows) {
         long long slot[kSlotRows];
         int pos[kSlotRows];
-        int b = -1;
+        int b = -1, last = -1, id = -1;          // the entry of the row before, and its page
 #pragma unroll
         for (int e = 0; e < kSlotRows; ++e) {
             slot[e] = -1;
             pos[e] = 0;
             if (t0 + e >= rows) continue;
             const int t = static_cast<int>(t0) + e;
-            if (b < 0 || t >= q_pre[b + 1]) b = share_of(q_pre, p.B, t);
+            if (b < 0 || t >= q_pre[b + 1]) {
+                b = share_of(q_pre, p.B, t);
+                last = -1;
+            }
             pos[e] = keep_s[b] + (t - q_pre[b]);
             const int entry = pos[e] >> p.page_shift;
-            const int id = entry < before_s[b] ? p.page_table[static_cast<size_t>(b) * p.max_pages + entry]
-                                               : taken(take[b] + entry - before_s[b]);
+            if (entry != last)
+                id = entry < before_s[b] ? p.page_table[static_cast<size_t>(b) * p.max_pages + entry]
+                                         : taken(take[b] + entry - before_s[b]);
+            last = entry;
             if (id >= 0 && id < p.num_pages)
                 slot[e] = (static_cast<long long>(id) << p.page_shift) + (pos[e] & (p.page_size - 1));
             else
@@ -204,13 +217,11 @@ __global__ void __launch_bounds__(THREADS) paged_step_kernel(const StepParams p,
         }
     }
 
-    // who is last writes in place
-    __syncthreads();
+    // who was last to read writes in place
     if (gridDim.x > 1) {
         if (tid == 0) {
             __threadfence();
-            ticket = atomicAdd(p.ws + kStepTicket, 1u);
-            __threadfence();
+            ticket = drawn;
         }
         __syncthreads();
         if (ticket != gridDim.x - 1) return;
