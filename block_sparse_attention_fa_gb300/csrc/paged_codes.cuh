@@ -230,11 +230,7 @@ __device__ __forceinline__ void load_codes(const PagedScaledParams& p, const CUt
             ++nu;
         }
         const float2 scales_next = next.tiles > 0 ? scales_of(next) : make_float2(0.f, 0.f);
-        // (bits of numbers that are not negative are in their order)
-        largest = fmaxf(largest, __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(scales.y, 0.f)))));
-        float least = fmaxf(fmaxf(scales.y, largest * kLeastRatio), kLeastScale);
-        if (scales.y != scales.y) least = scales.y;
-        const float lv = log2f(least), iv = 1.f / least;
+        float lv = 0.f, iv = 0.f;
         for (int e = 0; e < now.tiles; ++e, ++g) {
             const int kb = now.s.hull.tile(now.k + e), st = g % ST;
             const bool here = mine == e;
@@ -256,7 +252,16 @@ __device__ __forceinline__ void load_codes(const PagedScaledParams& p, const CUt
             }
             last[st] = g;
             if (PART == kLoadV) continue;
-            // what else the consumers need of the tile, and only then the loader's arrival
+            // what else the consumers need of the tile, and only then the loader's
+            // arrival; the first copies do not wait for the scales
+            if (e == 0) {
+                // (bits of numbers that are not negative are in their order)
+                largest = fmaxf(largest, __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(scales.y, 0.f)))));
+                float least = fmaxf(fmaxf(scales.y, largest * kLeastRatio), kLeastScale);
+                if (scales.y != scales.y) least = scales.y;
+                lv = log2f(least);
+                iv = 1.f / least;
+            }
             float* const sc = reinterpret_cast<float*>(smem + L::kScale + st * L::kScaleStage);
             if (here) {
                 sc[at] = scales.x;

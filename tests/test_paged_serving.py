@@ -331,6 +331,34 @@ def test_what_a_cache_may_be(fa):  # noqa: F811
 
 
 @gpu
+@pytest.mark.parametrize("n,Hq", [(1, 2), (3, 8), (60, 4)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_pages_that_several_sequences_name(fa, n, Hq, D):  # noqa: F811
+    """A prefix read through every sequence's own row of the table."""
+    bt = Batch8([n, n, n], [n + 400, n + 330, n + 320], 2, D, 32, shared=320, kind="any")
+    bt.shared = 0
+    run8(fa, bt, Hq)
+
+
+@gpu
+@pytest.mark.parametrize("n,Hq", [(1, 2), (3, 8), (60, 4)])
+@pytest.mark.parametrize("shared", [0, 64])
+def test_bad_sequences_are_reported(fa, n, Hq, shared):  # noqa: F811
+    """More new tokens than max_q_len, a page that is not there: a status, and the others' rows as they should be."""
+    bt = Batch8([n, n + 1, n, n], [n + 100 + shared, n + 90 + shared, n + 80 + shared, n + 70 + shared], 2, 64, 16, shared=shared)
+    q = bt.queries(Hq)
+    dev, s = bt.device8()
+    dev[2][2, (bt.kv[2] - 1) // 16] = 1 << 30
+    o, lse = fa.fwd_paged(torch.from_numpy(q).cuda().to(torch.bfloat16), *dev, **s, max_q_len=n, shared_len=shared)
+    with pytest.raises(fa.FAError) as e:
+        fa.default_workspace("cuda").check()
+    assert e.value.status == fa.ERR_DEVICE_CHECK
+    ro, rl, A = reference(bt, q, "causal", 0, 0)
+    rl[bt.q_start[1]:bt.q_start[3]] = np.nan     # (not compared)
+    compare8((o, lse), (ro, rl, A), bt)
+
+
+@gpu
 def test_append_without_a_prompt_then_read_far_apart(fa):  # noqa: F811
     """An append of prompts of every length, then attention over just them."""
     new = [1, 15, 16, 17, 33, 200]
