@@ -189,14 +189,15 @@ __device__ __forceinline__ void load_codes(const PagedScaledParams& p, const CUt
         return PART != kLoadV && b.id >= 0 ? make_float2(p.k_scale[x], p.v_scale[x]) : make_float2(0.f, 0.f);
     };
     int g = 0, nu = 0;
-    bool ok = true, marked = false;
+    bool ok = true, marked = false, first = true;
     Batch now, next{};
-    next_batch(next);
-    now = next;
-    float2 scales = now.tiles > 0 ? scales_of(now) : make_float2(0.f, 0.f);
+    float2 scales, scales_next{};
     float largest = 0.f;                           // of v's scales in the unit
     next_batch(next);
-    for (;;) {
+    for (;; first = false) {
+        now = next;
+        scales = scales_next;
+        next_batch(next);
         const bool fresh = now.tiles == 0 || now.k == now.s.k0;
         if (PART == kLoadV) {
             if (now.tiles == 0) break;
@@ -229,7 +230,9 @@ __device__ __forceinline__ void load_codes(const PagedScaledParams& p, const CUt
             }
             ++nu;
         }
-        const float2 scales_next = next.tiles > 0 ? scales_of(next) : make_float2(0.f, 0.f);
+        // (the first batch's scales need its page ids, which Q does not wait for)
+        if (first) scales = scales_of(now);
+        scales_next = scales_of(next);
         float lv = 0.f, iv = 0.f;
         for (int e = 0; e < now.tiles; ++e, ++g) {
             const int kb = now.s.hull.tile(now.k + e), st = g % ST;
@@ -277,9 +280,6 @@ __device__ __forceinline__ void load_codes(const PagedScaledParams& p, const CUt
             if (lane == 0) mbar_arrive(full_bar(st));
         }
         if (!ok) break;
-        now = next;
-        scales = scales_next;
-        next_batch(next);
     }
     // every issued copy lands before the CTA exits
     if (lane == 0) {
