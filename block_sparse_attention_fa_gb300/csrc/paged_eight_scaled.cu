@@ -29,11 +29,12 @@
 // scales.  The maximum is raised (and O and l rescaled) only when a score is 2^8
 // past it, which one vote of the warp tells.
 //
-// Two warps load (paged_codes.cuh); their issue of pages of 16 keys bounds ragged
-// batches, DRAM the long ones.  8 sequences of 32768 tokens, 8 kv heads of 128
-// columns: 90.4 us, 79.1 at the copy rate (bf16 cache: 163).  128 of up to 4096, 8
-// kv heads of 64 columns, pages of 16: 76.6 us, 41.0 at the copy rate.  One of 520
-// tokens: 9.9.
+// DRAM bounds long contexts; ragged batches on pages of 16 keys the chain of a tile
+// in each warp, some 1800 cycles of 2500, and the two loader warps' issue
+// (paged_codes.cuh), evenly.  8 sequences of 32768 tokens, 8 kv heads of 128
+// columns: 89.7 us, 79.1 at the copy rate (bf16 cache: 163).  128 of up to 4096, 8
+// kv heads of 64 columns, pages of 16: 75.3 us, 41.0 at the copy rate.  One of 520
+// tokens: 9.6, most of it the first run through the code.
 //
 // V rows of keys that no row of the unit sees are cleared in shared memory before
 // the product: their P is 0, but 0 x NaN is not.
