@@ -17,7 +17,12 @@
 // the table, or from the stack by the same formula, never from another CTA.  The
 // last CTA to have read the lengths (a counter in the workspace, 0 between
 // launches) writes what may be written in place: the lengths and the count.  One
-// CTA does up to kRowsEach rows; what it costs is latency.
+// CTA does up to kRowsEach rows.
+//
+// What it costs is latency, load after load: 5.1 us for 64 sequences with a token
+// each, 8.1 for 256 with 61000 rows, 13.0 for 512 with 1.2 million (2.1 for their 14
+// MB at the copy rate).  The ticket is drawn as soon as the lengths are read: at
+// the end it took 1 and 2 us more.
 #include <algorithm>
 
 #include "paged.cuh"
