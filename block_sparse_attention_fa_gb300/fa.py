@@ -706,11 +706,16 @@ def _paged_kv(k_cache, v_cache, page_table, kv_len, q_start, total_q, dev, scale
             or k_cache.get_device() != dev or v_cache.get_device() != dev:
         raise ValueError("k_cache and v_cache must be contiguous CUDA bf16 tensors [num_pages, Hkv, page_size, D] "
                          "on the rows' device (float8_e4m3fn where k_scale and v_scale are given)")
-    for name, t, dims in (("page_table", page_table, 2), ("kv_len", kv_len, 1), ("q_start", q_start, 1)):
-        if t.dtype is not torch.int32 or t.dim() != dims or t.get_device() != dev or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous int32 tensor of {dims} dimensions on the rows' device")
-    B, max_pages = page_table.shape
-    if kv_len.numel() != B or q_start.numel() != B + 1:
+    i32, table, lens, starts = torch.int32, page_table.shape, kv_len.shape, q_start.shape
+    if len(table) != 2 or len(lens) != 1 or len(starts) != 1 \
+            or page_table.dtype is not i32 or kv_len.dtype is not i32 or q_start.dtype is not i32 \
+            or page_table.get_device() != dev or kv_len.get_device() != dev or q_start.get_device() != dev \
+            or not page_table.is_contiguous() or not kv_len.is_contiguous() or not q_start.is_contiguous():
+        for name, t, dims in (("page_table", page_table, 2), ("kv_len", kv_len, 1), ("q_start", q_start, 1)):
+            if t.dtype is not i32 or t.dim() != dims or t.get_device() != dev or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous int32 tensor of {dims} dimensions on the rows' device")
+    B, max_pages = table
+    if lens[0] != B or starts[0] != B + 1:
         raise ValueError(f"page_table has {B} rows: kv_len must hold {B} lengths and q_start {B + 1} offsets "
                          f"(got {kv_len.numel()}, {q_start.numel()})")
     num_pages, Hkv, page, D = shape
@@ -722,12 +727,12 @@ def _scales(k_scale, v_scale, k_cache, dev):
     """The packed fa_paged_scales; None for a cache without scales (bf16)."""
     if k_scale is None and v_scale is None:
         return None
-    want = k_cache.shape[:2]
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        if t is None or t.dtype is not torch.float32 or t.shape != want or t.get_device() != dev \
-                or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous float32 tensor [num_pages, Hkv] = {tuple(want)} on the "
-                             "cache's device (k_scale and v_scale come together)")
+    want, f32 = k_cache.shape[:2], torch.float32
+    if k_scale is None or v_scale is None or k_scale.dtype is not f32 or v_scale.dtype is not f32 \
+            or k_scale.shape != want or v_scale.shape != want or k_scale.get_device() != dev \
+            or v_scale.get_device() != dev or not k_scale.is_contiguous() or not v_scale.is_contiguous():
+        raise ValueError(f"k_scale and v_scale come together: contiguous float32 tensors [num_pages, Hkv] = {tuple(want)} "
+                         "on the cache's device")
     return _PAGED_SCALES.pack(k_scale.data_ptr(), v_scale.data_ptr())
 
 
