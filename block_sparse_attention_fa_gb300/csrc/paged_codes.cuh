@@ -19,10 +19,6 @@ static_assert(kKeys == 1 << kShift, "keys of a tile");
 constexpr int kSegs = 4;
 // Entries of the line's index: fewer than the bf16 kernel has room for.
 constexpr int kCodeEntries = 300;
-// v's scales as exponents (log2 and reciprocal): one below 2^-80 of the largest so
-// far in the unit, or below 2^-90, counts as that (l, a sum of P / scale with P up to
-// 2^8, holds 2^30 keys of it).
-constexpr float kLeastRatio = 8.271806125530277e-25f, kLeastScale = 8.077935669463161e-28f;
 enum CodeSite : uint32_t { S_PC_FULL = 112, S_PC_EMPTY, S_PC_DRAIN, S_PC_Q, S_PC_Q_EMPTY };
 
 // Shared memory of such a kernel: the ring of tiles, `EXTRA` bytes of the

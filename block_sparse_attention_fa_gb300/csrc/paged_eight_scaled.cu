@@ -21,13 +21,14 @@
 //     are the product's rows 0-7, the odd ones 8-15.
 // A code is converted once, to f16, which holds it exactly; so does it a row of Q
 // scaled by a power of two, and P is rounded to f16's 11 bits.  k's scale is applied
-// to S in fp32.  v's is part of P's exponent: with x the score in base 2 and
-// lv = log2(v's scale), one for 16 keys (of a page), M the running maximum of x + lv,
+// to S in fp32.  v's is part of P's exponent: with x the score in base 2,
+// lv = log2(v's scale), one for 16 keys (of a page), and M a reference below the
+// largest x + lv (kPHead),
 //     P = 2^(x + lv - M),   l = sum of P / (v's scale),
 // so that O accumulates in the products, P's roundings are relative to the largest
 // share that any key has in O, and O / l and M + log2 l are what they are without
-// scales.  The maximum is raised (and O and l rescaled) only when a score is 2^8
-// past it, which one vote of the warp tells.
+// scales.  M is raised (and O and l rescaled) only when an x + lv is past it by kPTop,
+// which one vote of the warp tells.
 //
 // DRAM bounds long contexts; ragged batches on pages of 16 keys the chain of a tile
 // in each warp, some 1800 cycles of 2500, and the two loader warps' issue
@@ -45,7 +46,6 @@ namespace {
 
 constexpr int kWarps = 4;                        // consumers, 32 keys each; warps 4 and 5 load
 constexpr int kRows = 8;
-constexpr float kLazyMax = 8.f;
 static_assert(kKeys == 32 * kWarps, "32 keys to a warp");
 
 // Beside the ring and the queues: two warps' O, every warp's [rows] maximum and sum.
@@ -254,14 +254,15 @@ paged_eight_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
                 }
             }
             const float top[2] = {fmaxf(fmax3(x[0][0], x[0][2], x[1][0]), x[1][2]), fmaxf(fmax3(x[0][1], x[0][3], x[1][1]), x[1][3])};
-            if (__any_sync(0xffffffffu, top[0] > m[0] + kLazyMax || top[1] > m[1] + kLazyMax)) {
+            if (__any_sync(0xffffffffu, top[0] > m[0] + kPTop || top[1] > m[1] + kPTop)) {
                 float alpha[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float to = fmaxf(top[e], m[e]);
+                    float to = top[e];
                     to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, 4));
                     to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, 8));
                     to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, 16));
+                    to = fmaxf(to - kPHead, m[e]);
                     alpha[e] = to == m[e] ? 1.f : ex2_approx(m[e] - to);
                     m[e] = to;
                     l[e] *= alpha[e];

@@ -34,6 +34,20 @@ struct StepParams {
 // columns, where 32 would be 256 keys).
 constexpr int kPagedSmallScaledKeys = 128;
 
+// P over codes is an f16 operand, whose numbers end at 2^16, lose bits below 2^-14 and
+// are 0 below 2^-25.  So P is 2^(x - M) with a reference M that lies below the largest
+// x: by kPHead when M is set, and M is raised once an x is past it by kPTop.  A key down
+// to 2^-(kPHead + 14) of the largest keeps 11 bits, and 2^-(kPHead + 25) of it is what
+// is lost below.  (l and M leave out nothing: O / l and M + log2 l are the same
+// with any M.)  A larger head means more rescales: 4 chunks of up to 1024 tokens on up
+// to 8192 keys 219.4 us with 7, 220.3 with 8 (as with a reference at the maximum that
+// is raised by 2^8), 221.9 with 9 and 226.4 with 11; single tokens the same with all.
+constexpr float kPTop = 15.f, kPHead = 8.f;
+// v's scales as exponents (log2 and reciprocal): one below 2^-80 of the largest so
+// far in the unit, or below 2^-82, counts as that (l, a sum of P / scale with P up to
+// 2^kPTop, holds 2^30 keys of it).
+constexpr float kLeastRatio = 8.271806125530277e-25f, kLeastScale = 2.0679515313825692e-25f;
+
 cudaError_t launch_kv_append_scaled(const AppendScaledParams& p, cudaStream_t s);
 cudaError_t launch_paged_step(const StepParams& p, cudaStream_t s);
 cudaError_t launch_paged_small_scaled(const PagedScaledParams& p, const CUtensorMap& tk, const CUtensorMap& tv,

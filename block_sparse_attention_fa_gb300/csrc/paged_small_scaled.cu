@@ -5,10 +5,11 @@
 //
 // What differs from paged_small.cu.  The codes come into shared memory as they are
 // and are converted in registers, each once per CTA, to f16, which holds them
-// exactly; so does it a row of Q scaled by a power of two, and P, at most 1, is
-// rounded to f16's 11 bits instead of bf16's 8.  Products and sums are fp32's, k's
-// scale is applied to S and v's to the product of 16 keys, which are of one page:
-// any scales will do.
+// exactly; so does it a row of Q scaled by a power of two, and P, at most 2^15 (kPTop),
+// is rounded to f16's 11 bits instead of bf16's 8.  Products and sums are fp32's, k's
+// scale is applied to S and v's, with P's 2^15 taken out again, to the product of 16
+// keys, which are of one page: any scales will do (below 2^-111 a v scale with the
+// 2^-15 is a subnormal number, and keeps 8 bits down to 2^-126).
 //
 // A thread's 32 bits of a row of codes are four adjacent columns where a matrix
 // product's operand has two and two: K's columns go to the product in another
@@ -29,6 +30,7 @@ namespace {
 constexpr int kWarps = 8;                        // consumers; warp 8 loads
 constexpr int kRows = kPagedSmallRows;
 static_assert(kKeys == 16 * kWarps, "16 keys to a warp");
+constexpr float kPDown = 1.f / 32768.f;          // 2^-kPTop
 
 // Beside the ring and the queues: P, and every warp's [rows] maximum and sum.
 constexpr uint32_t kPRow = 2u * kKeys + 16u;     // 16 bytes of padding: rows on distinct banks
@@ -276,7 +278,7 @@ paged_small_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
                 const float m_new = fmaxf(fmaxf(fmaxf(fmaxf(a.x, a.y), fmaxf(a.z, a.w)),
                                                 fmaxf(fmaxf(b.x, b.y), fmaxf(b.z, b.w))), m[e]);
                 alpha[e] = m_new == m[e] ? 1.f : ex2_approx(m[e] - m_new);
-                const float nm = m_new == -CUDART_INF_F ? 0.f : -m_new;
+                const float nm = m_new == -CUDART_INF_F ? 0.f : kPTop - m_new;
                 m[e] = m_new;
                 l[e] *= alpha[e];
 #pragma unroll
@@ -308,7 +310,7 @@ paged_small_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
                 for (int e = 0; e < 2; ++e) {
                     uint32_t pa[4];
                     ldsm4(p_row + 32 * (ks + e), pa);
-                    const float v_scale = sc[kKeys / 16 + (16 * (ks + e) >> by_page)];
+                    const float v_scale = sc[kKeys / 16 + (16 * (ks + e) >> by_page)] * kPDown;
                     float y[4];
                     mma_f16_from_0(y, pa, lo[2 * e], lo[2 * e + 1]);
 #pragma unroll
@@ -331,7 +333,7 @@ paged_small_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
         for (int e = 0; e < 2; ++e) {
             l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
             l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
-            if (tq == 0) ssum[(gr + 8 * e) * kWarps + warp] = l[e];
+            if (tq == 0) ssum[(gr + 8 * e) * kWarps + warp] = l[e] * kPDown;
         }
         consumers_sync();
         const bool whole = s.begins() && s.ends();

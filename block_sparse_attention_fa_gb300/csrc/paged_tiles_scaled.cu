@@ -17,15 +17,15 @@
 // P V keeps P at 11 bits, in f16.  V's codes become f16, which holds them exactly:
 // four more warps (12-15) convert 64-key halves from a ring of codes to one of
 // operands.  v's scales cannot stay out of P, for a product adds up keys of many
-// pages: with x the score in base 2, lv = log2(v's scale) and M the running maximum
-// of x + lv,
+// pages: with x the score in base 2, lv = log2(v's scale) and M a reference below the
+// largest x + lv (kPHead, or with fp32 output kPTop),
 //     P = 2^(x + lv - M),   l = sum of P / (v's scale),
-// so that P is at most 1 (2^8 before M is raised), its roundings are relative to
-// the largest share that any key has in O, and one exponential serves both sums;
-// O / l and M + log2 l are what they are without scales.  The scale is the same for
-// 16 columns (of one page).  A scale below 2^-80 of the largest so far in the unit,
-// or below 2^-90, counts as that: what such a page adds to O is nothing beside the
-// others, and l keeps all of its keys.  k's scale and the row's stay with S.
+// so that P is at most 2^kPTop, its roundings are relative to the largest share that
+// any key has in O, and one exponential serves both sums; O / l and M + log2 l are
+// what they are without scales.  The scale is the same for 16 columns (of one page).
+// A scale below 2^-80 of the largest so far in the unit, or below 2^-82, counts as
+// that: what such a page adds to O is nothing beside the others, and l keeps all of
+// its keys.  k's scale and the row's stay with S.
 //
 // What bounds it is the chain of a 64-key half, 1500 to 1700 cycles of softmax
 // alone: 4 chunks of up to 1024 tokens on up to 8192 keys, 32 heads on 8 of 128
@@ -47,9 +47,6 @@ constexpr int kThreads8 = 512;
 // build.py checks the launch count.
 constexpr uint32_t kRegsSoftmax8 = 184, kRegsOther8 = 88, kRegsConvert8 = 56;
 static_assert(2 * kRegsSoftmax8 + kRegsOther8 + kRegsConvert8 == 4 * 128, "register split must match the launch");
-constexpr float kLazyMax8 = 8.f;               // (0 with fp32 output)
-constexpr float kLeastRatio = 8.271806125530277e-25f;      // 2^-80
-constexpr float kLeastScale = 8.077935669463161e-28f;      // 2^-90
 constexpr int kMaxRing8 = 4;
 // Tiles whose scales are kept.  K(g) is loaded once S of tile g - stages is done,
 // which came after P of the tile before that: the loader is at most five tiles
@@ -561,7 +558,7 @@ paged_tiles_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
         const float sl2 = p.scale * kPagedLog2e;
         const SoftCap cap = soft_cap(p.score.softcap, SCORE == FA_SCORE_SOFTCAP ? p.scale : 1.f);
         const bool out32 = (p.flags & FA_OUT_FP32) != 0;
-        const float lazy = out32 ? 0.f : kLazyMax8;
+        const float head = out32 ? kPTop : kPHead;
         uint32_t n = 0, uq = 0, g = 0;                 // g: tiles of all units
         bool ok = true;
         PagedMeta meta{};
@@ -755,7 +752,7 @@ paged_tiles_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
                                 for (int e = 0; e < 32; ++e) x[32 * c + e] = (see >> e) & 1u ? x[32 * c + e] : -CUDART_INF_F;
                             }
                         }
-                        float m_new = m;
+                        float top = -CUDART_INF_F;
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
                             const float* const y = x + 16 * c;
@@ -764,13 +761,13 @@ paged_tiles_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
                             b = fmax3(b, y[8], y[9]);
                             a = fmax3(a, y[10], y[11]);
                             b = fmax3(b, y[12], y[13]);
-                            m_new = fmaxf(m_new, fmaf(fmax3(fmaxf(a, b), y[14], y[15]), sc[c], lv[c]));
+                            top = fmaxf(top, fmaf(fmax3(fmaxf(a, b), y[14], y[15]), sc[c], lv[c]));
                         }
                         const bool unset = m == -CUDART_INF_F;
-                        const bool need = !unset && m_new > m + lazy;
-                        const float alpha = need ? ex2_approx(m - m_new) : 1.f;
+                        const bool need = !unset && top > m + kPTop;
+                        const float to = top - head, alpha = need ? ex2_approx(m - to) : 1.f;
                         if (need) l *= alpha;
-                        if (unset || need) m = m_new;
+                        if (unset || need) m = to;
                         const float m0 = m == -CUDART_INF_F ? 0.f : m;
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {

@@ -197,9 +197,12 @@ fa_status fa_kv_append_scaled(const fa_paged_kv *c, const fa_paged_scales *scale
  * that the codes stand for.  Scales, sums and products are fp32's; a query's
  * elements keep their 8 bits down to 2^-10 of the row's largest, and an absolute
  * error of 2^-18 of that below (where more than 16 rows go per sequence and kv
- * head; exactly otherwise); P is rounded to 11 significant bits.  Except for 9 to
+ * head; exactly otherwise); P is rounded to 11 significant bits where a key's
+ * share in o (its probability times its page's v scale) is at least 2^-22 of the
+ * row's largest, and by up to 2^-33 of that largest below; for 9 to 16 rows that
+ * goes by the probability alone, and holds to 2^-29 and 2^-40.  Except for 9 to
  * 16 rows, a v scale below 2^-80 of the largest one that the rows have seen, or
- * below 2^-90, counts as that.
+ * below 2^-82, counts as that.
  * scratch: fa_paged_scratch_bytes().                                        */
 fa_status fa_fwd_paged_scaled(const fa_paged_kv *c, const fa_paged_scales *scales, const fa_paged_fwd_args *a,
                               const fa_mask_desc *mask, const fa_score_desc *sc, void *scratch, size_t scratch_bytes,

@@ -1,0 +1,151 @@
+"""What the cache held in 8 bits keeps of small shares: keys far below the largest
+score, pages whose scales are far apart, sums over keys whose scales grow.
+
+A key's share is 2^(its score in base 2) x (its page's v scale): what it adds to O,
+for a code of 1.  The scores here are products of few bits (one element of q and k
+is not 0), so that they are exact but for the fp32 scales: at most 8 roundings of
+2^-24 on numbers below 256, 2^-13 in the exponent, and ex2.approx's 2^-22.
+
+Tolerances, per column.  P is rounded to f16 at up to 2^15, and its reference lies
+at least 2^8 of that below the largest share (where P takes v's scale with it), or 2^15
+below the largest 2^score (9 to 16 rows, where it does not): half a step is 2^-11 of
+the share, or, of the largest, 2^-25 / 2^8 = 2^-33 (2^-25 / 2^15 = 2^-40, times the
+key's own v scale).  With w the exact weights and c the codes
+     |O - exact| <= sum_j max(2^-11 share_j, floor_j) |c_j| / sum 2^score + 2^-12 sum_j w_j |v_j|,
+the last for the exponent (2^-13 ln 2) and for fp32 sums (chains of at most 300 parts
+and 64 products: 2^-15).  lse: 2^-13 ln 2 and 2^-15 of its sum.
+"""
+import functools
+
+import numpy as np
+import pytest
+import torch
+
+from tests.test_paged import fa  # noqa: F401  (the fixture)
+from tests.test_paged_scaled import codes_of, e4m3
+
+gpu = pytest.mark.gpu
+PAGE = 64
+
+
+@functools.lru_cache(4)
+def uniform_codes(seed, shape):
+    return e4m3(np.random.default_rng(seed).uniform(-0.2, 1.0, shape) * 448)
+
+
+def codes(seed, shape):
+    """e4m3 numbers, most of them of the last binades, with a mean that is not 0."""
+    return uniform_codes(seed, shape).copy()
+
+
+class Keys:
+    """B sequences of n keys each of one kv head, a page after the other; scores[j] = k_codes[j] k_scale q0 / 16."""
+
+    def __init__(self, B, k_code, k_scale, v_code, v_scale, D):
+        # k_code [n], k_scale and v_scale [pages], v_code [n, D]: the same for every sequence
+        self.B, self.D, self.n = B, D, len(k_code)
+        pages = self.n // PAGE
+        assert pages * PAGE == self.n
+        self.k_code, self.k_scale, self.v_code, self.v_scale = k_code, k_scale.astype(np.float32), v_code, v_scale.astype(np.float32)
+        k = np.zeros((pages, 1, PAGE, D))
+        k[:, 0, :, 0] = k_code.reshape(pages, PAGE)
+        each = lambda x: torch.cat([x] * B)     # noqa: E731
+        self.kc = each(codes_of(k).cuda().view(torch.uint8)).view(torch.float8_e4m3fn)
+        self.vc = each(codes_of(v_code.reshape(pages, 1, PAGE, D)).cuda().view(torch.uint8)).view(torch.float8_e4m3fn)
+        s = lambda x: each(torch.from_numpy(x.astype(np.float32)).cuda()[:, None]).contiguous()     # noqa: E731
+        self.scales = dict(k_scale=s(k_scale), v_scale=s(v_scale))
+        self.table = torch.arange(B * pages, dtype=torch.int32, device="cuda").view(B, pages)
+        self.kv = torch.full((B,), self.n, dtype=torch.int32, device="cuda")
+
+    def run(self, fa, rows, shared=0, out_fp32=True):  # noqa: F811
+        """`rows` query heads of one token per sequence (n = 1), q0 a little more from row to row."""
+        q0 = 16 + np.arange(rows) * 0.125
+        q = torch.zeros((self.B, rows, self.D), dtype=torch.bfloat16, device="cuda")
+        q[..., 0] = torch.from_numpy(q0).cuda().to(torch.bfloat16)
+        starts = torch.arange(self.B + 1, dtype=torch.int32, device="cuda")
+        table = self.table
+        if shared:
+            table = table.clone()
+            table[:, :shared // PAGE] = self.table[0, :shared // PAGE]
+        o, lse = fa.fwd_paged(q, self.kc, self.vc, table, self.kv, starts, **self.scales, max_q_len=1, mask="full",
+                              shared_len=shared, scale=1 / 16, out_fp32=out_fp32)
+        fa.default_workspace("cuda").check()
+        return o.double().cpu().numpy(), lse.double().cpu().numpy(), q0
+
+    def check(self, got, rows, few, bf16_out=False):
+        """few: P without v's scale (9 to 16 rows and no prefix)."""
+        o, lse, q0 = got
+        assert np.isfinite(o).all() and np.isfinite(lse).all()
+        ks, vs = (np.repeat(x.astype(np.float64), PAGE) for x in (self.k_scale, self.v_scale))
+        for r in range(rows):
+            score = q0[r] / 16 * self.k_code * ks
+            p = np.exp(score - score.max())
+            total = p.sum()
+            share = p * vs
+            floor = 2.0 ** -40 * vs if few else 2.0 ** -33 * share.max()
+            if 8 < rows <= 16:                   # (a prefix's part of the keys, and the others)
+                floor = np.maximum(floor, 2.0 ** -40 * vs)
+            ro, A = (p * vs) @ self.v_code / total, (p * vs) @ np.abs(self.v_code) / total
+            tol = np.maximum(2.0 ** -11 * share, floor) @ np.abs(self.v_code) / total + 2.0 ** -12 * A
+            if bf16_out:
+                tol = tol + 2.0 ** -8 * np.abs(ro)
+            err = np.abs(o[:, r] - ro)
+            assert (err <= tol).all(), f"row {r}: o off by {np.nanmax(err / np.maximum(tol, 1e-300)):.2f} of what it may"
+            rl = np.log(total) + score.max()
+            assert np.abs(lse[:, r] - rl).max() <= 2.0 ** -13, f"row {r}: lse off by {np.abs(lse[:, r] - rl).max()}"
+
+
+# rows per kv head, and what a prefix of half the keys makes of them: every kernel
+KERNELS = [(4, False), (12, False), (40, False), (4, True), (12, True), (40, True)]
+
+
+def few(rows, shared):
+    return 8 < rows <= 16 and not shared
+
+
+@gpu
+@pytest.mark.parametrize("rows,prefix", KERNELS)
+@pytest.mark.parametrize("nats", [17, 18, 20])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("first", [True, False])
+@pytest.mark.parametrize("B,n", [(1, 1 << 15), (300, 1 << 12)])
+def test_a_sink_of_small_value(fa, rows, prefix, nats, D, first, B, n):  # noqa: F811
+    """One key with a value of 0 far above all others, which are all of O (one sequence: over all CTAs, a part of it
+    to each; many: a sequence or so to each)."""
+    k = np.full(n, -256.0)
+    v = codes(1, (n, D))
+    sink = 5 if first else n - 3
+    k[sink], v[sink] = 0.0, 0.0
+    r = np.random.default_rng(nats)
+    bt = Keys(B, k, nats / 256.0 * r.uniform(0.98, 1.0, n // PAGE), v, 2.0 ** -9 * r.uniform(0.7, 1.4, n // PAGE), D)
+    shared = n // 2 if prefix else 0
+    bt.check(bt.run(fa, rows, shared), rows, few(rows, prefix))
+
+
+@gpu
+@pytest.mark.parametrize("rows,prefix", KERNELS)
+@pytest.mark.parametrize("apart", [12, 20, 24, 30])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("B", [1, 40])
+def test_columns_that_only_small_pages_have(fa, rows, prefix, apart, D, B):  # noqa: F811
+    """Pages whose v scales are 2^apart of the others', which are 0 in the even columns."""
+    n = 2048
+    r = np.random.default_rng(apart)
+    large = r.permutation(n // PAGE) < 8
+    v = codes(2, (n, D))
+    v[np.repeat(large, PAGE)[:, None] & (np.arange(D) % 2 == 0)] = 0.0
+    bt = Keys(B, e4m3(r.uniform(-40, 0, n)), r.uniform(0.02, 0.03, n // PAGE), v,
+              np.where(large, 1.0, 2.0 ** -apart) * r.uniform(0.7, 1.0, n // PAGE), D)
+    bt.check(bt.run(fa, rows, n // 2 if prefix else 0), rows, few(rows, prefix))
+
+
+@gpu
+@pytest.mark.parametrize("rows,prefix", KERNELS)
+@pytest.mark.parametrize("D", [64, 128])
+def test_the_same_in_bf16(fa, rows, prefix, D):  # noqa: F811
+    """As above with an output of 16 bits, where the running maximum may be passed."""
+    n, r = 4096, np.random.default_rng(3)
+    k = e4m3(-256 * r.uniform(0, 1, n))
+    bt = Keys(3, np.sort(k), np.full(n // PAGE, 20 / 256.0), codes(5, (n, D)),
+              2.0 ** r.integers(-20, 1, n // PAGE), D)
+    bt.check(bt.run(fa, rows, n // 2 if prefix else 0, out_fp32=False), rows, few(rows, prefix), bf16_out=True)
