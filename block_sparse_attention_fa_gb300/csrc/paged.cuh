@@ -201,6 +201,25 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, 
         : "memory");
 }
 
+// With v's scales in M (a cache held in 8 bits) l may be 2^80 before a scale of 2^100
+// comes, so that 2^d, by which M's step multiplies l, is less than an fp32 number while
+// l 2^d counts: l times it in two steps.
+__device__ __forceinline__ float times_2_to(float l, float d) {
+    const float half = ex2_approx(0.5f * d);
+    return l * half * half;
+}
+// Nor may such an M weigh parts of a row that are to be joined: l and M times powers of
+// two (and O by what is returned), so that l is 2^-17 to 2^-16 and M says what the part
+// is worth.  (O is then 2^-16 of a value at most, so that no sum of parts overflows.)
+__device__ __forceinline__ float even_out(float& m, float& l) {
+    if (l == 0.f) return 1.f;
+    const int k = min(((__float_as_int(l) >> 23) & 255) - 127, 109);
+    const float f = __int_as_float((110 - k) << 23);
+    m += static_cast<float>(k + 17);
+    l *= f;
+    return f;
+}
+
 // Where a row's partials lie: `count` rows of a kernel's slots, from `first`
 // on: slots 2 c + 1, 2 (c + 1), 2 (c + 2), .. of `stride` rows each (or the
 // one partial that is kept by row).

@@ -264,8 +264,8 @@ paged_eight_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
                     to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, 16));
                     to = fmaxf(to - kPHead, m[e]);
                     alpha[e] = to == m[e] ? 1.f : ex2_approx(m[e] - to);
+                    l[e] = alpha[e] == 0.f ? times_2_to(l[e], m[e] - to) : l[e] * alpha[e];
                     m[e] = to;
-                    l[e] *= alpha[e];
                 }
 #pragma unroll
                 for (int c = 0; c < kChunks; ++c) {
@@ -331,7 +331,7 @@ paged_eight_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
                 const float2 t = ml_s[w * L::kRows + 2 * tq + e];
-                sum[e] = fmaf(t.y, ex2_approx(t.x - ref), sum[e]);
+                sum[e] += times_2_to(t.y, t.x - ref);
             }
             const float f = ex2_approx(m[e] - ref);
             m[e] = top;
@@ -372,7 +372,7 @@ paged_eight_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
                 const long long row = (long long)(s.q0 + at) * p.Hq + s.h * p.group + r - at * p.group;
                 const bool last = whole && !p.join_rows;
                 const long long slot = whole ? row : (2LL * cta + (s.begins() ? 1 : 0)) * kPagedSmallRows + r;
-                const float inv = !last ? 1.f : sum[e] == 0.f ? 0.f : 1.f / sum[e];      // a NaN stays one
+                const float inv = !last ? even_out(m[e], sum[e]) : sum[e] == 0.f ? 0.f : 1.f / sum[e];      // a NaN stays one
                 if (last && !(p.flags & FA_OUT_FP32)) {
                     uint16_t* const dst = static_cast<uint16_t*>(p.o) + row * D + 2 * gr;
 #pragma unroll

@@ -603,7 +603,7 @@ paged_tiles_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
                 uint8_t* const dst = static_cast<uint8_t*>(last ? p.o : static_cast<void*>(whole ? p.parts.row_o : p.parts.slot_o)) +
                                      at * (D * (f32 ? 4 : 2));
                 const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31u) == 0;
-                const float inv = !last ? 1.f : l == 0.f ? 0.f : 1.f / l;
+                const float inv = !last ? even_out(m, l) : l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t o[32];
@@ -765,8 +765,15 @@ paged_tiles_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
                         }
                         const bool unset = m == -CUDART_INF_F;
                         const bool need = !unset && top > m + kPTop;
-                        const float to = top - head, alpha = need ? ex2_approx(m - to) : 1.f;
-                        if (need) l *= alpha;
+                        const bool raise = __any_sync(0xffffffffu, need);
+                        const float to = top - head;
+                        float alpha = 1.f;
+                        if (raise) {
+                            // (in two steps: see times_2_to)
+                            const float half = need ? ex2_approx(0.5f * (m - to)) : 1.f;
+                            alpha = half * half;
+                            l = l * half * half;
+                        }
                         if (unset || need) m = to;
                         const float m0 = m == -CUDART_INF_F ? 0.f : m;
 #pragma unroll
@@ -791,7 +798,7 @@ paged_tiles_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
                         }
                         // O holds the products of the unit's earlier halves; wait
                         // for the last of them and scale
-                        if (__any_sync(0xffffffffu, need)) {
+                        if (raise) {
                             const uint32_t prev = 2 * n + h - 1;
                             if (!mbar_wait_warp(bar(T_O_UPD + t), prev & 1, wc, S_T_UPD)) { ok = false; break; }
                             tc_fence_after();

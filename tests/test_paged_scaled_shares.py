@@ -149,3 +149,19 @@ def test_the_same_in_bf16(fa, rows, prefix, D):  # noqa: F811
     bt = Keys(3, np.sort(k), np.full(n // PAGE, 20 / 256.0), codes(5, (n, D)),
               2.0 ** r.integers(-20, 1, n // PAGE), D)
     bt.check(bt.run(fa, rows, n // 2 if prefix else 0, out_fp32=False), rows, few(rows, prefix), bf16_out=True)
+
+
+@gpu
+@pytest.mark.parametrize("rows,prefix", KERNELS)
+@pytest.mark.parametrize("small,large", [(0.0, 2.0 ** 20), (0.0, 2.0 ** 100), (2.0 ** -100, 2.0 ** 60), (2.0 ** -60, 2.0 ** 100)])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("B,n", [(1, 256), (1, 8192), (160, 512)])
+@pytest.mark.parametrize("order", ["grow", "shrink", "mixed"])
+def test_scales_that_grow(fa, rows, prefix, small, large, D, B, n, order):  # noqa: F811
+    """Pages with v scales of 0 or nearly that, then large ones: lse is that of all keys, and O over it."""
+    r = np.random.default_rng(n)
+    at = np.arange(n // PAGE) < n // PAGE // 2
+    at = {"grow": at, "shrink": ~at, "mixed": r.permutation(at)}[order]
+    bt = Keys(B, e4m3(r.uniform(-40, 0, n)), r.uniform(0.02, 0.03, n // PAGE), codes(4, (n, D)),
+              np.where(at, small, large * r.uniform(0.7, 1.0, n // PAGE)), D)
+    bt.check(bt.run(fa, rows, n // 2 if prefix else 0), rows, few(rows, prefix))
