@@ -314,6 +314,11 @@ kv_append_scaled_kernel(const AppendParams q, const AppendScaledParams p, int q_
     const int parts = (p.c.Hkv + heads - 1) / heads;
     const int u = at / parts;
     append_page<D>(p, u, (at - u * parts) * heads, threads_per_head, at == 0);
+    // the first of these CTAs reports: its unit was found among the first sequences, the
+    // others have not been looked at (after the unit: 2048 sequences are eight loads more)
+    if (at == 0) {
+        for (int b = kAppendThreads + threadIdx.x; b < p.c.B; b += kAppendThreads) seq_info(p.c, b, INT_MAX, 0, p.ws);
+    }
 }
 
 }  // namespace
