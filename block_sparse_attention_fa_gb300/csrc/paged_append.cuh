@@ -46,7 +46,8 @@ struct Place {
     size_t kv_row;
 };
 
-// One warp finds the place of row t.
+// One warp finds the place of row t.  (Its numbers may have been written by the kernel
+// before this one, a step say, while this one had started: plain loads.)
 __device__ __forceinline__ Place place_of(const AppendParams& p, int t, int lane) {
     Place none{-1, 0};
     // the sequence of row t: how many of q_start[1 ..] are <= t
@@ -54,7 +55,7 @@ __device__ __forceinline__ Place place_of(const AppendParams& p, int t, int lane
     for (int b0 = 0; b0 < p.c.B; b0 += 128) {
         int ends[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) ends[k] = __ldg(p.c.q_start + min(b0 + 32 * k + lane, p.c.B - 1) + 1);
+        for (int k = 0; k < 4; ++k) ends[k] = load_i32(p.c.q_start + min(b0 + 32 * k + lane, p.c.B - 1) + 1);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             b += __popc(__ballot_sync(0xffffffffu, b0 + 32 * k + lane < p.c.B && ends[k] <= t));
@@ -64,8 +65,8 @@ __device__ __forceinline__ Place place_of(const AppendParams& p, int t, int lane
     if (s.n == 0) return none;
     const bool placed = t >= s.q0 && t < s.q0 + s.n;         // (not where q_start decreases)
     const int i = placed ? s.kv - s.n + (t - s.q0) : 0;
-    const int at = p.positions ? __ldg(p.positions + t) : i;
-    const int page = __ldg(p.c.page_table + (size_t)b * p.c.max_pages + (i >> p.c.page_shift));
+    const int at = p.positions ? load_i32(p.positions + t) : i;
+    const int page = load_i32(p.c.page_table + (size_t)b * p.c.max_pages + (i >> p.c.page_shift));
     if (!placed || page < 0 || page >= p.c.num_pages || (p.rot && (at < 0 || at >= p.rope_len))) {
         if (lane == 0) report_sequence(p.ws, b);
         return none;
