@@ -459,7 +459,8 @@ fa_status fa_paged_step(const fa_paged_step_args* a, void* workspace, void* stre
         for (int j = i + 1; j < kArrays; ++j) {
             const uintptr_t x = reinterpret_cast<uintptr_t>(arrays[i].p), y = reinterpret_cast<uintptr_t>(arrays[j].p);
             if (!x || !y || arrays[i].bytes == 0 || arrays[j].bytes == 0) continue;
-            if (x == y && ((i == 0 && (j == 7 || j == 8)) || (i == 1 && j == 10))) continue;     // in place
+            // in place (keep_len only as kv_len itself: a step that cannot be made leaves it as it was)
+            if (x == y && ((i == 0 && (j == 7 || (j == 8 && a->keep_len == a->kv_len))) || (i == 1 && j == 10))) continue;
             if (x < y + arrays[j].bytes && y < x + arrays[i].bytes)
                 return fail(FA_ERR_INVALID_ARG, "%s and %s overlap", arrays[i].name, arrays[j].name);
         }

@@ -223,8 +223,8 @@ fa_status fa_fwd_paged_scaled(const fa_paged_kv *c, const fa_paged_scales *scale
  * entry first.  (So a step that gives pages back undoes the one that took
  * them.)  The first S entries of every row are a prefix's that all sequences
  * share and stay as they are; keep_len may reach up to S x P there.
- *   new_len, keep_len, kv_len   device int32 [B]; keep_len may be NULL: all are
- *               kept.
+ *   new_len, keep_len, kv_len   device int32 [B]; keep_len may be NULL, or
+ *               kv_len itself: all are kept.
  *   page_table  device int32 [B][max_pages], in and out.  Entries that are
  *               given back stay there, and mean nothing.
  *   free_pages  device int32 [num_pages], in and out: the stack, its bottom first.

@@ -1,10 +1,12 @@
-"""fa_paged_step beside its neighbours: appends that follow at once."""
+"""fa_paged_step beside its neighbours: appends that follow at once, arrays that are the same."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
 
-from tests.test_paged import fa  # noqa: F401  (fa: the fixture)
-from tests.test_paged_step import Server, mixed, same, step
+from tests.test_paged import FAKE, fa  # noqa: F401  (fa: the fixture)
+from tests.test_paged_step import Server, _args, mixed, same, step
 
 gpu = pytest.mark.gpu
 
@@ -98,3 +100,39 @@ def test_an_append_of_what_the_one_before_it_rotated(fa, bits):  # noqa: F811
     fa.default_workspace("cuda").check()
     for other in got[1:]:
         assert all(torch.equal(a, b) for a, b in zip(got[0], other))
+
+
+# ------------------------------------------------------------- keep_len as an output
+def test_keep_len_is_no_output(fa):  # noqa: F811
+    """A step that cannot be made writes kv_len to kv_len_out: that must not be what it kept."""
+    lib, a = fa.load_library(), _args(fa)
+    for kw in (dict(kv_len_out=a.keep_len), dict(kv_len_out=a.keep_len + 4), dict(kv_len_out=a.kv_len, keep_len=a.kv_len + 8)):
+        assert lib.fa_paged_step(ctypes.byref(_args(fa, **kw)), FAKE, None) == fa.ERR_INVALID_ARG
+        assert b"kv_len_out and keep_len overlap" in lib.fa_last_error()
+
+
+@gpu
+@pytest.mark.parametrize("pad", [0, 6000])
+def test_keep_len_may_be_kv_len(fa, pad):  # noqa: F811
+    """All tokens kept, said by the same array; in place or not; and where the step cannot be made."""
+    old = [32, 50, 9, 0]
+    for place in (True, False):
+        s = Server(old, old, [1, 70, 2, 33], 16, pad=pad)
+        d = s.device()
+        d["keep"] = d["kv"]
+        out = d["kv"] if place else torch.empty_like(d["kv"])
+        same(d, step(fa, s, d, kv_len_out=out), s.want(), kv=out)
+        fa.default_workspace("cuda").check()
+        s = Server(old, old, [1, 70, 2, 33], 16, pad=pad, spare=0)
+        s.count -= 1                             # a page too few, for the last sequence
+        d = s.device()
+        d["keep"] = d["kv"]
+        out = d["kv"] if place else torch.empty_like(d["kv"])
+        got = step(fa, s, d, kv_len_out=out)
+        with pytest.raises(fa.FAError, match="sequence 3"):
+            fa.default_workspace("cuda").check()
+        assert np.array_equal(out.cpu().numpy(), old) and not got[0].any()
+    s = Server(old, [30, 50, 9, 0], [1, 1, 1, 1], 16)
+    d = s.device()
+    with pytest.raises(fa.FAError, match="overlap"):
+        step(fa, s, d, kv_len_out=d["keep"])
