@@ -17,7 +17,8 @@ static_assert(kKeys == 1 << kShift, "keys of a tile");
 // Units that the consumers read where the loader puts them.  It writes unit nu once
 // all of them have begun unit nu - 2, and so are done with nu - 3.
 constexpr int kSegs = 4;
-// Entries of the line's index: fewer than the bf16 kernel has room for.
+// Entries of the line's index: what two CTAs on an SM leave room for (the assertion
+// below; 16 rows of 128 columns have 268 bytes to spare).
 constexpr int kCodeEntries = 300;
 enum CodeSite : uint32_t { S_PC_FULL = 112, S_PC_EMPTY, S_PC_DRAIN, S_PC_Q, S_PC_Q_EMPTY };
 

@@ -6,10 +6,11 @@
 //
 // S = Q K^T takes K's codes as they are: its operands are 8-bit.  Q, which is
 // bf16, becomes the sum of two e4m3 numbers: a row is scaled by a power of two
-// to a largest element in [224, 448], hi = e4m3(q), lo = e4m3(q - hi), and
+// to a largest element in (224, 448], hi = e4m3(q), lo = e4m3(q - hi), and
 // S = hi K^T + lo K^T into one accumulator.  A bf16 number has 8 significant
-// bits, hi and lo 4 each, so that this is exact for elements from 2^-10 of the
-// row's largest on, and off by at most 2^-18 of that below.  Two 8-bit products
+// bits, hi and lo 4 each, and lo's last one is at least 2^-9: this is exact for
+// elements of 1/4 and more, 2^-9.8 of the row's largest, and off by at most 2^-10,
+// 2^-17.8 of that, below.  Two 8-bit products
 // cost what a bf16 one does (a product takes twice the columns at once), and K
 // is neither converted nor moved again.  The softmax warps split their rows of Q
 // in place, in shared memory.

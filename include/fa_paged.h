@@ -194,15 +194,19 @@ fa_status fa_kv_append_scaled(const fa_paged_kv *c, const fa_paged_scales *scale
                               void *workspace, void *stream);
 
 /* fa_fwd_paged over a cache held in 8 bits: the same softmax over the values
- * that the codes stand for.  Scales, sums and products are fp32's; a query's
- * elements keep their 8 bits down to 2^-10 of the row's largest, and an absolute
- * error of 2^-18 of that below (where more than 16 rows go per sequence and kv
- * head; exactly otherwise); P is rounded to 11 significant bits where a key's
- * share in o (its probability times its page's v scale) is at least 2^-22 of the
- * row's largest, and by up to 2^-33 of that largest below; for 9 to 16 rows that
- * goes by the probability alone, and holds to 2^-29 and 2^-40.  Except for 9 to
- * 16 rows, a v scale below 2^-80 of the largest one that the rows have seen, or
- * below 2^-82, counts as that.
+ * that the codes stand for.  Scales, sums and products are fp32's (a k scale
+ * times an element of q stays below 2^120).  By rows per sequence and kv head
+ * (max_q_len x Hq / Hkv), and for the keys of a shared prefix as for more than 16:
+ *   more than 16   a query's elements keep their 8 bits from 2^-9.8 of the row's
+ *                  largest on, and are off by up to 2^-17.8 of that below; exact
+ *                  for fewer rows.
+ *   not 9 to 16    P is rounded to 11 significant bits where a key's share in o
+ *                  (its probability times its page's v scale) is at least 2^-22 of
+ *                  the row's largest, and by up to 2^-33 of that largest below.  A
+ *                  v scale below 2^-80 of the largest one that the rows have seen,
+ *                  or below 2^-82, counts as that.
+ *   9 to 16        P is rounded so by the probability alone, from 2^-29 of the
+ *                  largest on, and by up to 2^-40 of it below; any v scales.
  * scratch: fa_paged_scratch_bytes().                                        */
 fa_status fa_fwd_paged_scaled(const fa_paged_kv *c, const fa_paged_scales *scales, const fa_paged_fwd_args *a,
                               const fa_mask_desc *mask, const fa_score_desc *sc, void *scratch, size_t scratch_bytes,

@@ -165,3 +165,39 @@ def test_scales_that_grow(fa, rows, prefix, small, large, D, B, n, order):  # no
     bt = Keys(B, e4m3(r.uniform(-40, 0, n)), r.uniform(0.02, 0.03, n // PAGE), codes(4, (n, D)),
               np.where(at, small, large * r.uniform(0.7, 1.0, n // PAGE)), D)
     bt.check(bt.run(fa, rows, n // 2 if prefix else 0), rows, few(rows, prefix))
+
+
+@gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("prefix", [False, True])
+def test_elements_of_q_far_below_the_row_s_largest(fa, D, prefix):  # noqa: F811
+    """In the kernel for many rows, and for a prefix with any, q is the sum of two e4m3 numbers, a row's largest element at
+    224 to 448 of their units: exact down to 2^-2 of a unit, 2^-9.8 of the largest, and off by half of lo's least step,
+    2^-10 of a unit or 2^-17.8 of the largest, below.  One key whose first element is 0 and whose second is 448: its score
+    is lse, q1 x 448 / 16 but for fp32's 4 roundings."""
+    Hq, r = 64, np.random.default_rng(1)
+    q = np.zeros((1, Hq, D))
+    q[0, :, 0] = r.choice([225 / 256, 226 / 256, 1.0, 1.25, 1.75, 447 / 256 - 1 / 256], Hq)
+    q[0, :, 1] = 2.0 ** -r.integers(8, 20, Hq) * r.integers(128, 256, Hq) / 128
+    q[0, ::7, 1] = 255 / 256 / 1024              # the largest that the split may miss
+    q[0, 1::7, 1] = 2.0 ** -9                    # and one that it holds
+    qd = torch.from_numpy(q).cuda().to(torch.bfloat16)
+    assert (qd.double().cpu().numpy() == q).all()
+    pages = 2 if prefix else 1
+    k = torch.zeros((pages, 1, PAGE, D), device="cuda")
+    k[..., 1] = 448
+    v = torch.ones((pages, 1, PAGE, D), device="cuda")
+    one = torch.ones((pages, 1), device="cuda")
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")     # noqa: E731
+    n = PAGE + 1 if prefix else 1
+    f8 = torch.float8_e4m3fn
+    o, lse = fa.fwd_paged(qd, k.to(f8), v.to(f8), i32(*range(pages)).view(1, -1), i32(n), i32(0, 1), k_scale=one, v_scale=one.clone(),
+                          max_q_len=1, mask="full", shared_len=PAGE if prefix else 0, scale=1 / 16, out_fp32=True)
+    fa.default_workspace("cuda").check()
+    top, score = q[0, :, 0], q[0, :, 1] * 448 / 16
+    off = np.abs(lse.double().cpu().numpy()[0] - score - np.log(n))
+    exact = q[0, :, 1] >= 2.0 ** -9 * top
+    # (lse itself is rounded, and the prefix's products are summed: 2^-20)
+    assert exact.any() and (off[exact] <= 2.0 ** -20 * 8).all()
+    assert (~exact).any() and (off[~exact] <= 2.0 ** -17.8 * (top * 448 / 16)[~exact] + 2.0 ** -17).all()
+    assert torch.allclose(o.float(), torch.ones_like(o.float()), atol=1e-6)
