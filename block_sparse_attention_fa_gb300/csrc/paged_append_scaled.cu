@@ -143,15 +143,13 @@ __device__ __forceinline__ void append_page(const AppendScaledParams& p, int u, 
         int ea, eb;
         pieces(x, rot, ea, eb);
         const uint16_t* const from = src + static_cast<long long>(row0 + x / kItems) * step;
-        // (plain loads here and below, but for the tables of the rotation: what the kernel
-        // before this one writes, it may still be writing when this one starts)
-        *reinterpret_cast<uint4*>(w.a) = *reinterpret_cast<const uint4*>(from + ea);
-        *reinterpret_cast<uint4*>(w.b) = *reinterpret_cast<const uint4*>(from + eb);
+        load_now(from + ea, w.a);
+        load_now(from + eb, w.b);
     };
     // the token's row of the tables; -1: it has no place
     auto place = [&](int x) {
         if (!p.rot) return 0;
-        const int at = p.positions ? load_i32(p.positions + row0 + x / kItems) : lo + x / kItems;
+        const int at = p.positions ? load_now(p.positions + row0 + x / kItems) : lo + x / kItems;
         if (at >= 0 && at < p.rope_len) return at;
         report_sequence(p.ws, b);
         return -1;
