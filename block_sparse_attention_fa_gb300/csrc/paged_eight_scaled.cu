@@ -33,8 +33,8 @@
 // DRAM bounds long contexts; ragged batches on pages of 16 keys the chain of a tile
 // in each warp, some 1800 cycles of 2500, and the two loader warps' issue
 // (paged_codes.cuh), evenly.  8 sequences of 32768 tokens, 8 kv heads of 128
-// columns: 89.7 us, 79.1 at the copy rate (bf16 cache: 163).  128 of up to 4096, 8
-// kv heads of 64 columns, pages of 16: 75.3 us, 41.0 at the copy rate.  One of 520
+// columns: 89.5 us, 79.1 at the copy rate (bf16 cache: 163).  128 of up to 4096, 8
+// kv heads of 64 columns, pages of 16: 75.5 us, 41.0 at the copy rate.  One of 520
 // tokens: 9.6, most of it the first run through the code.
 //
 // V rows of keys that no row of the unit sees are cleared in shared memory before

@@ -30,7 +30,7 @@
 //
 // What bounds it is the chain of a 64-key half, 1500 to 1700 cycles of softmax
 // alone: 4 chunks of up to 1024 tokens on up to 8192 keys, 32 heads on 8 of 128
-// columns, take 220 us (187 over bf16, 116 at the bf16 rate); without V's
+// columns, take 221 us (187 over bf16, 116 at the bf16 rate); without V's
 // conversion 215, with half of S's products 210, without either, the exponentials
 // and most of P V 197.  A shared prefix of 16384 keys for 64 tokens takes 28: its
 // first products start after 8, the partials' stores take 4.
