@@ -208,16 +208,26 @@ __device__ __forceinline__ float times_2_to(float l, float d) {
     const float half = ex2_approx(0.5f * d);
     return l * half * half;
 }
-// Nor may such an M weigh parts of a row that are to be joined: l and M times powers of
-// two (and O by what is returned), so that l is 2^-17 to 2^-16 and M says what the part
-// is worth.  (O is then 2^-16 of a value at most, so that no sum of parts overflows.)
+// Nor may such an M weigh parts of a row that are to be joined, where their l are more
+// than 2^90 apart: outside of 2^-16 .. 2^75 l and M times powers of two (and O by what is
+// returned), so that l is 2^-17 to 2^-16 and M says what the part is worth.  (O is then
+// 2^-16 of a value at most, so that no sum of parts overflows.  Inside, M stays as it
+// is, for the sum may be rounded where M is past 2^20.)
 __device__ __forceinline__ float even_out(float& m, float& l) {
-    if (l == 0.f) return 1.f;
     const int k = min(((__float_as_int(l) >> 23) & 255) - 127, 109);
+    if (l == 0.f || (k >= -16 && k < 75)) return 1.f;
     const float f = __int_as_float((110 - k) << 23);
     m += static_cast<float>(k + 17);
     l *= f;
     return f;
+}
+
+// P, two f16 numbers: 65504 beyond that (2^kPTop is half of it, but a reference that far
+// below scores past 2^24 is rounded, and an infinity would be no weight), NaN stays.
+__device__ __forceinline__ uint32_t pack_p(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
 }
 
 // Where a row's partials lie: `count` rows of a kernel's slots, from `first`

@@ -286,8 +286,8 @@ paged_eight_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
                 const float iv = sc[3 * (kKeys / 16) + page[u]];
                 l[0] = fmaf(w[0] + w[2], iv, l[0]);
                 l[1] = fmaf(w[1] + w[3], iv, l[1]);
-                pb[u][0] = transpose_8x8(pack_f16x2(w[0], w[1]));
-                pb[u][1] = transpose_8x8(pack_f16x2(w[2], w[3]));
+                pb[u][0] = transpose_8x8(pack_p(w[0], w[1]));
+                pb[u][1] = transpose_8x8(pack_p(w[2], w[3]));
             }
             // O^T += V^T P^T, 16 columns at a time
 #pragma unroll

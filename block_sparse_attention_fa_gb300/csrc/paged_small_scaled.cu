@@ -286,7 +286,7 @@ paged_small_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
                     const float p0 = ex2_approx(x[nt][2 * e] + nm), p1 = ex2_approx(x[nt][2 * e + 1] + nm);
                     l[e] += p0 + p1;
                     *reinterpret_cast<uint32_t*>(smem + L::kP + (gr + 8 * e) * kPRow + 2 * (16 * warp + 8 * nt + 2 * tq)) =
-                        pack_f16x2(p0, p1);
+                        pack_p(p0, p1);
                 }
             }
 #pragma unroll

@@ -791,7 +791,7 @@ paged_tiles_scaled_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
                                     exp2_pair(p0, p1, x[16 * q + 2 * e], x[16 * q + 2 * e + 1], sc[q], nm);
                                     const int a2 = (e & 1) * 2;
                                     fadd2(rs[a2], rs[a2 + 1], rs[a2], rs[a2 + 1], p0, p1);
-                                    pk[8 * u + e] = pack_f16x2(p0, p1);
+                                    pk[8 * u + e] = pack_p(p0, p1);
                                 }
                                 l = fmaf((rs[0] + rs[1]) + (rs[2] + rs[3]), iv[q], l);
                             }

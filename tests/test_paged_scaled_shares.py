@@ -201,3 +201,24 @@ def test_elements_of_q_far_below_the_row_s_largest(fa, D, prefix):  # noqa: F811
     assert exact.any() and (off[exact] <= 2.0 ** -20 * 8).all()
     assert (~exact).any() and (off[~exact] <= 2.0 ** -17.8 * (top * 448 / 16)[~exact] + 2.0 ** -17).all()
     assert torch.allclose(o.float(), torch.ones_like(o.float()), atol=1e-6)
+
+
+@gpu
+@pytest.mark.parametrize("rows,prefix,most", [(4, False, 34), (12, False, 34), (40, False, 23), (40, True, 23)])
+@pytest.mark.parametrize("power", [20, 23, 24, 25, 26, 27, 28, 30, 34])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("B", [3, 400])
+def test_scores_past_20_bits(fa, rows, prefix, most, power, sign, B):  # noqa: F811
+    """Scores so large that a reference 8 or 15 below them is rounded, by up to 16: all are the same, so that O is the mean.
+    (P may end up at 2^16, which f16 ends just below: 2^-11 of O.  In the kernel for many rows the product of S and its
+    scale is not rounded but the reference is, by half a unit of scores past 2^23, and P may be anything beyond.)"""
+    if power > most:
+        return
+    n, D = 512, 64
+    bt = Keys(B, np.full(n, sign * 256.0), np.full(n // PAGE, 2.0 ** (power - 8)), codes(6, (n, D)), np.ones(n // PAGE), D)
+    o, lse, q0 = bt.run(fa, rows, n // 2 if prefix else 0)
+    assert np.isfinite(o).all() and np.isfinite(lse).all()
+    mean, A = bt.v_code.mean(0), np.abs(bt.v_code).mean(0)
+    assert (np.abs(o - mean) <= (2.0 ** -10 + 2.0 ** -12) * A).all()
+    score = q0 * sign * 2.0 ** (power - 4)
+    assert (np.abs(lse - (score + np.log(n))) <= np.abs(score) * 2.0 ** -21 + 2.0 ** -13).all()
